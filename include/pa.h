@@ -376,6 +376,150 @@ PA_API pa_status pa_mixed_step(const pa_decode_part *decode, const pa_prefill_pa
                         pa_dtype out_dtype, pa_stream_t stream);
 
 /*
+ * The bounded cache.  The pages' cache grows with every token; these calls
+ * bound what one sequence costs, in two ways that the pages do not describe
+ * (this library's extensions).  A sliding window with a few first tokens that
+ * stay visible (pa_decode_window, pa_prefill_chunk_window): what lies between
+ * is not read any more, and its blocks can be given back (pa_bm_release_window).
+ * Eviction by accumulated attention weight (pa_decode_weights, pa_evict): the
+ * decode adds up what each cached token received, and from time to time the
+ * cache goes back to a budget, keeping the tokens that received most.
+ */
+
+/*
+ * pa_decode_window -- pa_decode with a sliding window and first tokens that
+ * stay visible.  Sequence i's query, at position L - 1 (L = seq_lens[i]), sees
+ *     p < num_sinks  or  p >= L - window
+ * and out[i][h] is the softmax-weighted sum over those p alone.  L == 0 yields
+ * a zero row; any other query sees at least itself.
+ *
+ *   window      >= 1: tokens up to and including the query's own that it sees
+ *   num_sinks   >= 0: first tokens that stay visible
+ *   block_tables  as for pa_decode; the entries of blocks without a visible
+ *               token are not read and may hold anything
+ *   workspace   >= pa_decode_window_workspace_bytes(...) bytes for the same
+ *               arguments, else as for pa_decode
+ *   all other arguments as for pa_decode.
+ * Every shape of pa_decode is served, by the tensor-core decode whatever
+ * pa_set_decode_kernel says: the kernel walks the visible blocks as one
+ * shortened sequence.  K and V of tokens that are not visible never reach the
+ * result, whatever they hold (NaN included).
+ */
+PA_API size_t pa_decode_window_workspace_bytes(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
+                                               int32_t head_dim, int32_t block_size, int32_t max_seq_len,
+                                               int32_t window, int32_t num_sinks, int32_t partition_size);
+PA_API pa_status pa_decode_window(const void *q, pa_dtype q_dtype, int32_t num_seqs, int32_t num_q_heads,
+                                  const void *k_cache, const void *v_cache, const pa_kv_cache *cache,
+                                  const int32_t *block_tables, int32_t max_blocks_per_seq, const int32_t *seq_lens,
+                                  int32_t max_seq_len, int32_t window, int32_t num_sinks, float scale,
+                                  int32_t partition_size, void *workspace, size_t workspace_bytes, void *out,
+                                  pa_dtype out_dtype, pa_stream_t stream);
+
+/*
+ * pa_prefill_chunk_window -- pa_prefill_chunk with a sliding window and first
+ * tokens that stay visible.  The row at position t sees
+ *     p <= t  and  (p < num_sinks  or  p > t - window).
+ *   window, num_sinks  as for pa_decode_window (a row at position t sees what
+ *               pa_decode_window's query of a sequence of t + 1 tokens sees)
+ *   block_tables  the entries of blocks in which no row of the chunk sees a
+ *               token are not read
+ *   all other arguments as for pa_prefill_chunk.
+ * Every shape of pa_prefill_chunk is served on the tensor cores.  Tokens that
+ * no row of the chunk sees never reach the result, whatever they hold; V of
+ * a token that some row of the chunk sees has to be finite (a row that does
+ * not see it may share a tile with one that does).
+ */
+PA_API pa_status pa_prefill_chunk_window(const void *q_chunk, pa_dtype q_dtype, const int32_t *cu_q_lens,
+                                         const int32_t *q_start, int32_t num_chunks, int32_t max_q_len,
+                                         int32_t num_q_heads, const void *k_cache, const void *v_cache,
+                                         const pa_kv_cache *cache, const int32_t *block_tables,
+                                         int32_t max_blocks_per_seq, const int32_t *seq_lens, int32_t max_seq_len,
+                                         int32_t window, int32_t num_sinks, float scale, void *out,
+                                         pa_dtype out_dtype, pa_stream_t stream);
+
+/*
+ * pa_decode_weights -- pa_decode that also accumulates the attention weight of
+ * every cached token.  With a = softmax_p(scale * q[i][h] . K_i[p][g]) as in
+ * pa_decode, for every position p < L of sequence i and KV head g
+ *     w = sum over the query heads h of g of a[h][p]
+ *     weights[r][g][p] = (p < fresh_from[i] ? decay * weights[r][g][p] : 0) + w
+ * with r = weight_rows[i].  The sum over p of w is the number of query heads
+ * per KV head.  Entries at p >= L are left as they are.
+ *
+ *   weights      device fp32 [num_weight_rows][num_kv_heads][weights_stride],
+ *                16-byte aligned; weights_stride >= max_seq_len
+ *   weight_rows  device int32 [num_seqs], distinct, or NULL: sequence i uses
+ *                row i.  Rows of weights that no sequence names are untouched.
+ *   fresh_from   device int32 [num_seqs], or NULL for L - 1: tokens from there
+ *                on have no running weight yet, and what weights holds for them
+ *                is not read (0: the first decode after a prompt)
+ *   decay        finite; 1 adds up, 0 keeps only this step's weights
+ *   workspace    >= pa_decode_weights_workspace_bytes(...) bytes (it holds one
+ *                fp32 score per query head and token), else as for pa_decode
+ *   all other arguments as for pa_decode, seq_lens[i] <= max_seq_len included.
+ * out equals pa_decode's within the decode tolerance.  A row of weight_rows
+ * outside [0, num_weight_rows) sets PA_ERR_DEVICE_CHECK and is skipped.
+ */
+PA_API size_t pa_decode_weights_workspace_bytes(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
+                                                int32_t head_dim, int32_t max_seq_len, int32_t partition_size);
+PA_API pa_status pa_decode_weights(const void *q, pa_dtype q_dtype, int32_t num_seqs, int32_t num_q_heads,
+                                   const void *k_cache, const void *v_cache, const pa_kv_cache *cache,
+                                   const int32_t *block_tables, int32_t max_blocks_per_seq, const int32_t *seq_lens,
+                                   int32_t max_seq_len, float scale, int32_t partition_size, void *workspace,
+                                   size_t workspace_bytes, void *out, pa_dtype out_dtype, float *weights,
+                                   int64_t weights_stride, int32_t num_weight_rows, const int32_t *weight_rows,
+                                   const int32_t *fresh_from, float decay, pa_stream_t stream);
+
+/*
+ * pa_evict -- bring every sequence of more than `budget` cached tokens back to
+ * `budget`, per KV head, in place.
+ *
+ * Slot s of sequence i (L = seq_lens[i] slots, T = num_tokens[i] tokens seen
+ * since its start) holds, for KV head g, the token of position
+ *     pos(s) = s < ordered_from[i] ? positions[r][g][s] : T - L + s.
+ * Protected tokens (pos < num_sinks or pos >= T - num_recent) stay; of the
+ * others those of largest weights[r][g][s], so that `budget` stay in all
+ * (equal weights: the lowest slot; NaN counts as the smallest weight).  Kept
+ * tokens of slots < budget stay where they are; kept tokens of slots >= budget
+ * move, in slot order, into the slots < budget that became free, in slot
+ * order.  A sequence of at most `budget` tokens moves nothing.  With n =
+ * min(L, budget), for every slot s < n and the token now in it:
+ *     new_weights[r][g][s], new_positions[r][g][s]  its weight and position,
+ *     new_seq_lens[i] = n,
+ * and K and V of its head are in slot s of the block table.  The slots from n
+ * on hold no token of the sequence any more; pa_bm_truncate gives their blocks
+ * back.  Attention does not depend on the order of the cached tokens, so the
+ * decodes run on as they are with the new lengths; appended tokens go to slots
+ * n, n + 1, ..., and the next call's ordered_from is n.  (The windowed calls
+ * take slots for positions: they do not combine with an evicted cache.)
+ *
+ *   k_cache, v_cache  device pools described by *cache; no block that holds a
+ *                slot < n may be shared with another sequence (pa_bm_unshare)
+ *   block_tables device int32 [num_seqs][max_blocks_per_seq]
+ *   seq_lens     device int32 [num_seqs], each <= max_seq_len
+ *   num_tokens, ordered_from  device int32 [num_seqs]; L <= num_tokens,
+ *                0 <= ordered_from <= L (0 before the first eviction)
+ *   budget       >= 1 and >= num_sinks + num_recent, both >= 0
+ *   weights, positions, new_weights, new_positions  device fp32 / int32
+ *                [num_weight_rows][num_kv_heads][weights_stride]; the new
+ *                arrays may be the old ones or must not overlap them
+ *   weight_rows  as for pa_decode_weights
+ *   new_seq_lens device int32 [num_seqs]; may be seq_lens itself
+ *   workspace    device, >= pa_evict_workspace_bytes(...) bytes, 256-byte
+ *                aligned; its contents on entry are ignored
+ * A sequence whose metadata is out of range sets PA_ERR_DEVICE_CHECK and is
+ * left as it is; so is a move whose block id is out of range.
+ */
+PA_API size_t pa_evict_workspace_bytes(int32_t num_seqs, int32_t num_kv_heads, int32_t max_seq_len, int32_t budget);
+PA_API pa_status pa_evict(void *k_cache, void *v_cache, const pa_kv_cache *cache, int32_t num_seqs,
+                          const int32_t *block_tables, int32_t max_blocks_per_seq, const int32_t *seq_lens,
+                          int32_t max_seq_len, const int32_t *num_tokens, const int32_t *ordered_from, int32_t budget,
+                          int32_t num_sinks, int32_t num_recent, const float *weights, const int32_t *positions,
+                          float *new_weights, int32_t *new_positions, int64_t weights_stride, int32_t num_weight_rows,
+                          const int32_t *weight_rows, int32_t *new_seq_lens, void *workspace, size_t workspace_bytes,
+                          pa_stream_t stream);
+
+/*
  * pa_get_device_error -- read and clear the current device's error word.
  * Synchronises `stream`, then stores into *code the first device-side status
  * recorded since the last clear (PA_OK if none): PA_ERR_DEVICE_CHECK for
@@ -432,6 +576,22 @@ PA_API pa_status pa_selftest_wait_timeout(pa_stream_t stream);
  *  - pa_bm_block_table: copy the sequence's table into `table` (host int32,
  *    `capacity` entries); *num_blocks and *seq_len receive its size and length
  *    (set even when capacity is too small, which returns PA_ERR_INVALID_ARG).
+ *  - pa_bm_unshare: before pa_evict, make every block that holds a position
+ *    < num_tokens of `seq` its own: a shared one is replaced by a fresh copy
+ *    (pairs as pa_bm_append gives them, at most one per block; run
+ *    pa_copy_blocks on them first), and none of them is found by prefix reuse
+ *    any more, as its contents are about to change.  PA_ERR_NO_BLOCKS if the
+ *    free blocks do not cover the copies; PA_ERR_INVALID_ARG with *num_cow = the
+ *    pairs needed if cow_capacity is too small.  Nothing changes on error.
+ *  - pa_bm_truncate: after pa_evict, keep the first new_len positions of `seq`
+ *    and release the blocks behind them.  Later blocks of the sequence take no
+ *    part in prefix reuse (unless new_len is 0).
+ *  - pa_bm_release_window: release the blocks of `seq` that no later query sees
+ *    under a sliding window (window, num_sinks as for pa_decode_window): those
+ *    that hold only positions in [num_sinks, len + 1 - window), len the
+ *    sequence's length.  Call it once the attention over the appended tokens is
+ *    enqueued.  Their entries in the block table become -1; the length and the
+ *    other entries stay.  *num_released receives their number.
  *  - pa_bm_get_stats: pool occupancy.
  * Not thread-safe: one manager per thread, or external locking.
  */
@@ -459,6 +619,11 @@ PA_API pa_status pa_bm_free(pa_block_manager *bm, int32_t seq);
 PA_API pa_status pa_bm_block_table(const pa_block_manager *bm, int32_t seq,
                                    int32_t *table, int32_t capacity,
                                    int32_t *num_blocks, int32_t *seq_len);
+PA_API pa_status pa_bm_unshare(pa_block_manager *bm, int32_t seq, int32_t num_tokens, int32_t *cow_pairs,
+                               int32_t cow_capacity, int32_t *num_cow);
+PA_API pa_status pa_bm_truncate(pa_block_manager *bm, int32_t seq, int32_t new_len);
+PA_API pa_status pa_bm_release_window(pa_block_manager *bm, int32_t seq, int32_t window, int32_t num_sinks,
+                                      int32_t *num_released);
 PA_API pa_status pa_bm_get_stats(const pa_block_manager *bm, pa_bm_stats *stats);
 
 /* Static, human-readable name of a status code. */

@@ -21,6 +21,8 @@ __all__ = [
     "pa_prefill_chunk", "pa_get_device_error", "pa_status_string", "pa_selftest_wait_timeout",
     "BlockManager", "PaBmStats", "pa_set_decode_kernel", "decode_kernel", "DECODE_KERNELS", "pa_decode_write",
     "pa_mixed_step", "PaDecodePart", "PaPrefillPart",
+    "pa_decode_window_workspace_bytes", "pa_decode_window", "pa_prefill_chunk_window",
+    "pa_decode_weights_workspace_bytes", "pa_decode_weights", "pa_evict_workspace_bytes", "pa_evict",
 ]
 
 PA_F16, PA_BF16, PA_FP8_E4M3, PA_F32 = 0, 1, 2, 3
@@ -93,6 +95,21 @@ def lib() -> ctypes.CDLL:
                                        I32, P, I32, F, P, ctypes.c_int, P]
         L.pa_mixed_step.argtypes = [ctypes.POINTER(PaDecodePart), ctypes.POINTER(PaPrefillPart), ctypes.c_int, I32,
                                     P, P, ctypes.POINTER(PaKvCache), F, ctypes.c_int, P]
+        CACHE = ctypes.POINTER(PaKvCache)
+        L.pa_decode_window_workspace_bytes.argtypes = [I32] * 9
+        L.pa_decode_window_workspace_bytes.restype = SZ
+        L.pa_decode_window.argtypes = [P, ctypes.c_int, I32, I32, P, P, CACHE, P, I32, P, I32, I32, I32, F, I32, P, SZ,
+                                       P, ctypes.c_int, P]
+        L.pa_prefill_chunk_window.argtypes = [P, ctypes.c_int, P, P, I32, I32, I32, P, P, CACHE, P, I32, P, I32, I32,
+                                              I32, F, P, ctypes.c_int, P]
+        L.pa_decode_weights_workspace_bytes.argtypes = [I32] * 6
+        L.pa_decode_weights_workspace_bytes.restype = SZ
+        L.pa_decode_weights.argtypes = [P, ctypes.c_int, I32, I32, P, P, CACHE, P, I32, P, I32, F, I32, P, SZ, P,
+                                        ctypes.c_int, P, I64, I32, P, P, F, P]
+        L.pa_evict_workspace_bytes.argtypes = [I32] * 4
+        L.pa_evict_workspace_bytes.restype = SZ
+        L.pa_evict.argtypes = [P, P, CACHE, I32, P, I32, P, I32, P, P, I32, I32, I32, P, P, P, P, I64, I32, P, P, P, SZ,
+                               P]
         L.pa_get_device_error.argtypes = [P, ctypes.POINTER(I32)]
         L.pa_set_decode_kernel.argtypes = [I32]
         L.pa_selftest_wait_timeout.argtypes = [P]
@@ -108,10 +125,15 @@ def lib() -> ctypes.CDLL:
         L.pa_bm_free.argtypes = [VP, I32]
         L.pa_bm_block_table.argtypes = [VP, I32, P, I32, ctypes.POINTER(I32), ctypes.POINTER(I32)]
         L.pa_bm_get_stats.argtypes = [VP, ctypes.POINTER(PaBmStats)]
+        L.pa_bm_unshare.argtypes = [VP, I32, I32, P, I32, ctypes.POINTER(I32)]
+        L.pa_bm_truncate.argtypes = [VP, I32, I32]
+        L.pa_bm_release_window.argtypes = [VP, I32, I32, I32, ctypes.POINTER(I32)]
         for name in ("pa_reshape_and_cache", "pa_copy_blocks", "pa_decode", "pa_prefill_chunk", "pa_set_decode_kernel",
                      "pa_decode_write", "pa_mixed_step",
                      "pa_get_device_error", "pa_selftest_wait_timeout", "pa_bm_create", "pa_bm_new_sequence",
-                     "pa_bm_fork", "pa_bm_append", "pa_bm_free", "pa_bm_block_table", "pa_bm_get_stats"):
+                     "pa_bm_fork", "pa_bm_append", "pa_bm_free", "pa_bm_block_table", "pa_bm_get_stats",
+                     "pa_decode_window", "pa_prefill_chunk_window", "pa_decode_weights", "pa_evict", "pa_bm_unshare",
+                     "pa_bm_truncate", "pa_bm_release_window"):
             getattr(L, name).restype = ctypes.c_int
         _lib = L
     return _lib
@@ -276,6 +298,121 @@ def pa_mixed_step(q: torch.Tensor, block_tables: torch.Tensor, seq_lens: torch.T
                             _dtype_code(out.dtype), _stream(stream)), "pa_mixed_step")
 
 
+def _i32(t: torch.Tensor | None, name: str) -> int | None:
+    if t is not None and t.dtype != torch.int32:
+        raise TypeError(f"{name} must be int32")
+    return _dev(t, name)
+
+
+def pa_decode_window_workspace_bytes(num_seqs: int, num_q_heads: int, num_kv_heads: int, head_dim: int,
+                                     block_size: int, max_seq_len: int, window: int, num_sinks: int,
+                                     partition_size: int = 0) -> int:
+    return int(lib().pa_decode_window_workspace_bytes(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size,
+                                                      max_seq_len, window, num_sinks, partition_size))
+
+
+def pa_decode_window(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, cache: PaKvCache,
+                     block_tables: torch.Tensor, seq_lens: torch.Tensor, max_seq_len: int, window: int,
+                     num_sinks: int, scale: float, out: torch.Tensor, workspace: torch.Tensor | None = None,
+                     partition_size: int = 0, stream=None) -> None:
+    """pa_decode over the first ``num_sinks`` and the last ``window`` tokens of each sequence.
+    ``workspace``: uint8 tensor of >= pa_decode_window_workspace_bytes(...) bytes."""
+    B, hq, _ = q.shape
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _ok(lib().pa_decode_window(_dev(q, "q"), _dtype_code(q.dtype), B, hq, _dev(k_cache, "k_cache"),
+                               _dev(v_cache, "v_cache"), ctypes.byref(cache), _i32(block_tables, "block_tables"),
+                               block_tables.shape[1], _i32(seq_lens, "seq_lens"), int(max_seq_len), int(window),
+                               int(num_sinks), float(scale), int(partition_size), _dev(workspace, "workspace"),
+                               ws_bytes, _dev(out, "out"), _dtype_code(out.dtype), _stream(stream)),
+        "pa_decode_window")
+
+
+def pa_prefill_chunk_window(q_chunk: torch.Tensor, cu_q_lens: torch.Tensor, q_start: torch.Tensor, max_q_len: int,
+                            k_cache: torch.Tensor, v_cache: torch.Tensor, cache: PaKvCache,
+                            block_tables: torch.Tensor, seq_lens: torch.Tensor, max_seq_len: int, window: int,
+                            num_sinks: int, scale: float, out: torch.Tensor, stream=None) -> None:
+    """pa_prefill_chunk in which the row at position t sees p <= t with p < num_sinks or p > t - window."""
+    _ok(lib().pa_prefill_chunk_window(_dev(q_chunk, "q_chunk"), _dtype_code(q_chunk.dtype),
+                                      _i32(cu_q_lens, "cu_q_lens"), _i32(q_start, "q_start"), q_start.shape[0],
+                                      int(max_q_len), q_chunk.shape[1], _dev(k_cache, "k_cache"),
+                                      _dev(v_cache, "v_cache"), ctypes.byref(cache),
+                                      _i32(block_tables, "block_tables"), block_tables.shape[1],
+                                      _i32(seq_lens, "seq_lens"), int(max_seq_len), int(window), int(num_sinks),
+                                      float(scale), _dev(out, "out"), _dtype_code(out.dtype), _stream(stream)),
+        "pa_prefill_chunk_window")
+
+
+def _weights_shape(t: torch.Tensor, name: str, dtype: torch.dtype, hkv: int) -> int:
+    if t.dtype != dtype or t.dim() != 3 or t.shape[1] != hkv:
+        raise ValueError(f"{name} must be {dtype} [rows, num_kv_heads, stride]")
+    return _dev(t, name)
+
+
+def pa_decode_weights_workspace_bytes(num_seqs: int, num_q_heads: int, num_kv_heads: int, head_dim: int,
+                                      max_seq_len: int, partition_size: int = 0) -> int:
+    return int(lib().pa_decode_weights_workspace_bytes(num_seqs, num_q_heads, num_kv_heads, head_dim, max_seq_len,
+                                                       partition_size))
+
+
+def pa_decode_weights(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, cache: PaKvCache,
+                      block_tables: torch.Tensor, seq_lens: torch.Tensor, max_seq_len: int, scale: float,
+                      out: torch.Tensor, weights: torch.Tensor, weight_rows: torch.Tensor | None = None,
+                      fresh_from: torch.Tensor | None = None, decay: float = 1.0,
+                      workspace: torch.Tensor | None = None, partition_size: int = 0, stream=None) -> None:
+    """pa_decode that also adds each cached token's softmax weight, summed over the query heads of its KV head, to
+    ``weights`` (float32 [rows, Hkv, stride >= max_seq_len]).  Sequence i uses row weight_rows[i] (int32 [B]; None: i);
+    tokens from fresh_from[i] on (int32 [B]; None: the last) have no running weight yet; older ones are multiplied by
+    ``decay`` first.  ``workspace``: uint8 tensor of >= pa_decode_weights_workspace_bytes(...) bytes."""
+    B, hq, _ = q.shape
+    for t, name in ((weight_rows, "weight_rows"), (fresh_from, "fresh_from")):
+        if t is not None and tuple(t.shape) != (B,):
+            raise ValueError(f"{name} must have one entry per sequence")
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _ok(lib().pa_decode_weights(_dev(q, "q"), _dtype_code(q.dtype), B, hq, _dev(k_cache, "k_cache"),
+                                _dev(v_cache, "v_cache"), ctypes.byref(cache), _i32(block_tables, "block_tables"),
+                                block_tables.shape[1], _i32(seq_lens, "seq_lens"), int(max_seq_len), float(scale),
+                                int(partition_size), _dev(workspace, "workspace"), ws_bytes, _dev(out, "out"),
+                                _dtype_code(out.dtype),
+                                _weights_shape(weights, "weights", torch.float32, k_cache.shape[1]),
+                                weights.shape[2], weights.shape[0], _i32(weight_rows, "weight_rows"),
+                                _i32(fresh_from, "fresh_from"), float(decay), _stream(stream)), "pa_decode_weights")
+
+
+def pa_evict_workspace_bytes(num_seqs: int, num_kv_heads: int, max_seq_len: int, budget: int) -> int:
+    return int(lib().pa_evict_workspace_bytes(num_seqs, num_kv_heads, max_seq_len, budget))
+
+
+def pa_evict(k_cache: torch.Tensor, v_cache: torch.Tensor, cache: PaKvCache, block_tables: torch.Tensor,
+             seq_lens: torch.Tensor, max_seq_len: int, num_tokens: torch.Tensor, ordered_from: torch.Tensor,
+             budget: int, num_sinks: int, num_recent: int, weights: torch.Tensor, positions: torch.Tensor,
+             new_weights: torch.Tensor, new_positions: torch.Tensor, new_seq_lens: torch.Tensor,
+             weight_rows: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None) -> None:
+    """Bring every sequence of more than ``budget`` cached tokens back to ``budget``, per KV head and in place: the
+    first ``num_sinks`` and the last ``num_recent`` tokens and those of largest weight stay.  seq_lens, num_tokens,
+    ordered_from, new_seq_lens: int32 [B]; weights (float32) and positions (int32) [rows, Hkv, stride >= max_seq_len],
+    the new ones of the same shape (they may be the same tensors).  ``workspace``: uint8 tensor of >=
+    pa_evict_workspace_bytes(...) bytes."""
+    hkv, B = k_cache.shape[1], seq_lens.shape[0]
+    for t, name in ((num_tokens, "num_tokens"), (ordered_from, "ordered_from"), (new_seq_lens, "new_seq_lens"),
+                    (weight_rows, "weight_rows")):
+        if t is not None and tuple(t.shape) != (B,):
+            raise ValueError(f"{name} must have one entry per sequence")
+    for t in (positions, new_weights, new_positions):
+        if t.shape != weights.shape:
+            raise ValueError("weights, positions, new_weights and new_positions must have one shape")
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _ok(lib().pa_evict(_dev(k_cache, "k_cache"), _dev(v_cache, "v_cache"), ctypes.byref(cache), B,
+                       _i32(block_tables, "block_tables"), block_tables.shape[1], _i32(seq_lens, "seq_lens"),
+                       int(max_seq_len), _i32(num_tokens, "num_tokens"), _i32(ordered_from, "ordered_from"),
+                       int(budget), int(num_sinks), int(num_recent),
+                       _weights_shape(weights, "weights", torch.float32, hkv),
+                       _weights_shape(positions, "positions", torch.int32, hkv),
+                       _weights_shape(new_weights, "new_weights", torch.float32, hkv),
+                       _weights_shape(new_positions, "new_positions", torch.int32, hkv), weights.shape[2],
+                       weights.shape[0], _i32(weight_rows, "weight_rows"), _i32(new_seq_lens, "new_seq_lens"),
+                       _dev(workspace, "workspace"), ws_bytes, _stream(stream)), "pa_evict")
+
+
 def pa_get_device_error(stream=None) -> int:
     """Synchronise the stream, then read and clear the device error word."""
     code = ctypes.c_int32(0)
@@ -359,6 +496,27 @@ class BlockManager:
                                None if ids is None else ids.ctypes.data, slots.ctypes.data if num_tokens else None,
                                pairs.ctypes.data, 1, ctypes.byref(ncow)), "pa_bm_append")
         return slots, pairs[:ncow.value].copy()
+
+    def unshare(self, seq: int, num_tokens: int):
+        """Before an eviction: make the blocks of the first num_tokens positions the sequence's own.  Returns the
+        copy-on-write pairs int32[k, 2] to run pa_copy_blocks on first."""
+        import numpy as np
+        pairs = np.empty((-(-int(num_tokens) // self.block_size), 2), dtype=np.int32)
+        ncow = ctypes.c_int32()
+        _ok(lib().pa_bm_unshare(self._h, int(seq), int(num_tokens), pairs.ctypes.data if len(pairs) else None,
+                                len(pairs), ctypes.byref(ncow)), "pa_bm_unshare")
+        return pairs[:ncow.value].copy()
+
+    def truncate(self, seq: int, new_len: int) -> None:
+        """After an eviction: keep the first new_len positions, release the blocks behind them."""
+        _ok(lib().pa_bm_truncate(self._h, int(seq), int(new_len)), "pa_bm_truncate")
+
+    def release_window(self, seq: int, window: int, num_sinks: int) -> int:
+        """Release the blocks that no later query sees under a sliding window (table entry -1); returns how many."""
+        n = ctypes.c_int32()
+        _ok(lib().pa_bm_release_window(self._h, int(seq), int(window), int(num_sinks), ctypes.byref(n)),
+            "pa_bm_release_window")
+        return n.value
 
     def free(self, seq: int) -> None:
         _ok(lib().pa_bm_free(self._h, int(seq)), "pa_bm_free")

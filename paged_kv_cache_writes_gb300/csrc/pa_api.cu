@@ -7,6 +7,7 @@
 #include <cudaTypedefs.h>
 
 #include <cmath>
+#include <initializer_list>
 #include <mutex>
 
 #include "pa_common.cuh"
@@ -291,12 +292,11 @@ struct MixedPrefill {
   int num_chunks;
 };
 
-pa_status decode_impl(const void *q, pa_dtype q_dtype, int32_t num_seqs, int32_t num_q_heads,
-                      const void *k_cache, const void *v_cache, const pa_kv_cache *cache,
-                      const int32_t *block_tables, int32_t max_blocks_per_seq, const int32_t *seq_lens,
-                      int32_t max_seq_len, float scale, int32_t partition_size, void *workspace,
-                      size_t workspace_bytes, void *out, pa_dtype out_dtype, pa_stream_t stream,
-                      const NewTokens *nt, const MixedPrefill *mix = nullptr) {
+// The argument checks every decode shares; the pointers only when there is work.
+pa_status check_decode(const void *q, pa_dtype q_dtype, int32_t num_seqs, int32_t num_q_heads, const void *k_cache,
+                       const void *v_cache, const pa_kv_cache *cache, const int32_t *block_tables,
+                       int32_t max_blocks_per_seq, const int32_t *seq_lens, int32_t max_seq_len, float scale,
+                       int32_t partition_size, const void *out, pa_dtype out_dtype) {
   pa_status st = check_cache(cache);
   if (st != PA_OK) return st;
   const pa_kv_cache &c = *cache;
@@ -310,20 +310,14 @@ pa_status decode_impl(const void *q, pa_dtype q_dtype, int32_t num_seqs, int32_t
       !aligned(block_tables, 4) || !aligned(seq_lens, 4))
     return PA_ERR_INVALID_ARG;
   if ((st = check_pools(k_cache, v_cache)) != PA_OK) return st;
-  if (num_seqs > kMaxDecodeRows) return PA_ERR_UNSUPPORTED;
+  return num_seqs > kMaxDecodeRows ? PA_ERR_UNSUPPORTED : PA_OK;
+}
 
-  const int ps = effective_partition(partition_size);
-  const int64_t parts64 = std::max<int64_t>(1, ((int64_t)max_seq_len + ps - 1) / ps);
-  if (parts64 > kMaxPartitions) return PA_ERR_UNSUPPORTED;
-  const int parts = (int)parts64;
-  const int gqa = num_q_heads / c.num_kv_heads;
-  const bool use_tc = g_decode_kernel.load(std::memory_order_relaxed) == PA_DECODE_KERNEL_AUTO &&
-                      decode_tc_supported(c.head_dim, gqa, c.kv_dtype);
-  const int hpc = use_tc ? gqa : heads_per_cta(gqa);   // query heads per work unit
-  if ((double)num_seqs * parts * num_q_heads / hpc >= 2147483647.0) return PA_ERR_UNSUPPORTED;
-  const WorkspaceLayout w = decode_workspace_layout(num_seqs, num_q_heads, c.head_dim, parts);
-  if (!workspace || !aligned(workspace, 256) || workspace_bytes < w.total) return PA_ERR_INVALID_ARG;
-
+// The parameters every decode shares (hpc: query heads per work unit).
+DecodeParams decode_params(const void *q, int32_t num_seqs, int32_t num_q_heads, const pa_kv_cache &c,
+                           const int32_t *block_tables, int32_t max_blocks_per_seq, const int32_t *seq_lens, float scale,
+                           int ps, int parts, int hpc, const WorkspaceLayout &w, void *workspace, void *out,
+                           pa_dtype out_dtype) {
   DecodeParams p{};
   p.q = q;
   p.out = out;
@@ -334,7 +328,7 @@ pa_status decode_impl(const void *q, pa_dtype q_dtype, int32_t num_seqs, int32_t
   p.num_seqs = num_seqs;
   p.num_q_heads = num_q_heads;
   p.num_kv_heads = c.num_kv_heads;
-  p.groups = gqa / hpc;
+  p.groups = num_q_heads / c.num_kv_heads / hpc;
   p.block_size = c.block_size;
   p.num_blocks = c.num_blocks;
   p.partition_size = ps;
@@ -353,6 +347,41 @@ pa_status decode_impl(const void *q, pa_dtype q_dtype, int32_t num_seqs, int32_t
   p.tile_shift = c.block_size == 32 ? 1 : 0;
   p.kv_rows = c.num_kv_heads * c.block_size;
   p.err = device_error_word();
+  return p;
+}
+
+// Tensor maps of the tensor-core decode: one box per cache block of one KV head.
+bool encode_decode_tc_maps(PoolMaps *m, const void *k_cache, const void *v_cache, const pa_kv_cache &c) {
+  if (c.kv_dtype == PA_FP8_E4M3)
+    return encode_pool_map_fp8_blocks(&m->k, k_cache, c) && encode_pool_map_fp8_blocks(&m->v, v_cache, c);
+  return encode_pool_map_atoms(&m->k, k_cache, c) && encode_pool_map_atoms(&m->v, v_cache, c);
+}
+
+pa_status decode_impl(const void *q, pa_dtype q_dtype, int32_t num_seqs, int32_t num_q_heads,
+                      const void *k_cache, const void *v_cache, const pa_kv_cache *cache,
+                      const int32_t *block_tables, int32_t max_blocks_per_seq, const int32_t *seq_lens,
+                      int32_t max_seq_len, float scale, int32_t partition_size, void *workspace,
+                      size_t workspace_bytes, void *out, pa_dtype out_dtype, pa_stream_t stream,
+                      const NewTokens *nt, const MixedPrefill *mix = nullptr) {
+  pa_status st = check_decode(q, q_dtype, num_seqs, num_q_heads, k_cache, v_cache, cache, block_tables,
+                              max_blocks_per_seq, seq_lens, max_seq_len, scale, partition_size, out, out_dtype);
+  if (st != PA_OK || num_seqs == 0) return st;
+  const pa_kv_cache &c = *cache;
+
+  const int ps = effective_partition(partition_size);
+  const int64_t parts64 = std::max<int64_t>(1, ((int64_t)max_seq_len + ps - 1) / ps);
+  if (parts64 > kMaxPartitions) return PA_ERR_UNSUPPORTED;
+  const int parts = (int)parts64;
+  const int gqa = num_q_heads / c.num_kv_heads;
+  const bool use_tc = g_decode_kernel.load(std::memory_order_relaxed) == PA_DECODE_KERNEL_AUTO &&
+                      decode_tc_supported(c.head_dim, gqa, c.kv_dtype);
+  const int hpc = use_tc ? gqa : heads_per_cta(gqa);   // query heads per work unit
+  if ((double)num_seqs * parts * num_q_heads / hpc >= 2147483647.0) return PA_ERR_UNSUPPORTED;
+  const WorkspaceLayout w = decode_workspace_layout(num_seqs, num_q_heads, c.head_dim, parts);
+  if (!workspace || !aligned(workspace, 256) || workspace_bytes < w.total) return PA_ERR_INVALID_ARG;
+
+  const DecodeParams p = decode_params(q, num_seqs, num_q_heads, c, block_tables, max_blocks_per_seq, seq_lens, scale,
+                                       ps, parts, hpc, w, workspace, out, out_dtype);
   if (!p.err) return PA_ERR_CUDA;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e;
@@ -364,7 +393,7 @@ pa_status decode_impl(const void *q, pa_dtype q_dtype, int32_t num_seqs, int32_t
     tp.s_mult = p.q_mult;
     tp.k_scale = c.k_scale;
     tp.v_scale = c.v_scale;
-    tp.jobs = reinterpret_cast<DecodeMergeJob *>(ws + w.jobs_off);
+    tp.jobs = reinterpret_cast<DecodeMergeJob *>(static_cast<char *>(workspace) + w.jobs_off);
     if (nt) {
       tp.k_new = nt->k;
       tp.v_new = nt->v;
@@ -372,10 +401,7 @@ pa_status decode_impl(const void *q, pa_dtype q_dtype, int32_t num_seqs, int32_t
       tp.new_slots = nt->slots;
     }
     PoolMaps maps{};
-    const bool fp8_cache = c.kv_dtype == PA_FP8_E4M3;
-    if (fp8_cache ? (!encode_pool_map_fp8_blocks(&maps.k, k_cache, c) || !encode_pool_map_fp8_blocks(&maps.v, v_cache, c))
-                  : (!encode_pool_map_atoms(&maps.k, k_cache, c) || !encode_pool_map_atoms(&maps.v, v_cache, c)))
-      return PA_ERR_CUDA;
+    if (!encode_decode_tc_maps(&maps, k_cache, v_cache, c)) return PA_ERR_CUDA;
     if (mix) {   // the prefill tiles join the decode's grid (pa_mixed_tc.cuh)
       PrefillTcParams pt = mix->t;
       pt.err = p.err;
@@ -444,14 +470,258 @@ pa_status pa_decode_write(const void *q, pa_dtype q_dtype, int32_t num_seqs, int
 
 namespace pa {
 namespace {
+// Workspace of the bounded-cache decodes: pa_decode's over the packed rows,
+// then (pa_decode_weights) the scores and the rows' softmax maxima and sums.
+struct BoundedLayout {
+  int ps, parts, shares, share_heads, rows;   // rows: score columns per token
+  WorkspaceLayout w;
+  size_t scores_off, row_ml_off, total;
+  int64_t score_stride;
+};
+
+// PA_OK, or why the shape is not served.
+pa_status bounded_layout(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                         int32_t block_size, int32_t max_seq_len, int32_t window, int32_t num_sinks,
+                         int32_t partition_size, bool weights, BoundedLayout *b) {
+  if (num_seqs < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || num_q_heads % num_kv_heads || max_seq_len < 0 ||
+      window < 1 || num_sinks < 0 || partition_size < 0 || partition_size % 32)
+    return PA_ERR_INVALID_ARG;
+  if ((head_dim != 64 && head_dim != 128) || (block_size != 16 && block_size != 32) || num_seqs > kMaxDecodeRows)
+    return PA_ERR_UNSUPPORTED;
+  const int64_t longest = window_max_packed(max_seq_len, window, num_sinks, block_size);
+  b->ps = effective_partition(partition_size);
+  const int64_t parts = std::max<int64_t>(1, (longest + b->ps - 1) / b->ps);
+  const int gqa = num_q_heads / num_kv_heads;
+  b->shares = decode_ext_shares(head_dim, gqa);
+  b->share_heads = (gqa + b->shares - 1) / b->shares;
+  b->rows = decode_ext_rows(b->share_heads);
+  const int64_t units = (int64_t)num_kv_heads * b->shares;
+  if (parts > kMaxPartitions || units >= (1 << 19) || (double)num_seqs * parts * units >= 2147483647.0)
+    return PA_ERR_UNSUPPORTED;
+  b->parts = (int)parts;
+  b->w = decode_workspace_layout(num_seqs, num_q_heads, head_dim, parts);
+  b->score_stride = parts * b->ps;
+  b->scores_off = b->w.total;
+  b->row_ml_off = b->scores_off + (weights ? (size_t)num_seqs * units * b->score_stride * b->rows * 4 : 0);
+  b->total = b->row_ml_off + (weights ? round256((size_t)num_seqs * num_q_heads * 8) : 0);
+  return PA_OK;
+}
+
+// Workspace of pa_evict: the rows' new lengths, then each head's list of moves
+// (a count padded to 16 bytes; destinations, sources, sources' positions).
+struct EvictLayout {
+  size_t lists_off, total;
+  int64_t list_cap, list_stride;
+};
+bool evict_layout(int32_t num_seqs, int32_t num_kv_heads, int32_t max_seq_len, int32_t budget, EvictLayout *l) {
+  if (num_seqs < 0 || num_kv_heads <= 0 || max_seq_len < 0 || budget < 1) return false;
+  const int64_t moves = std::min<int64_t>(budget, std::max<int64_t>(0, (int64_t)max_seq_len - budget));
+  l->list_cap = (moves + 3) / 4 * 4;
+  l->list_stride = 4 + 3 * l->list_cap;
+  l->lists_off = round256((size_t)num_seqs * 4);
+  l->total = l->lists_off + round256((size_t)num_seqs * num_kv_heads * l->list_stride * 4);
+  return true;
+}
+
+// The weights half of a bounded-cache decode.
+struct Weights {
+  float *weights;
+  int64_t stride;
+  int32_t num_rows;
+  const int32_t *rows, *fresh_from;
+  float decay;
+};
+
+pa_status bounded_decode(const void *q, pa_dtype q_dtype, int32_t num_seqs, int32_t num_q_heads, const void *k_cache,
+                         const void *v_cache, const pa_kv_cache *cache, const int32_t *block_tables,
+                         int32_t max_blocks_per_seq, const int32_t *seq_lens, int32_t max_seq_len, int32_t window,
+                         int32_t num_sinks, float scale, int32_t partition_size, void *workspace,
+                         size_t workspace_bytes, void *out, pa_dtype out_dtype, const Weights *wt, pa_stream_t stream) {
+  pa_status st = check_decode(q, q_dtype, num_seqs, num_q_heads, k_cache, v_cache, cache, block_tables,
+                              max_blocks_per_seq, seq_lens, max_seq_len, scale, partition_size, out, out_dtype);
+  if (st != PA_OK) return st;
+  const pa_kv_cache &c = *cache;
+  BoundedLayout b;
+  if ((st = bounded_layout(num_seqs, num_q_heads, c.num_kv_heads, c.head_dim, c.block_size, max_seq_len, window,
+                           num_sinks, partition_size, wt != nullptr, &b)) != PA_OK)
+    return st;
+  if (num_seqs == 0) return PA_OK;
+  if (!workspace || !aligned(workspace, 256) || workspace_bytes < b.total) return PA_ERR_INVALID_ARG;
+  if (wt && (!wt->weights || !aligned(wt->weights, 16) || !aligned(wt->rows, 4) || !aligned(wt->fresh_from, 4) ||
+             wt->stride < max_seq_len || wt->num_rows < (wt->rows ? 1 : num_seqs) || !std::isfinite(wt->decay)))
+    return PA_ERR_INVALID_ARG;
+  DecodeTcParams tp{};
+  tp.d = decode_params(q, num_seqs, num_q_heads, c, block_tables, max_blocks_per_seq, seq_lens, scale, b.ps, b.parts,
+                       num_q_heads / c.num_kv_heads, b.w, workspace, out, out_dtype);
+  if (!tp.d.err) return PA_ERR_CUDA;
+  char *ws = static_cast<char *>(workspace);
+  tp.k_cache = k_cache;
+  tp.v_cache = v_cache;
+  tp.s_mult = tp.d.q_mult;
+  tp.jobs = reinterpret_cast<DecodeMergeJob *>(ws + b.w.jobs_off);
+  tp.window = window;
+  tp.num_sinks = num_sinks;
+  tp.shares = b.shares;
+  tp.share_heads = b.share_heads;
+  if (wt) {
+    tp.scores = reinterpret_cast<float *>(ws + b.scores_off);
+    tp.score_stride = b.score_stride;
+    tp.row_ml = reinterpret_cast<float2 *>(ws + b.row_ml_off);
+  }
+  PoolMaps maps{};
+  if (!encode_decode_tc_maps(&maps, k_cache, v_cache, c)) return PA_ERR_CUDA;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  if (c.kv_dtype == PA_BF16) e = launch_decode_ext_bf16(tp, c.head_dim, maps, s);
+  else if (c.kv_dtype == PA_F16) e = launch_decode_ext_f16(tp, c.head_dim, maps, s);
+  else if (q_dtype == PA_BF16) e = launch_decode_ext_fp8_bf16q(tp, c.head_dim, maps, s);
+  else e = launch_decode_ext_fp8_f16q(tp, c.head_dim, maps, s);
+  if (e != cudaSuccess) return PA_ERR_CUDA;
+  if (!wt) return PA_OK;
+  WeightsParams wp{};
+  wp.scores = tp.scores;
+  wp.score_stride = b.score_stride;
+  wp.score_rows = b.rows;
+  wp.row_ml = tp.row_ml;
+  wp.seq_lens = seq_lens;
+  wp.num_seqs = num_seqs;
+  wp.num_q_heads = num_q_heads;
+  wp.num_kv_heads = c.num_kv_heads;
+  wp.shares = b.shares;
+  wp.share_heads = b.share_heads;
+  // rows past the block table's capacity or max_seq_len were reported and cut by the decode
+  wp.max_len = (int32_t)std::min<int64_t>(max_seq_len, (int64_t)max_blocks_per_seq * c.block_size);
+  wp.weights = wt->weights;
+  wp.weights_stride = wt->stride;
+  wp.num_weight_rows = wt->num_rows;
+  wp.weight_rows = wt->rows;
+  wp.fresh_from = wt->fresh_from;
+  wp.decay = wt->decay;
+  wp.err = tp.d.err;
+  return launch_decode_weights(wp, s) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+}  // namespace
+}  // namespace pa
+
+extern "C" {
+
+size_t pa_decode_window_workspace_bytes(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                                        int32_t block_size, int32_t max_seq_len, int32_t window, int32_t num_sinks,
+                                        int32_t partition_size) {
+  BoundedLayout b;
+  return bounded_layout(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, max_seq_len, window, num_sinks,
+                        partition_size, false, &b) == PA_OK
+             ? b.total
+             : 0;
+}
+
+pa_status pa_decode_window(const void *q, pa_dtype q_dtype, int32_t num_seqs, int32_t num_q_heads, const void *k_cache,
+                           const void *v_cache, const pa_kv_cache *cache, const int32_t *block_tables,
+                           int32_t max_blocks_per_seq, const int32_t *seq_lens, int32_t max_seq_len, int32_t window,
+                           int32_t num_sinks, float scale, int32_t partition_size, void *workspace,
+                           size_t workspace_bytes, void *out, pa_dtype out_dtype, pa_stream_t stream) {
+  return bounded_decode(q, q_dtype, num_seqs, num_q_heads, k_cache, v_cache, cache, block_tables, max_blocks_per_seq,
+                        seq_lens, max_seq_len, window, num_sinks, scale, partition_size, workspace, workspace_bytes,
+                        out, out_dtype, nullptr, stream);
+}
+
+size_t pa_evict_workspace_bytes(int32_t num_seqs, int32_t num_kv_heads, int32_t max_seq_len, int32_t budget) {
+  EvictLayout l;
+  return evict_layout(num_seqs, num_kv_heads, max_seq_len, budget, &l) ? l.total : 0;
+}
+
+pa_status pa_evict(void *k_cache, void *v_cache, const pa_kv_cache *cache, int32_t num_seqs,
+                   const int32_t *block_tables, int32_t max_blocks_per_seq, const int32_t *seq_lens,
+                   int32_t max_seq_len, const int32_t *num_tokens, const int32_t *ordered_from, int32_t budget,
+                   int32_t num_sinks, int32_t num_recent, const float *weights, const int32_t *positions,
+                   float *new_weights, int32_t *new_positions, int64_t weights_stride, int32_t num_weight_rows,
+                   const int32_t *weight_rows, int32_t *new_seq_lens, void *workspace, size_t workspace_bytes,
+                   pa_stream_t stream) {
+  pa_status st = check_cache(cache);
+  if (st != PA_OK) return st;
+  const pa_kv_cache &c = *cache;
+  EvictLayout l;
+  if (max_blocks_per_seq <= 0 || num_sinks < 0 || num_recent < 0 || (int64_t)num_sinks + num_recent > budget ||
+      !evict_layout(num_seqs, c.num_kv_heads, max_seq_len, budget, &l))
+    return PA_ERR_INVALID_ARG;
+  if (num_seqs == 0) return PA_OK;
+  for (const void *q : {(const void *)block_tables, (const void *)seq_lens, (const void *)num_tokens,
+                        (const void *)ordered_from, (const void *)weights, (const void *)positions,
+                        (const void *)new_weights, (const void *)new_positions, (const void *)new_seq_lens})
+    if (!q || !aligned(q, 4)) return PA_ERR_INVALID_ARG;
+  if (!aligned(weight_rows, 4) || weights_stride < max_seq_len || num_weight_rows < (weight_rows ? 1 : num_seqs))
+    return PA_ERR_INVALID_ARG;
+  if ((st = check_pools(k_cache, v_cache)) != PA_OK) return st;
+  if (!workspace || !aligned(workspace, 256) || workspace_bytes < l.total) return PA_ERR_INVALID_ARG;
+  EvictParams p{};
+  p.k_cache = static_cast<char *>(k_cache);
+  p.v_cache = static_cast<char *>(v_cache);
+  p.row_bytes = c.head_dim * dtype_bytes(c.kv_dtype);
+  p.num_blocks = c.num_blocks;
+  p.num_seqs = num_seqs;
+  p.num_kv_heads = c.num_kv_heads;
+  p.block_size = c.block_size;
+  p.block_tables = block_tables;
+  p.max_blocks_per_seq = max_blocks_per_seq;
+  p.seq_lens = seq_lens;
+  p.max_seq_len = max_seq_len;
+  p.num_tokens = num_tokens;
+  p.ordered_from = ordered_from;
+  p.budget = budget;
+  p.num_sinks = num_sinks;
+  p.num_recent = num_recent;
+  p.weights = weights;
+  p.positions = positions;
+  p.new_weights = new_weights;
+  p.new_positions = new_positions;
+  p.stride = weights_stride;
+  p.num_weight_rows = num_weight_rows;
+  p.weight_rows = weight_rows;
+  p.new_seq_lens = new_seq_lens;
+  p.lens = static_cast<int32_t *>(workspace);
+  p.lists = reinterpret_cast<int32_t *>(static_cast<char *>(workspace) + l.lists_off);
+  p.list_stride = l.list_stride;
+  p.list_cap = l.list_cap;
+  p.err = device_error_word();
+  if (!p.err) return PA_ERR_CUDA;
+  return launch_evict(p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+size_t pa_decode_weights_workspace_bytes(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                                         int32_t max_seq_len, int32_t partition_size) {
+  BoundedLayout b;   // no window: the block size does not matter
+  return bounded_layout(num_seqs, num_q_heads, num_kv_heads, head_dim, 16, max_seq_len, INT32_MAX, 0, partition_size,
+                        true, &b) == PA_OK
+             ? b.total
+             : 0;
+}
+
+pa_status pa_decode_weights(const void *q, pa_dtype q_dtype, int32_t num_seqs, int32_t num_q_heads,
+                            const void *k_cache, const void *v_cache, const pa_kv_cache *cache,
+                            const int32_t *block_tables, int32_t max_blocks_per_seq, const int32_t *seq_lens,
+                            int32_t max_seq_len, float scale, int32_t partition_size, void *workspace,
+                            size_t workspace_bytes, void *out, pa_dtype out_dtype, float *weights,
+                            int64_t weights_stride, int32_t num_weight_rows, const int32_t *weight_rows,
+                            const int32_t *fresh_from, float decay, pa_stream_t stream) {
+  const Weights wt{weights, weights_stride, num_weight_rows, weight_rows, fresh_from, decay};
+  return bounded_decode(q, q_dtype, num_seqs, num_q_heads, k_cache, v_cache, cache, block_tables, max_blocks_per_seq,
+                        seq_lens, max_seq_len, INT32_MAX, 0, scale, partition_size, workspace, workspace_bytes, out,
+                        out_dtype, &wt, stream);
+}
+
+}  // extern "C"
+
+namespace pa {
+namespace {
 // pa_prefill_chunk's argument checks.  PA_OK with *empty set: nothing to do;
-// otherwise *tc tells whether the tensor-core kernel applies, and then t holds
-// its parameters.
+// otherwise *tc tells whether the tensor-core kernel applies (any_shape: it
+// always does), and then t holds its parameters.
 pa_status prefill_prepare(const void *q_chunk, pa_dtype q_dtype, const int32_t *cu_q_lens, const int32_t *q_start,
                           int32_t num_chunks, int32_t max_q_len, int32_t num_q_heads, const void *k_cache,
                           const void *v_cache, const pa_kv_cache *cache, const int32_t *block_tables,
                           int32_t max_blocks_per_seq, const int32_t *seq_lens, int32_t max_seq_len, float scale,
-                          void *out, pa_dtype out_dtype, bool *empty, bool *tc, PrefillTcParams *tp) {
+                          void *out, pa_dtype out_dtype, bool *empty, bool *tc, PrefillTcParams *tp,
+                          bool any_shape = false) {
   *empty = false;
   *tc = false;
   pa_status st = check_cache(cache);
@@ -475,7 +745,7 @@ pa_status prefill_prepare(const void *q_chunk, pa_dtype q_dtype, const int32_t *
   if (rows > 2147483647ll || num_q_heads > 65535) return PA_ERR_UNSUPPORTED;
   const bool fp8 = c.kv_dtype == PA_FP8_E4M3;
   const int gqa = num_q_heads / c.num_kv_heads;
-  if (prefill_tc_supported(c.head_dim, gqa)) {
+  if (any_shape || prefill_tc_supported(c.head_dim, gqa)) {
     // tensor-core tiles: 128 GQA-packed rows x 128-key tiles (pa_prefill_tc.cuh)
     *tc = true;
     PrefillTcParams &t = *tp;
@@ -570,6 +840,41 @@ pa_status pa_prefill_chunk(const void *q_chunk, pa_dtype q_dtype, const int32_t 
   return dispatch_attention(q_dtype, c, p, maps, (int)rows, s) == cudaSuccess
              ? PA_OK
              : PA_ERR_CUDA;
+}
+
+pa_status pa_prefill_chunk_window(const void *q_chunk, pa_dtype q_dtype, const int32_t *cu_q_lens,
+                                  const int32_t *q_start, int32_t num_chunks, int32_t max_q_len, int32_t num_q_heads,
+                                  const void *k_cache, const void *v_cache, const pa_kv_cache *cache,
+                                  const int32_t *block_tables, int32_t max_blocks_per_seq, const int32_t *seq_lens,
+                                  int32_t max_seq_len, int32_t window, int32_t num_sinks, float scale, void *out,
+                                  pa_dtype out_dtype, pa_stream_t stream) {
+  bool empty = false, use_tc = false;
+  PrefillTcParams t{};
+  pa_status st = prefill_prepare(q_chunk, q_dtype, cu_q_lens, q_start, num_chunks, max_q_len, num_q_heads, k_cache,
+                                 v_cache, cache, block_tables, max_blocks_per_seq, seq_lens, max_seq_len, scale, out,
+                                 out_dtype, &empty, &use_tc, &t, true);
+  if (st != PA_OK) return st;
+  if (window < 1 || num_sinks < 0) return PA_ERR_INVALID_ARG;
+  if (empty) return PA_OK;
+  const pa_kv_cache &c = *cache;
+  const int gqa = num_q_heads / c.num_kv_heads;
+  t.window = window;
+  t.num_sinks = num_sinks;
+  t.shares = (gqa + kPrefillWindowHeads - 1) / kPrefillWindowHeads;
+  t.share_heads = (gqa + t.shares - 1) / t.shares;
+  t.err = device_error_word();
+  if (!t.err) return PA_ERR_CUDA;
+  PoolMaps maps{};   // fp8: the loaders copy whole cache blocks with bulk-tensor boxes
+  if (c.kv_dtype == PA_FP8_E4M3 &&
+      (!encode_pool_map_fp8_blocks(&maps.k, k_cache, c) || !encode_pool_map_fp8_blocks(&maps.v, v_cache, c)))
+    return PA_ERR_CUDA;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  if (c.kv_dtype == PA_BF16) e = launch_prefill_window_bf16(t, maps, c.head_dim, num_chunks, s);
+  else if (c.kv_dtype == PA_F16) e = launch_prefill_window_f16(t, maps, c.head_dim, num_chunks, s);
+  else if (q_dtype == PA_BF16) e = launch_prefill_window_fp8_bf16q(t, maps, c.head_dim, num_chunks, s);
+  else e = launch_prefill_window_fp8_f16q(t, maps, c.head_dim, num_chunks, s);
+  return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
 pa_status pa_mixed_step(const pa_decode_part *d, const pa_prefill_part *pf, pa_dtype q_dtype, int32_t num_q_heads,

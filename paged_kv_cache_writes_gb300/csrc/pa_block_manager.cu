@@ -19,7 +19,10 @@
 //    token ids (hash of the previous full block, then the block's ids).  When
 //    an append fills a whole logical block whose ids match a block already in
 //    the pool, that block is shared instead of allocated and its tokens get
-//    slot -1 (pa_reshape_and_cache skips them: their K/V are already there).
+//    slot -1 (pa_reshape_and_cache skips them: their K/V are already there);
+//  * a bounded cache: blocks made a sequence's own before an eviction rewrites
+//    them, blocks behind a shortened sequence released, and blocks that a
+//    sliding window has left released out of the middle (table entry -1).
 // Not thread-safe: one manager per thread, or external locking.
 #include <algorithm>
 #include <cstdint>
@@ -73,14 +76,18 @@ struct pa_block_manager {
     return b;
   }
   void release(int32_t b) {
+    if (b < 0) return;   // released under a sliding window
     if (--ref[b] == 0) {
-      if (hash_of[b]) {
-        auto it = cache.find(hash_of[b]);
-        if (it != cache.end() && it->second == b) cache.erase(it);
-        hash_of[b] = 0;
-      }
+      forget(b);
       free_list.push_back(b);
     }
+  }
+  // the block is no longer found by prefix reuse
+  void forget(int32_t b) {
+    if (!hash_of[b]) return;
+    auto it = cache.find(hash_of[b]);
+    if (it != cache.end() && it->second == b) cache.erase(it);
+    hash_of[b] = 0;
   }
   bool valid_seq(int32_t s) const { return s >= 0 && s < (int32_t)seqs.size() && seqs[s].live; }
 };
@@ -137,7 +144,8 @@ pa_status pa_bm_fork(pa_block_manager *bm, int32_t parent, int32_t *child) {
   if (!bm || !child || !bm->valid_seq(parent)) return PA_ERR_INVALID_ARG;
   try {
     Seq c = bm->seqs[parent];
-    for (int32_t b : c.blocks) ++bm->ref[b];
+    for (int32_t b : c.blocks)
+      if (b >= 0) ++bm->ref[b];
     bm->seqs.push_back(std::move(c));
   } catch (...) {
     return PA_ERR_UNSUPPORTED;
@@ -218,6 +226,73 @@ pa_status pa_bm_append(pa_block_manager *bm, int32_t seq, int32_t num_tokens, co
       s.chain_known = false;
     }
   }
+  return PA_OK;
+}
+
+pa_status pa_bm_unshare(pa_block_manager *bm, int32_t seq, int32_t num_tokens, int32_t *cow_pairs,
+                        int32_t cow_capacity, int32_t *num_cow) {
+  if (!bm || !num_cow || !bm->valid_seq(seq) || num_tokens < 0 || cow_capacity < 0) return PA_ERR_INVALID_ARG;
+  *num_cow = 0;
+  Seq &s = bm->seqs[seq];
+  if (num_tokens > s.len) return PA_ERR_INVALID_ARG;
+  const size_t n = ((size_t)num_tokens + bm->block_size - 1) / bm->block_size;
+  int32_t need = 0;
+  for (size_t i = 0; i < n; ++i) need += s.blocks[i] >= 0 && bm->ref[s.blocks[i]] > 1;
+  if (need > (int32_t)bm->free_list.size()) return PA_ERR_NO_BLOCKS;
+  if (need > cow_capacity || (need > 0 && !cow_pairs)) {
+    *num_cow = need;
+    return PA_ERR_INVALID_ARG;
+  }
+  for (size_t i = 0; i < n; ++i) {
+    const int32_t b = s.blocks[i];
+    if (b < 0) continue;
+    if (bm->ref[b] > 1) {
+      const int32_t dst = bm->take();
+      bm->release(b);
+      s.blocks[i] = dst;
+      cow_pairs[2 * *num_cow] = b;
+      cow_pairs[2 * *num_cow + 1] = dst;
+      ++*num_cow;
+    } else {
+      bm->forget(b);
+    }
+  }
+  if (n > 0) s.chain_known = false;   // its blocks no longer hold the prefix their hashes stood for
+  return PA_OK;
+}
+
+pa_status pa_bm_truncate(pa_block_manager *bm, int32_t seq, int32_t new_len) {
+  if (!bm || !bm->valid_seq(seq) || new_len < 0 || new_len > bm->seqs[seq].len) return PA_ERR_INVALID_ARG;
+  Seq &s = bm->seqs[seq];
+  if (new_len == s.len) return PA_OK;
+  const int32_t bs = bm->block_size;
+  const size_t n = ((size_t)new_len + bs - 1) / bs;
+  // a last block that is kept in part cannot be appended to without a block in the table
+  if (new_len % bs && s.blocks[n - 1] < 0) return PA_ERR_INVALID_ARG;
+  for (size_t i = n; i < s.blocks.size(); ++i) bm->release(s.blocks[i]);
+  s.blocks.resize(n);
+  s.len = new_len;
+  // the kept part of a full block will be written behind: it is no longer the block its hash names
+  // (a shared one is copied before that write, and keeps its name)
+  if (new_len % bs && bm->ref[s.blocks[n - 1]] == 1) bm->forget(s.blocks[n - 1]);
+  s.chain = 0;
+  s.chain_known = new_len == 0;
+  return PA_OK;
+}
+
+pa_status pa_bm_release_window(pa_block_manager *bm, int32_t seq, int32_t window, int32_t num_sinks,
+                               int32_t *num_released) {
+  if (!bm || !num_released || !bm->valid_seq(seq) || window < 1 || num_sinks < 0) return PA_ERR_INVALID_ARG;
+  *num_released = 0;
+  Seq &s = bm->seqs[seq];
+  const int64_t bs = bm->block_size, first = (num_sinks + bs - 1) / bs;
+  const int64_t end = (s.len + 1 - (int64_t)window) / bs;   // blocks that end at or before the next query's window
+  for (int64_t i = first; i < end && i < (int64_t)s.blocks.size(); ++i)
+    if (s.blocks[i] >= 0) {
+      bm->release(s.blocks[i]);
+      s.blocks[i] = -1;
+      ++*num_released;
+    }
   return PA_OK;
 }
 

@@ -1,0 +1,8 @@
+// pa_decode_ext_bf16.cu -- bounded-cache decode instantiations for a bf16 cache.
+#include "pa_decode_tc.cuh"
+
+namespace pa {
+cudaError_t launch_decode_ext_bf16(const DecodeTcParams &p, int head_dim, const PoolMaps &m, cudaStream_t s) {
+  return launch_decode_ext<__nv_bfloat16, __nv_bfloat16>(p, head_dim, m, s);
+}
+}  // namespace pa

@@ -95,6 +95,7 @@
 #include "pa_decode.cuh"
 #include "pa_internal.h"
 #include "pa_tcgen05.cuh"
+#include "pa_window.cuh"
 
 namespace pa {
 
@@ -127,7 +128,42 @@ struct DecodeTcParams {
   int64_t new_stride;
   const int64_t *new_slots;
   float k_scale, v_scale;
+  // Bounded-cache decodes (kernels built with kExt).  A unit is (row,
+  // partition, KV head, share of the head's query group): groups wider than
+  // the kernel's rows are cut into `shares` of share_heads query heads (the
+  // last may have fewer), and a unit's `kvh` is kvh * shares + share.
+  int32_t window;            // tokens up to the query's own that it sees (INT32_MAX: all)
+  int32_t num_sinks;         // first tokens that stay visible
+  int32_t shares, share_heads;
+  float *scores;             // null, or [row][kvh * shares + share][score_stride tokens][G] scores in log2 units
+  int64_t score_stride;
+  float2 *row_ml;            // with scores: [row][query head] (maximum, 1 / sum) of the softmax, log2 units
 };
+
+// A row's length and, with kExt, its packed length under the window, both
+// checked as checked_len does (the table must hold the row, the partitions
+// its packed tokens).
+template <bool kExt>
+__device__ __forceinline__ int checked_packed_len(const DecodeTcParams &tp, int row, bool report, WindowSpan *span) {
+  const DecodeParams &p = tp.d;
+  if constexpr (!kExt) {
+    return checked_len(p, row, report);
+  } else {
+    int L = __ldg(p.seq_lens + row);
+    const int64_t cap = (int64_t)p.max_blocks_per_seq * p.block_size, packed = (int64_t)p.max_partitions * p.partition_size;
+    bool bad = L < 0 || L > cap;
+    L = L < 0 ? 0 : L > cap ? (int)cap : L;
+    const WindowSpan w = window_span(window_low(L, tp.window), tp.num_sinks, 4 + p.tile_shift);
+    L -= w.skip_blocks << (4 + p.tile_shift);
+    if (L > packed) {
+      bad = true;
+      L = (int)packed;
+    }
+    if (bad && report) record_error(p.err, PA_ERR_DEVICE_CHECK);
+    if (span) *span = w;
+    return L;
+  }
+}
 
 namespace dtc {
 
@@ -174,6 +210,15 @@ struct TcUnit {
   int32_t valid, row, kvh, part, tok_begin, ntok, nparts, qscale;
   int32_t blk[kMaxTiles * 8];
 };
+
+// Whether P goes into the second product as hi + lo: for a bf16 cache (8 bits
+// would be too few), and in the bounded-cache decodes for an f16 cache too,
+// whose softmax sum is then that of the unrounded P, as the accumulated
+// weights need it (with f16 P the sum is off by up to 2^-11).
+template <typename KV, typename QT, bool kExt>
+constexpr bool split_p() {
+  return !std::is_same<KV, uint8_t>::value && (kExt || std::is_same<QT, __nv_bfloat16>::value);
+}
 
 // e4m3 terms per query value with an fp8 cache: two hold a bf16 value's 8
 // significant bits, three an f16 value's 11; 1 (no split) for 16-bit caches.
@@ -292,9 +337,13 @@ __device__ __forceinline__ float warp_reduce_heads(float (&v)[G], int lane) {
 }
 
 // The descriptor's header, copied to registers (the block ids stay in shared memory).
+// kExt: the descriptor's ntok packs ntok | gap_lo << 10 | gap_hi << 20, the
+// unit's keys gap_lo .. gap_hi - 1 (of at most 512) being outside the window.
 struct UnitHdr {
   int32_t valid, row, kvh, part, tok_begin, ntok, nparts, qscale;
+  int32_t gap_lo, gap_hi;
 };
+template <bool kExt = false>
 __device__ __forceinline__ UnitHdr read_unit(const TcUnit *u) {
   const volatile int32_t *s = reinterpret_cast<const volatile int32_t *>(u);
   UnitHdr r;
@@ -306,6 +355,12 @@ __device__ __forceinline__ UnitHdr read_unit(const TcUnit *u) {
   r.ntok = s[5];
   r.nparts = s[6];
   r.qscale = s[7];
+  r.gap_lo = r.gap_hi = 0;
+  if constexpr (kExt) {
+    r.gap_lo = (r.ntok >> 10) & 1023;
+    r.gap_hi = (r.ntok >> 20) & 1023;
+    r.ntok &= 1023;
+  }
   return r;
 }
 
@@ -344,7 +399,10 @@ __device__ __forceinline__ int32_t query_scale_bits(float amax) {
 // The decode CTA, for decode_tc_kernel and for the decode CTAs of the mixed
 // kernel (pa_mixed_tc.cuh).  Warps past the eight roles (a wider mixed block)
 // only take part in the two CTA-wide barriers.
-template <typename KV, typename QT, int G, int D = 128, int NL = 1, bool kSepMerge = false, bool kPadRows = false>
+// kExt: a sliding window with first tokens that stay visible, groups cut into
+// shares, and the scores written out (the bounded-cache decodes).
+template <typename KV, typename QT, int G, int D = 128, int NL = 1, bool kSepMerge = false, bool kPadRows = false,
+          bool kExt = false>
 __device__ __forceinline__ void decode_tc_body(const DecodeTcParams &tp, const CUtensorMap *tmap_k,
                                                const CUtensorMap *tmap_v) {
   using namespace tc;
@@ -358,7 +416,7 @@ __device__ __forceinline__ void decode_tc_body(const DecodeTcParams &tp, const C
   // MMA operands: the cache's type (bf16 / f16 with a 16-bit cache, the queries
   // in the same type; e4m3 with an fp8 cache, the queries and P as two e4m3 terms)
   constexpr bool kBf16 = std::is_same<QT, __nv_bfloat16>::value && !kFp8;
-  constexpr bool kSplit = kBf16;            // bf16 cache: P as hi + lo
+  constexpr bool kSplit = split_p<KV, QT, kExt>();   // 16-bit caches: P as hi + lo
   constexpr int kQTerms = QTerms<KV, QT>::value;
   using GE = TcGeo<G, kSplit, kFp8, kQTerms, D>;
   // The MMA warp consumes the ring in order, so a loader's wait for the consumption of
@@ -457,7 +515,24 @@ __device__ __forceinline__ void decode_tc_body(const DecodeTcParams &tp, const C
   const int hq = p.num_q_heads;
   // query heads per KV head: G, or with kPadRows 1..G, a unit's rows gr..G-1 then being
   // padding, with q = 0 (finite scores and softmax), never read from or written to global memory
-  const int gr = kPadRows ? hq / hkv : G;
+  const int gr_all = kPadRows ? hq / hkv : G;
+  const int hkv_units = kExt ? hkv * tp.shares : hkv;   // units per (row, partition)
+  // a unit's KV head, its first query head and how many it has
+  struct Heads {
+    int kvh, h0, n;
+  };
+  auto heads_of = [&](int kvh) {
+    Heads r{kvh, kvh * gr_all, gr_all};
+    if constexpr (kExt) {
+      if (tp.shares > 1) {
+        r.kvh = kvh / tp.shares;
+        const int first = (kvh - r.kvh * tp.shares) * tp.share_heads;
+        r.h0 = r.kvh * gr_all + first;
+        r.n = min(tp.share_heads, gr_all - first);
+      }
+    }
+    return r;
+  };
 
   // Merge the split row of record t of the grid-wide merge list (its ready flag
   // acquired by lane 0): out = sum_p 2^(m_p - M) acc_p / sum_p 2^(m_p - M) l_p
@@ -469,7 +544,9 @@ __device__ __forceinline__ void decode_tc_body(const DecodeTcParams &tp, const C
            __shfl_sync(0xffffffffu, (uint32_t)word, 0);
     const int job_row = (int)(word >> 32), job_kvh = (int)((word >> 13) & 0x7ffffu), job_np = (int)(word & 0x1fffu);
     __syncwarp();   // lane 0's acquire of the record orders every lane's reads of the partials
-    const int64_t head0 = (int64_t)job_row * hq + (int64_t)job_kvh * gr;
+    const Heads jh = heads_of(job_kvh);
+    const int gr = jh.n;
+    const int64_t head0 = (int64_t)job_row * hq + jh.h0;
     float m[G], l[G];
     float4 acc[G];
 #pragma unroll
@@ -498,7 +575,8 @@ __device__ __forceinline__ void decode_tc_body(const DecodeTcParams &tp, const C
 #pragma unroll
         for (int h = 0; h < G; ++h) {
           const float mn = fmaxf(m[h], ml[k][h].x);
-          const float so = fast_exp2(m[h] - mn), sn = fast_exp2(ml[k][h].x - mn);
+          const float mr = kExt && mn == kNegInf ? 0.f : mn;   // a partition may lie in the gap
+          const float so = fast_exp2(m[h] - mr), sn = fast_exp2(ml[k][h].x - mr);
           m[h] = mn;
           l[h] = l[h] * so + ml[k][h].y * sn;
           acc[h] = make_float4(acc[h].x * so + a[k][h].x * sn, acc[h].y * so + a[k][h].y * sn,
@@ -508,8 +586,10 @@ __device__ __forceinline__ void decode_tc_body(const DecodeTcParams &tp, const C
     }
 #pragma unroll
     for (int h = 0; h < G; ++h) {
-      const float om = p.v_hs ? p.out_mult * __ldg(p.v_hs + job_kvh) : p.out_mult;
+      const float om = p.v_hs ? p.out_mult * __ldg(p.v_hs + jh.kvh) : p.out_mult;
       const float inv = l[h] > 0.f ? om / l[h] : 0.f;
+      if constexpr (kExt)
+        if (tp.scores && lane == 0 && h < gr) tp.row_ml[head0 + h] = make_float2(m[h], l[h] > 0.f ? 1.f / l[h] : 0.f);
       const int64_t o0 = (head0 + h) * kD + 4 * lane;
       if (4 * lane >= kD || h >= gr) continue;   // head_dim 64: lanes 0..15; padding rows
       store_out<QT>(p.out, o0, p.out_f32 != 0, acc[h].x * inv);
@@ -582,9 +662,9 @@ __device__ __forceinline__ void decode_tc_body(const DecodeTcParams &tp, const C
       const int ib = u % kInfo, b = u & 1;
       ok = wait_all(&info_full[ib], (u / kInfo) & 1);
       if (!ok) break;
-      const UnitHdr cur = read_unit(&info[ib]);
+      const UnitHdr cur = read_unit<kExt>(&info[ib]);
       const int nt = num_tiles(cur);
-      float c = p.k_hs && cur.valid ? c0 * __ldg(p.k_hs + cur.kvh) : c0;
+      float c = p.k_hs && cur.valid ? c0 * __ldg(p.k_hs + heads_of(cur.kvh).kvh) : c0;
       if constexpr (kFp8) c *= __frcp_rn(__int_as_float(cur.valid ? cur.qscale : 127 << 23));   // exact: 2^-e
       // scores of this unit in log2 units, t = s * scale * log2(e); masked keys -inf
       float t[kMaxTiles][G];
@@ -600,7 +680,8 @@ __device__ __forceinline__ void decode_tc_body(const DecodeTcParams &tp, const C
           if (j < nt) {
             float raw[GE::kSCols];
             tmem_ld_cols<GE::kSCols>(col_s(b, j) + lane_base, raw);
-            const bool kv = j * kKeys + tid < cur.ntok;
+            const int key = j * kKeys + tid;
+            const bool kv = key < cur.ntok && !(kExt && key >= cur.gap_lo && key < cur.gap_hi);
 #pragma unroll
             for (int h = 0; h < G; ++h) {
               // fp8: hi + lo / 16, or hi + (mid + lo / 16) / 16
@@ -609,6 +690,14 @@ __device__ __forceinline__ void decode_tc_body(const DecodeTcParams &tp, const C
                                               : raw[h];
               t[j][h] = kv ? sv * c : kNegInf;
               mloc[h] = fmaxf(mloc[h], t[j][h]);
+            }
+            if constexpr (kExt) {
+              if (tp.scores && key < cur.ntok) {   // G consecutive floats per key, a warp's keys consecutive
+                float4 *dst = reinterpret_cast<float4 *>(
+                    tp.scores + (((int64_t)cur.row * hkv_units + cur.kvh) * tp.score_stride + cur.tok_begin + key) * G);
+#pragma unroll
+                for (int h = 0; h < G; h += 4) dst[h / 4] = make_float4(t[j][h], t[j][h + 1], t[j][h + 2], t[j][h + 3]);
+              }
             }
           } else {
 #pragma unroll
@@ -680,7 +769,13 @@ __device__ __forceinline__ void decode_tc_body(const DecodeTcParams &tp, const C
           for (int h = 0; h < G; ++h) {
             const float msub = m_cur[h] == kNegInf ? 0.f : m_cur[h];
             const float pv = fast_exp2(t[j][h] - msub);
-            if constexpr (kSplit) {
+            if constexpr (kSplit && !kBf16) {
+              // hi = p rounded to f16, lo = p - hi (exact in fp32) rounded: within 2^-22 of p, or 2^-25
+              const __half hv = __float2half_rn(pv), lv = __float2half_rn(pv - __half2float(hv));
+              *reinterpret_cast<__half *>(pt + h * 128 + ((ck ^ (h & 7)) << 4)) = hv;
+              *reinterpret_cast<__half *>(pt + (G + h) * 128 + ((ck ^ ((G + h) & 7)) << 4)) = lv;
+              l_part[h] += pv;
+            } else if constexpr (kSplit) {
               // hi = p truncated to bf16, lo = (p - hi) truncated; hi + lo is within 2^-15 of p
               const uint32_t hi = __float_as_uint(pv) & 0xffff0000u;
               const float lo = pv - __uint_as_float(hi);
@@ -713,7 +808,9 @@ __device__ __forceinline__ void decode_tc_body(const DecodeTcParams &tp, const C
         }
         tc_fence_before();
         mbar_arrive(&o_free[bp]);
-        const int64_t head0 = (int64_t)prev.row * hq + (int64_t)prev.kvh * gr;
+        const Heads ph = heads_of(prev.kvh);
+        const int gr = ph.n;
+        const int64_t head0 = (int64_t)prev.row * hq + ph.h0;
         const int d = tid;            // with head_dim 64, lanes 64..127 repeat 0..63: not stored
         // the two column halves of O^T: bf16 p = hi + lo; fp8 256 p = hi + lo / 16
         auto o_val = [&](int h) {
@@ -723,8 +820,11 @@ __device__ __forceinline__ void decode_tc_body(const DecodeTcParams &tp, const C
 #pragma unroll
           for (int h = 0; h < G; ++h) {
             const float val = o_val(h);
-            const float om = p.v_hs ? p.out_mult * __ldg(p.v_hs + prev.kvh) : p.out_mult;
+            const float om = p.v_hs ? p.out_mult * __ldg(p.v_hs + ph.kvh) : p.out_mult;
             const float inv = l_prev[h] > 0.f ? om / l_prev[h] : 0.f;
+            if constexpr (kExt)
+              if (tp.scores && tid == h && h < gr)
+                tp.row_ml[head0 + h] = make_float2(m_prev[h], l_prev[h] > 0.f ? 1.f / l_prev[h] : 0.f);
             if (d < kD && h < gr) store_out<QT>(p.out, (head0 + h) * kD + d, p.out_f32 != 0, val * inv);
           }
         } else {
@@ -779,31 +879,34 @@ __device__ __forceinline__ void decode_tc_body(const DecodeTcParams &tp, const C
       }
       const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, issue));
       const CUtensorMap *map = is_k ? tmap_k : tmap_v;
+      const int kvh = heads_of(un.kvh).kvh;
       if constexpr (!kFp8) {
         const int atoms = bs >> 3;
         if (lane == 0) mbar_arrive_expect_tx(full_bar, boxes * atoms * kAtomB);
         __syncwarp();
         if (issue) {
           uint8_t *dst = smem + GE::kOffRing + slot * GE::kSlotBytes + lane * atoms * kAtomB;
-          if constexpr (kD == 128) tma_load_4d(dst, map, full_bar, 0, 0, 0, (bi * hkv + un.kvh) * atoms);
-          else tma_load_3d(dst, map, full_bar, 0, 0, (bi * hkv + un.kvh) * atoms);
+          if constexpr (kD == 128) tma_load_4d(dst, map, full_bar, 0, 0, 0, (bi * hkv + kvh) * atoms);
+          else tma_load_3d(dst, map, full_bar, 0, 0, (bi * hkv + kvh) * atoms);
         }
       } else {
         if (lane == 0) mbar_arrive_expect_tx(full_bar, boxes * bs * kD);
         __syncwarp();
         if (issue)
           tma_load_2d(smem + GE::kOffRing + slot * GE::kSlotBytes + lane * bs * kD, map, full_bar, 0,
-                      (bi * hkv + un.kvh) * bs);
+                      (bi * hkv + kvh) * bs);
       }
     };
     // Q^T rows of a unit (16-bit caches): the G query heads of the KV head, 2 * kD bytes each
     auto load_q = [&](const UnitHdr &cur, int b) {
+      const Heads ch = heads_of(cur.kvh);
+      const int gr = ch.n;
 #pragma unroll
       for (int e = lane; e < G * kRowChunks; e += 32) {
         const int h = e / kRowChunks, c16 = e % kRowChunks;
         const bool real = !kPadRows || h < gr;   // padding rows are zero-filled (nothing read)
         const char *src = static_cast<const char *>(p.q) +
-                          (real ? (((int64_t)cur.row * hq + (int64_t)cur.kvh * gr + h) * kD) * 2 + c16 * 16 : 0);
+                          (real ? (((int64_t)cur.row * hq + ch.h0 + h) * kD) * 2 + c16 * 16 : 0);
         cp_async16(smem + GE::kOffQ + b * GE::kQBytes + (c16 >> 3) * (kNS * 128) + h * 128 +
                        (((c16 & 7) ^ (h & 7)) << 4),
                    src, real ? 16u : 0u);
@@ -818,7 +921,7 @@ __device__ __forceinline__ void decode_tc_body(const DecodeTcParams &tp, const C
       const int ib = u % kInfo, ibp = (u + kInfo - 1) % kInfo, b = u & 1;
       ok = wait_all(&info_full[ib], (u / kInfo) & 1);
       if (!ok) break;
-      const UnitHdr cur = read_unit(&info[ib]);
+      const UnitHdr cur = read_unit<kExt>(&info[ib]);
       const int ntc = num_tiles(cur), ntp = num_tiles(prev);
       if (ldr == 0 && !kFp8 && cur.valid) {
         if (u >= 2) {
@@ -855,7 +958,7 @@ __device__ __forceinline__ void decode_tc_body(const DecodeTcParams &tp, const C
     // id of run (lane & 7) of tile (lane >> 3) is read by lane `lane`.  fp8:
     // the unit's query scale from the largest |q| of its G query rows.
     const int bs = p.block_size;
-    const int total_units = __ldcg(&p.hdr->num_items) * hkv;
+    const int total_units = __ldcg(&p.hdr->num_items) * hkv_units;
     const int64_t cap = min((int64_t)p.max_blocks_per_seq * bs, (int64_t)p.max_partitions * p.partition_size);
     bool ok = true;
     // Store a new token's 16 bytes x (lanes 0-15: K, 16-31: V; elements 8c ..
@@ -898,11 +1001,16 @@ __device__ __forceinline__ void decode_tc_body(const DecodeTcParams &tp, const C
       const int id = id0 + (lane & (kClaim - 1));
       const bool valid = lane < kClaim && id < total_units;
       int item = 0, L = 0;
-      if (valid) item = __ldg(p.items + id / hkv);
+      if (valid) item = __ldg(p.items + id / hkv_units);
       const int row = item >> 12, part = item & 4095;
+      WindowSpan span{0, 0, 0, 0};
       if (valid) {
-        L = __ldg(p.seq_lens + row);
-        if (L < 0 || L > cap) L = L < 0 ? 0 : (int)cap;   // reported by the plan kernel
+        if constexpr (kExt) {
+          L = checked_packed_len<true>(tp, row, false, &span);   // packed tokens from here on
+        } else {
+          L = __ldg(p.seq_lens + row);
+          if (L < 0 || L > cap) L = L < 0 ? 0 : (int)cap;   // reported by the plan kernel
+        }
       }
       const int tok_begin = part * p.partition_size;
       const int ntok = valid ? max(0, min(L, tok_begin + p.partition_size) - tok_begin) : 0;
@@ -914,12 +1022,19 @@ __device__ __forceinline__ void decode_tc_body(const DecodeTcParams &tp, const C
         const int rk = __shfl_sync(0xffffffffu, row, k);
         const int tb = __shfl_sync(0xffffffffu, tok_begin, k);
         const int nk = __shfl_sync(0xffffffffu, ntok, k);
-        const int kvk = __shfl_sync(0xffffffffu, id % hkv, k);
+        const int unit_kvh = __shfl_sync(0xffffffffu, id % hkv_units, k);
+        const Heads kh = heads_of(unit_kvh);
+        const int kvk = kh.kvh, gr = kh.n;
+        int head_blocks = 0, skip_blocks = 0;
+        if constexpr (kExt) {
+          head_blocks = __shfl_sync(0xffffffffu, span.head_blocks, k);
+          skip_blocks = __shfl_sync(0xffffffffu, span.skip_blocks, k);
+        }
         const int pk = __shfl_sync(0xffffffffu, part, k);
         const int npk = __shfl_sync(0xffffffffu, nparts, k);
         // fused step: the row's new token goes with its last partition; its loads
         // are in flight with the block-table reads below
-        const bool wr = tp.k_new != nullptr && vk && pk == npk - 1;
+        const bool wr = !kExt && tp.k_new != nullptr && vk && pk == npk - 1;
         int64_t new_slot = -1;
         uint4 new_x = make_uint4(0, 0, 0, 0);
         float new_sc = 1.f;
@@ -946,7 +1061,7 @@ __device__ __forceinline__ void decode_tc_body(const DecodeTcParams &tp, const C
           };
           uint4 qw[kQIt];
           float amax = 0.f;
-          const char *q0 = static_cast<const char *>(p.q) + ((int64_t)rk * hq + (int64_t)kvk * gr) * kD * 2;
+          const char *q0 = static_cast<const char *>(p.q) + ((int64_t)rk * hq + kh.h0) * kD * 2;
 #pragma unroll
           for (int i = 0; i < kQIt; ++i) {
             const bool real = !kPadRows || (lane + 32 * i) / kCPH < gr;   // padding rows: zeros
@@ -985,7 +1100,9 @@ __device__ __forceinline__ void decode_tc_body(const DecodeTcParams &tp, const C
         const int key0 = tb + (lane >> 3) * kKeys + 16 * (lane & 7);
         int32_t blk = -1;
         if (vk && key0 < tb + nk) {
-          const int32_t bi = __ldg(p.block_tables + (int64_t)rk * p.max_blocks_per_seq + key0 / bs);
+          int lb = key0 / bs;
+          if (kExt && lb >= head_blocks) lb += skip_blocks;
+          const int32_t bi = __ldg(p.block_tables + (int64_t)rk * p.max_blocks_per_seq + lb);
           if (bi < 0 || bi >= p.num_blocks) record_error(p.err, PA_ERR_DEVICE_CHECK);
           else blk = bi;
         }
@@ -1005,10 +1122,15 @@ __device__ __forceinline__ void decode_tc_body(const DecodeTcParams &tp, const C
         if (lane == k) {
           dst->valid = vk;
           dst->row = rk;
-          dst->kvh = vk ? kvk : 0;
+          dst->kvh = vk ? unit_kvh : 0;
           dst->part = part;
           dst->tok_begin = tb;
-          dst->ntok = nk;
+          if constexpr (kExt) {
+            const int g0 = min(max(span.gap_lo - tb, 0), 512), g1 = min(max(span.gap_hi - tb, 0), 512);
+            dst->ntok = nk | (g0 << 10) | (g1 << 20);
+          } else {
+            dst->ntok = nk;
+          }
           dst->nparts = nparts;
           dst->qscale = qscale;
         }
@@ -1054,7 +1176,7 @@ __device__ __forceinline__ void decode_tc_body(const DecodeTcParams &tp, const C
               int old;
               asm volatile("atom.release.gpu.global.add.s32 %0, [%1], 1;"
                            : "=r"(old)
-                           : "l"(p.ws_count + (int64_t)r.x * hq + (int64_t)r.y * gr)
+                           : "l"(p.ws_count + (int64_t)r.x * hq + heads_of(r.y).h0)
                            : "memory");
               if (old == r.z - 1) {
                 asm volatile("fence.acq_rel.gpu;" ::: "memory");
@@ -1137,7 +1259,7 @@ __device__ __forceinline__ void decode_tc_body(const DecodeTcParams &tp, const C
       const int ib = u % kInfo, b = u & 1;
       ok = wait_all(&info_full[ib], (u / kInfo) & 1);
       if (!ok) break;
-      const UnitHdr cur = read_unit(&info[ib]);
+      const UnitHdr cur = read_unit<kExt>(&info[ib]);
       if (cur.valid) {
         // S^T(u, j) = K_j . Q^T into buffer b (its previous reader: the softmax of u-2)
         const int nt = num_tiles(cur);
@@ -1218,6 +1340,21 @@ __device__ __forceinline__ void decode_tc_body(const DecodeTcParams &tp, const C
             fence_async_smem();   // the zeroed rows (generic proxy) -> the MMAs' reads
             __syncwarp();
           }
+          if constexpr (kExt) {
+            // the same for the keys outside the window: P is 0, their rows may hold anything
+            const int z0 = max(prev.gap_lo - j * kKeys, 0), z1 = min(prev.gap_hi - j * kKeys, nvalid);
+            if (z0 < z1) {
+              constexpr int kRowC = kFp8 ? kD / 16 : kRowChunks;
+              for (int e = lane; e < (z1 - z0) * kRowC; e += 32) {
+                const int r = z0 + e / kRowC, c = e % kRowC;
+                uint8_t *dst = kFp8 ? vt + r * kD + c * 16
+                                    : vt + (r >> 3) * kAtomB + (c >> 3) * 1024 + (r & 7) * 128 + (c & 7) * 16;
+                *reinterpret_cast<uint4 *>(dst) = make_uint4(0, 0, 0, 0);
+              }
+              fence_async_smem();
+              __syncwarp();
+            }
+          }
           // P^T was fenced by the softmax warps before p_full; the tile came by bulk copy
           tc_fence_after();
           if (leader) {
@@ -1272,11 +1409,11 @@ __device__ __forceinline__ void decode_tc_body(const DecodeTcParams &tp, const C
   }
 }
 
-template <typename KV, typename QT, int G, int D, bool kPadRows>
+template <typename KV, typename QT, int G, int D, bool kPadRows, bool kExt>
 __global__ void __launch_bounds__(dtc::Roles::threads_for(dtc::Roles::loaders(G), dtc::Roles::sep_merge(G)), 1)
     decode_tc_kernel(const DecodeTcParams tp, const __grid_constant__ CUtensorMap tmap_k,
                      const __grid_constant__ CUtensorMap tmap_v) {
-  decode_tc_body<KV, QT, G, D, dtc::Roles::loaders(G), dtc::Roles::sep_merge(G), kPadRows>(tp, &tmap_k, &tmap_v);
+  decode_tc_body<KV, QT, G, D, dtc::Roles::loaders(G), dtc::Roles::sep_merge(G), kPadRows, kExt>(tp, &tmap_k, &tmap_v);
 }
 
 // One CTA: count the split rows' merges and clear the merge list, and list
@@ -1287,8 +1424,12 @@ __global__ void __launch_bounds__(dtc::Roles::threads_for(dtc::Roles::loaders(G)
 // rows' completion counters.  Long rows are then finished, and merged, while
 // shorter ones still run, and the smallest units come last, which evens out
 // the CTAs' finishing times.  An empty row lists one item of zero tokens.
-template <int kUnused>
-__global__ void __launch_bounds__(1024) decode_tc_plan_kernel(DecodeParams p, DecodeMergeJob *jobs) {
+// kExt: lengths are the rows' packed lengths under the window.
+template <bool kExt>
+__global__ void __launch_bounds__(1024) decode_tc_plan_kernel(DecodeTcParams tp) {
+  const DecodeParams &p = tp.d;
+  DecodeMergeJob *jobs = tp.jobs;
+  const int hkv_units = kExt ? p.num_kv_heads * tp.shares : p.num_kv_heads;
   // launched as a programmatic dependent of what precedes it on the stream
   // (the previous step's decode among others): its launch overlaps that grid's
   // end, and nothing of the workspace is touched before that grid is complete
@@ -1304,11 +1445,11 @@ __global__ void __launch_bounds__(1024) decode_tc_plan_kernel(DecodeParams p, De
   __shared__ int split_rows;
   for (int64_t i = tid; i < (int64_t)p.num_seqs * p.num_q_heads; i += blockDim.x) p.ws_count[i] = 0;
   if (p.max_partitions > 1)   // the merge list exists only when a row can be split
-    for (int64_t i = tid; i < (int64_t)p.num_seqs * p.num_kv_heads; i += blockDim.x) jobs[i].word = 0;
+    for (int64_t i = tid; i < (int64_t)p.num_seqs * hkv_units; i += blockDim.x) jobs[i].word = 0;
   for (int i = tid; i < nkeys; i += blockDim.x) base[i] = 0;
   if (tid == 0) split_rows = 0;
   __syncthreads();
-  auto len_of = [&](int r, bool report) { return checked_len(p, r, report); };
+  auto len_of = [&](int r, bool report) { return checked_packed_len<kExt>(tp, r, report, nullptr); };
   auto nparts_of = [&](int L) { return max(1, (L + p.partition_size - 1) / p.partition_size); };
   auto slot_of = [&](int L, int np) { return nkeys - 1 - (np > 1 ? 3 + np : (L + dtc::kKeys - 1) / dtc::kKeys); };
   for (int r = tid; r < p.num_seqs; r += blockDim.x) {
@@ -1328,7 +1469,7 @@ __global__ void __launch_bounds__(1024) decode_tc_plan_kernel(DecodeParams p, De
     p.hdr->next_unit = 0;
     p.hdr->pad[0] = 0;                              // merge records appended
     p.hdr->pad[1] = 0;                              // merge records taken
-    p.hdr->pad[2] = split_rows * p.num_kv_heads;    // one per split (row, KV head)
+    p.hdr->pad[2] = split_rows * hkv_units;         // one per split (row, KV head)
   }
   __syncthreads();
   for (int r = tid; r < p.num_seqs; r += blockDim.x) {
@@ -1342,8 +1483,8 @@ __global__ void __launch_bounds__(1024) decode_tc_plan_kernel(DecodeParams p, De
 // programmatic dependent.
 // The plan kernel, launched as a programmatic dependent of the stream's
 // previous work (it waits for that work before touching anything).
-template <int kUnused = 0>
-cudaError_t launch_decode_tc_plan(const DecodeParams &d, DecodeMergeJob *jobs, cudaStream_t s) {
+template <bool kExt = false>
+cudaError_t launch_decode_tc_plan(const DecodeTcParams &tp, cudaStream_t s) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(1);
   cfg.blockDim = dim3(1024);
@@ -1354,17 +1495,16 @@ cudaError_t launch_decode_tc_plan(const DecodeParams &d, DecodeMergeJob *jobs, c
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, decode_tc_plan_kernel<0>, d, jobs);
+  return cudaLaunchKernelEx(&cfg, decode_tc_plan_kernel<kExt>, tp);
 }
 
-template <typename KV, typename QT, int G, int D, bool kPadRows>
+template <typename KV, typename QT, int G, int D, bool kPadRows, bool kExt = false>
 cudaError_t launch_decode_tc_one(const DecodeTcParams &p, const PoolMaps &m, cudaStream_t s) {
-  constexpr bool kSplit = std::is_same<QT, __nv_bfloat16>::value && !std::is_same<KV, uint8_t>::value;
   constexpr int smem =
-      dtc::TcGeo<G, kSplit, std::is_same<KV, uint8_t>::value, dtc::QTerms<KV, QT>::value, D>::kSmemBytes;
-  cudaError_t e = launch_decode_tc_plan(p.d, p.jobs, s);
+      dtc::TcGeo<G, dtc::split_p<KV, QT, kExt>(), std::is_same<KV, uint8_t>::value, dtc::QTerms<KV, QT>::value, D>::kSmemBytes;
+  cudaError_t e = launch_decode_tc_plan<kExt>(p, s);
   if (e != cudaSuccess) return e;
-  if ((e = ensure_smem_limit<decode_tc_kernel<KV, QT, G, D, kPadRows>>(smem)) != cudaSuccess) return e;
+  if ((e = ensure_smem_limit<decode_tc_kernel<KV, QT, G, D, kPadRows, kExt>>(smem)) != cudaSuccess) return e;
   int sms = 0;
   if ((e = current_sm_count(&sms)) != cudaSuccess) return e;
   // programmatic dependent launch: the decode grid's set-up overlaps the plan kernel
@@ -1378,7 +1518,7 @@ cudaError_t launch_decode_tc_one(const DecodeTcParams &p, const PoolMaps &m, cud
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, decode_tc_kernel<KV, QT, G, D, kPadRows>, p, m.k, m.v);
+  return cudaLaunchKernelEx(&cfg, decode_tc_kernel<KV, QT, G, D, kPadRows, kExt>, p, m.k, m.v);
 }
 
 // m: tensor maps over the pools, one box per cache block of one KV head: 16-bit
@@ -1401,6 +1541,23 @@ cudaError_t launch_decode_tc(const DecodeTcParams &p, int gqa, int head_dim, con
   if (gqa <= 4) return launch_decode_tc_one<KV, QT, 4, 128, kPadRows>(p, m, s);
   if (gqa <= 8) return launch_decode_tc_one<KV, QT, 8, 128, kPadRows>(p, m, s);
   if (gqa <= 16) return launch_decode_tc_one<KV, QT, 16, 128, kPadRows>(p, m, s);
+  return cudaErrorInvalidValue;
+}
+
+// The bounded-cache decodes (kExt): every group size, a share of at most 16
+// (head_dim 64: 8) query heads per unit, run padded to 4, 8 or 16 rows.
+template <typename KV, typename QT>
+cudaError_t launch_decode_ext(const DecodeTcParams &p, int head_dim, const PoolMaps &m, cudaStream_t s) {
+  switch (decode_ext_rows(p.share_heads)) {
+    case 4:
+      return head_dim == 64 ? launch_decode_tc_one<KV, QT, 4, 64, true, true>(p, m, s)
+                            : launch_decode_tc_one<KV, QT, 4, 128, true, true>(p, m, s);
+    case 8:
+      return head_dim == 64 ? launch_decode_tc_one<KV, QT, 8, 64, true, true>(p, m, s)
+                            : launch_decode_tc_one<KV, QT, 8, 128, true, true>(p, m, s);
+    case 16:
+      if (head_dim == 128) return launch_decode_tc_one<KV, QT, 16, 128, true, true>(p, m, s);
+  }
   return cudaErrorInvalidValue;
 }
 

@@ -157,6 +157,69 @@ cudaError_t launch_decode_tc_fp8_bf16q(const DecodeTcParams &p, int gqa, int hea
 cudaError_t launch_decode_tc_fp8_f16q(const DecodeTcParams &p, int gqa, int head_dim, const PoolMaps &m,
                                       cudaStream_t s);
 
+// Bounded-cache decodes (pa_decode_window, pa_decode_weights): the tensor-core
+// decode with packed rows (pa_window.cuh), for every group size.  A group wider
+// than 16 query heads (head_dim 64: 8) is cut into shares, each its own unit; a
+// share runs padded to 4, 8 or 16 rows.
+constexpr int decode_ext_shares(int head_dim, int gqa) {
+  const int most = head_dim == 64 ? 8 : 16;
+  return (gqa + most - 1) / most;
+}
+constexpr int decode_ext_rows(int share_heads) { return share_heads <= 4 ? 4 : share_heads <= 8 ? 8 : 16; }
+cudaError_t launch_decode_ext_bf16(const DecodeTcParams &p, int head_dim, const PoolMaps &m, cudaStream_t s);
+cudaError_t launch_decode_ext_f16(const DecodeTcParams &p, int head_dim, const PoolMaps &m, cudaStream_t s);
+cudaError_t launch_decode_ext_fp8_bf16q(const DecodeTcParams &p, int head_dim, const PoolMaps &m, cudaStream_t s);
+cudaError_t launch_decode_ext_fp8_f16q(const DecodeTcParams &p, int head_dim, const PoolMaps &m, cudaStream_t s);
+
+// The second half of pa_decode_weights: each cached token's softmax weight from
+// the scores the decode left in the workspace (pa_weights.cu).
+struct WeightsParams {
+  const float *scores;        // [num_seqs][num_kv_heads * shares][score_stride][score_rows], log2 units
+  int64_t score_stride;
+  int32_t score_rows;         // 4, 8 or 16: a token's scores, of which the share's heads count
+  const float2 *row_ml;       // [num_seqs][num_q_heads] (maximum, 1 / sum)
+  const int32_t *seq_lens;
+  int32_t num_seqs, num_q_heads, num_kv_heads, shares, share_heads;
+  int32_t max_len;            // longest row served
+  float *weights;             // [num_weight_rows][num_kv_heads][weights_stride]
+  int64_t weights_stride;
+  int32_t num_weight_rows;
+  const int32_t *weight_rows;  // null: row i
+  const int32_t *fresh_from;   // null: the last token
+  float decay;
+  int32_t *err;
+};
+cudaError_t launch_decode_weights(const WeightsParams &p, cudaStream_t s);
+
+// Eviction by accumulated attention weight (pa_evict.cu).
+struct EvictParams {
+  char *k_cache, *v_cache;
+  int32_t row_bytes;          // bytes of one token's K (or V) row of one head
+  int64_t num_blocks;
+  int32_t num_seqs, num_kv_heads, block_size;
+  const int32_t *block_tables;
+  int32_t max_blocks_per_seq;
+  const int32_t *seq_lens;
+  int32_t max_seq_len;
+  const int32_t *num_tokens, *ordered_from;
+  int32_t budget, num_sinks, num_recent;
+  const float *weights;       // [num_weight_rows][num_kv_heads][stride], as the three below
+  const int32_t *positions;
+  float *new_weights;
+  int32_t *new_positions;
+  int64_t stride;
+  int32_t num_weight_rows;
+  const int32_t *weight_rows;  // null: row i
+  int32_t *new_seq_lens;
+  // workspace: the rows' new lengths, and per (row, head) the number of moves, then their
+  // destinations, sources and the sources' positions (list_cap each)
+  int32_t *lens;
+  int32_t *lists;
+  int64_t list_stride, list_cap;
+  int32_t *err;
+};
+cudaError_t launch_evict(const EvictParams &p, cudaStream_t s);
+
 // One launch for a prefill chunk batch and a decode batch (pa_mixed_tc.cuh):
 // both on the tensor cores, head_dim 128, 4 or 8 query heads per KV head.
 constexpr bool mixed_tc_supported(int head_dim, int gqa) { return head_dim == 128 && (gqa == 4 || gqa == 8); }
@@ -181,5 +244,16 @@ cudaError_t launch_prefill_tc_fp8_bf16q(const PrefillTcParams &p, const PoolMaps
                                         cudaStream_t s);
 cudaError_t launch_prefill_tc_fp8_f16q(const PrefillTcParams &p, const PoolMaps &m, int gqa, int num_chunks,
                                        cudaStream_t s);
+
+// Chunked prefill under a sliding window (head_dim 64 and 128, any group).
+constexpr int kPrefillWindowHeads = 128;   // query heads a CTA row packs at most
+cudaError_t launch_prefill_window_bf16(const PrefillTcParams &p, const PoolMaps &m, int head_dim, int num_chunks,
+                                       cudaStream_t s);
+cudaError_t launch_prefill_window_f16(const PrefillTcParams &p, const PoolMaps &m, int head_dim, int num_chunks,
+                                      cudaStream_t s);
+cudaError_t launch_prefill_window_fp8_bf16q(const PrefillTcParams &p, const PoolMaps &m, int head_dim, int num_chunks,
+                                            cudaStream_t s);
+cudaError_t launch_prefill_window_fp8_f16q(const PrefillTcParams &p, const PoolMaps &m, int head_dim, int num_chunks,
+                                           cudaStream_t s);
 
 }  // namespace pa

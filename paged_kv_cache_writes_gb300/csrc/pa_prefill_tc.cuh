@@ -66,6 +66,7 @@
 #include "pa_common.cuh"
 #include "pa_internal.h"
 #include "pa_tcgen05.cuh"
+#include "pa_window.cuh"
 
 namespace pa {
 
@@ -91,6 +92,12 @@ struct PrefillTcParams {
   const float *k_hs;           // fp8, optional: [Hkv] per-head scales multiplying s_mult / out_mult
   const float *v_hs;
   int32_t *err;
+  // kernels built with kWin: a sliding window with first tokens that stay
+  // visible, and query groups of any size, each cut into `shares` of
+  // share_heads heads (the last may have fewer) that a CTA row packs
+  int32_t window;
+  int32_t num_sinks;
+  int32_t shares, share_heads;
 };
 
 namespace tc {
@@ -130,8 +137,7 @@ struct Roles {
 };
 constexpr float kRescaleLog2 = 8.f;
 
-constexpr int kQBytes = kM * kD * 2;        // one Q tile: 2 panels x [128 rows x 128 B]
-constexpr int kTileBytes = kN * kD * 2;     // 2 panels x [128 rows x 128 B]
+// a Q tile, and a K or V tile: D / 64 panels of [128 rows x 128 B] (Layout::kQBytes, kTileBytes)
 constexpr int kTilePanel = kN * 128;        // 16 KB
 constexpr int kLoaders = 128;               // threads of the load warps
 constexpr int kCodeTile = kN * kD;          // fp8 codes of one K or V tile (128 rows x 128 B)
@@ -141,9 +147,10 @@ constexpr int kNumBars = 4 * kStages + 3 * 4 + 2 + 4 * kMaxCodeStages;
 // Shared-memory map, bytes from a 1024-aligned base (128-byte swizzle atoms).
 // fp8 caches with one Q tile: kCStages tiles of codes (K then V) after the
 // 16-bit K/V stages.
-template <int QT, bool kFp8 = false>
+template <int QT, bool kFp8 = false, int D = 128>
 struct Layout {
-  static constexpr int kCStages = (kFp8 && QT == 1) ? kMaxCodeStages : 0;
+  static constexpr int kQBytes = kM * D * 2, kTileBytes = kN * D * 2;
+  static constexpr int kCStages = (kFp8 && QT == 1 && D == 128) ? kMaxCodeStages : 0;
   static constexpr int kOffQ = 0;
   static constexpr int kOffK = kOffQ + QT * kQBytes;
   static constexpr int kOffV = kOffK + kStages * kTileBytes;
@@ -159,19 +166,26 @@ struct Layout {
 
 // The prefill CTA (chunk x row block bx, KV head by), for prefill_tc_kernel and
 // for the prefill CTAs of the mixed kernel (pa_mixed_tc.cuh).
-template <typename KV, typename QT, int G, int kQTiles>
+// G: query heads per KV head; with kWin 0, the group then being p.share_heads
+// heads, rows past the last whole token of the CTA's tiles left idle.
+template <typename KV, typename QT, int G, int kQTiles, int D = 128, bool kWin = false>
 __device__ __forceinline__ void prefill_tc_body(const PrefillTcParams &p, int bx, int by, const CUtensorMap *tmap_k,
                                                 const CUtensorMap *tmap_v) {
   using namespace tc;
-  using L = Layout<kQTiles, std::is_same<KV, uint8_t>::value>;
+  static_assert(D == 64 || D == 128, "head_dim 64 or 128");
+  static_assert(kWin == (G == 0) && (kWin || D == 128), "any group and head_dim 64 with kWin only");
+  constexpr int kD = D;                       // head_dim (hides tc::kD)
+  using L = Layout<kQTiles, std::is_same<KV, uint8_t>::value, D>;
   using R = Roles<kQTiles>;
+  constexpr int kQBytes = L::kQBytes, kTileBytes = L::kTileBytes;
   constexpr int kSoftmax = R::kSoftmax, kLoadWarp0 = R::kLoadWarp0, kMmaWarp = R::kMmaWarp;
   constexpr int kTmemCols = R::kTmemCols;
   constexpr int kBufs = R::kBufs;
   constexpr bool kFp8 = std::is_same<KV, uint8_t>::value;
   constexpr bool kBf16 = std::is_same<QT, __nv_bfloat16>::value;
   constexpr bool kSplit = kBf16 && !kFp8;   // bf16 cache: P as hi + lo
-  constexpr int BR = kQTiles * kM / G;      // token rows per CTA
+  const int gr = kWin ? p.share_heads : G;
+  const int BR = kQTiles * kM / (kWin ? gr : G);      // token rows per CTA
   constexpr bool kF16Ops = kFp8 || !kBf16;   // f16 MMA operands (f16 cache, or any fp8 cache)
   constexpr uint32_t kAB = kF16Ops ? 0u : 1u;
   const float kNegInf = -__int_as_float(0x7f800000);
@@ -195,10 +209,12 @@ __device__ __forceinline__ void prefill_tc_body(const PrefillTcParams &p, int bx
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int c = bx / p.row_blocks, rb = bx % p.row_blocks;
-  const int g = by;
+  const int g = kWin ? by / p.shares : by;   // KV head
+  const int h_first = kWin ? (by - g * p.shares) * gr : 0;             // the share's first head of the group
+  const int gqa = kWin ? p.num_q_heads / p.num_kv_heads : G;
   const int cu0 = __ldg(p.cu_q_lens + c), nrows = __ldg(p.cu_q_lens + c + 1) - cu0;
   const int qs = __ldg(p.q_start + c);
-  if (tid == 0 && g == 0 && rb == 0) {
+  if (tid == 0 && by == 0 && rb == 0) {
     const int64_t len = (int64_t)qs + nrows;
     if (nrows < 0 || nrows > p.max_q_len || qs < 0 || __ldg(p.seq_lens + c) != len ||
         len > (int64_t)p.max_blocks_per_seq * p.block_size)
@@ -209,9 +225,21 @@ __device__ __forceinline__ void prefill_tc_body(const PrefillTcParams &p, int bx
   // keys this chunk may read: its sequence, clamped to the block table
   const int64_t cap = (int64_t)p.max_blocks_per_seq * p.block_size;
   const int64_t len64 = (int64_t)qs + nrows;
-  const int seq_eff = len64 <= 0 ? 0 : (int)(len64 < cap ? len64 : cap);
+  int seq_eff = len64 <= 0 ? 0 : (int)(len64 < cap ? len64 : cap);
   const int r_last = min(r0 + BR, nrows) - 1;
-  const int kv_end = min(seq_eff, max(0, qs + r_last + 1));   // keys this CTA needs
+  int kv_end = min(seq_eff, max(0, qs + r_last + 1));   // keys this CTA needs
+  // kWin: from here on keys are packed positions (pa_window.cuh) of the keys that
+  // some row of the CTA may see, its first row reaching back furthest; keys of
+  // [gap_lo, gap_hi) are seen by none of its rows.
+  const int bs_log2 = p.block_size == 32 ? 5 : 4;
+  WindowSpan span{0, 0, 0, 0};
+  int skip = 0;   // tokens left out between the two parts
+  if constexpr (kWin) {
+    span = window_span(min(window_low(max(0, qs + r0 + 1), p.window), seq_eff), p.num_sinks, bs_log2);
+    skip = span.skip_blocks << bs_log2;
+    seq_eff -= skip;
+    kv_end = max(0, kv_end - skip);
+  }
   const int nkt = (kv_end + kN - 1) / kN;                      // key tiles (may be 0)
   const int32_t *table = p.block_tables + (int64_t)c * p.max_blocks_per_seq;
 
@@ -250,11 +278,12 @@ __device__ __forceinline__ void prefill_tc_body(const PrefillTcParams &p, int bx
     // ===================================================== softmax warps (Q tile t = warp / 4)
     const int m = tid;                         // packed row
     const int t = m / kM;
-    const int rl = m / G, hq = m % G;
-    const bool row_ok = r0 + rl < nrows;
-    const int head = g * G + hq;
-    // keys this row attends to: positions < lim
-    const int lim = row_ok ? min(seq_eff, max(0, qs + r0 + rl + 1)) : 0;
+    const int rl = m / (kWin ? gr : G), hq = m % (kWin ? gr : G);
+    const bool row_ok = r0 + rl < nrows && (!kWin || (rl < BR && h_first + hq < gqa));
+    const int head = g * gqa + h_first + hq;
+    // keys this row attends to: positions < lim, with kWin but not those in [num_sinks, row_low)
+    const int lim = row_ok ? min(seq_eff, max(0, qs + r0 + rl + 1) - skip) : 0;
+    const int row_low = kWin ? window_low(max(0, qs + r0 + rl + 1), p.window) - skip : 0;
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     // scores are scaled by |s_mult| in the exponent; a negative scale flips q's sign instead
     float cmul = fabsf(p.s_mult) * (p.k_hs ? __ldg(p.k_hs + g) : 1.f);
@@ -266,10 +295,10 @@ __device__ __forceinline__ void prefill_tc_body(const PrefillTcParams &p, int bx
       if constexpr (kFp8 && kBf16) {
         // f16 operands: the row times 2^e (its largest element in [2^14, 2^15)), rounded to f16;
         // the scores are multiplied back by 2^-e
-        uint4 v[16];
+        uint4 v[kD / 8];
         float amax = 0.f;
 #pragma unroll
-        for (int ch = 0; ch < 16; ++ch) {
+        for (int ch = 0; ch < kD / 8; ++ch) {
           v[ch] = row_ok ? __ldg(reinterpret_cast<const uint4 *>(src) + ch) : make_uint4(0, 0, 0, 0);
           const uint32_t ws[4] = {v[ch].x, v[ch].y, v[ch].z, v[ch].w};
 #pragma unroll
@@ -282,7 +311,7 @@ __device__ __forceinline__ void prefill_tc_body(const PrefillTcParams &p, int bx
         const float sc = __uint_as_float((uint32_t)(e + 127) << 23);
         cmul *= __uint_as_float((uint32_t)(127 - e) << 23);
 #pragma unroll
-        for (int ch = 0; ch < 16; ++ch) {
+        for (int ch = 0; ch < kD / 8; ++ch) {
           const uint32_t ws[4] = {v[ch].x, v[ch].y, v[ch].z, v[ch].w};
           uint32_t o[4];
 #pragma unroll
@@ -296,7 +325,7 @@ __device__ __forceinline__ void prefill_tc_body(const PrefillTcParams &p, int bx
         }
       } else {
 #pragma unroll
-        for (int ch = 0; ch < 16; ++ch) {
+        for (int ch = 0; ch < kD / 8; ++ch) {
           uint4 v = row_ok ? __ldg(reinterpret_cast<const uint4 *>(src) + ch) : make_uint4(0, 0, 0, 0);
           v.x ^= qflip; v.y ^= qflip; v.z ^= qflip; v.w ^= qflip;
           *reinterpret_cast<uint4 *>(qt + (ch >> 3) * (kM * 128) + mr * 128 + (((ch & 7) ^ (mr & 7)) << 4)) = v;
@@ -322,7 +351,10 @@ __device__ __forceinline__ void prefill_tc_body(const PrefillTcParams &p, int bx
       // keys at or past this row's limit are masked, but only tiles that reach
       // some row's limit (the causal diagonal, the sequence end) need the test
       const int nvis = lim - j * kN;
-      const bool full_tile = __all_sync(0xffffffffu, nvis >= kN);
+      const int g0 = kWin ? p.num_sinks - j * kN : 0, glen = kWin ? max(0, row_low - j * kN - g0) : 0;
+      const bool full_tile =
+          __all_sync(0xffffffffu, nvis >= kN && (!kWin || glen == 0 || g0 >= kN || g0 + glen <= 0));
+      auto hidden = [&](int i) { return i >= nvis || (kWin && (uint32_t)(i - g0) < (uint32_t)glen); };
       // pass 1: the tile maximum
       float mx[8];
 #pragma unroll
@@ -334,7 +366,7 @@ __device__ __forceinline__ void prefill_tc_body(const PrefillTcParams &p, int bx
         if (!full_tile) {
 #pragma unroll
           for (int i = 0; i < 32; ++i)
-            if (32 * ck + i >= nvis) sv[i] = kNegInf;
+            if (hidden(32 * ck + i)) sv[i] = kNegInf;
         }
 #pragma unroll
         for (int i = 0; i < 16; ++i) mx[i & 7] = fmax3(mx[i & 7], sv[2 * i], sv[2 * i + 1]);
@@ -383,8 +415,8 @@ __device__ __forceinline__ void prefill_tc_body(const PrefillTcParams &p, int bx
             const float2 a = ffma2(make_float2(sv[2 * k], sv[2 * k + 1]), cc, nm);
             float2 pk = make_float2(fast_exp2(a.x), fast_exp2(a.y));
             if (!full_tile) {
-              if (i0 >= nvis) pk.x = 0.f;
-              if (i0 + 1 >= nvis) pk.y = 0.f;
+              if (hidden(i0)) pk.x = 0.f;
+              if (hidden(i0 + 1)) pk.y = 0.f;
             }
             if constexpr (kSplit) {
               // bf16 cache: hi = p rounded to bf16, lo = p - hi (exact in fp32) rounded to
@@ -466,7 +498,9 @@ __device__ __forceinline__ void prefill_tc_body(const PrefillTcParams &p, int bx
         const int key = jt * kN + 32 * lw + 16 * (lane & 1);
         win = -1;
         if (jt < nkt && key < seq_eff) {
-          const int32_t bi = __ldg(table + key / p.block_size);
+          int lb = key / p.block_size;
+          if (kWin && lb >= span.head_blocks) lb += span.skip_blocks;
+          const int32_t bi = __ldg(table + lb);
           if (bi < 0 || bi >= p.num_blocks) record_error(p.err, PA_ERR_DEVICE_CHECK);
           else win = bi;
         }
@@ -480,14 +514,22 @@ __device__ __forceinline__ void prefill_tc_body(const PrefillTcParams &p, int bx
       row0 = ((int64_t)max(blk, 0) * p.num_kv_heads + g) * p.block_size + (key0 % p.block_size);
       return blk < 0 ? 0 : min(16, seq_eff - key0);
     };
+    // whether row rr of run r of tile j holds a key that some row of the CTA may see
+    // (nval: the run's rows that hold data); the others are zero-filled
+    auto seen = [&](int j, int r, int rr, int nval) {
+      if (!kWin) return rr < nval;
+      const int key = j * kN + 32 * lw + 16 * r + rr;
+      return rr < nval && !(key >= span.gap_lo && key < span.gap_hi);
+    };
     bool ok = true;
     auto wait_slot = [&](uint64_t *bar, uint32_t parity) {
       ok = __all_sync(0xffffffffu, wait_or_abort(bar, parity, p.err, abort_flag));
       return ok;
     };
     if constexpr (!kFp8) {
-      // 16-bit rows (256 B): per instruction 2 rows x 16 chunks of 16 B
-      const int q = lane & 15, pn = q >> 3, cq = q & 7;
+      // 16-bit rows: per instruction 2 rows x 16 chunks of 16 B (head_dim 64: 4 rows x 8 chunks)
+      constexpr int kC = kD / 8, kRI = 32 / kC;   // chunks per row, rows per instruction
+      const int q = lane % kC, pn = q >> 3, cq = q & 7;
       for (int j = 0; j < nkt && ok; ++j) {
         const int s = j % kStages;
         const uint32_t ph_prev = ((j / kStages) - 1) & 1;
@@ -503,10 +545,10 @@ __device__ __forceinline__ void prefill_tc_body(const PrefillTcParams &p, int bx
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const int rr = 2 * i + (lane >> 4);             // row among the run's 16
+            for (int i = 0; i < 16 / kRI; ++i) {
+              const int rr = kRI * i + lane / kC;             // row among the run's 16
               const int row = 32 * lw + 16 * r + rr;           // row of the tile
-              const bool v = rr < nval[r];
+              const bool v = seen(j, r, rr, nval[r]);
               const char *src = v ? pool + (row0[r] + rr) * kRowBytes + q * 16 : pool;
               cp_async16(tile + row * 128 + ((cq ^ (row & 7)) << 4), src, v ? 16u : 0u);
             }
@@ -559,7 +601,7 @@ __device__ __forceinline__ void prefill_tc_body(const PrefillTcParams &p, int bx
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int rr = 4 * i + (lane >> 3), row = 32 * lw + 16 * r + rr;
-            const uint4 cw = rr < nval ? *reinterpret_cast<const uint4 *>(cst + which * kCodeTile + row * 128 +
+            const uint4 cw = seen(j, r, rr, nval) ? *reinterpret_cast<const uint4 *>(cst + which * kCodeTile + row * 128 +
                                                                             ((q ^ (row & 7)) << 4))
                                        : make_uint4(0, 0, 0, 0);
             uint32_t o[8];
@@ -583,22 +625,23 @@ __device__ __forceinline__ void prefill_tc_body(const PrefillTcParams &p, int bx
         wait_or_abort(&cbar[jj % kCS], (jj / kCS) & 1, p.err, abort_flag);
     } else {
       // fp8 rows (128 B), two Q tiles: per instruction 4 rows x 8 words of 16
-      // codes.  A tile is four quarters (K run 0, K run 1, V run 0, V run 1).
+      // codes (head_dim 64, any number of Q tiles: 8 rows x 4 words).  A tile is four quarters (K run 0, K run 1, V run 0, V run 1).
       // The loads run kPf quarters (half a tile) ahead of the widening into
       // shared memory.
       constexpr int kPf = 2;
-      const int q = lane & 7, pn = q >> 2, c0 = (2 * q) & 7;
-      auto load = [&](int j, int qi, uint4 (&w)[4]) {
+      constexpr int kC = kD / 16, kRI = 32 / kC, kIt = 16 / kRI;   // words per row, rows per instruction, instructions
+      const int q = lane % kC, pn = q >> 2, c0 = (2 * q) & 7;
+      auto load = [&](int j, int qi, uint4 (&w)[kIt]) {
         int64_t row0;
         const int nval = rows_of(j, qi & 1, row0);
         const char *pool = (qi >> 1) ? vpool : kpool;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int rr = 4 * i + (lane >> 3);
-          w[i] = rr < nval ? ld_nc16(pool + (row0 + rr) * kRowBytes + q * 16) : make_uint4(0, 0, 0, 0);
+        for (int i = 0; i < kIt; ++i) {
+          const int rr = kRI * i + lane / kC;
+          w[i] = seen(j, qi & 1, rr, nval) ? ld_nc16(pool + (row0 + rr) * kRowBytes + q * 16) : make_uint4(0, 0, 0, 0);
         }
       };
-      uint4 buf[kPf][4];   // quarter g of the load order in buf[g % kPf]
+      uint4 buf[kPf][kIt];   // quarter g of the load order in buf[g % kPf]
 #pragma unroll
       for (int g = 0; g < kPf; ++g)
         if (g / 4 < nkt) load(g / 4, g % 4, buf[g]);
@@ -610,10 +653,10 @@ __device__ __forceinline__ void prefill_tc_body(const PrefillTcParams &p, int bx
           const int which = qi >> 1, r = qi & 1;
           if (r == 0 && j >= kStages && !wait_slot(which ? &v_free[s] : &k_free[s], ph_prev)) break;
           uint8_t *tile = smem + (which ? L::kOffV : L::kOffK) + s * kTileBytes + pn * kTilePanel;
-          uint4 (&cur)[4] = buf[qi % kPf];
+          uint4 (&cur)[kIt] = buf[qi % kPf];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int row = 32 * lw + 16 * r + 4 * i + (lane >> 3);
+          for (int i = 0; i < kIt; ++i) {
+            const int row = 32 * lw + 16 * r + kRI * i + lane / kC;
             uint32_t o[8];
             widen16<__half>(cur[i], o);   // the MMAs take f16 operands with an fp8 cache
             uint8_t *dst = tile + row * 128;
@@ -786,6 +829,52 @@ cudaError_t launch_prefill_tc(const PrefillTcParams &p, const PoolMaps &m, int g
     case 16: return launch_prefill_tc_one<KV, QT, 16>(p, m, num_chunks, num_sms, s);
     default: return cudaErrorInvalidValue;
   }
+}
+
+// ---------------------------------------------------------------------------
+// pa_prefill_chunk_window: the same tiles over the packed keys of a sliding
+// window with first tokens that stay visible (pa_window.cuh).  A CTA of BR
+// token rows walks window + BR + sinks keys instead of the whole context.
+// One kernel for every group size (the group is a run-time number: one
+// division per thread) and for head_dim 64 and 128.
+template <typename KV, typename QT, int kQTiles, int D>
+__global__ void __launch_bounds__(tc::Roles<kQTiles>::kThreads, 1)
+    prefill_window_kernel(const PrefillTcParams p, const __grid_constant__ CUtensorMap tmap_k,
+                          const __grid_constant__ CUtensorMap tmap_v) {
+  prefill_tc_body<KV, QT, 0, kQTiles, D, true>(p, blockIdx.x, blockIdx.y, &tmap_k, &tmap_v);
+}
+
+template <typename KV, typename QT, int kQTiles, int D>
+cudaError_t launch_prefill_window_tiles(const PrefillTcParams &p0, const PoolMaps &m, int num_chunks, cudaStream_t s) {
+  constexpr int smem = tc::Layout<kQTiles, std::is_same<KV, uint8_t>::value, D>::kSmemBytes;
+  PrefillTcParams p = p0;
+  const int BR = kQTiles * tc::kM / p.share_heads;
+  p.row_blocks = (p.max_q_len + BR - 1) / BR;
+  cudaError_t e = ensure_smem_limit<prefill_window_kernel<KV, QT, kQTiles, D>>(smem);
+  if (e != cudaSuccess) return e;
+  const int64_t gx = (int64_t)num_chunks * p.row_blocks, gy = (int64_t)p.num_kv_heads * p.shares;
+  if (gx > 2147483647ll || gy > 65535) return cudaErrorInvalidValue;
+  prefill_window_kernel<KV, QT, kQTiles, D>
+      <<<dim3((unsigned)gx, (unsigned)gy), tc::Roles<kQTiles>::kThreads, smem, s>>>(p, m.k, m.v);
+  return cudaGetLastError();
+}
+
+template <typename KV, typename QT, int D>
+cudaError_t launch_prefill_window_one(const PrefillTcParams &p, const PoolMaps &m, int num_chunks, cudaStream_t s) {
+  int num_sms = 0;
+  if (current_sm_count(&num_sms) != cudaSuccess) return cudaErrorUnknown;
+  const int br2 = 2 * tc::kM / p.share_heads;
+  const int64_t two = (int64_t)num_chunks * ((p.max_q_len + br2 - 1) / br2) * p.num_kv_heads * p.shares;
+  if (two >= num_sms) return launch_prefill_window_tiles<KV, QT, 2, D>(p, m, num_chunks, s);
+  return launch_prefill_window_tiles<KV, QT, 1, D>(p, m, num_chunks, s);
+}
+
+template <typename KV, typename QT>
+cudaError_t launch_prefill_window(const PrefillTcParams &p, const PoolMaps &m, int head_dim, int num_chunks,
+                                  cudaStream_t s) {
+  if (head_dim == 64) return launch_prefill_window_one<KV, QT, 64>(p, m, num_chunks, s);
+  if (head_dim == 128) return launch_prefill_window_one<KV, QT, 128>(p, m, num_chunks, s);
+  return cudaErrorInvalidValue;
 }
 
 }  // namespace pa

@@ -1,0 +1,10 @@
+// pa_prefill_window_fp8_bf16q.cu -- sliding-window chunked-prefill instantiations
+// for an fp8-e4m3 cache with bf16 queries.
+#include "pa_prefill_tc.cuh"
+
+namespace pa {
+cudaError_t launch_prefill_window_fp8_bf16q(const PrefillTcParams &p, const PoolMaps &m, int head_dim, int num_chunks,
+                                           cudaStream_t s) {
+  return launch_prefill_window<uint8_t, __nv_bfloat16>(p, m, head_dim, num_chunks, s);
+}
+}  // namespace pa

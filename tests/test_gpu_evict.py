@@ -1,0 +1,123 @@
+"""pa_evict on the GPU: which tokens stay, where they go, and what happens to everything else, bit for bit against the
+plain form (tests/_bounded.py)."""
+import pytest
+import torch
+
+import paged_kv_cache_writes_gb300 as pa
+from _bounded import Cache, evict
+
+pytestmark = pytest.mark.gpu
+
+
+def bits(t):
+    t = t.contiguous()
+    return t.view({1: torch.uint8, 2: torch.int16, 4: torch.int32}[t.element_size()]).cpu()
+
+
+def evict_case(lens, hkv, d, bs, kv, budget, sinks, recent, seed=0, seen=None, old=None, rows=None, pad=0, alias=False,
+               weights=None, most=None):
+    c = Cache(lens, hkv, d, bs, kv, seed)
+    c.k, c.v = (x if kv == "fp8" else torch.nan_to_num(x) for x in (c.k, c.v))
+    g = torch.Generator().manual_seed(seed + 1)
+    n = len(lens)
+    most = most or max(max(lens), 1)
+    seen, old = seen or list(lens), old or [0] * n
+    at = rows or list(range(n))
+    held = max(at) + 2
+    w = torch.rand((held, hkv, most + pad), generator=g) if weights is None else weights
+    p = torch.full(w.shape, -9, dtype=torch.int32)
+    for i in range(n):
+        for h in range(hkv):   # distinct earlier positions, in any order
+            p[at[i], h, :old[i]] = torch.randperm(max(1, seen[i] - lens[i] + old[i]), generator=g)[:old[i]].to(torch.int32)
+    k, v, tables, desc = c.device(pa)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    dw, dp, dl = w.cuda(), p.cuda(), i32(lens)
+    nw, np_, nl = (dw, dp, dl) if alias else (torch.full_like(dw, 7.0), torch.full_like(dp, 7), i32([-5] * n))
+    ws = torch.full((pa.pa_evict_workspace_bytes(n, hkv, most, budget),), 0xFF, dtype=torch.uint8, device="cuda")
+    pa.pa_evict(k, v, desc, tables, dl, most, i32(seen), i32(old), budget, sinks, recent, dw, dp, nw, np_, nl,
+                None if rows is None else i32(rows), ws)
+    assert pa.pa_get_device_error() == 0
+    want_k, want_v = c.k.clone(), c.v.clone()
+    want_w, want_p = (w.clone(), p.clone()) if alias else (torch.full_like(w, 7.0), torch.full_like(p, 7))
+    for i, m in enumerate(lens):
+        t = c.tables[i].tolist()
+        for h in range(hkv):
+            src, pos = evict(w[at[i], h], p[at[i], h], m, seen[i], old[i], budget, sinks, recent)
+            for j, s in enumerate(src):
+                want_w[at[i], h, j], want_p[at[i], h, j] = w[at[i], h, s], pos[s]
+                if s != j:
+                    want_k[t[j // bs], h, j % bs] = c.k[t[s // bs], h, s % bs]
+                    want_v[t[j // bs], h, j % bs] = c.v[t[s // bs], h, s % bs]
+    assert nl.tolist() == [min(m, budget) for m in lens]
+    assert torch.equal(np_.cpu(), want_p)
+    assert torch.equal(bits(nw), bits(want_w))
+    assert torch.equal(bits(k), bits(want_k)) and torch.equal(bits(v), bits(want_v))
+
+
+@pytest.mark.parametrize("kv", ["bf16", "f16", "fp8"])
+@pytest.mark.parametrize("d,bs", [(64, 16), (128, 16), (128, 32)])
+def test_types(kv, d, bs):
+    evict_case([1, 20, 64, 65, 200, 333], 3, d, bs, kv, 64, 4, 10, seed=d + bs)
+
+
+@pytest.mark.parametrize("budget,sinks,recent", [(1, 0, 0), (1, 1, 0), (1, 0, 1), (7, 3, 4), (50, 0, 0), (50, 20, 30), (1000, 4, 4)])
+def test_budgets(budget, sinks, recent):
+    evict_case([1, 2, 49, 50, 51, 400], 2, 64, 16, "f16", budget, sinks, recent, seed=budget)
+
+
+def test_again_after_an_eviction():
+    evict_case([120, 101, 140, 100], 2, 64, 16, "bf16", 100, 4, 30, seen=[500, 101, 900, 777], old=[100, 0, 100, 100], seed=4)
+
+
+def test_in_place_metadata():
+    evict_case([120, 101, 140, 30], 2, 64, 16, "bf16", 100, 4, 30, seen=[500, 101, 900, 30], old=[100, 0, 100, 0], alias=True, seed=5)
+
+
+def test_named_rows_and_padded_strides():
+    evict_case([120, 101, 140], 2, 64, 32, "bf16", 90, 4, 30, rows=[4, 0, 2], pad=11, seed=6)
+
+
+def test_empty_sequences():
+    evict_case([0, 100, 0], 2, 64, 16, "bf16", 50, 4, 30, seed=7)
+
+
+@pytest.mark.parametrize("kind", ["equal", "zeros", "special"])
+def test_ties_and_special_weights(kind):
+    lens = [300, 1500]
+    w = torch.full((3, 2, 1500), 0.25)
+    if kind == "zeros":
+        w = torch.where(torch.rand(w.shape, generator=torch.Generator().manual_seed(1)) < 0.5, 0.0, -0.0)
+    elif kind == "special":
+        g = torch.Generator().manual_seed(2)
+        pick = torch.randint(0, 8, w.shape, generator=g)
+        values = torch.tensor([float("nan"), float("inf"), -float("inf"), 0.0, -0.0, 1e-45, -3.0, 3.4e38])
+        w = values[pick]
+    evict_case(lens, 2, 64, 16, "f16", 128, 4, 20, weights=w, seed=8)
+
+
+@pytest.mark.parametrize("n,budget", [(1024, 1023), (1025, 1024), (4096, 2048), (5000, 4999), (9000, 31), (20011, 10007)])
+def test_lengths(n, budget):
+    evict_case([n], 1, 64, 16, "bf16", budget, 4, 16, seed=n)
+
+
+def test_a_bound_above_every_length():
+    evict_case([120, 101], 2, 64, 16, "bf16", 90, 4, 30, most=5000, seed=9)
+
+
+def test_bad_metadata_is_reported_and_skipped():
+    c = Cache([100, 100, 100, 100], 2, 64, 16, "bf16", 11)
+    k, v, tables, desc = c.device(pa)
+    before_k = bits(k)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    w = torch.rand((4, 2, 100), device="cuda")
+    p = torch.zeros((4, 2, 100), dtype=torch.int32, device="cuda")
+    ws = torch.empty(pa.pa_evict_workspace_bytes(4, 2, 100, 50), dtype=torch.uint8, device="cuda")
+    for lens, rows in (([101, 0, 0, 0], None), ([-1, 0, 0, 0], None), ([100, 0, 0, 0], [4, 0, 1, 2]), ([100, 0, 0, 0], [-1, 0, 1, 2])):
+        nl = i32([9] * 4)
+        pa.pa_evict(k, v, desc, tables, i32(lens), 100, i32([200] * 4), i32([0] * 4), 50, 0, 0, w, p, w, p, nl,
+                    None if rows is None else i32(rows), ws)
+        assert pa.pa_get_device_error() == 4
+        assert torch.equal(bits(k), before_k) and nl.tolist() == lens
+    tables[0, :3] = c.num_blocks           # destinations out of range: reported, those rows stay
+    pa.pa_evict(k, v, desc, tables, i32([100, 0, 0, 0]), 100, i32([100] * 4), i32([0] * 4), 50, 0, 0, w, p, w, p, i32([0] * 4), None, ws)
+    assert pa.pa_get_device_error() == 4
