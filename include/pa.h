@@ -496,7 +496,7 @@ PA_API pa_status pa_decode_weights(const void *q, pa_dtype q_dtype, int32_t num_
  *   k_cache, v_cache  device pools described by *cache; no block that holds a
  *                slot < n may be shared with another sequence (pa_bm_unshare)
  *   block_tables device int32 [num_seqs][max_blocks_per_seq]
- *   seq_lens     device int32 [num_seqs], each <= max_seq_len
+ *   seq_lens     device int32 [num_seqs], each <= max_seq_len (at most 2^30)
  *   num_tokens, ordered_from  device int32 [num_seqs]; L <= num_tokens,
  *                0 <= ordered_from <= L (0 before the first eviction)
  *   budget       >= 1 and >= num_sinks + num_recent, both >= 0
@@ -504,7 +504,7 @@ PA_API pa_status pa_decode_weights(const void *q, pa_dtype q_dtype, int32_t num_
  *                [num_weight_rows][num_kv_heads][weights_stride]; the new
  *                arrays may be the old ones or must not overlap them
  *   weight_rows  as for pa_decode_weights
- *   new_seq_lens device int32 [num_seqs]; may be seq_lens itself
+ *   new_seq_lens device int32 [num_seqs]; must not overlap seq_lens
  *   workspace    device, >= pa_evict_workspace_bytes(...) bytes, 256-byte
  *                aligned; its contents on entry are ignored
  * A sequence whose metadata is out of range sets PA_ERR_DEVICE_CHECK and is

@@ -507,19 +507,18 @@ pa_status bounded_layout(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_h
   return PA_OK;
 }
 
-// Workspace of pa_evict: the rows' new lengths, then each head's list of moves
-// (a count padded to 16 bytes; destinations, sources, sources' positions).
+// Workspace of pa_evict: each head's list of moves (destinations, then sources).
 struct EvictLayout {
-  size_t lists_off, total;
+  size_t total;
   int64_t list_cap, list_stride;
 };
+constexpr int32_t kMaxEvictLen = 1 << 30;   // slots are counted in int32, with room for a rounding up
 bool evict_layout(int32_t num_seqs, int32_t num_kv_heads, int32_t max_seq_len, int32_t budget, EvictLayout *l) {
-  if (num_seqs < 0 || num_kv_heads <= 0 || max_seq_len < 0 || budget < 1) return false;
+  if (num_seqs < 0 || num_kv_heads <= 0 || max_seq_len < 0 || max_seq_len > kMaxEvictLen || budget < 1) return false;
   const int64_t moves = std::min<int64_t>(budget, std::max<int64_t>(0, (int64_t)max_seq_len - budget));
   l->list_cap = (moves + 3) / 4 * 4;
-  l->list_stride = 4 + 3 * l->list_cap;
-  l->lists_off = round256((size_t)num_seqs * 4);
-  l->total = l->lists_off + round256((size_t)num_seqs * num_kv_heads * l->list_stride * 4);
+  l->list_stride = 2 * l->list_cap;
+  l->total = std::max<size_t>(256, round256((size_t)num_seqs * num_kv_heads * l->list_stride * 4));
   return true;
 }
 
@@ -649,6 +648,9 @@ pa_status pa_evict(void *k_cache, void *v_cache, const pa_kv_cache *cache, int32
                         (const void *)ordered_from, (const void *)weights, (const void *)positions,
                         (const void *)new_weights, (const void *)new_positions, (const void *)new_seq_lens})
     if (!q || !aligned(q, 4)) return PA_ERR_INVALID_ARG;
+  // the sequences' heads read seq_lens while one of them writes the new length
+  const uintptr_t a = reinterpret_cast<uintptr_t>(seq_lens), b = reinterpret_cast<uintptr_t>(new_seq_lens);
+  if ((a < b ? b - a : a - b) < (uintptr_t)num_seqs * 4) return PA_ERR_INVALID_ARG;
   if (!aligned(weight_rows, 4) || weights_stride < max_seq_len || num_weight_rows < (weight_rows ? 1 : num_seqs))
     return PA_ERR_INVALID_ARG;
   if ((st = check_pools(k_cache, v_cache)) != PA_OK) return st;
@@ -678,8 +680,7 @@ pa_status pa_evict(void *k_cache, void *v_cache, const pa_kv_cache *cache, int32
   p.num_weight_rows = num_weight_rows;
   p.weight_rows = weight_rows;
   p.new_seq_lens = new_seq_lens;
-  p.lens = static_cast<int32_t *>(workspace);
-  p.lists = reinterpret_cast<int32_t *>(static_cast<char *>(workspace) + l.lists_off);
+  p.lists = static_cast<int32_t *>(workspace);
   p.list_stride = l.list_stride;
   p.list_cap = l.list_cap;
   p.err = device_error_word();

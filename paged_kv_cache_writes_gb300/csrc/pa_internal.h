@@ -211,9 +211,7 @@ struct EvictParams {
   int32_t num_weight_rows;
   const int32_t *weight_rows;  // null: row i
   int32_t *new_seq_lens;
-  // workspace: the rows' new lengths, and per (row, head) the number of moves, then their
-  // destinations, sources and the sources' positions (list_cap each)
-  int32_t *lens;
+  // workspace: per (row, head) the moves' destinations, then their sources (list_cap each)
   int32_t *lists;
   int64_t list_stride, list_cap;
   int32_t *err;

@@ -106,10 +106,12 @@ def test_prefill_chunk_window_refusals(pa, kw, desc_kw, want):
     (dict(seen=FAKE + 2), {}, 1), (dict(old=None), {}, 1), (dict(w=None), {}, 1), (dict(p=FAKE + 1), {}, 1),
     (dict(nw=None), {}, 1), (dict(np=None), {}, 1), (dict(nl=None), {}, 1), (dict(stride=99), {}, 1), (dict(rows=3), {}, 1),
     (dict(k=None), {}, 1), (dict(ws=None), {}, 1), (dict(ws=FAKE + 8), {}, 1), (dict(wsb=16), {}, 1),
+    (dict(nl=FAKE + 0x100000), {}, 1), (dict(nl=FAKE + 0x100000 + 12), {}, 1), (dict(nl=FAKE + 0x100000 - 12), {}, 1),   # on seq_lens
+    (dict(msl=2 ** 30 + 1, stride=2 ** 31, mb=2 ** 30), {}, 1),
     ({}, dict(block_size=64), 2), ({}, dict(kv_dtype=3), 2),
 ])
 def test_evict_refusals(pa, kw, desc_kw, want):
-    a = dict(k=FAKE, v=FAKE, n=4, bt=FAKE, mb=8, sl=FAKE, msl=100, seen=FAKE, old=FAKE, budget=50, sinks=4, recent=8, w=FAKE,
+    a = dict(k=FAKE, v=FAKE, n=4, bt=FAKE, mb=8, sl=FAKE + 0x100000, msl=100, seen=FAKE, old=FAKE, budget=50, sinks=4, recent=8, w=FAKE,
              p=FAKE, nw=FAKE, np=FAKE, stride=100, rows=4, wr=None, nl=FAKE, ws=FAKE, wsb=1 << 30)
     a.update(kw)
     d = desc(pa, **desc_kw)

@@ -32,7 +32,8 @@ def evict_case(lens, hkv, d, bs, kv, budget, sinks, recent, seed=0, seen=None, o
     k, v, tables, desc = c.device(pa)
     i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
     dw, dp, dl = w.cuda(), p.cuda(), i32(lens)
-    nw, np_, nl = (dw, dp, dl) if alias else (torch.full_like(dw, 7.0), torch.full_like(dp, 7), i32([-5] * n))
+    nw, np_ = (dw, dp) if alias else (torch.full_like(dw, 7.0), torch.full_like(dp, 7))
+    nl = i32([-5] * n)
     ws = torch.full((pa.pa_evict_workspace_bytes(n, hkv, most, budget),), 0xFF, dtype=torch.uint8, device="cuda")
     pa.pa_evict(k, v, desc, tables, dl, most, i32(seen), i32(old), budget, sinks, recent, dw, dp, nw, np_, nl,
                 None if rows is None else i32(rows), ws)
@@ -98,6 +99,12 @@ def test_ties_and_special_weights(kind):
 @pytest.mark.parametrize("n,budget", [(1024, 1023), (1025, 1024), (4096, 2048), (5000, 4999), (9000, 31), (20011, 10007)])
 def test_lengths(n, budget):
     evict_case([n], 1, 64, 16, "bf16", budget, 4, 16, seed=n)
+
+
+@pytest.mark.parametrize("most", [600, 20000, 400000, 1 << 20])
+def test_cluster_sizes(most):
+    # the bound on the lengths decides how many CTAs share a head and whether the keys fit in shared memory
+    evict_case([600, 333, 100], 2, 64, 16, "bf16", 150, 4, 30, most=most, seed=most, weights=torch.randint(0, 40, (4, 2, most)) / 8)
 
 
 def test_a_bound_above_every_length():
