@@ -139,32 +139,31 @@ def lib() -> ctypes.CDLL:
     return _lib
 
 
+_DTYPE_CODES = {torch.float16: PA_F16, torch.bfloat16: PA_BF16, torch.uint8: PA_FP8_E4M3,
+                torch.float8_e4m3fn: PA_FP8_E4M3, torch.float32: PA_F32}
+
+
 def _dtype_code(t: torch.dtype) -> int:
-    if t == torch.float16:
-        return PA_F16
-    if t == torch.bfloat16:
-        return PA_BF16
-    if t in (torch.uint8, torch.float8_e4m3fn):
-        return PA_FP8_E4M3
-    if t == torch.float32:
-        return PA_F32
-    raise TypeError(f"unsupported dtype {t}")
+    code = _DTYPE_CODES.get(t)
+    if code is None:
+        raise TypeError(f"unsupported dtype {t}")
+    return code
 
 
 def _stream(stream) -> int:
     if stream is None:
-        stream = torch.cuda.current_stream()
+        # the current stream's handle; making a torch.cuda.Stream of it first takes 2.8 us of a call
+        torch.cuda.is_initialized() or torch.cuda.init()
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def _dev(t: torch.Tensor | None, name: str) -> int | None:
     if t is None:
         return None
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    if t.is_cuda and t.is_contiguous():
+        return t.data_ptr()
+    raise ValueError(f"{name} must be a CUDA tensor" if not t.is_cuda else f"{name} must be contiguous")
 
 
 def _ok(status: int, where: str) -> None:
@@ -298,10 +297,40 @@ def pa_mixed_step(q: torch.Tensor, block_tables: torch.Tensor, seq_lens: torch.T
                             _dtype_code(out.dtype), _stream(stream)), "pa_mixed_step")
 
 
-def _i32(t: torch.Tensor | None, name: str) -> int | None:
-    if t is not None and t.dtype != torch.int32:
-        raise TypeError(f"{name} must be int32")
-    return _dev(t, name)
+class _Args:
+    """Checks of a call's tensors: on the current device, contiguous, of the type asked for."""
+    __slots__ = ("device",)
+
+    def __init__(self):
+        torch.cuda.is_initialized() or torch.cuda.init()
+        self.device = torch._C._cuda_getDevice()
+
+    def __call__(self, t: torch.Tensor, name: str, dtype: torch.dtype | None = None) -> int:
+        if t.get_device() == self.device and t.is_contiguous() and (dtype is None or t.dtype == dtype):
+            return t.data_ptr()
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if t.get_device() != self.device:
+            raise ValueError(f"{name} must be on the current device, cuda:{self.device}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        raise TypeError(f"{name} must be {dtype}")
+
+    def maybe(self, t: torch.Tensor | None, name: str, dtype: torch.dtype | None = None) -> int | None:
+        return None if t is None else self(t, name, dtype)
+
+    def of_sequences(self, t: torch.Tensor | None, name: str, n: int) -> int | None:
+        if t is None:
+            return None
+        if t.dim() != 1 or t.shape[0] != n:
+            raise ValueError(f"{name} must have one entry per sequence")
+        return self(t, name, torch.int32)
+
+    def stream(self, stream) -> int:
+        return torch._C._cuda_getCurrentRawStream(self.device) if stream is None else _stream(stream)
+
+
+_I32, _F32 = torch.int32, torch.float32
 
 
 def pa_decode_window_workspace_bytes(num_seqs: int, num_q_heads: int, num_kv_heads: int, head_dim: int,
@@ -317,14 +346,15 @@ def pa_decode_window(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tens
                      partition_size: int = 0, stream=None) -> None:
     """pa_decode over the first ``num_sinks`` and the last ``window`` tokens of each sequence.
     ``workspace``: uint8 tensor of >= pa_decode_window_workspace_bytes(...) bytes."""
+    a = _Args()
     B, hq, _ = q.shape
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _ok(lib().pa_decode_window(_dev(q, "q"), _dtype_code(q.dtype), B, hq, _dev(k_cache, "k_cache"),
-                               _dev(v_cache, "v_cache"), ctypes.byref(cache), _i32(block_tables, "block_tables"),
-                               block_tables.shape[1], _i32(seq_lens, "seq_lens"), int(max_seq_len), int(window),
-                               int(num_sinks), float(scale), int(partition_size), _dev(workspace, "workspace"),
-                               ws_bytes, _dev(out, "out"), _dtype_code(out.dtype), _stream(stream)),
-        "pa_decode_window")
+    status = lib().pa_decode_window(
+        a(q, "q"), _dtype_code(q.dtype), B, hq, a(k_cache, "k_cache"), a(v_cache, "v_cache"), ctypes.byref(cache),
+        a(block_tables, "block_tables", _I32), block_tables.shape[1], a.of_sequences(seq_lens, "seq_lens", B), max_seq_len,
+        window, num_sinks, scale, partition_size, a.maybe(workspace, "workspace"),
+        0 if workspace is None else workspace.nbytes, a(out, "out"), _dtype_code(out.dtype), a.stream(stream))
+    if status:
+        raise PaError(status, "pa_decode_window")
 
 
 def pa_prefill_chunk_window(q_chunk: torch.Tensor, cu_q_lens: torch.Tensor, q_start: torch.Tensor, max_q_len: int,
@@ -332,26 +362,29 @@ def pa_prefill_chunk_window(q_chunk: torch.Tensor, cu_q_lens: torch.Tensor, q_st
                             block_tables: torch.Tensor, seq_lens: torch.Tensor, max_seq_len: int, window: int,
                             num_sinks: int, scale: float, out: torch.Tensor, stream=None) -> None:
     """pa_prefill_chunk in which the row at position t sees p <= t with p < num_sinks or p > t - window."""
-    _ok(lib().pa_prefill_chunk_window(_dev(q_chunk, "q_chunk"), _dtype_code(q_chunk.dtype),
-                                      _i32(cu_q_lens, "cu_q_lens"), _i32(q_start, "q_start"), q_start.shape[0],
-                                      int(max_q_len), q_chunk.shape[1], _dev(k_cache, "k_cache"),
-                                      _dev(v_cache, "v_cache"), ctypes.byref(cache),
-                                      _i32(block_tables, "block_tables"), block_tables.shape[1],
-                                      _i32(seq_lens, "seq_lens"), int(max_seq_len), int(window), int(num_sinks),
-                                      float(scale), _dev(out, "out"), _dtype_code(out.dtype), _stream(stream)),
-        "pa_prefill_chunk_window")
-
-
-def _weights_shape(t: torch.Tensor, name: str, dtype: torch.dtype, hkv: int) -> int:
-    if t.dtype != dtype or t.dim() != 3 or t.shape[1] != hkv:
-        raise ValueError(f"{name} must be {dtype} [rows, num_kv_heads, stride]")
-    return _dev(t, name)
+    a = _Args()
+    n = q_start.shape[0]
+    status = lib().pa_prefill_chunk_window(
+        a(q_chunk, "q_chunk"), _dtype_code(q_chunk.dtype), a.of_sequences(cu_q_lens, "cu_q_lens", n + 1),
+        a.of_sequences(q_start, "q_start", n), n, max_q_len, q_chunk.shape[1], a(k_cache, "k_cache"),
+        a(v_cache, "v_cache"), ctypes.byref(cache), a(block_tables, "block_tables", _I32), block_tables.shape[1],
+        a.of_sequences(seq_lens, "seq_lens", n), max_seq_len, window, num_sinks, scale, a(out, "out"),
+        _dtype_code(out.dtype), a.stream(stream))
+    if status:
+        raise PaError(status, "pa_prefill_chunk_window")
 
 
 def pa_decode_weights_workspace_bytes(num_seqs: int, num_q_heads: int, num_kv_heads: int, head_dim: int,
                                       max_seq_len: int, partition_size: int = 0) -> int:
     return int(lib().pa_decode_weights_workspace_bytes(num_seqs, num_q_heads, num_kv_heads, head_dim, max_seq_len,
                                                        partition_size))
+
+
+def _weights_rows(weights: torch.Tensor, hkv: int):
+    """(rows, stride) of a weights array [rows, num_kv_heads, stride]."""
+    if weights.dim() != 3 or weights.shape[1] != hkv:
+        raise ValueError("weights must be [rows, num_kv_heads, stride]")
+    return weights.shape[0], weights.shape[2]
 
 
 def pa_decode_weights(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, cache: PaKvCache,
@@ -363,19 +396,18 @@ def pa_decode_weights(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Ten
     ``weights`` (float32 [rows, Hkv, stride >= max_seq_len]).  Sequence i uses row weight_rows[i] (int32 [B]; None: i);
     tokens from fresh_from[i] on (int32 [B]; None: the last) have no running weight yet; older ones are multiplied by
     ``decay`` first.  ``workspace``: uint8 tensor of >= pa_decode_weights_workspace_bytes(...) bytes."""
+    a = _Args()
     B, hq, _ = q.shape
-    for t, name in ((weight_rows, "weight_rows"), (fresh_from, "fresh_from")):
-        if t is not None and tuple(t.shape) != (B,):
-            raise ValueError(f"{name} must have one entry per sequence")
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _ok(lib().pa_decode_weights(_dev(q, "q"), _dtype_code(q.dtype), B, hq, _dev(k_cache, "k_cache"),
-                                _dev(v_cache, "v_cache"), ctypes.byref(cache), _i32(block_tables, "block_tables"),
-                                block_tables.shape[1], _i32(seq_lens, "seq_lens"), int(max_seq_len), float(scale),
-                                int(partition_size), _dev(workspace, "workspace"), ws_bytes, _dev(out, "out"),
-                                _dtype_code(out.dtype),
-                                _weights_shape(weights, "weights", torch.float32, k_cache.shape[1]),
-                                weights.shape[2], weights.shape[0], _i32(weight_rows, "weight_rows"),
-                                _i32(fresh_from, "fresh_from"), float(decay), _stream(stream)), "pa_decode_weights")
+    rows, stride = _weights_rows(weights, cache.num_kv_heads)
+    status = lib().pa_decode_weights(
+        a(q, "q"), _dtype_code(q.dtype), B, hq, a(k_cache, "k_cache"), a(v_cache, "v_cache"), ctypes.byref(cache),
+        a(block_tables, "block_tables", _I32), block_tables.shape[1], a.of_sequences(seq_lens, "seq_lens", B), max_seq_len,
+        scale, partition_size, a.maybe(workspace, "workspace"), 0 if workspace is None else workspace.nbytes,
+        a(out, "out"), _dtype_code(out.dtype), a(weights, "weights", _F32), stride, rows,
+        a.of_sequences(weight_rows, "weight_rows", B), a.of_sequences(fresh_from, "fresh_from", B), decay,
+        a.stream(stream))
+    if status:
+        raise PaError(status, "pa_decode_weights")
 
 
 def pa_evict_workspace_bytes(num_seqs: int, num_kv_heads: int, max_seq_len: int, budget: int) -> int:
@@ -392,25 +424,22 @@ def pa_evict(k_cache: torch.Tensor, v_cache: torch.Tensor, cache: PaKvCache, blo
     ordered_from, new_seq_lens: int32 [B]; weights (float32) and positions (int32) [rows, Hkv, stride >= max_seq_len],
     the new ones of the same shape (they may be the same tensors).  ``workspace``: uint8 tensor of >=
     pa_evict_workspace_bytes(...) bytes."""
-    hkv, B = k_cache.shape[1], seq_lens.shape[0]
-    for t, name in ((num_tokens, "num_tokens"), (ordered_from, "ordered_from"), (new_seq_lens, "new_seq_lens"),
-                    (weight_rows, "weight_rows")):
-        if t is not None and tuple(t.shape) != (B,):
-            raise ValueError(f"{name} must have one entry per sequence")
-    for t in (positions, new_weights, new_positions):
-        if t.shape != weights.shape:
-            raise ValueError("weights, positions, new_weights and new_positions must have one shape")
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _ok(lib().pa_evict(_dev(k_cache, "k_cache"), _dev(v_cache, "v_cache"), ctypes.byref(cache), B,
-                       _i32(block_tables, "block_tables"), block_tables.shape[1], _i32(seq_lens, "seq_lens"),
-                       int(max_seq_len), _i32(num_tokens, "num_tokens"), _i32(ordered_from, "ordered_from"),
-                       int(budget), int(num_sinks), int(num_recent),
-                       _weights_shape(weights, "weights", torch.float32, hkv),
-                       _weights_shape(positions, "positions", torch.int32, hkv),
-                       _weights_shape(new_weights, "new_weights", torch.float32, hkv),
-                       _weights_shape(new_positions, "new_positions", torch.int32, hkv), weights.shape[2],
-                       weights.shape[0], _i32(weight_rows, "weight_rows"), _i32(new_seq_lens, "new_seq_lens"),
-                       _dev(workspace, "workspace"), ws_bytes, _stream(stream)), "pa_evict")
+    a = _Args()
+    B = seq_lens.shape[0]
+    rows, stride = _weights_rows(weights, cache.num_kv_heads)
+    shape = weights.shape
+    if positions.shape != shape or new_weights.shape != shape or new_positions.shape != shape:
+        raise ValueError("weights, positions, new_weights and new_positions must have one shape")
+    status = lib().pa_evict(
+        a(k_cache, "k_cache"), a(v_cache, "v_cache"), ctypes.byref(cache), B, a(block_tables, "block_tables", _I32),
+        block_tables.shape[1], a.of_sequences(seq_lens, "seq_lens", B), max_seq_len,
+        a.of_sequences(num_tokens, "num_tokens", B), a.of_sequences(ordered_from, "ordered_from", B), budget, num_sinks,
+        num_recent, a(weights, "weights", _F32), a(positions, "positions", _I32), a(new_weights, "new_weights", _F32),
+        a(new_positions, "new_positions", _I32), stride, rows, a.of_sequences(weight_rows, "weight_rows", B),
+        a.of_sequences(new_seq_lens, "new_seq_lens", B), a.maybe(workspace, "workspace"),
+        0 if workspace is None else workspace.nbytes, a.stream(stream))
+    if status:
+        raise PaError(status, "pa_evict")
 
 
 def pa_get_device_error(stream=None) -> int:

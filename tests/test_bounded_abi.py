@@ -136,17 +136,30 @@ def test_workspace_sizes(pa):
     assert pa.pa_evict_workspace_bytes(4, 8, 100, 200) > 0
 
 
-def test_binding_checks(pa):
+def test_binding_checks(pa, monkeypatch):
+    """The binding refuses tensors that are not on the current device, of another shape or type, before the call."""
+    monkeypatch.setattr(torch.cuda, "is_initialized", lambda: True)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
     k = torch.zeros((4, 2, 16, 64), dtype=torch.bfloat16)
     d = pa.kv_cache_desc(k)
     q = torch.zeros((1, 4, 64), dtype=torch.bfloat16)
     t, n = torch.zeros((1, 4), dtype=torch.int32), torch.zeros(1, dtype=torch.int32)
     w, p = torch.zeros((1, 2, 64)), torch.zeros((1, 2, 64), dtype=torch.int32)
-    with pytest.raises(ValueError):       # not on the GPU
+    with pytest.raises(ValueError, match="CUDA tensor"):
         pa.pa_decode_window(q, k, k, d, t, n, 10, 5, 1, 0.1, q)
-    with pytest.raises(ValueError):
-        pa.pa_decode_weights(q, k, k, d, t, n, 10, 0.1, q, w, fresh_from=torch.zeros(2, dtype=torch.int32))
-    with pytest.raises(ValueError):       # one shape for all four
+    with pytest.raises(ValueError, match="CUDA tensor"):
+        pa.pa_prefill_chunk_window(q, n, n, 1, k, k, d, t, n, 10, 5, 1, 0.1, q)
+    with pytest.raises(ValueError, match="num_kv_heads"):
+        pa.pa_decode_weights(q, k, k, d, t, n, 10, 0.1, q, torch.zeros((1, 3, 64)))
+    with pytest.raises(ValueError, match="one shape"):
         pa.pa_evict(k, k, d, t, n, 10, n, n, 5, 1, 1, w, p, w, p[:, :, :5], n)
-    with pytest.raises(ValueError):
-        pa.pa_evict(k, k, d, t, n, 10, n, torch.zeros(3, dtype=torch.int32), 5, 1, 1, w, p, w, p, n)
+    # the checks of one tensor, the device's number aside
+    a = pa._Args()
+    a.device = -1                       # what a CPU tensor says of itself
+    assert a(q, "q") == q.data_ptr() and a.maybe(None, "q") is None and a.of_sequences(None, "n", 1) is None
+    with pytest.raises(ValueError, match="one entry per sequence"):
+        a.of_sequences(n, "n", 2)
+    for bad, why in ((lambda: a(q.transpose(1, 2), "q"), ValueError), (lambda: a.of_sequences(w[0, 0, :1], "n", 1), (TypeError, ValueError)),
+                     (lambda: a(w, "w", torch.int32), (TypeError, ValueError))):
+        with pytest.raises(why):
+            bad()
