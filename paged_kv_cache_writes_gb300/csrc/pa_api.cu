@@ -474,6 +474,7 @@ namespace {
 // then (pa_decode_weights) the scores and the rows' softmax maxima and sums.
 struct BoundedLayout {
   int ps, parts, shares, share_heads, rows;   // rows: score columns per token
+  bool direct;
   WorkspaceLayout w;
   size_t scores_off, row_ml_off, total;
   int64_t score_stride;
@@ -489,15 +490,21 @@ pa_status bounded_layout(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_h
   if ((head_dim != 64 && head_dim != 128) || (block_size != 16 && block_size != 32) || num_seqs > kMaxDecodeRows)
     return PA_ERR_UNSUPPORTED;
   const int64_t longest = window_max_packed(max_seq_len, window, num_sinks, block_size);
-  b->ps = effective_partition(partition_size);
-  const int64_t parts = std::max<int64_t>(1, (longest + b->ps - 1) / b->ps);
   const int gqa = num_q_heads / num_kv_heads;
   b->shares = decode_ext_shares(head_dim, gqa);
   b->share_heads = (gqa + b->shares - 1) / b->shares;
   b->rows = decode_ext_rows(b->share_heads);
   const int64_t units = (int64_t)num_kv_heads * b->shares;
+  b->ps = effective_partition(partition_size);
+  if (partition_size == 0) {
+    // few rows: shorter partitions, down to 64 tokens, while every unit still has an SM of its own
+    const int64_t most = kPlanSms / std::max<int64_t>(1, num_seqs * units);   // partitions per row
+    if (most > 1) b->ps = (int)std::min<int64_t>(b->ps, std::max<int64_t>(64, ((longest + most - 1) / most + 31) / 32 * 32));
+  }
+  const int64_t parts = std::max<int64_t>(1, (longest + b->ps - 1) / b->ps);
   if (parts > kMaxPartitions || units >= (1 << 19) || (double)num_seqs * parts * units >= 2147483647.0)
     return PA_ERR_UNSUPPORTED;
+  b->direct = num_seqs <= kDirectRows && num_seqs * parts * units <= kDirectUnits;
   b->parts = (int)parts;
   b->w = decode_workspace_layout(num_seqs, num_q_heads, head_dim, parts);
   b->score_stride = parts * b->ps;
@@ -562,6 +569,7 @@ pa_status bounded_decode(const void *q, pa_dtype q_dtype, int32_t num_seqs, int3
   tp.num_sinks = num_sinks;
   tp.shares = b.shares;
   tp.share_heads = b.share_heads;
+  tp.direct = b.direct;
   if (wt) {
     tp.scores = reinterpret_cast<float *>(ws + b.scores_off);
     tp.score_stride = b.score_stride;
@@ -576,28 +584,42 @@ pa_status bounded_decode(const void *q, pa_dtype q_dtype, int32_t num_seqs, int3
   else if (q_dtype == PA_BF16) e = launch_decode_ext_fp8_bf16q(tp, c.head_dim, maps, s);
   else e = launch_decode_ext_fp8_f16q(tp, c.head_dim, maps, s);
   if (e != cudaSuccess) return PA_ERR_CUDA;
-  if (!wt) return PA_OK;
-  WeightsParams wp{};
-  wp.scores = tp.scores;
-  wp.score_stride = b.score_stride;
-  wp.score_rows = b.rows;
-  wp.row_ml = tp.row_ml;
-  wp.seq_lens = seq_lens;
-  wp.num_seqs = num_seqs;
-  wp.num_q_heads = num_q_heads;
-  wp.num_kv_heads = c.num_kv_heads;
-  wp.shares = b.shares;
-  wp.share_heads = b.share_heads;
-  // rows past the block table's capacity or max_seq_len were reported and cut by the decode
-  wp.max_len = (int32_t)std::min<int64_t>(max_seq_len, (int64_t)max_blocks_per_seq * c.block_size);
-  wp.weights = wt->weights;
-  wp.weights_stride = wt->stride;
-  wp.num_weight_rows = wt->num_rows;
-  wp.weight_rows = wt->rows;
-  wp.fresh_from = wt->fresh_from;
-  wp.decay = wt->decay;
-  wp.err = tp.d.err;
-  return launch_decode_weights(wp, s) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+  FinishParams f{};
+  f.seq_lens = seq_lens;
+  f.max_blocks_per_seq = max_blocks_per_seq;
+  f.bs_log2 = 4 + tp.d.tile_shift;
+  f.window = window;
+  f.num_sinks = num_sinks;
+  f.partition_size = b.ps;
+  f.max_partitions = b.parts;
+  f.num_seqs = num_seqs;
+  f.num_q_heads = num_q_heads;
+  f.num_kv_heads = c.num_kv_heads;
+  f.shares = b.shares;
+  f.share_heads = b.share_heads;
+  f.direct = b.direct;
+  f.ws_acc = tp.d.ws_acc;
+  f.ws_ml = tp.d.ws_ml;
+  f.out_mult = tp.d.out_mult;
+  f.v_hs = tp.d.v_hs;
+  f.out = out;
+  f.out_dtype = out_dtype;
+  f.score_rows = b.rows;
+  f.err = tp.d.err;
+  if (wt) {
+    f.scores = tp.scores;
+    f.score_stride = b.score_stride;
+    f.row_ml = tp.row_ml;
+    // rows past max_seq_len or the block table's capacity were cut by the decode
+    f.max_len = (int32_t)std::min<int64_t>(max_seq_len, (int64_t)max_blocks_per_seq * c.block_size);
+    f.weights = wt->weights;
+    f.weights_stride = wt->stride;
+    f.num_weight_rows = wt->num_rows;
+    f.weight_rows = wt->rows;
+    f.fresh_from = wt->fresh_from;
+    f.decay = wt->decay;
+  }
+  return launch_decode_finish(f, c.head_dim, s) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 }  // namespace
 }  // namespace pa

@@ -90,6 +90,7 @@
 // completed.
 #pragma once
 
+#include <algorithm>
 #include <type_traits>
 
 #include "pa_decode.cuh"
@@ -138,30 +139,39 @@ struct DecodeTcParams {
   float *scores;             // null, or [row][kvh * shares + share][score_stride tokens][G] scores in log2 units
   int64_t score_stride;
   float2 *row_ml;            // with scores: [row][query head] (maximum, 1 / sum) of the softmax, log2 units
+                             // (direct: of the rows with one partition)
+  // 1: no plan kernel and no merging in this launch (at most kDirectRows rows).  CTA b takes the
+  // turns b, b + grid, ... of the units (row, partition, kvh) that hold tokens, and pa_finish.cu's
+  // kernel merges the split rows afterwards.
+  int32_t direct;
 };
 
-// A row's length and, with kExt, its packed length under the window, both
-// checked as checked_len does (the table must hold the row, the partitions
-// its packed tokens).
+// The packed length under the window of a row of L tokens, and where its cut
+// is; the table must hold the row, the partitions its packed tokens.
+__device__ __forceinline__ int packed_len_of(const DecodeTcParams &tp, int L, bool report, WindowSpan *span) {
+  const DecodeParams &p = tp.d;
+  const int64_t cap = (int64_t)p.max_blocks_per_seq * p.block_size, packed = (int64_t)p.max_partitions * p.partition_size;
+  bool bad = L < 0 || L > cap;
+  L = L < 0 ? 0 : L > cap ? (int)cap : L;
+  const WindowSpan w = window_span(window_low(L, tp.window), tp.num_sinks, 4 + p.tile_shift);
+  L -= w.skip_blocks << (4 + p.tile_shift);
+  if (L > packed) {
+    bad = true;
+    L = (int)packed;
+  }
+  if (bad && report) record_error(p.err, PA_ERR_DEVICE_CHECK);
+  if (span) *span = w;
+  return L;
+}
+
+// A row's length or, with kExt, its packed length, checked.
 template <bool kExt>
 __device__ __forceinline__ int checked_packed_len(const DecodeTcParams &tp, int row, bool report, WindowSpan *span) {
   const DecodeParams &p = tp.d;
   if constexpr (!kExt) {
     return checked_len(p, row, report);
   } else {
-    int L = __ldg(p.seq_lens + row);
-    const int64_t cap = (int64_t)p.max_blocks_per_seq * p.block_size, packed = (int64_t)p.max_partitions * p.partition_size;
-    bool bad = L < 0 || L > cap;
-    L = L < 0 ? 0 : L > cap ? (int)cap : L;
-    const WindowSpan w = window_span(window_low(L, tp.window), tp.num_sinks, 4 + p.tile_shift);
-    L -= w.skip_blocks << (4 + p.tile_shift);
-    if (L > packed) {
-      bad = true;
-      L = (int)packed;
-    }
-    if (bad && report) record_error(p.err, PA_ERR_DEVICE_CHECK);
-    if (span) *span = w;
-    return L;
+    return packed_len_of(tp, __ldg(p.seq_lens + row), report, span);
   }
 }
 
@@ -601,7 +611,9 @@ __device__ __forceinline__ void decode_tc_body(const DecodeTcParams &tp, const C
   // Claim records of the merge list and merge them until every one is claimed:
   // the warps that have finished their own role help drain the list at the end
   // of the kernel.  Waiting for a claimed record is bounded (PA_ERR_TIMEOUT).
+  const bool direct = kExt && tp.direct != 0;
   auto drain = [&]() {
+    if (direct) return;
     const int total_jobs = __ldcg(&p.hdr->pad[2]);
     for (;;) {
       if (*abort_flag) return;
@@ -842,7 +854,7 @@ __device__ __forceinline__ void decode_tc_body(const DecodeTcParams &tp, const C
             p.ws_ml[(head0 + tid) * p.max_partitions + prev.part] = make_float2(mv, lv);
           }
         }
-        if (prev.nparts > 1 && !hand_over(prev.row, prev.kvh, prev.nparts)) {
+        if (prev.nparts > 1 && !direct && !hand_over(prev.row, prev.kvh, prev.nparts)) {
           ok = false;
           break;
         }
@@ -868,6 +880,9 @@ __device__ __forceinline__ void decode_tc_body(const DecodeTcParams &tp, const C
     const int bs = p.block_size;
     const int ldr = warp == kLoadWarp ? 0 : warp - kLoadWarp1 + 1;   // this warp's share: positions = ldr mod NL
     bool ok = true;
+    // K and V are read once: first to be evicted, so that they leave the L2 to what is read again (the scores, the
+    // partial results); 64 sequences of 64/8 heads and 4100 visible tokens: 178 -> 167 us
+    const uint64_t policy = kExt ? l2_evict_first() : 0;
     auto issue_tile = [&](const UnitHdr &un, int info_idx, int j, bool is_k, int slot) {
       uint64_t *full_bar = &slot_full[slot];
       const int nvalid = min(kKeys, un.ntok - j * kKeys);
@@ -886,15 +901,17 @@ __device__ __forceinline__ void decode_tc_body(const DecodeTcParams &tp, const C
         __syncwarp();
         if (issue) {
           uint8_t *dst = smem + GE::kOffRing + slot * GE::kSlotBytes + lane * atoms * kAtomB;
-          if constexpr (kD == 128) tma_load_4d(dst, map, full_bar, 0, 0, 0, (bi * hkv + kvh) * atoms);
+          if constexpr (kExt && kD == 128) tma_load_4d(dst, map, full_bar, 0, 0, 0, (bi * hkv + kvh) * atoms, policy);
+          else if constexpr (kExt) tma_load_3d(dst, map, full_bar, 0, 0, (bi * hkv + kvh) * atoms, policy);
+          else if constexpr (kD == 128) tma_load_4d(dst, map, full_bar, 0, 0, 0, (bi * hkv + kvh) * atoms);
           else tma_load_3d(dst, map, full_bar, 0, 0, (bi * hkv + kvh) * atoms);
         }
       } else {
         if (lane == 0) mbar_arrive_expect_tx(full_bar, boxes * bs * kD);
         __syncwarp();
-        if (issue)
-          tma_load_2d(smem + GE::kOffRing + slot * GE::kSlotBytes + lane * bs * kD, map, full_bar, 0,
-                      (bi * hkv + kvh) * bs);
+        uint8_t *dst = smem + GE::kOffRing + slot * GE::kSlotBytes + lane * bs * kD;
+        if (kExt && issue) tma_load_2d(dst, map, full_bar, 0, (bi * hkv + kvh) * bs, policy);
+        else if (issue) tma_load_2d(dst, map, full_bar, 0, (bi * hkv + kvh) * bs);
       }
     };
     // Q^T rows of a unit (16-bit caches): the G query heads of the KV head, 2 * kD bytes each
@@ -958,7 +975,37 @@ __device__ __forceinline__ void decode_tc_body(const DecodeTcParams &tp, const C
     // id of run (lane & 7) of tile (lane >> 3) is read by lane `lane`.  fp8:
     // the unit's query scale from the largest |q| of its G query rows.
     const int bs = p.block_size;
-    const int total_units = __ldcg(&p.hdr->num_items) * hkv_units;
+    const int total_units = direct ? 0 : __ldcg(&p.hdr->num_items) * hkv_units;
+    // direct: rows 32 c + lane, their partitions and the running sum of them; the units of all
+    // rows in order are dealt to the CTAs in turn
+    int cursor = 0, live_units = 0;
+    int row_len[kDirectRows / 32], row_parts[kDirectRows / 32], row_end[kDirectRows / 32];
+    if (direct) {
+      int before = 0;
+#pragma unroll
+      for (int c = 0; c < kDirectRows / 32; ++c) {
+        const int r = 32 * c + lane;
+        row_len[c] = r < p.num_seqs ? __ldg(p.seq_lens + r) : 0;
+        row_parts[c] = 0;
+        row_end[c] = 0;
+      }
+#pragma unroll
+      for (int c = 0; c < kDirectRows / 32; ++c) {
+        if (32 * c < p.num_seqs) {
+          if (32 * c + lane < p.num_seqs)
+            row_parts[c] = max(1, (packed_len_of(tp, row_len[c], blockIdx.x == 0, nullptr) + p.partition_size - 1) / p.partition_size);
+          int x = row_parts[c];
+#pragma unroll
+          for (int off = 1; off < 32; off <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, x, off);
+            if (lane >= off) x += y;
+          }
+          row_end[c] = before + x;
+          before = __shfl_sync(0xffffffffu, row_end[c], 31);
+        }
+      }
+      live_units = before * hkv_units;
+    }
     const int64_t cap = min((int64_t)p.max_blocks_per_seq * bs, (int64_t)p.max_partitions * p.partition_size);
     bool ok = true;
     // Store a new token's 16 bytes x (lanes 0-15: K, 16-31: V; elements 8c ..
@@ -994,22 +1041,62 @@ __device__ __forceinline__ void decode_tc_body(const DecodeTcParams &tp, const C
       for (int k = 0; k < kClaim && ok; ++k)
         if (u + k >= kInfo) ok = wait_all(&info_free[(u + k) % kInfo], (((u + k) / kInfo) - 1) & 1);
       if (!ok) break;
-      int id0 = 0;
-      if (lane == 0) id0 = atomicAdd(&p.hdr->next_unit, kClaim);
-      id0 = __shfl_sync(0xffffffffu, id0, 0);
-      // lane k < kClaim resolves unit id0 + k
-      const int id = id0 + (lane & (kClaim - 1));
-      const bool valid = lane < kClaim && id < total_units;
-      int item = 0, L = 0;
-      if (valid) item = __ldg(p.items + id / hkv_units);
-      const int row = item >> 12, part = item & 4095;
+      // lane k < kClaim resolves the claim's unit k
+      int unit_lane = 0, row = 0, part = 0, L = 0;   // unit_lane: its kvh
+      bool valid = false;
       WindowSpan span{0, 0, 0, 0};
-      if (valid) {
-        if constexpr (kExt) {
-          L = checked_packed_len<true>(tp, row, false, &span);   // packed tokens from here on
-        } else {
-          L = __ldg(p.seq_lens + row);
-          if (L < 0 || L > cap) L = L < 0 ? 0 : (int)cap;   // reported by the plan kernel
+      if (direct) {
+        // lane k: the CTA's turn cursor + k, the turn-th unit that holds tokens (or is an empty row's only one)
+        const int turn = blockIdx.x + (cursor + lane) * gridDim.x;
+        valid = lane < kClaim && turn < live_units;
+        cursor += kClaim;
+        const int item = turn / hkv_units;
+        unit_lane = turn - item * hkv_units;
+#pragma unroll
+        for (int k = 0; k < kClaim; ++k) {
+          const int it = __shfl_sync(0xffffffffu, item, k);
+          int r = 0, first = 0;   // the row whose partitions hold item `it`, and its first item
+#pragma unroll
+          for (int c = kDirectRows / 32 - 1; c >= 0; --c) {
+            if (32 * c >= p.num_seqs) continue;
+            const uint32_t m = __ballot_sync(0xffffffffu, row_end[c] > it);
+            if (m) {
+              r = 32 * c + __ffs(m) - 1;
+              first = __shfl_sync(0xffffffffu, row_end[c] - row_parts[c], __ffs(m) - 1);
+            }
+          }
+          if (lane == k) {
+            row = r;
+            part = it - first;
+          }
+        }
+        int raw = 0;
+#pragma unroll
+        for (int c = 0; c < kDirectRows / 32; ++c) {
+          if (32 * c < p.num_seqs) {
+            const int x = __shfl_sync(0xffffffffu, row_len[c], row & 31);
+            if (c == row >> 5) raw = x;
+          }
+        }
+        if (valid) L = packed_len_of(tp, raw, false, &span);
+      } else {
+        int id0 = 0;
+        if (lane == 0) id0 = atomicAdd(&p.hdr->next_unit, kClaim);
+        id0 = __shfl_sync(0xffffffffu, id0, 0);
+        const int id = id0 + (lane & (kClaim - 1));
+        valid = lane < kClaim && id < total_units;
+        int item = 0;
+        if (valid) item = __ldg(p.items + id / hkv_units);
+        row = item >> 12;
+        part = item & 4095;
+        unit_lane = id % hkv_units;
+        if (valid) {
+          if constexpr (kExt) {
+            L = checked_packed_len<true>(tp, row, false, &span);   // packed tokens from here on
+          } else {
+            L = __ldg(p.seq_lens + row);
+            if (L < 0 || L > cap) L = L < 0 ? 0 : (int)cap;   // reported by the plan kernel
+          }
         }
       }
       const int tok_begin = part * p.partition_size;
@@ -1022,7 +1109,7 @@ __device__ __forceinline__ void decode_tc_body(const DecodeTcParams &tp, const C
         const int rk = __shfl_sync(0xffffffffu, row, k);
         const int tb = __shfl_sync(0xffffffffu, tok_begin, k);
         const int nk = __shfl_sync(0xffffffffu, ntok, k);
-        const int unit_kvh = __shfl_sync(0xffffffffu, id % hkv_units, k);
+        const int unit_kvh = __shfl_sync(0xffffffffu, unit_lane, k);
         const Heads kh = heads_of(unit_kvh);
         const int kvk = kh.kvh, gr = kh.n;
         int head_blocks = 0, skip_blocks = 0;
@@ -1155,9 +1242,9 @@ __device__ __forceinline__ void decode_tc_body(const DecodeTcParams &tp, const C
     // With kSepMerge another warp merges from the start, and this one only
     // counts: a merge (one or more dependent L2 round trips, several µs under
     // the decode's memory load) no longer delays the appends behind it.
-    const int total_jobs = __ldcg(&p.hdr->pad[2]);
+    const int total_jobs = direct ? 0 : __ldcg(&p.hdr->pad[2]);
     int nrep = 0, t = -1;
-    bool local_done = false, list_done = kSepMerge;
+    bool local_done = false, list_done = kSepMerge || direct;
     uint64_t t_idle = global_timer_ns();
     for (;;) {
       if (*abort_flag) break;
@@ -1502,11 +1589,12 @@ template <typename KV, typename QT, int G, int D, bool kPadRows, bool kExt = fal
 cudaError_t launch_decode_tc_one(const DecodeTcParams &p, const PoolMaps &m, cudaStream_t s) {
   constexpr int smem =
       dtc::TcGeo<G, dtc::split_p<KV, QT, kExt>(), std::is_same<KV, uint8_t>::value, dtc::QTerms<KV, QT>::value, D>::kSmemBytes;
-  cudaError_t e = launch_decode_tc_plan<kExt>(p, s);
-  if (e != cudaSuccess) return e;
+  cudaError_t e = cudaSuccess;
+  if (!(kExt && p.direct) && (e = launch_decode_tc_plan<kExt>(p, s)) != cudaSuccess) return e;
   if ((e = ensure_smem_limit<decode_tc_kernel<KV, QT, G, D, kPadRows, kExt>>(smem)) != cudaSuccess) return e;
   int sms = 0;
   if ((e = current_sm_count(&sms)) != cudaSuccess) return e;
+  if (kExt && p.direct) sms = (int)std::min<int64_t>(sms, (int64_t)p.d.num_seqs * p.d.max_partitions * p.d.num_kv_heads * p.shares);
   // programmatic dependent launch: the decode grid's set-up overlaps the plan kernel
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)sms);

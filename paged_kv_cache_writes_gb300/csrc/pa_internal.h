@@ -171,15 +171,40 @@ cudaError_t launch_decode_ext_f16(const DecodeTcParams &p, int head_dim, const P
 cudaError_t launch_decode_ext_fp8_bf16q(const DecodeTcParams &p, int head_dim, const PoolMaps &m, cudaStream_t s);
 cudaError_t launch_decode_ext_fp8_f16q(const DecodeTcParams &p, int head_dim, const PoolMaps &m, cudaStream_t s);
 
-// The second half of pa_decode_weights: each cached token's softmax weight from
-// the scores the decode left in the workspace (pa_weights.cu).
-struct WeightsParams {
+// Bounded-cache decodes of at most kDirectRows rows and kDirectUnits units (row,
+// partition, KV head share), counted at the longest row, run without the plan kernel and its
+// scheduling (pa_decode_tc.cuh, `direct`).  Measured, plan against direct: one
+// row of 4100 visible tokens 22.4 / 11.5 us (152 units), 16 rows of 1000 24.3 /
+// 20.6 us (384), 64 rows of 400 33.5 / 27.0 us (512), one row of 9700 among 19
+// short ones 25.1 / 20.9 us (2888); but 256 rows of log-normal lengths 275 / 307
+// us (32768): with many units of uneven lengths the plan's order and the claims
+// balance the CTAs better than fixed turns.  kPlanSms: the GPU's 152 SMs, which
+// the host's choice of the partition size aims at (a workspace size is asked for
+// without a GPU).
+constexpr int kPlanSms = 152;
+constexpr int kDirectUnits = 8 * kPlanSms;
+constexpr int kDirectRows = 128;   // a lane of the scheduler warp keeps four rows
+
+// The second launch of the bounded-cache decodes (pa_finish.cu): the merge of
+// split rows (direct) and each cached token's softmax weight (weights).
+struct FinishParams {
+  const int32_t *seq_lens;
+  int32_t max_blocks_per_seq, bs_log2, window, num_sinks, partition_size, max_partitions;
+  int32_t num_seqs, num_q_heads, num_kv_heads, shares, share_heads;
+  int32_t direct;
+  uint32_t merge_blocks;      // CTAs that merge, in front (set by the launcher)
+  int32_t chunks;             // CTAs per (row, KV head) that do weights (set by the launcher)
+  const float *ws_acc;        // [num_seqs][num_q_heads][max_partitions][head_dim]
+  const float2 *ws_ml;        // [num_seqs][num_q_heads][max_partitions]
+  float out_mult;
+  const float *v_hs;
+  void *out;
+  int32_t out_dtype;
+  // weights (null: none)
   const float *scores;        // [num_seqs][num_kv_heads * shares][score_stride][score_rows], log2 units
   int64_t score_stride;
   int32_t score_rows;         // 4, 8 or 16: a token's scores, of which the share's heads count
   const float2 *row_ml;       // [num_seqs][num_q_heads] (maximum, 1 / sum)
-  const int32_t *seq_lens;
-  int32_t num_seqs, num_q_heads, num_kv_heads, shares, share_heads;
   int32_t max_len;            // longest row served
   float *weights;             // [num_weight_rows][num_kv_heads][weights_stride]
   int64_t weights_stride;
@@ -189,7 +214,7 @@ struct WeightsParams {
   float decay;
   int32_t *err;
 };
-cudaError_t launch_decode_weights(const WeightsParams &p, cudaStream_t s);
+cudaError_t launch_decode_finish(const FinishParams &p, int head_dim, cudaStream_t s);
 
 // Eviction by accumulated attention weight (pa_evict.cu).
 struct EvictParams {

@@ -78,7 +78,8 @@ def test_decode_empty_sequences():
     assert (o[0] == 0).all() and (o[2] == 0).all() and (o[1] != 0).any()
 
 
-def test_decode_without_a_cut_equals_pa_decode():
+def test_decode_without_a_cut_agrees_with_pa_decode():
+    # the two cut rows into partitions of their own: each is within its bound of the exact result
     c = Cache(LENS, 2, 128, 16, "bf16", 7)
     q = torch.randn((len(LENS), 16, 128), generator=torch.Generator().manual_seed(8)).bfloat16().cuda()
     o = decode(c, q.cpu(), 2 ** 31 - 1, 0, 0.09)
@@ -87,7 +88,9 @@ def test_decode_without_a_cut_equals_pa_decode():
     ws = torch.empty(pa.pa_decode_workspace_bytes(len(LENS), 16, 2, 128, max(LENS)), dtype=torch.uint8, device="cuda")
     ref = torch.empty((len(LENS), 16, 128), dtype=torch.float32, device="cuda")
     pa.pa_decode(q, k, v, desc, tables, lens, max(LENS), 0.09, ref, ws)
-    assert torch.equal(o, ref)
+    for i, n in enumerate(LENS):
+        _, bound, _, _ = attend(q[i:i + 1].cpu(), c.rows("k", i, n), c.rows("v", i, n), torch.ones((1, n), dtype=bool), 0.09, "bf16", "f32")
+        assert ((o[i:i + 1].double() - ref[i:i + 1].double()).abs().cpu() <= 2 * bound).all()
 
 
 def test_decode_bad_metadata_is_reported():
