@@ -887,10 +887,8 @@ pa_status pa_prefill_chunk_window(const void *q_chunk, pa_dtype q_dtype, const i
   t.share_heads = (gqa + t.shares - 1) / t.shares;
   t.err = device_error_word();
   if (!t.err) return PA_ERR_CUDA;
-  PoolMaps maps{};   // fp8: the loaders copy whole cache blocks with bulk-tensor boxes
-  if (c.kv_dtype == PA_FP8_E4M3 &&
-      (!encode_pool_map_fp8_blocks(&maps.k, k_cache, c) || !encode_pool_map_fp8_blocks(&maps.v, v_cache, c)))
-    return PA_ERR_CUDA;
+  PoolMaps maps{};   // the loaders copy whole cache blocks with bulk-tensor boxes
+  if (!encode_decode_tc_maps(&maps, k_cache, v_cache, c)) return PA_ERR_CUDA;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e;
   if (c.kv_dtype == PA_BF16) e = launch_prefill_window_bf16(t, maps, c.head_dim, num_chunks, s);

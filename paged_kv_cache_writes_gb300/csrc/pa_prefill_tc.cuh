@@ -126,6 +126,7 @@ constexpr int kStages = 2;      // K/V tiles in flight
 // Warp roles and tensor-memory size for a CTA of QT Q tiles (1 or 2).
 template <int QT>
 struct Roles {
+  static constexpr int kStages = tc::kStages;
   static constexpr int kSoftmax = QT * 128;           // softmax threads (warps 0 .. 4*QT-1)
   static constexpr int kLoadWarp0 = kSoftmax / 32;    // the next 4 warps load
   static constexpr int kMmaWarp = kLoadWarp0 + 4;     // the last warp issues the MMAs
@@ -134,6 +135,28 @@ struct Roles {
   // scores are computed while the softmax works), one with two Q tiles
   static constexpr int kBufs = QT == 1 ? 2 : 1;
   static constexpr int kTmemCols = 512;               // QT*kBufs*128 score/P columns, then QT*128 of O
+};
+// The windowed kernel (kWin): one Q tile per CTA.  kPair: two CTAs share an SM,
+// each with one K/V stage, one score/P buffer and half of tensor memory, so that
+// one CTA's set-up, softmax and epilogue run under the other's MMAs; else one CTA
+// has the SM, with two stages, two score buffers and two softmax threads per row.
+// One warp loads a 16-bit cache's tiles (bulk-tensor boxes), four an fp8 one's.
+template <bool kPair, bool kFp8>
+struct WinRoles {
+  static constexpr int kSoftmax = kPair ? 128 : 256;
+  static constexpr int kLoadWarp0 = kSoftmax / 32;
+  static constexpr int kMmaWarp = kLoadWarp0 + (kFp8 ? 4 : 1);
+  static constexpr int kThreads = (4 + kLoadWarp0 + (kFp8 ? 1 : 0)) * 32;
+  // Role of a warp: the MMAs are issued by warp 0 and the loads by the next ones, the softmax by warps 4 on
+  __device__ static int role(int w) {
+    if (w >= 4 && w < 4 + kLoadWarp0) return w - 4;
+    if (w == 0) return kMmaWarp;
+    const int l = w < 4 ? w - 1 : 3;   // loader
+    return l < (kFp8 ? 4 : 1) ? kLoadWarp0 + l : kMmaWarp + 1;
+  }
+  static constexpr int kBufs = kPair ? 1 : 2;
+  static constexpr int kStages = kPair ? 1 : 2;
+  static constexpr int kTmemCols = kPair ? 256 : 512;
 };
 constexpr float kRescaleLog2 = 8.f;
 
@@ -147,18 +170,21 @@ constexpr int kNumBars = 4 * kStages + 3 * 4 + 2 + 4 * kMaxCodeStages;
 // Shared-memory map, bytes from a 1024-aligned base (128-byte swizzle atoms).
 // fp8 caches with one Q tile: kCStages tiles of codes (K then V) after the
 // 16-bit K/V stages.
-template <int QT, bool kFp8 = false, int D = 128>
+// kWin: the softmax warps' exchange (floats [2][128] and [128]) behind the barriers.
+template <int QT, bool kFp8 = false, int D = 128, int kStages = tc::kStages, bool kWin = false>
 struct Layout {
   static constexpr int kQBytes = kM * D * 2, kTileBytes = kN * D * 2;
-  static constexpr int kCStages = (kFp8 && QT == 1 && D == 128) ? kMaxCodeStages : 0;
+  static constexpr int kCStages = (kFp8 && QT == 1 && D == 128 && kStages == tc::kStages) ? kMaxCodeStages : 0;
   static constexpr int kOffQ = 0;
   static constexpr int kOffK = kOffQ + QT * kQBytes;
   static constexpr int kOffV = kOffK + kStages * kTileBytes;
   static constexpr int kOffCode = kOffV + kStages * kTileBytes;
   static constexpr int kOffBar = kOffCode + kCStages * 2 * kCodeTile;
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;
-  static constexpr int kSmemBytes = kOffMisc + 64 + 1024;  // + alignment slack
+  static constexpr int kOffExch = kOffMisc + 64;
+  static constexpr int kSmemBytes = kOffExch + (kWin ? 3 * 128 * 4 : 0) + 1024;  // + alignment slack
   static_assert(kSmemBytes <= 227 * 1024, "shared memory");
+  static_assert(kOffExch % 4 == 0, "aligned floats");
   static_assert(kOffCode % 1024 == 0 && kCodeTile % 1024 == 0, "1024-byte swizzle atoms for the code boxes");
 };
 
@@ -168,24 +194,32 @@ struct Layout {
 // for the prefill CTAs of the mixed kernel (pa_mixed_tc.cuh).
 // G: query heads per KV head; with kWin 0, the group then being p.share_heads
 // heads, rows past the last whole token of the CTA's tiles left idle.
-template <typename KV, typename QT, int G, int kQTiles, int D = 128, bool kWin = false>
+template <typename KV, typename QT, int G, int kQTiles, int D = 128, bool kWin = false, bool kPair = false,
+          bool kLo = true>
 __device__ __forceinline__ void prefill_tc_body(const PrefillTcParams &p, int bx, int by, const CUtensorMap *tmap_k,
                                                 const CUtensorMap *tmap_v) {
   using namespace tc;
   static_assert(D == 64 || D == 128, "head_dim 64 or 128");
   static_assert(kWin == (G == 0) && (kWin || D == 128), "any group and head_dim 64 with kWin only");
   constexpr int kD = D;                       // head_dim (hides tc::kD)
-  using L = Layout<kQTiles, std::is_same<KV, uint8_t>::value, D>;
-  using R = Roles<kQTiles>;
+  static_assert(!kWin || kQTiles == 1, "the windowed kernel has one Q tile per CTA");
+  using R = std::conditional_t<kWin, WinRoles<kPair, std::is_same<KV, uint8_t>::value>, Roles<kQTiles>>;
+  constexpr int kStages = R::kStages;         // (hides tc::kStages)
+  using L = Layout<kQTiles, std::is_same<KV, uint8_t>::value, D, kStages, kWin>;
   constexpr int kQBytes = L::kQBytes, kTileBytes = L::kTileBytes;
   constexpr int kSoftmax = R::kSoftmax, kLoadWarp0 = R::kLoadWarp0, kMmaWarp = R::kMmaWarp;
   constexpr int kTmemCols = R::kTmemCols;
   constexpr int kBufs = R::kBufs;
   constexpr bool kFp8 = std::is_same<KV, uint8_t>::value;
   constexpr bool kBf16 = std::is_same<QT, __nv_bfloat16>::value;
-  constexpr bool kSplit = kBf16 && !kFp8;   // bf16 cache: P as hi + lo
+  constexpr bool kSplit = kBf16 && !kFp8 && kLo;   // bf16 cache: P as hi + lo
+  // K and V tiles come as bulk-tensor boxes of whole cache blocks, in atoms of 8 keys (all panels) of kAtom
+  // bytes; else the loaders write panels of 128 keys
+  constexpr bool kBoxes = kWin && !kFp8;
+  constexpr int kAtom = 8 * 2 * kD;
+  constexpr int kGroup = kWin ? 1 : G;
   const int gr = kWin ? p.share_heads : G;
-  const int BR = kQTiles * kM / (kWin ? gr : G);      // token rows per CTA
+  const int BR = kQTiles * kM / (kWin ? gr : kGroup);      // token rows per CTA
   constexpr bool kF16Ops = kFp8 || !kBf16;   // f16 MMA operands (f16 cache, or any fp8 cache)
   constexpr uint32_t kAB = kF16Ops ? 0u : 1u;
   const float kNegInf = -__int_as_float(0x7f800000);
@@ -207,7 +241,9 @@ __device__ __forceinline__ void prefill_tc_body(const PrefillTcParams &p, int bx
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::kOffMisc);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::kOffMisc + 8);
 
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31;
+  int warp = tid >> 5;
+  if constexpr (kWin) warp = R::role(warp);
   const int c = bx / p.row_blocks, rb = bx % p.row_blocks;
   const int g = kWin ? by / p.shares : by;   // KV head
   const int h_first = kWin ? (by - g * p.shares) * gr : 0;             // the share's first head of the group
@@ -245,8 +281,8 @@ __device__ __forceinline__ void prefill_tc_body(const PrefillTcParams &p, int bx
 
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(&k_full[s], kLoaders);
-      mbar_init(&v_full[s], kLoaders);
+      mbar_init(&k_full[s], kBoxes ? 1 : kLoaders);   // boxes: one expect-tx arrival
+      mbar_init(&v_full[s], kBoxes ? 1 : kLoaders);
       mbar_init(&k_free[s], 1);
       mbar_init(&v_free[s], 1);
     }
@@ -274,16 +310,317 @@ __device__ __forceinline__ void prefill_tc_body(const PrefillTcParams &p, int bx
   auto sbuf = [&](int t, int b) { return tmem + (uint32_t)((t * kBufs + b) * kN); };
   auto obuf = [&](int t) { return tmem + (uint32_t)(kQTiles * kBufs * kN + t * kD); };
 
-  if (warp < kLoadWarp0) {
+  if (kWin && warp < kLoadWarp0) {
+    if constexpr (kWin) {
+      // ===================================================== softmax warps, windowed kernel
+      // Thread m of each of the kGroups groups owns packed row m.  With two groups (one CTA per SM, few CTAs)
+      // they share a row: 64 keys of every tile each, half of the row's elements of Q and O each; what they
+      // tell each other (maxima, sums) goes through shared memory between barriers of 64 threads, two warps.
+      constexpr int kGroups = R::kSoftmax / 128;
+      constexpr int kOwn = kN / kGroups;           // keys per thread and tile
+      const int grp = warp >> 2, m = tid & 127, quad = warp & 3;
+      const int rl = m / gr, hq = m % gr;
+      const bool row_ok = r0 + rl < nrows && rl < BR && h_first + hq < gqa;
+      const int64_t row_elem = row_ok ? ((int64_t)(cu0 + r0 + rl) * p.num_q_heads + g * gqa + h_first + hq) * kD : -1;
+      // the row sees keys < lim but for those in [num_sinks, row_low), packed positions
+      // (idle rows, with q = 0, see everything: they are not stored, and need no masking)
+      const int lim = row_ok ? min(seq_eff, max(0, qs + r0 + rl + 1) - skip) : 1 << 30;
+      const int row_low = row_ok ? window_low(max(0, qs + r0 + rl + 1), p.window) - skip : 0;
+      const uint32_t lane_base = (uint32_t)(quad * 32) << 16;
+      // scores are scaled by |s_mult| in the exponent; a negative scale flips q's sign instead.  A masked score of
+      // -inf has to stay -inf whatever the scale (a scale of 0 gives scores of about 0).
+      float cmul = fmaxf(fabsf(p.s_mult) * (p.k_hs ? __ldg(p.k_hs + g) : 1.f), 1e-30f);
+      const uint32_t qflip = p.s_mult < 0.f ? 0x80008000u : 0u;
+      float *exch = reinterpret_cast<float *>(smem + L::kOffExch);   // [2][128], then the rows' score factors [128]
+      auto pair_sync = [&]() { asm volatile("bar.sync %0, 64;" ::"r"(1 + quad) : "memory"); };
+      auto all_sync = [&]() { asm volatile("bar.sync 5, %0;" ::"n"(R::kSoftmax) : "memory"); };
+      {
+        // Stage Q: a warp brings its own 32 rows, kC lanes of 16 bytes per row (each group its part of the row;
+        // fp8 caches, whose rows are scaled by their largest element: group 0 the whole row)
+        constexpr bool kScaled = kFp8 && kBf16;
+        constexpr int kC = kD / 8 / (kScaled ? 1 : kGroups), kRI = 32 / kC;   // chunks per row, rows per instruction
+        if (!kScaled || grp == 0) {
+          uint4 v[kC];
+#pragma unroll
+          for (int i = 0; i < kC; ++i) {
+            const int64_t e = __shfl_sync(0xffffffffu, row_elem, i * kRI + lane / kC);
+            // (idle rows read row 0, and are zeroed: a branch around each load would wait for it)
+            v[i] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const QT *>(p.q) + max(e, (int64_t)0)) +
+                         (kScaled ? 0 : grp * kC) + lane % kC);
+          }
+#pragma unroll
+          for (int i = 0; i < kC; ++i)
+            if (__shfl_sync(0xffffffffu, (int)row_ok, i * kRI + lane / kC) == 0) v[i] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+          for (int i = 0; i < kC; ++i) {
+            const int mr = quad * 32 + i * kRI + lane / kC, ch = (kScaled ? 0 : grp * kC) + lane % kC;
+            uint32_t ws[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+            if constexpr (kScaled) {
+              // f16 operands: the row times 2^e (its largest element in [2^14, 2^15)), rounded to f16
+              float amax = 0.f;
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                amax = fmaxf(amax, fmaxf(__uint_as_float((ws[k] << 16) & 0x7fffffffu),
+                                         __uint_as_float(ws[k] & 0x7fff0000u)));   // NaN ignored
+#pragma unroll
+              for (int off = kC / 2; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
+              const int eb = max(1, (int)((__float_as_uint(amax) >> 23) & 0xff));
+              const int e = amax > 0.f ? max(-126, min(126, 141 - eb)) : 0;
+              const float sc = __uint_as_float((uint32_t)(e + 127) << 23);
+              if (lane % kC == 0) exch[256 + mr] = __uint_as_float((uint32_t)(127 - e) << 23);   // 2^-e
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const float2 f = unpack2(ws[k], __nv_bfloat16{});
+                const __half2 h = __floats2half2_rn(f.x * sc, f.y * sc);
+                ws[k] = *reinterpret_cast<const uint32_t *>(&h);
+              }
+            }
+            *reinterpret_cast<uint4 *>(smem + L::kOffQ + (ch >> 3) * (kM * 128) + mr * 128 + (((ch & 7) ^ (mr & 7)) << 4)) =
+                make_uint4(ws[0] ^ qflip, ws[1] ^ qflip, ws[2] ^ qflip, ws[3] ^ qflip);
+          }
+        }
+        fence_async_smem();
+        mbar_arrive(q_ready);
+        if constexpr (kScaled) {
+          all_sync();
+          cmul = fmaxf(cmul * exch[256 + m], 1e-30f);
+        }
+      }
+
+      float m_ref = kNegInf;                     // reference maximum, log2 units
+      float2 lacc[4] = {{0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}};   // partial row sums
+      const float2 ones = make_float2(1.f, 1.f);
+      bool ok = true;
+      auto wait_all = [&](uint64_t *bar, uint32_t parity) {
+        return __all_sync(0xffffffffu, mbar_try_wait(bar, parity) || wait_or_abort(bar, parity, p.err, abort_flag));
+      };
+      // The scores are read from tensor memory once into registers, but for fp8 caches with two CTAs per SM (whose four
+      // loader warps leave 96 registers per thread): those in chunks of 32, twice (maximum, then probabilities), each
+      // read while the one before is worked on.
+      constexpr bool kTwice = kGroups == 1;
+      constexpr int kChunks = kOwn / 32, kHeld = kTwice ? 2 : kChunks;   // chunks of 32 scores, and how many in registers
+      for (int j = 0; j < nkt; ++j) {
+        const int b = j % kBufs;
+        ok = wait_all(&s_full[b], (j / kBufs) & 1) && ok;
+        if (kGroups == 1 && !ok) break;   // two groups: the partner may be at a barrier; go through them without work to do
+        const uint32_t sb = sbuf(0, b) + lane_base + grp * kOwn;
+        tc_fence_after();
+        // of the tile's keys (this group's: from 0 on) the row sees those below nvis but for the glen from g0 on;
+        // most tiles are seen whole by every row of the warp
+        const int key0 = j * kN + grp * kOwn;
+        const int nvis = lim - key0, g0 = p.num_sinks - key0, g1 = row_low - key0;
+        const bool full_tile = __all_sync(0xffffffffu, nvis >= kOwn && (g0 >= g1 || g0 >= kOwn || g1 <= 0));
+        float mx[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) mx[i] = kNegInf;
+        float sv[kHeld][32];
+        auto take_max = [&](float (&v)[32]) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) mx[i & 7] = fmax3(mx[i & 7], v[2 * i], v[2 * i + 1]);
+        };
+        // bits [0, n) of a word
+        auto below = [](int n) { return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u; };
+        auto mask = [&](int ck, float (&v)[32]) {   // hidden scores of chunk ck to -inf
+          const uint32_t seen = below(nvis - 32 * ck) & ~(below(g1 - 32 * ck) & ~below(g0 - 32 * ck));
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (!(seen >> i & 1u)) v[i] = kNegInf;
+        };
+        if constexpr (!kTwice) {
+#pragma unroll
+          for (int ck = 0; ck < kChunks; ++ck) tmem_ld32_start(sb + 32 * ck, sv[ck]);
+#pragma unroll
+          for (int ck = 0; ck < kChunks; ++ck) {
+            tmem_ld32_finish(sv[ck]);   // (the first one waits for all)
+            if (!full_tile) mask(ck, sv[ck]);
+            take_max(sv[ck]);
+          }
+        } else {
+          if (!full_tile) {   // mask in place: the second pass then finds -inf
+#pragma unroll 1
+            for (int ck = 0; ck < kChunks; ++ck) {
+              tmem_ld32_start(sb + 32 * ck, sv[0]);
+              tmem_ld32_finish(sv[0]);
+              mask(ck, sv[0]);
+              take_max(sv[0]);
+              tmem_st32(sb + 32 * ck, sv[0]);
+            }
+          } else {
+            tmem_ld32_start(sb, sv[0]);
+#pragma unroll
+            for (int ck = 0; ck < kChunks; ++ck) {
+              tmem_ld32_finish(sv[ck & 1]);
+              if (ck + 1 < kChunks) tmem_ld32_start(sb + 32 * (ck + 1), sv[(ck + 1) & 1]);
+              take_max(sv[ck & 1]);
+            }
+          }
+          tmem_ld32_start(sb, sv[0]);   // for the second pass
+        }
+        float mr = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
+                         fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7])));
+        if constexpr (kGroups == 2) {
+          exch[grp * 128 + m] = mr;
+          pair_sync();
+          mr = fmaxf(mr, exch[(grp ^ 1) * 128 + m]);
+          pair_sync();
+        }
+        const float mt = mr == kNegInf ? kNegInf : mr * cmul;   // tile maximum, log2 units
+        const bool rescale = mt > m_ref + tc::kRescaleLog2;
+        if (__any_sync(0xffffffffu, rescale)) {
+          const float alpha = rescale ? fast_exp2(m_ref - mt) : 1.f;
+          if constexpr (kTwice) tmem_ld32_finish(sv[0]);
+          if (j > 0) {
+            // O holds the P.V of tiles 0 .. j-1: wait for the last of them, then rescale (this group's part) in place
+            ok = wait_all(&o_done[0], (j - 1) & 1) && ok;
+            if (kGroups == 1 && !ok) break;
+            tc_fence_after();
+#pragma unroll 1
+            for (int c0 = grp * (kD / kGroups); c0 < (grp + 1) * (kD / kGroups); c0 += 16) {
+              float o[16];
+              uint32_t ow[16];
+              tmem_ld16(obuf(0) + lane_base + c0, o);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) ow[i] = __float_as_uint(o[i] * alpha);
+              tmem_st16(obuf(0) + lane_base + c0, ow);
+            }
+            if constexpr (kGroups == 2) {   // the other group's half of P must not meet this group's O before it is rescaled
+              tmem_wait_st();
+              tc_fence_before();
+              pair_sync();
+              tc_fence_after();
+            }
+          }
+          if (rescale) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) lacc[i] = make_float2(lacc[i].x * alpha, lacc[i].y * alpha);
+            m_ref = mt;
+          }
+        }
+        // p = 2^(s * |s_mult| - m_ref), 16 keys at a time, written over those keys' own 16 score columns; the P.V MMAs
+        // of a half of the tile (64 keys) start when it is written
+        const float msub = m_ref == kNegInf ? 0.f : m_ref;
+        const float2 cc = make_float2(cmul, cmul), nm = make_float2(-msub, -msub);
+#pragma unroll
+        for (int ck = 0; ck < kChunks; ++ck) {
+          float (&v)[32] = sv[ck % kHeld];
+          if constexpr (kTwice) {
+            tmem_ld32_finish(v);
+            if (ck + 1 < kChunks) tmem_ld32_start(sb + 32 * (ck + 1), sv[(ck + 1) & 1]);
+          }
+#pragma unroll
+          for (int hh = 0; hh < 2; ++hh) {   // keys 32ck + 16hh .. +15
+            uint32_t w[8], wl[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const int i0 = 16 * hh + 2 * k;
+              const float2 a = ffma2(make_float2(v[i0], v[i0 + 1]), cc, nm);
+              const float2 pk = make_float2(fast_exp2(a.x), fast_exp2(a.y));
+              if constexpr (kBf16 && !kFp8 && !kLo) {   // rounded to bf16, the sum that of the rounded P
+                uint32_t hw;
+                asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(hw) : "f"(pk.y), "f"(pk.x));
+                w[k] = hw;
+                lacc[k & 3] = ffma2(make_float2(__uint_as_float(hw << 16), __uint_as_float(hw & 0xffff0000u)), ones, lacc[k & 3]);
+              } else if constexpr (kSplit) {   // hi + lo, as in the other kernel
+                uint32_t hw, lw2;
+                asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(hw) : "f"(pk.y), "f"(pk.x));
+                w[k] = hw;
+                const float2 lo = ffma2(make_float2(__uint_as_float(hw << 16), __uint_as_float(hw & 0xffff0000u)),
+                                        make_float2(-1.f, -1.f), pk);
+                asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(lw2) : "f"(lo.y), "f"(lo.x));
+                wl[k] = lw2;
+                lacc[k & 3] = ffma2(pk, ones, lacc[k & 3]);
+              } else {
+                w[k] = f16x2_rn_add(pk.x, pk.y, lacc[k & 3]);
+              }
+            }
+            tmem_st8(sb + 32 * ck + 16 * hh, w);
+            if constexpr (kSplit) tmem_st8(sb + 32 * ck + 16 * hh + 8, wl);
+          }
+          if (ck == kChunks - 1 || (kGroups == 1 && ck == 1)) {   // a half of the tile is written
+            tmem_wait_st();
+            tc_fence_before();
+            mbar_arrive(&p_full[2 * b + (kGroups == 2 ? grp : ck >> 1)]);
+          }
+        }
+      }
+      float l = ((lacc[0].x + lacc[0].y) + (lacc[1].x + lacc[1].y)) + ((lacc[2].x + lacc[2].y) + (lacc[3].x + lacc[3].y));
+      // O is complete once the last tile's P.V has finished; with two score buffers, the scores of that tile came when
+      // the P.V before the previous one was complete, so the previous one is waited for first
+      if (ok && kBufs == 2 && nkt > 1) ok = wait_all(&o_done[0], (nkt - 2) & 1);
+      if (ok && nkt > 0) ok = wait_all(&o_done[0], (nkt - 1) & 1);
+      all_sync();   // Q is staged and no longer read: its place (and K's behind it) takes the output on its way
+      if constexpr (kGroups == 2) {
+        exch[grp * 128 + m] = l;
+        pair_sync();
+        l += exch[(grp ^ 1) * 128 + m];
+      }
+      if (ok) {
+        tc_fence_after();
+        const float inv = l > 0.f ? p.out_mult * (p.v_hs ? __ldg(p.v_hs + g) : 1.f) / l : 0.f;
+        // Up to 128 bytes of each of the warp's 32 rows at a time: written by the rows' threads (16-byte chunk c of row
+        // r at chunk c ^ (r & 7)), then stored by 8 (or 4) lanes per row
+        uint8_t *stage = smem + L::kOffQ + warp * 4096;
+        auto emit = [&](auto f32) {
+          constexpr bool kF32 = decltype(f32)::value;
+          constexpr int kPart = kD / kGroups;                            // this thread's elements of its row
+          constexpr int kCols = 32;                                      // elements at a time
+          constexpr int kCh = kCols * (kF32 ? 4 : 2) / 16, kRI = 32 / kCh;   // chunks per row, rows per instruction
+          int64_t e[kCh];
+#pragma unroll
+          for (int i = 0; i < kCh; ++i) e[i] = __shfl_sync(0xffffffffu, row_elem, i * kRI + lane / kCh);
+          // (a loop, not unrolled: this code runs once per CTA, and fetching it costs more than running it)
+#pragma unroll 1
+          for (int c0 = grp * kPart; c0 < (grp + 1) * kPart; c0 += kCols) {
+            float o[kCols / 32][32];
+#pragma unroll
+            for (int k = 0; k < kCols / 32; ++k)
+              if (nkt > 0) tmem_ld32_start(obuf(0) + lane_base + c0 + 32 * k, o[k]);
+#pragma unroll
+            for (int k = 0; k < kCols / 32; ++k) {
+              if (nkt > 0) {
+                tmem_ld32_finish(o[k]);
+              } else {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) o[k][i] = 0.f;
+              }
+            }
+#pragma unroll
+            for (int i = 0; i < kCh; ++i) {
+              uint4 x;
+              if constexpr (kF32) {
+                x = make_uint4(__float_as_uint(o[0][4 * i] * inv), __float_as_uint(o[0][4 * i + 1] * inv),
+                               __float_as_uint(o[0][4 * i + 2] * inv), __float_as_uint(o[0][4 * i + 3] * inv));
+              } else {
+                const float *v = &o[i >> 2][8 * (i & 3)];
+                x = make_uint4(pack2(v[0] * inv, v[1] * inv, QT{}), pack2(v[2] * inv, v[3] * inv, QT{}),
+                               pack2(v[4] * inv, v[5] * inv, QT{}), pack2(v[6] * inv, v[7] * inv, QT{}));
+              }
+              *reinterpret_cast<uint4 *>(stage + lane * 128 + ((i ^ (lane & 7)) << 4)) = x;
+            }
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < kCh; ++i) {
+              const int r = i * kRI + lane / kCh, ch = lane % kCh;
+              const uint4 x = *reinterpret_cast<const uint4 *>(stage + r * 128 + ((ch ^ (r & 7)) << 4));
+              if (e[i] >= 0)
+                *reinterpret_cast<uint4 *>(static_cast<char *>(p.out) + (e[i] + c0) * (kF32 ? 4 : 2) + ch * 16) = x;
+            }
+            __syncwarp();
+          }
+        };
+        if (p.out_f32) emit(std::true_type{});
+        else emit(std::false_type{});
+      }
+    }
+  } else if (warp < kLoadWarp0) {
     // ===================================================== softmax warps (Q tile t = warp / 4)
     const int m = tid;                         // packed row
     const int t = m / kM;
-    const int rl = m / (kWin ? gr : G), hq = m % (kWin ? gr : G);
-    const bool row_ok = r0 + rl < nrows && (!kWin || (rl < BR && h_first + hq < gqa));
-    const int head = g * gqa + h_first + hq;
-    // keys this row attends to: positions < lim, with kWin but not those in [num_sinks, row_low)
-    const int lim = row_ok ? min(seq_eff, max(0, qs + r0 + rl + 1) - skip) : 0;
-    const int row_low = kWin ? window_low(max(0, qs + r0 + rl + 1), p.window) - skip : 0;
+    const int rl = m / kGroup, hq = m % kGroup;
+    const bool row_ok = r0 + rl < nrows;
+    const int head = g * kGroup + hq;
+    // keys this row attends to: positions < lim
+    const int lim = row_ok ? min(seq_eff, max(0, qs + r0 + rl + 1)) : 0;
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     // scores are scaled by |s_mult| in the exponent; a negative scale flips q's sign instead
     float cmul = fabsf(p.s_mult) * (p.k_hs ? __ldg(p.k_hs + g) : 1.f);
@@ -351,10 +688,7 @@ __device__ __forceinline__ void prefill_tc_body(const PrefillTcParams &p, int bx
       // keys at or past this row's limit are masked, but only tiles that reach
       // some row's limit (the causal diagonal, the sequence end) need the test
       const int nvis = lim - j * kN;
-      const int g0 = kWin ? p.num_sinks - j * kN : 0, glen = kWin ? max(0, row_low - j * kN - g0) : 0;
-      const bool full_tile =
-          __all_sync(0xffffffffu, nvis >= kN && (!kWin || glen == 0 || g0 >= kN || g0 + glen <= 0));
-      auto hidden = [&](int i) { return i >= nvis || (kWin && (uint32_t)(i - g0) < (uint32_t)glen); };
+      const bool full_tile = __all_sync(0xffffffffu, nvis >= kN);
       // pass 1: the tile maximum
       float mx[8];
 #pragma unroll
@@ -366,7 +700,7 @@ __device__ __forceinline__ void prefill_tc_body(const PrefillTcParams &p, int bx
         if (!full_tile) {
 #pragma unroll
           for (int i = 0; i < 32; ++i)
-            if (hidden(32 * ck + i)) sv[i] = kNegInf;
+            if (32 * ck + i >= nvis) sv[i] = kNegInf;
         }
 #pragma unroll
         for (int i = 0; i < 16; ++i) mx[i & 7] = fmax3(mx[i & 7], sv[2 * i], sv[2 * i + 1]);
@@ -415,8 +749,8 @@ __device__ __forceinline__ void prefill_tc_body(const PrefillTcParams &p, int bx
             const float2 a = ffma2(make_float2(sv[2 * k], sv[2 * k + 1]), cc, nm);
             float2 pk = make_float2(fast_exp2(a.x), fast_exp2(a.y));
             if (!full_tile) {
-              if (hidden(i0)) pk.x = 0.f;
-              if (hidden(i0 + 1)) pk.y = 0.f;
+              if (i0 >= nvis) pk.x = 0.f;
+              if (i0 + 1 >= nvis) pk.y = 0.f;
             }
             if constexpr (kSplit) {
               // bf16 cache: hi = p rounded to bf16, lo = p - hi (exact in fp32) rounded to
@@ -526,7 +860,48 @@ __device__ __forceinline__ void prefill_tc_body(const PrefillTcParams &p, int bx
       ok = __all_sync(0xffffffffu, wait_or_abort(bar, parity, p.err, abort_flag));
       return ok;
     };
-    if constexpr (!kFp8) {
+    if constexpr (kBoxes) {
+      // one box per cache block that holds a key < kv_end, straight into the tile
+      const int bs = p.block_size, atoms = bs >> 3, per_tile = kN / bs;
+      auto block = [&](int j) -> int32_t {   // lane i: the id of block i of tile j, -1: none, or out of range
+        const int key = j * kN + lane * bs;
+        if (lane >= per_tile || j >= nkt || key >= kv_end) return -1;
+        int lb = key / bs;
+        if (lb >= span.head_blocks) lb += span.skip_blocks;
+        const int32_t bi = __ldg(table + lb);
+        if (bi >= 0 && bi < p.num_blocks) return bi;
+        record_error(p.err, PA_ERR_DEVICE_CHECK);
+        return -1;
+      };
+      int32_t next = block(0);
+      int filled[2] = {0, 0};   // K and V tiles whose boxes are issued
+      for (int j = 0; j < nkt && ok; ++j) {
+        const int s = j % kStages;
+        const int32_t bi = next;
+        next = block(j + 1);
+        const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, bi >= 0));
+#pragma unroll
+        for (int which = 0; which < 2; ++which) {
+          if (j >= kStages && !wait_slot(which ? &v_free[s] : &k_free[s], ((j / kStages) - 1) & 1)) break;
+          uint64_t *full = which ? &v_full[s] : &k_full[s];
+          if (lane == 0) mbar_arrive_expect_tx(full, boxes * atoms * kAtom);
+          __syncwarp();
+          if (bi >= 0) {
+            uint8_t *dst = smem + (which ? L::kOffV : L::kOffK) + s * kTileBytes + lane * atoms * kAtom;
+            const CUtensorMap *map = which ? tmap_v : tmap_k;
+            const int32_t at = (int32_t)(((int64_t)bi * p.num_kv_heads + g) * atoms);
+            if constexpr (kD == 128) tma_load_4d(dst, map, full, 0, 0, 0, at);
+            else tma_load_3d(dst, map, full, 0, 0, at);
+          }
+          ++filled[which];
+        }
+      }
+      // given up: no box in flight at exit (bounded waits)
+      if (!ok)
+        for (int which = 0; which < 2; ++which)
+          for (int t = max(0, filled[which] - kStages); t < filled[which]; ++t)
+            mbar_wait(which ? &v_full[t % kStages] : &k_full[t % kStages], (t / kStages) & 1, p.err);
+    } else if constexpr (!kFp8) {
       // 16-bit rows: per instruction 2 rows x 16 chunks of 16 B (head_dim 64: 4 rows x 8 chunks)
       constexpr int kC = kD / 8, kRI = 32 / kC;   // chunks per row, rows per instruction
       const int q = lane % kC, pn = q >> 3, cq = q & 7;
@@ -681,6 +1056,105 @@ __device__ __forceinline__ void prefill_tc_body(const PrefillTcParams &p, int bx
       }
     }
     if constexpr (!kFp8) cp_async_wait_all();
+  } else if (kWin && warp == kMmaWarp) {
+    if constexpr (kWin) {
+      // ===================================================== MMA issue, windowed kernel
+      // Per key tile j: O += P(j) V_j, half a tile of P at a time, then S(j + kBufs) = Q K^T over the buffer P(j) was
+      // in, once that P.V is complete.  Keys past kv_end take part up to the end of their group of 16.
+      const bool leader = elect_one();
+      const uint32_t idesc_s = umma_idesc(kAB, kN, false);
+      const uint32_t idesc_o = umma_idesc(kAB, kD, true);
+      const uint32_t kv_k = smem_u32(smem + L::kOffK), kv_v = smem_u32(smem + L::kOffV);
+      const uint64_t qdesc = umma_desc(smem_u32(smem + L::kOffQ), 16);
+      const uint64_t kdesc0 = kBoxes ? umma_desc_sbo(kv_k, 16, kAtom) : umma_desc(kv_k, 16);
+      const uint64_t vdesc0 = kBoxes ? umma_desc_sbo(kv_v, 1024, kAtom) : umma_desc(kv_v, kTilePanel);
+      constexpr uint32_t kKPanel = kBoxes ? 1024 : kTilePanel, kVStep = kBoxes ? 2 * kAtom : 16 * 128;
+      auto wait_all = [&](uint64_t *bar, uint32_t parity) {
+        return __all_sync(0xffffffffu, mbar_try_wait(bar, parity) || wait_or_abort(bar, parity, p.err, abort_flag));
+      };
+      bool ok = nkt == 0 || wait_all(q_ready, 0);
+      bool issued = false;
+      auto issue_s = [&](int j) {   // S(j), its K tile waited for
+        const uint64_t kd = kdesc0 + (((j % kStages) * kTileBytes) >> 4);
+        if (leader) {
+#pragma unroll 1
+          for (int k = 0; k < kD / 16; ++k)
+            umma(sbuf(0, j % kBufs), qdesc + (((k >> 2) * (kM * 128) + (k & 3) * 32) >> 4),
+                 kd + (((k >> 2) * kKPanel + (k & 3) * 32) >> 4), idesc_s, k > 0 ? 1u : 0u);
+          umma_commit(&s_full[j % kBufs]);
+          umma_commit(&k_free[j % kStages]);
+        }
+        __syncwarp();
+        issued = true;
+      };
+      for (int j = 0; j < kBufs && j < nkt && ok; ++j) {
+        ok = wait_all(&k_full[j % kStages], (j / kStages) & 1);
+        if (!ok) break;
+        tc_fence_after();
+        issue_s(j);
+      }
+      for (int j = 0; j < nkt && ok; ++j) {
+        const int s = j % kStages, b = j % kBufs, jn = j + kBufs;
+        ok = wait_all(&v_full[s], (j / kStages) & 1);
+        if (!ok) break;
+        const int nvalid = min(kN, kv_end - j * kN), groups = (nvalid + 15) >> 4;
+        if constexpr (kBoxes) {
+          // rows of V that no row of the CTA sees, in the groups that take part: they may hold anything, and P is 0
+          // there, so they are zeroed (fp8 caches: the loaders wrote zeros)
+          uint8_t *vt = smem + L::kOffV + s * kTileBytes;
+          auto zero_rows = [&](int r0, int r1) {
+            constexpr int kRowC = kD / 8;
+            for (int e = lane; e < (r1 - r0) * kRowC; e += 32) {
+              const int r = r0 + e / kRowC, c = e % kRowC;
+              *reinterpret_cast<uint4 *>(vt + (r >> 3) * kAtom + (c >> 3) * 1024 + (r & 7) * 128 + (c & 7) * 16) =
+                  make_uint4(0, 0, 0, 0);
+            }
+          };
+          const int z0 = max(span.gap_lo - j * kN, 0), z1 = min(span.gap_hi - j * kN, nvalid);
+          if (nvalid < 16 * groups || z0 < z1) {
+            zero_rows(nvalid, 16 * groups);
+            if (z0 < z1) zero_rows(z0, z1);
+            fence_async_smem();   // generic stores -> the MMAs' reads
+            __syncwarp();
+          }
+        }
+        const uint64_t vd = vdesc0 + ((s * kTileBytes) >> 4);
+        for (int h = 0; h < 2 && ok; ++h) {
+          ok = wait_all(&p_full[2 * b + h], (j / kBufs) & 1);
+          if (!ok) break;
+          tc_fence_after();
+          if (leader) {
+            // keys 16kk..16kk+15: P hi at column 16kk, lo at 16kk+8.  A loop, not unrolled: between its turns the warp's
+            // code is pushed out of the instruction cache by the softmax's (unrolled, its first 8 MMAs took 1600 clocks
+            // to issue, the next 8 530)
+            const int k1 = min(groups, (h + 1) * (kN / 32));
+#pragma unroll 1
+            for (int kk = h * (kN / 32); kk < k1; ++kk) {
+              umma_ts(obuf(0), sbuf(0, b) + 16 * kk, vd + ((kk * kVStep) >> 4), idesc_o, j > 0 || kk > 0 ? 1u : 0u);
+              if constexpr (kSplit) umma_ts(obuf(0), sbuf(0, b) + 16 * kk + 8, vd + ((kk * kVStep) >> 4), idesc_o, 1u);
+            }
+            if (h == 1) {
+              umma_commit(&o_done[0]);
+              umma_commit(&v_free[s]);
+            }
+          }
+          __syncwarp();
+          issued = true;
+        }
+        if (ok && jn < nkt) {
+          ok = wait_all(&k_full[jn % kStages], (jn / kStages) & 1) && wait_all(&o_done[0], j & 1);
+          if (!ok) break;
+          tc_fence_after();
+          issue_s(jn);
+        }
+      }
+      // every MMA issued above is complete before tensor memory is freed
+      if (issued) {
+        if (leader) umma_commit(fin);
+        __syncwarp();
+        mbar_wait(fin, 0, p.err);
+      }
+    }
   } else if (warp == kMmaWarp) {
     // ===================================================== MMA issue (warp kMmaWarp; warps
     // past it, in a larger block such as the mixed launch's, have no role)
@@ -837,36 +1311,50 @@ cudaError_t launch_prefill_tc(const PrefillTcParams &p, const PoolMaps &m, int g
 // token rows walks window + BR + sinks keys instead of the whole context.
 // One kernel for every group size (the group is a run-time number: one
 // division per thread) and for head_dim 64 and 128.
-template <typename KV, typename QT, int kQTiles, int D>
-__global__ void __launch_bounds__(tc::Roles<kQTiles>::kThreads, 1)
+//
+// A bf16 cache's P: hi + lo for an fp32 output (kLo), rounded once to bf16 (to
+// nearest, the softmax sum that of the rounded P, so that the output stays a
+// convex combination of V rows) for a bf16 output, whose own rounding is as
+// large: the error against 64 bits goes from 1.7e-3 to 2.3e-3 of the output's
+// norm, and a third of the MMAs go away.
+template <typename KV, typename QT, int D, bool kPair, bool kLo>
+__global__ void __launch_bounds__((tc::WinRoles<kPair, std::is_same<KV, uint8_t>::value>::kThreads), kPair ? 2 : 1)
     prefill_window_kernel(const PrefillTcParams p, const __grid_constant__ CUtensorMap tmap_k,
                           const __grid_constant__ CUtensorMap tmap_v) {
-  prefill_tc_body<KV, QT, 0, kQTiles, D, true>(p, blockIdx.x, blockIdx.y, &tmap_k, &tmap_v);
+  prefill_tc_body<KV, QT, 0, 1, D, true, kPair, kLo>(p, blockIdx.x, blockIdx.y, &tmap_k, &tmap_v);
 }
 
-template <typename KV, typename QT, int kQTiles, int D>
-cudaError_t launch_prefill_window_tiles(const PrefillTcParams &p0, const PoolMaps &m, int num_chunks, cudaStream_t s) {
-  constexpr int smem = tc::Layout<kQTiles, std::is_same<KV, uint8_t>::value, D>::kSmemBytes;
-  PrefillTcParams p = p0;
-  const int BR = kQTiles * tc::kM / p.share_heads;
-  p.row_blocks = (p.max_q_len + BR - 1) / BR;
-  cudaError_t e = ensure_smem_limit<prefill_window_kernel<KV, QT, kQTiles, D>>(smem);
+template <typename KV, typename QT, int D, bool kPair, bool kLo>
+cudaError_t launch_prefill_window_tiles(const PrefillTcParams &p, const PoolMaps &m, dim3 grid, cudaStream_t s) {
+  using R = tc::WinRoles<kPair, std::is_same<KV, uint8_t>::value>;
+  constexpr int smem = tc::Layout<1, std::is_same<KV, uint8_t>::value, D, R::kStages, true>::kSmemBytes;
+  static_assert(!kPair || 2 * (smem + 1024) <= 228 * 1024, "two CTAs per SM");
+  cudaError_t e = ensure_smem_limit<prefill_window_kernel<KV, QT, D, kPair, kLo>>(smem);
   if (e != cudaSuccess) return e;
-  const int64_t gx = (int64_t)num_chunks * p.row_blocks, gy = (int64_t)p.num_kv_heads * p.shares;
-  if (gx > 2147483647ll || gy > 65535) return cudaErrorInvalidValue;
-  prefill_window_kernel<KV, QT, kQTiles, D>
-      <<<dim3((unsigned)gx, (unsigned)gy), tc::Roles<kQTiles>::kThreads, smem, s>>>(p, m.k, m.v);
+  prefill_window_kernel<KV, QT, D, kPair, kLo><<<grid, R::kThreads, smem, s>>>(p, m.k, m.v);
   return cudaGetLastError();
 }
 
 template <typename KV, typename QT, int D>
-cudaError_t launch_prefill_window_one(const PrefillTcParams &p, const PoolMaps &m, int num_chunks, cudaStream_t s) {
+cudaError_t launch_prefill_window_one(const PrefillTcParams &p0, const PoolMaps &m, int num_chunks, cudaStream_t s) {
   int num_sms = 0;
   if (current_sm_count(&num_sms) != cudaSuccess) return cudaErrorUnknown;
-  const int br2 = 2 * tc::kM / p.share_heads;
-  const int64_t two = (int64_t)num_chunks * ((p.max_q_len + br2 - 1) / br2) * p.num_kv_heads * p.shares;
-  if (two >= num_sms) return launch_prefill_window_tiles<KV, QT, 2, D>(p, m, num_chunks, s);
-  return launch_prefill_window_tiles<KV, QT, 1, D>(p, m, num_chunks, s);
+  PrefillTcParams p = p0;
+  const int BR = tc::kM / p.share_heads;   // token rows per CTA
+  p.row_blocks = (p.max_q_len + BR - 1) / BR;
+  const int64_t gx = (int64_t)num_chunks * p.row_blocks, gy = (int64_t)p.num_kv_heads * p.shares;
+  if (gx > 2147483647ll || gy > 65535) return cudaErrorInvalidValue;
+  const dim3 grid((unsigned)gx, (unsigned)gy);
+  // one CTA per SM while that is all there is
+  constexpr bool kBf16Cache = std::is_same<KV, __nv_bfloat16>::value;
+  // One CTA per SM while that is all there is: a 512-token chunk of 32/8 heads (128 CTAs) 17.5 us, as pairs 21.9;
+  // beyond that pairs: 8 chunks of 2048, 64/8 heads (8192 CTAs), 0.70 ms, one CTA per SM 0.87.
+  const bool pair = gx * gy > num_sms;
+  if (kBf16Cache && !p.out_f32)
+    return pair ? launch_prefill_window_tiles<KV, QT, D, true, !kBf16Cache>(p, m, grid, s)
+                : launch_prefill_window_tiles<KV, QT, D, false, !kBf16Cache>(p, m, grid, s);
+  return pair ? launch_prefill_window_tiles<KV, QT, D, true, true>(p, m, grid, s)
+              : launch_prefill_window_tiles<KV, QT, D, false, true>(p, m, grid, s);
 }
 
 template <typename KV, typename QT>

@@ -8,7 +8,8 @@ Bounds, per output element, from how the kernels compute (u = 2^-24):
   its largest element: + scale * 2^-21 * max |q| * sum |k|.  In log2 units t is rounded to fp32 twice and 2^t is
   within 2^-22: + 4 u |s| + 2^-22 in the exponent.
 * a softmax weight a is then off by at most (2 e + 2^-21) a, and sum a V by that times A = sum a |V|.
-* P in the second product: bf16 caches hi + lo, within 2^-15 (decode) or 2^-16 (prefill); f16 P rounded to nearest,
+* P in the second product: bf16 caches hi + lo, within 2^-15 (decode) or 2^-16 (prefill), or for a prefill's bf16 output
+  rounded to nearest, 2^-8, numerator and denominator: 2^-7 A; f16 P rounded to nearest,
   2^-11, numerator and denominator: 2^-10 A, and below 2^-14 to 2^-25: n 2^-25 max |V|; an fp8 decode holds 256 p to
   2^-8 of itself + 2^-14: 2^-8 A + n 2^-22 max |V|.  fp32 sums of n terms: 2^-24 (16 + n / 16) A.
 * the stored output: half a step of its type."""
@@ -121,7 +122,7 @@ def attend(q, k, v, seen, scale, kv, out, prefill=False):
     vmax = v0.abs().amax() if n else torch.tensor(0.0)
     rel = (2 * e + 2.0 ** -21)[..., None] + 2.0 ** -24 * (16 + count / 16)
     if kv == "bf16":
-        rel, low = rel + (2.0 ** -16 if prefill else 2.0 ** -15), 0.0
+        rel, low = rel + (2.0 ** -15 if not prefill else 2.0 ** -7 if out == "bf16" else 2.0 ** -16), 0.0
     elif kv == "f16" or prefill:
         rel, low = rel + 2.0 ** -10, count * 2.0 ** -25 * vmax
     else:
