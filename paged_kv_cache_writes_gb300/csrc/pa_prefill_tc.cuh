@@ -781,7 +781,9 @@ __device__ __forceinline__ void prefill_tc_body(const PrefillTcParams &p, int bx
     }
     const float l = ((lacc[0].x + lacc[0].y) + (lacc[1].x + lacc[1].y)) +
                     ((lacc[2].x + lacc[2].y) + (lacc[3].x + lacc[3].y));
-    // O is complete once the tile's last P.V has finished
+    // O is complete once the tile's last P.V has finished; with two score buffers, the last tile's scores came when the
+    // P.V before the previous one was complete, so the previous one is waited for first (phases of the same parity)
+    if (ok && kBufs == 2 && nkt > 1) ok = wait_all(&o_done[t], (nkt - 2) & 1);
     if (ok && nkt > 0) ok = wait_all(&o_done[t], (nkt - 1) & 1);
     if (ok) {
       tc_fence_after();
