@@ -514,7 +514,8 @@ pa_status bounded_layout(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_h
   return PA_OK;
 }
 
-// Workspace of pa_evict: each head's list of moves (destinations, then sources).
+// Workspace of pa_evict: each head's list of moves (their number padded to 16
+// bytes, destinations, sources).
 struct EvictLayout {
   size_t total;
   int64_t list_cap, list_stride;
@@ -524,7 +525,7 @@ bool evict_layout(int32_t num_seqs, int32_t num_kv_heads, int32_t max_seq_len, i
   if (num_seqs < 0 || num_kv_heads <= 0 || max_seq_len < 0 || max_seq_len > kMaxEvictLen || budget < 1) return false;
   const int64_t moves = std::min<int64_t>(budget, std::max<int64_t>(0, (int64_t)max_seq_len - budget));
   l->list_cap = (moves + 3) / 4 * 4;
-  l->list_stride = 2 * l->list_cap;
+  l->list_stride = 4 + 2 * l->list_cap;
   l->total = std::max<size_t>(256, round256((size_t)num_seqs * num_kv_heads * l->list_stride * 4));
   return true;
 }

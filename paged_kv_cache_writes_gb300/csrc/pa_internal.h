@@ -236,7 +236,7 @@ struct EvictParams {
   int32_t num_weight_rows;
   const int32_t *weight_rows;  // null: row i
   int32_t *new_seq_lens;
-  // workspace: per (row, head) the moves' destinations, then their sources (list_cap each)
+  // workspace: per (row, head) the number of moves (4 words), their destinations, their sources (list_cap each)
   int32_t *lists;
   int64_t list_stride, list_cap;
   int32_t *err;

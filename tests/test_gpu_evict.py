@@ -107,6 +107,18 @@ def test_cluster_sizes(most):
     evict_case([600, 333, 100], 2, 64, 16, "bf16", 150, 4, 30, most=most, seed=most, weights=torch.randint(0, 40, (4, 2, most)) / 8)
 
 
+@pytest.mark.parametrize("kv,d", [("bf16", 128), ("fp8", 64)])
+def test_many_moves(kv, d):
+    # more moves than one launch does: 24 x 4 heads of up to 2100 slots to 1000
+    evict_case([2100 - 37 * i for i in range(24)], 4, d, 32, kv, 1000, 4, 50, most=4000, seed=d)
+
+
+@pytest.mark.parametrize("seqs,most", [(8, 30000), (40, 12000)])
+def test_few_moves_under_a_large_bound(seqs, most):
+    # the bound promises many moves (and, with few sequences, a cluster per head), the lengths make few
+    evict_case([300 + i for i in range(seqs)], 2, 64, 16, "f16", 290, 4, 20, most=most, seed=seqs)
+
+
 def test_a_bound_above_every_length():
     evict_case([120, 101], 2, 64, 16, "bf16", 90, 4, 30, most=5000, seed=9)
 
