@@ -21,9 +21,9 @@
 //    a histogram of 8 KB took 2.5 us a pass: distributed shared memory gives an SM
 //    some 10 bytes a clock).  When all keys with the digits so far stay, the rest
 //    is not looked at;
-//  * each warp owns a contiguous run of slots, so that one count per warp, one
-//    scan over the warps and one over the cluster rank the equal keys, the
-//    freed slots and the moving tokens in slot order;
+//  * each warp owns a contiguous run of slots, a lane four in a row of every 128,
+//    so that one count per warp, one scan over the warps and one over the cluster
+//    rank the equal keys, the freed slots and the moving tokens in slot order;
 //  * a lane looks up one move's blocks and moves its metadata, then its warp
 //    copies the K and V rows of up to 32 moves, several rows in flight.  With few
 //    moves the cluster's warps share them, at the end of the same launch (the list
@@ -159,7 +159,7 @@ __device__ __forceinline__ void move_tokens(const EvictParams &p, const Head &h,
 template <int kLanes>
 __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const EvictParams p, int cluster, int cached, int smem_list, int split) {
   __shared__ __align__(16) Shared sh;
-  extern __shared__ uint32_t dynamic[];   // cached: this CTA's keys; smem_list: its list of moves
+  extern __shared__ __align__(16) uint32_t dynamic[];   // cached: this CTA's keys; smem_list: its list of moves
   // launched as a programmatic dependent: nothing is read before what precedes it is complete
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -202,8 +202,8 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const EvictParams p,
     return;
   }
 
-  // this CTA's slots [lo, hi), a multiple of 32 per warp
-  const int per_warp = ((L + cluster * kWarps - 1) / (cluster * kWarps) + 31) & ~31;
+  // this CTA's slots [lo, hi), a multiple of 128 per warp
+  const int per_warp = ((L + cluster * kWarps - 1) / (cluster * kWarps) + 127) & ~127;
   const int lo = min((int64_t)L, (int64_t)rank * kWarps * per_warp), hi = min((int64_t)L, lo + (int64_t)kWarps * per_warp);
   const int wlo = min(hi, lo + warp * per_warp), whi = min(hi, wlo + per_warp);
   auto key_of = [&](float x, int t) { return t < p.num_sinks || t >= seen - p.num_recent ? kProtected : weight_key(x); };
@@ -222,9 +222,22 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const EvictParams p,
       for (int i = 0; i < 4; ++i)
         if (s0 + 32 * i < whi) dynamic[s0 + 32 * i - lo] = key_of(x[i], t[i]);
     }
-    __syncwarp();   // a lane reads its own keys only
+    __syncwarp();   // a warp reads its own keys only
   }
-  auto key = [&](int s) { return cached ? dynamic[s - lo] : key_of(w[s], position(s)); };
+  // the keys of slots s .. s + 3 (s from lo on in steps of 4; slots past the warp's: 0, which `own` tells apart)
+  auto four_keys = [&](int s, uint32_t (&k)[4]) {
+    if (cached) {
+      const uint4 x = *reinterpret_cast<const uint4 *>(dynamic + (s - lo));   // (past the warp's: unused)
+      k[0] = x.x;
+      k[1] = x.y;
+      k[2] = x.z;
+      k[3] = x.w;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) k[j] = s + j < whi ? key_of(w[s + j], position(s + j)) : 0u;
+    }
+  };
+  const int mine = wlo + 4 * lane;   // the lane's first four slots
   barrier();   // the histograms are zeroed
 
   // ------------------------------------------------ the B-th largest key
@@ -235,14 +248,20 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const EvictParams p,
     const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
     const uint32_t digits = pass == 2 ? 1023u : 2047u;
     int *hist = cluster > 1 ? sh.own : sh.hist[pass];
+    int safe = 0;   // protected tokens of the lane, of which there are many
 #pragma unroll 1
-    for (int s0 = wlo; s0 < whi; s0 += 32) {
-      const uint32_t k = s0 + lane < whi ? key(s0 + lane) : 0u;
-      const bool in = s0 + lane < whi && (k & mask) == prefix;
-      const uint32_t safe = __ballot_sync(0xffffffffu, in && k == kProtected);
-      if (in && k != kProtected) atomicAdd(&hist[(k >> shift) & digits], 1);
-      if (safe && lane == 0) atomicAdd(&hist[digits], __popc(safe));
+    for (int s = mine; s < whi; s += 128) {
+      uint32_t k[4];
+      four_keys(s, k);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (s + j < whi && (k[j] & mask) == prefix) {
+          if (k[j] == kProtected) ++safe;
+          else atomicAdd(&hist[(k[j] >> shift) & digits], 1);
+        }
     }
+    safe = __reduce_add_sync(0xffffffffu, safe);
+    if (safe && lane == 0) atomicAdd(&hist[digits], safe);
     // thread t: kBinsPerThread bins counted from the largest digit down, over the cluster
     const int b0 = kBins - kBinsPerThread * (tid + 1);
     if (cluster > 1) {
@@ -306,10 +325,13 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const EvictParams p,
   if (rank_ties) {
     int n = 0;
 #pragma unroll 1
-    for (int s0 = wlo; s0 < whi; s0 += 32) {
-      const uint32_t k = s0 + lane < whi ? key(s0 + lane) : 0u;
-      n += __popc(__ballot_sync(0xffffffffu, s0 + lane < whi && (k & mask) == prefix));
+    for (int s = mine; s < whi; s += 128) {
+      uint32_t k[4];
+      four_keys(s, k);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) n += s + j < whi && (k[j] & mask) == prefix;
     }
+    n = __reduce_add_sync(0xffffffffu, n);
     if (lane == 0) sh.ties[warp] = n;
     __syncthreads();
     tie0 = __reduce_add_sync(0xffffffffu, lane < warp ? sh.ties[lane] : 0);
@@ -321,27 +343,38 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const EvictParams p,
       tie0 += __reduce_add_sync(0xffffffffu, lane < (int)rank ? n : 0);
     }
   }
-  // The kept slots of the warp's 32 from s0 on, `ties` equal keys before them
-  auto kept_of = [&](int s0, int &ties) {
-    const uint32_t k = s0 + lane < whi ? key(s0 + lane) : 0u;
-    const bool tie = s0 + lane < whi && (k & mask) == prefix;
-    bool kept = s0 + lane < whi && ((k & mask) > prefix || (tie && !rank_ties));
-    if (rank_ties) {
-      const uint32_t t = __ballot_sync(0xffffffffu, tie);
-      kept |= tie && ties + __popc(t & ((1u << lane) - 1)) < need;
-      ties += __popc(t);
-    }
+  // Which of the lane's four slots from s on stay, as bits; every lane calls it, `ties` equal keys before the warp's 128
+  auto kept_of = [&](int s, int &ties) {
+    uint32_t k[4], kept = 0, tie = 0;
+    if (s < whi) four_keys(s, k);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (s + j < whi) {
+        kept |= (uint32_t)((k[j] & mask) > prefix) << j;
+        tie |= (uint32_t)((k[j] & mask) == prefix) << j;
+      }
+    if (!rank_ties) return kept | tie;
+    const int end = warp_inclusive(__popc(tie));
+    int left = need - ties - (end - __popc(tie));   // how many of the lane's equal keys may stay
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (tie >> j & 1u) kept |= (uint32_t)(left-- > 0) << j;
+    ties += __shfl_sync(0xffffffffu, end, 31);
     return kept;
   };
+  // the slots s .. s + 3 that are the warp's, and those of them below B, as bits
+  auto first_bits = [](int n) { return n >= 4 ? 15u : n <= 0 ? 0u : (1u << n) - 1u; };
   {
     int nh = 0, nm = 0, ties = tie0;
 #pragma unroll 1
-    for (int s0 = wlo; s0 < whi; s0 += 32) {
-      const int s = s0 + lane;
-      const bool kept = kept_of(s0, ties);
-      nh += __popc(__ballot_sync(0xffffffffu, s < whi && s < B && !kept));
-      nm += __popc(__ballot_sync(0xffffffffu, kept && s >= B));
+    for (int s0 = wlo; s0 < whi; s0 += 128) {
+      const int s = s0 + 4 * lane;
+      const uint32_t kept = kept_of(s, ties), low = first_bits(B - s);
+      nh += __popc(first_bits(whi - s) & low & ~kept);
+      nm += __popc(kept & ~low);
     }
+    nh = __reduce_add_sync(0xffffffffu, nh);
+    nm = __reduce_add_sync(0xffffffffu, nm);
     if (lane == 0) {
       sh.holes[warp] = nh;
       sh.movers[warp] = nm;
@@ -375,21 +408,32 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const EvictParams p,
   {
     int ties = tie0;
 #pragma unroll 1
-    for (int s0 = wlo; s0 < whi; s0 += 32) {
-      const int s = s0 + lane;
-      const bool kept = kept_of(s0, ties);
-      const bool hole = s < whi && s < B && !kept, mover = kept && s >= B;
-      const uint32_t hb = __ballot_sync(0xffffffffu, hole), mb = __ballot_sync(0xffffffffu, mover);
-      const uint32_t below = (1u << lane) - 1;
-      if (hole) hole_list[hole0 + __popc(hb & below)] = s;
-      if (mover) mover_list[mover0 + __popc(mb & below)] = s;
-      hole0 += __popc(hb);
-      mover0 += __popc(mb);
-      if (kept && s < B) {   // stays where it is
-        const float x = w[s];
-        const int t = position(s);
-        p.new_weights[base + s] = x;
-        p.new_positions[base + s] = t;
+    for (int s0 = wlo; s0 < whi; s0 += 128) {
+      const int s = s0 + 4 * lane;
+      const uint32_t kept = kept_of(s, ties), low = first_bits(B - s);
+      const uint32_t hole = first_bits(whi - s) & low & ~kept, mover = kept & ~low;
+      const int own = __popc(hole) | __popc(mover) << 16;
+      const int end = warp_inclusive(own);   // both ranks in one scan: at most 128 each
+      int hi0 = hole0 + ((end - own) & 0xffff), mi0 = mover0 + ((end - own) >> 16);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (hole >> j & 1u) hole_list[hi0++] = s + j;
+        if (mover >> j & 1u) mover_list[mi0++] = s + j;
+      }
+      const int all = __shfl_sync(0xffffffffu, end, 31);
+      hole0 += all & 0xffff;
+      mover0 += all >> 16;
+      // the tokens that stay where they are, 32 consecutive slots at a time
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const uint32_t bits = __shfl_sync(0xffffffffu, kept & low, 8 * c + (lane >> 2));
+        const int t = s0 + 32 * c + lane;
+        if (bits >> (lane & 3) & 1u) {
+          const float x = w[t];
+          const int at_pos = position(t);
+          p.new_weights[base + t] = x;
+          p.new_positions[base + t] = at_pos;
+        }
       }
     }
   }
@@ -467,8 +511,8 @@ cudaError_t launch_lanes(const EvictParams &p, cudaStream_t s) {
   while (cluster < kMaxCluster && heads * cluster * 2 <= 2 * sms && p.max_seq_len / (2 * cluster) >= kThreads) cluster *= 2;
   while (cluster < kMaxCluster && p.max_seq_len / cluster > kCachedKeys) cluster *= 2;
   if (heads * cluster > 2147483647ll) return cudaErrorInvalidValue;
-  // a CTA's slots: per_warp rounded up to 32, times the warps
-  const int64_t slots = (((int64_t)p.max_seq_len + cluster * kWarps - 1) / (cluster * kWarps) + 31) / 32 * 32 * kWarps;
+  // a CTA's slots: per_warp rounded up to 128, times the warps
+  const int64_t slots = (((int64_t)p.max_seq_len + cluster * kWarps - 1) / (cluster * kWarps) + 127) / 128 * 128 * kWarps;
   const int cached = slots <= kCachedKeys;
   // the list of moves: behind the keys, 16 words in (an offset of 0 stands for the workspace)
   const int keys = cached ? (int)slots : 16;
