@@ -85,6 +85,13 @@
 //  * merge warp: merges split rows taken from a grid-wide list that the
 //    softmax warps append to, so the merging is shared by every CTA.
 //
+// Bounded-cache decodes (kExt: pa_decode_window, pa_decode_weights): the same
+// kernel over rows packed by a sliding window with visible first tokens
+// (pa_window.cuh), for any group size (wide groups cut into shares), K and V
+// loaded with an evict-first L2 policy, the scores written out for the weights.
+// Small batches run "direct": no plan kernel, the scheduler warp of each CTA
+// deals the units from the lengths, and pa_finish.cu merges the split rows.
+//
 // Every mbarrier wait is bounded (PA_ERR_TIMEOUT, after which the CTA
 // abandons its work); tensor memory is freed only after every issued MMA has
 // completed.

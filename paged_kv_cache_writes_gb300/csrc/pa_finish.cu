@@ -205,7 +205,7 @@ __device__ __forceinline__ void weights_cta(const FinishParams &p, int64_t block
 }
 
 template <int G, int D>
-__global__ void __launch_bounds__(kThreads) decode_finish_kernel(const FinishParams p) {
+__global__ void __launch_bounds__(kThreads, 4) decode_finish_kernel(const FinishParams p) {
   extern __shared__ __align__(16) float smem[];
   // launched as the decode's programmatic dependent
   asm volatile("griddepcontrol.wait;" ::: "memory");

@@ -56,6 +56,9 @@
 // even) and the softmax denominator sums the rounded P, so the output
 // remains a convex combination of V rows.
 //
+// pa_prefill_chunk_window (kWin) shares the set-up, the loaders of an fp8 cache
+// and the teardown, with softmax and MMA roles of its own, further down.
+//
 // Every mbarrier wait is bounded (PA_ERR_TIMEOUT, then the CTA abandons its
 // work); before tensor memory is freed the CTA waits for its outstanding MMAs
 // and copies.
