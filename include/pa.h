@@ -504,7 +504,8 @@ PA_API pa_status pa_decode_weights(const void *q, pa_dtype q_dtype, int32_t num_
  *                [num_weight_rows][num_kv_heads][weights_stride]; the new
  *                arrays may be the old ones or must not overlap them
  *   weight_rows  as for pa_decode_weights
- *   new_seq_lens device int32 [num_seqs]; must not overlap seq_lens
+ *   new_seq_lens device int32 [num_seqs]; must not overlap seq_lens,
+ *                num_tokens, ordered_from or weight_rows
  *   workspace    device, >= pa_evict_workspace_bytes(...) bytes, 256-byte
  *                aligned; its contents on entry are ignored
  * A sequence whose metadata is out of range sets PA_ERR_DEVICE_CHECK and is

@@ -326,6 +326,19 @@ class _Args:
             raise ValueError(f"{name} must have one entry per sequence")
         return self(t, name, torch.int32)
 
+    @staticmethod
+    def shapes(q: torch.Tensor, out: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, cache: PaKvCache,
+               block_tables: torch.Tensor, n: int) -> None:
+        """What the library cannot see: pools of the descriptor's shape, an output of the queries', a table row per
+        sequence."""
+        shape = k_cache.shape
+        if shape != v_cache.shape or shape != (cache.num_blocks, cache.num_kv_heads, cache.block_size, cache.head_dim):
+            raise ValueError("k_cache and v_cache must have the descriptor's shape")
+        if q is not None and (q.dim() != 3 or q.shape[2] != cache.head_dim or q.shape != out.shape):
+            raise ValueError("q and out must be [rows, num_q_heads, head_dim]")
+        if block_tables.dim() != 2 or block_tables.shape[0] != n:
+            raise ValueError("block_tables must have one row per sequence")
+
     def stream(self, stream) -> int:
         return torch._C._cuda_getCurrentRawStream(self.device) if stream is None else _stream(stream)
 
@@ -348,6 +361,7 @@ def pa_decode_window(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tens
     ``workspace``: uint8 tensor of >= pa_decode_window_workspace_bytes(...) bytes."""
     a = _Args()
     B, hq, _ = q.shape
+    a.shapes(q, out, k_cache, v_cache, cache, block_tables, B)
     status = lib().pa_decode_window(
         a(q, "q"), _dtype_code(q.dtype), B, hq, a(k_cache, "k_cache"), a(v_cache, "v_cache"), ctypes.byref(cache),
         a(block_tables, "block_tables", _I32), block_tables.shape[1], a.of_sequences(seq_lens, "seq_lens", B), max_seq_len,
@@ -364,6 +378,7 @@ def pa_prefill_chunk_window(q_chunk: torch.Tensor, cu_q_lens: torch.Tensor, q_st
     """pa_prefill_chunk in which the row at position t sees p <= t with p < num_sinks or p > t - window."""
     a = _Args()
     n = q_start.shape[0]
+    a.shapes(q_chunk, out, k_cache, v_cache, cache, block_tables, n)
     status = lib().pa_prefill_chunk_window(
         a(q_chunk, "q_chunk"), _dtype_code(q_chunk.dtype), a.of_sequences(cu_q_lens, "cu_q_lens", n + 1),
         a.of_sequences(q_start, "q_start", n), n, max_q_len, q_chunk.shape[1], a(k_cache, "k_cache"),
@@ -398,6 +413,7 @@ def pa_decode_weights(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Ten
     ``decay`` first.  ``workspace``: uint8 tensor of >= pa_decode_weights_workspace_bytes(...) bytes."""
     a = _Args()
     B, hq, _ = q.shape
+    a.shapes(q, out, k_cache, v_cache, cache, block_tables, B)
     rows, stride = _weights_rows(weights, cache.num_kv_heads)
     status = lib().pa_decode_weights(
         a(q, "q"), _dtype_code(q.dtype), B, hq, a(k_cache, "k_cache"), a(v_cache, "v_cache"), ctypes.byref(cache),
@@ -426,6 +442,7 @@ def pa_evict(k_cache: torch.Tensor, v_cache: torch.Tensor, cache: PaKvCache, blo
     pa_evict_workspace_bytes(...) bytes."""
     a = _Args()
     B = seq_lens.shape[0]
+    a.shapes(None, None, k_cache, v_cache, cache, block_tables, B)
     rows, stride = _weights_rows(weights, cache.num_kv_heads)
     shape = weights.shape
     if positions.shape != shape or new_weights.shape != shape or new_positions.shape != shape:

@@ -9,6 +9,7 @@
 #include <cmath>
 #include <initializer_list>
 #include <mutex>
+#include <utility>
 
 #include "pa_common.cuh"
 #include "pa_decode.cuh"
@@ -34,6 +35,10 @@ __global__ void selftest_wait_kernel(int32_t *err) {
 
 namespace {
 
+uintptr_t distance(const void *p, const void *q) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+  return a < b ? b - a : a - b;
+}
 bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 // Address of the current device's error word (a host-side name is not a
@@ -522,7 +527,9 @@ struct EvictLayout {
 };
 constexpr int32_t kMaxEvictLen = 1 << 30;   // slots are counted in int32, with room for a rounding up
 bool evict_layout(int32_t num_seqs, int32_t num_kv_heads, int32_t max_seq_len, int32_t budget, EvictLayout *l) {
-  if (num_seqs < 0 || num_kv_heads <= 0 || max_seq_len < 0 || max_seq_len > kMaxEvictLen || budget < 1) return false;
+  if (num_seqs < 0 || num_kv_heads <= 0 || max_seq_len < 0 || max_seq_len > kMaxEvictLen || budget < 1 ||
+      (int64_t)num_seqs * num_kv_heads > INT32_MAX)
+    return false;
   const int64_t moves = std::min<int64_t>(budget, std::max<int64_t>(0, (int64_t)max_seq_len - budget));
   l->list_cap = (moves + 3) / 4 * 4;
   l->list_stride = 4 + 2 * l->list_cap;
@@ -671,11 +678,15 @@ pa_status pa_evict(void *k_cache, void *v_cache, const pa_kv_cache *cache, int32
                         (const void *)ordered_from, (const void *)weights, (const void *)positions,
                         (const void *)new_weights, (const void *)new_positions, (const void *)new_seq_lens})
     if (!q || !aligned(q, 4)) return PA_ERR_INVALID_ARG;
-  // the sequences' heads read seq_lens while one of them writes the new length
-  const uintptr_t a = reinterpret_cast<uintptr_t>(seq_lens), b = reinterpret_cast<uintptr_t>(new_seq_lens);
-  if ((a < b ? b - a : a - b) < (uintptr_t)num_seqs * 4) return PA_ERR_INVALID_ARG;
+  // a sequence's heads read these while one of them writes its new length
+  for (const int32_t *q : {seq_lens, num_tokens, ordered_from, weight_rows})
+    if (q && distance(q, new_seq_lens) < (uintptr_t)num_seqs * 4) return PA_ERR_INVALID_ARG;
   if (!aligned(weight_rows, 4) || weights_stride < max_seq_len || num_weight_rows < (weight_rows ? 1 : num_seqs))
     return PA_ERR_INVALID_ARG;
+  // the new arrays are the old ones, or apart from them
+  const double array = (double)num_weight_rows * c.num_kv_heads * (double)weights_stride * 4;
+  for (const auto &[from, to] : {std::pair<const void *, const void *>{weights, new_weights}, {positions, new_positions}})
+    if (from != to && (double)distance(from, to) < array) return PA_ERR_INVALID_ARG;
   if ((st = check_pools(k_cache, v_cache)) != PA_OK) return st;
   if (!workspace || !aligned(workspace, 256) || workspace_bytes < l.total) return PA_ERR_INVALID_ARG;
   EvictParams p{};

@@ -26,9 +26,9 @@ class Cache:
     """A paged cache of random K and V for given lengths, on the CPU; `pools` gives the device copies.  Blocks that no
     sequence uses, and the tail of each last block, hold NaN; block-table entries behind the end are far out of range."""
 
-    def __init__(self, lens, hkv, d, bs, kv, seed, scales=(0.011, 0.013), per_head=False):
+    def __init__(self, lens, hkv, d, bs, kv, seed, scales=(0.011, 0.013), per_head=False, far=False):
         g = torch.Generator().manual_seed(seed)
-        self.lens, self.hkv, self.d, self.bs, self.kv = list(lens), hkv, d, bs, kv
+        self.lens, self.hkv, self.d, self.bs, self.kv, self.far = list(lens), hkv, d, bs, kv, far
         nblk = [-(-n // bs) for n in lens]
         self.num_blocks = sum(nblk) + 5
         order = torch.randperm(self.num_blocks, generator=g)
@@ -84,11 +84,17 @@ class Cache:
                 self.tables[i, j] = -1
 
     def device(self, pa):
-        """(k, v, tables, descriptor) on the GPU."""
-        k, v = self.k.cuda(), self.v.cuda()
+        """(k, v, tables, descriptor) on the GPU; far: at the end of pools whose byte offsets pass 32 bits."""
+        k, v, tables = self.k.cuda(), self.v.cuda(), self.tables
+        if self.far:
+            first = (5 << 30) // (k[0].numel() * k.element_size())
+            pools = [torch.empty((first + self.num_blocks, *k.shape[1:]), dtype=k.dtype, device="cuda") for _ in range(2)]
+            pools[0][first:], pools[1][first:] = k, v
+            k, v = pools
+            tables = torch.where((tables >= 0) & (tables < self.num_blocks), tables + first, tables)
         self.dev_scales = None if self.head_scales is None else [s.cuda() for s in self.head_scales]
         desc = pa.kv_cache_desc(k, self.k_scale, self.v_scale, *(self.dev_scales or (None, None)))
-        return k, v, self.tables.cuda(), desc
+        return k, v, tables.cuda(), desc
 
 
 def visible(t, n, window, sinks):

@@ -107,12 +107,15 @@ def test_prefill_chunk_window_refusals(pa, kw, desc_kw, want):
     (dict(nw=None), {}, 1), (dict(np=None), {}, 1), (dict(nl=None), {}, 1), (dict(stride=99), {}, 1), (dict(rows=3), {}, 1),
     (dict(k=None), {}, 1), (dict(ws=None), {}, 1), (dict(ws=FAKE + 8), {}, 1), (dict(wsb=16), {}, 1),
     (dict(nl=FAKE + 0x100000), {}, 1), (dict(nl=FAKE + 0x100000 + 12), {}, 1), (dict(nl=FAKE + 0x100000 - 12), {}, 1),   # on seq_lens
+    (dict(nl=FAKE + 0x200000 - 12), {}, 1), (dict(nl=FAKE + 0x300000 + 4), {}, 1), (dict(nl=FAKE + 0x400000, wr=FAKE + 0x400000), {}, 1),
+    (dict(nw=FAKE + 0x500000 + 64), {}, 1), (dict(np=FAKE + 0x600000 - 64), {}, 1),     # shifted against the old ones
+    (dict(n=2 ** 31 - 1, rows=2 ** 31 - 1), {}, 1),
     (dict(msl=2 ** 30 + 1, stride=2 ** 31, mb=2 ** 30), {}, 1),
     ({}, dict(block_size=64), 2), ({}, dict(kv_dtype=3), 2),
 ])
 def test_evict_refusals(pa, kw, desc_kw, want):
-    a = dict(k=FAKE, v=FAKE, n=4, bt=FAKE, mb=8, sl=FAKE + 0x100000, msl=100, seen=FAKE, old=FAKE, budget=50, sinks=4, recent=8, w=FAKE,
-             p=FAKE, nw=FAKE, np=FAKE, stride=100, rows=4, wr=None, nl=FAKE, ws=FAKE, wsb=1 << 30)
+    a = dict(k=FAKE, v=FAKE, n=4, bt=FAKE, mb=8, sl=FAKE + 0x100000, msl=100, seen=FAKE + 0x200000, old=FAKE + 0x300000, budget=50, sinks=4,
+             recent=8, w=FAKE + 0x500000, p=FAKE + 0x600000, nw=FAKE + 0x500000, np=FAKE + 0x600000, stride=100, rows=4, wr=None, nl=FAKE, ws=FAKE, wsb=1 << 30)
     a.update(kw)
     d = desc(pa, **desc_kw)
     assert pa.lib().pa_evict(a["k"], a["v"], ctypes.byref(d), a["n"], a["bt"], a["mb"], a["sl"], a["msl"], a["seen"], a["old"],
@@ -142,6 +145,14 @@ def test_binding_checks(pa, monkeypatch):
     monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
     k = torch.zeros((4, 2, 16, 64), dtype=torch.bfloat16)
     d = pa.kv_cache_desc(k)
+    with pytest.raises(ValueError, match="descriptor"):
+        pa._Args.shapes(None, None, k, k[:3], d, torch.zeros((1, 4)), 1)
+    with pytest.raises(ValueError, match="descriptor"):
+        pa._Args.shapes(None, None, k[:3], k[:3], d, torch.zeros((1, 4)), 1)
+    with pytest.raises(ValueError, match="q and out"):
+        pa._Args.shapes(torch.zeros((1, 4, 64)), torch.zeros((2, 4, 64)), k, k, d, torch.zeros((1, 4)), 1)
+    with pytest.raises(ValueError, match="one row"):
+        pa._Args.shapes(None, None, k, k, d, torch.zeros((1, 4)), 2)
     q = torch.zeros((1, 4, 64), dtype=torch.bfloat16)
     t, n = torch.zeros((1, 4), dtype=torch.int32), torch.zeros(1, dtype=torch.int32)
     w, p = torch.zeros((1, 2, 64)), torch.zeros((1, 2, 64), dtype=torch.int32)

@@ -123,6 +123,37 @@ def test_a_bound_above_every_length():
     evict_case([120, 101], 2, 64, 16, "bf16", 90, 4, 30, most=5000, seed=9)
 
 
+def test_blocks_past_32_bit_offsets():
+    c = Cache([200], 2, 128, 16, "bf16", 12, far=True)
+    k, v, tables, desc = c.device(pa)
+    t, far = tables[0].long().cpu(), k.shape[0] - c.num_blocks
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    w = torch.rand((1, 2, 200), generator=torch.Generator().manual_seed(3))
+    p = torch.zeros((1, 2, 200), dtype=torch.int32, device="cuda")
+    ws = torch.empty(pa.pa_evict_workspace_bytes(1, 2, 200, 90), dtype=torch.uint8, device="cuda")
+    pa.pa_evict(k, v, desc, tables, i32([200]), 200, i32([200]), i32([0]), 90, 4, 10, w.cuda(), p, w.cuda(), p.clone(),
+                i32([0]), workspace=ws)
+    assert pa.pa_get_device_error() == 0
+    for h in range(2):
+        src, _ = evict(w[0, h], p[0, h], 200, 200, 0, 90, 4, 10)
+        for j, s in enumerate(src):
+            assert torch.equal(bits(k[t[j // 16], h, j % 16]), bits(c.k[t[s // 16] - far, h, s % 16]))
+            assert torch.equal(bits(v[t[j // 16], h, j % 16]), bits(c.v[t[s // 16] - far, h, s % 16]))
+
+
+def test_more_protected_tokens_than_the_budget():
+    # positions that cannot be: every token says it is among the first; the lowest slots stay
+    c = Cache([100], 1, 64, 16, "bf16", 13)
+    k, v, tables, desc = c.device(pa)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    w, p = torch.rand((1, 1, 100), device="cuda"), torch.zeros((1, 1, 100), dtype=torch.int32, device="cuda")
+    nw, np_, nl = torch.zeros_like(w), torch.full_like(p, 7), i32([0])
+    ws = torch.empty(pa.pa_evict_workspace_bytes(1, 1, 100, 50), dtype=torch.uint8, device="cuda")
+    pa.pa_evict(k, v, desc, tables, i32([100]), 100, i32([500]), i32([100]), 50, 4, 0, w, p, nw, np_, nl, workspace=ws)
+    assert pa.pa_get_device_error() == 0
+    assert torch.equal(nw[0, 0, :50], w[0, 0, :50]) and (np_[0, 0, :50] == 0).all() and (np_[0, 0, 50:] == 7).all()
+
+
 def test_bad_metadata_is_reported_and_skipped():
     c = Cache([100, 100, 100, 100], 2, 64, 16, "bf16", 11)
     k, v, tables, desc = c.device(pa)

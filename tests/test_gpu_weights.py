@@ -76,6 +76,16 @@ def test_long_sequence():
     weights_case([9001], 16, 2, 128, 16, "bf16", "bf16", seed=6, out="bf16")
 
 
+def test_batches_past_the_direct_launch():
+    g = torch.Generator().manual_seed(1)
+    weights_case(torch.randint(0, 90, (140,), generator=g).tolist(), 4, 2, 64, 16, "bf16", "bf16", seed=8)
+    weights_case([3000, 5, 2900, 700] * 8, 16, 8, 64, 16, "f16", "f16", seed=9)
+
+
+def test_blocks_past_32_bit_offsets():
+    weights_case([40, 700], 8, 2, 128, 16, "bf16", "bf16", seed=11, far=True)
+
+
 def test_shared_blocks():
     """Two sequences over the same blocks each have weights of their own."""
     c = Cache([300], 2, 128, 16, "bf16", 8)

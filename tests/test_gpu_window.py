@@ -93,6 +93,19 @@ def test_decode_without_a_cut_agrees_with_pa_decode():
         assert ((o[i:i + 1].double() - ref[i:i + 1].double()).abs().cpu() <= 2 * bound).all()
 
 
+def test_decode_batches_past_the_direct_launch():
+    # more rows than a scheduler warp deals itself, and more units than fit: the plan kernel's path
+    g = torch.Generator().manual_seed(1)
+    decode_case(torch.randint(0, 90, (140,), generator=g).clamp(min=1).tolist(), 4, 2, 64, 16, "bf16", "bf16", 33, 3, seed=8)
+    decode_case([3000, 5, 2900, 700] * 8, 16, 8, 64, 16, "bf16", "bf16", 2500, 9, seed=9)
+
+
+@pytest.mark.parametrize("qt,kv", [("bf16", "bf16"), ("bf16", "fp8")])
+def test_blocks_past_32_bit_offsets(qt, kv):
+    decode_case([40, 700], 8, 2, 128, 16, qt, kv, 90, 5, seed=11, far=True)
+    chunk_case([(300, 130), (0, 77)], 8, 2, 128, 16, qt, kv, 90, 5, seed=12, far=True)
+
+
 def test_decode_bad_metadata_is_reported():
     c = Cache([100, 50], 2, 128, 16, "bf16", 9)
     q = torch.zeros((2, 4, 128), dtype=torch.bfloat16)
@@ -133,7 +146,7 @@ def chunk_case(chunks, hq, hkv, d, bs, qt, kv, window, sinks, seed=0, out="f32",
     pa.pa_prefill_chunk_window(q.cuda(), torch.tensor(cu, dtype=torch.int32, device="cuda"),
                                torch.tensor([s for s, _ in chunks], dtype=torch.int32, device="cuda"),
                                max(r for _, r in chunks), k, v, desc, tables,
-                               torch.tensor(lens, dtype=torch.int32, device="cuda"), max(lens), window, sinks, scale, o)
+                               torch.tensor(lens, dtype=torch.int32, device="cuda"), max(lens), window, sinks, scale, o[:total])
     assert pa.pa_get_device_error() == 0
     for i, (s, r) in enumerate(chunks):
         if r:
@@ -166,6 +179,11 @@ def test_chunk_two_tiles_per_cta(qt, kv, d):
 @pytest.mark.parametrize("out", ["bf16", "f32"])
 def test_chunk_output_types_and_negative_scale(out):
     chunk_case(CHUNKS, 8, 2, 128, 16, "bf16", "bf16", 64, 4, seed=3, out=out, scale=-0.05)
+
+
+def test_chunk_of_scale_zero_takes_the_mean():
+    chunk_case(CHUNKS, 8, 2, 128, 16, "bf16", "bf16", 64, 4, seed=6, scale=0.0)
+    chunk_case(CHUNKS, 8, 2, 64, 32, "bf16", "fp8", 64, 4, seed=7, scale=0.0)
 
 
 def test_chunk_per_head_scales():
