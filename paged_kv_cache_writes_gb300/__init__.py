@@ -329,14 +329,14 @@ class _Args:
     @staticmethod
     def shapes(q: torch.Tensor, out: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, cache: PaKvCache,
                block_tables: torch.Tensor, n: int) -> None:
-        """What the library cannot see: pools of the descriptor's shape, an output of the queries', a table row per
-        sequence."""
-        shape = k_cache.shape
-        if shape != v_cache.shape or shape != (cache.num_blocks, cache.num_kv_heads, cache.block_size, cache.head_dim):
+        """What the library cannot see: pools that hold what the descriptor says, an output of the queries' shape, a
+        table row per sequence."""
+        size = cache.num_blocks * cache.num_kv_heads * cache.block_size * cache.head_dim
+        if k_cache.numel() < size or v_cache.numel() < size:
             raise ValueError("k_cache and v_cache must have the descriptor's shape")
-        if q is not None and (q.dim() != 3 or q.shape[2] != cache.head_dim or q.shape != out.shape):
+        if q is not None and (q.shape != out.shape or q.shape[2] != cache.head_dim):
             raise ValueError("q and out must be [rows, num_q_heads, head_dim]")
-        if block_tables.dim() != 2 or block_tables.shape[0] != n:
+        if len(block_tables) != n:
             raise ValueError("block_tables must have one row per sequence")
 
     def stream(self, stream) -> int:

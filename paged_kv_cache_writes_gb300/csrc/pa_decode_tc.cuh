@@ -443,6 +443,10 @@ __device__ __forceinline__ void decode_tc_body(const DecodeTcParams &tp, const C
   constexpr int kRowChunks = kD * 2 / 16;     // 16-byte chunks of a 16-bit row
   constexpr int S = GE::kSlots, kNO = GE::kNO, kNS = GE::kNS;
   constexpr uint32_t kAB = kBf16 ? 1u : 0u;   // instruction-descriptor format: bf16 1, f16 0, e4m3 0
+  // small tiles (fp8) make the MMA warp's own instructions the bound: its MMAs and commits are predicated instead
+  // of branched around, its waits short.  33 sequences, head_dim 64, fp8: 23.8 -> 22.5 us; with a bf16 cache (one
+  // sequence, head_dim 128) 12.5 -> 13.1, so not there.
+  constexpr bool kLean = kExt && kFp8;
   const DecodeParams &p = tp.d;
   const float kNegInf = -__int_as_float(0x7f800000);
 
@@ -525,7 +529,8 @@ __device__ __forceinline__ void decode_tc_body(const DecodeTcParams &tp, const C
   auto col_s = [&](int b, int j) { return tmem + (uint32_t)((b * kMaxTiles + j) * kNS); };
   auto col_o = [&](int b) { return tmem + (uint32_t)(GE::kColO + b * kNO); };
   auto wait_all = [&](uint64_t *bar, uint32_t parity) {
-    return __all_sync(0xffffffffu, wait_or_abort(bar, parity, p.err, abort_flag));
+    // kLean: a phase that is complete already costs one look at its barrier, not the abort flag's read before it
+    return __all_sync(0xffffffffu, (kLean && mbar_try_wait(bar, parity)) || wait_or_abort(bar, parity, p.err, abort_flag));
   };
 
   const int hkv = p.num_kv_heads;
@@ -1324,10 +1329,18 @@ __device__ __forceinline__ void decode_tc_body(const DecodeTcParams &tp, const C
     const bool leader = elect_one();
     const uint32_t idesc_s = umma_idesc(kAB, kNS, false, false);
     const uint32_t idesc_o = umma_idesc(kAB, kNO, false, true);
-    // one MMA: kind::f8f6f4 for an fp8 cache, else kind::f16
-    auto mma = [&](uint32_t d, uint64_t a, uint64_t bdesc, uint32_t idesc, uint32_t acc) {
-      if constexpr (kFp8) umma_f8(d, a, bdesc, idesc, acc);
-      else umma(d, a, bdesc, idesc, acc);
+    // one MMA: kind::f8f6f4 for an fp8 cache, else kind::f16.  kLean: called by the whole warp, issued by the leader
+    auto mma_if = [&](bool on, uint32_t d, uint64_t a, uint64_t bdesc, uint32_t idesc, uint32_t acc) {
+      if constexpr (kLean) {
+        umma_f8_if(on && leader, d, a, bdesc, idesc, acc);
+      } else if (on) {
+        if constexpr (kFp8) umma_f8(d, a, bdesc, idesc, acc);
+        else umma(d, a, bdesc, idesc, acc);
+      }
+    };
+    auto commit = [&](uint64_t *bar) {
+      if constexpr (kLean) umma_commit_if(leader, bar);
+      else umma_commit(bar);
     };
     const uint32_t ring = smem_u32(smem + GE::kOffRing);
     const uint32_t qbuf = smem_u32(smem + GE::kOffQ);
@@ -1371,29 +1384,30 @@ __device__ __forceinline__ void decode_tc_body(const DecodeTcParams &tp, const C
           ok = wait_all(&slot_full[slot], (g_cons / S) & 1);
           if (!ok) break;
           tc_fence_after();   // the tile came by bulk copy (async proxy): no proxy fence
-          if (leader) {
+          if (kLean || leader) {
             const uint64_t kd = kdesc0 + dofs(slot * GE::kSlotBytes), qd = qdesc0 + dofs((kFp8 ? ib : b) * GE::kQBytes);
             const uint32_t dcol = col_s(b, j);
             if constexpr (kFp8) {
               // 32 elements (32 B of each kD-byte row) per MMA
 #pragma unroll
-              for (int k = 0; k < kD / 32; ++k) mma(dcol, kd + dofs(k * 32), qd + dofs(k * 32), idesc_s, k > 0 ? 1u : 0u);
+              for (int k = 0; k < kD / 32; ++k)
+                mma_if(true, dcol, kd + dofs(k * 32), qd + dofs(k * 32), idesc_s, k > 0 ? 1u : 0u);
             } else {
 #pragma unroll
               for (int k = 0; k < kD / 16; ++k)
-                mma(dcol, kd + dofs((k >> 2) * 1024 + (k & 3) * 32), qd + dofs((k >> 2) * (kNS * 128) + (k & 3) * 32),
-                    idesc_s, k > 0 ? 1u : 0u);
+                mma_if(true, dcol, kd + dofs((k >> 2) * 1024 + (k & 3) * 32),
+                       qd + dofs((k >> 2) * (kNS * 128) + (k & 3) * 32), idesc_s, k > 0 ? 1u : 0u);
             }
-            umma_commit(&slot_free[slot]);
+            commit(&slot_free[slot]);
           }
-          __syncwarp();
+          if constexpr (!kLean) __syncwarp();
           issued = true;
           ++g_cons;
         }
         if (!ok) break;
-        if (leader) {
-          umma_commit(&s_full[b]);
-          if constexpr (!kFp8) umma_commit(&q_free[b]);
+        if (kLean || leader) {
+          commit(&s_full[b]);
+          if constexpr (!kFp8) commit(&q_free[b]);
         }
         __syncwarp();
       }
@@ -1419,7 +1433,8 @@ __device__ __forceinline__ void decode_tc_body(const DecodeTcParams &tp, const C
           const int nvalid = min(kKeys, prev.ntok - j * kKeys);
           const int ngroups = (nvalid + kGroup - 1) / kGroup;
           uint8_t *vt = smem + GE::kOffRing + slot * GE::kSlotBytes;
-          if (nvalid % kGroup) {
+          const bool whole = kExt && prev.ntok % kGroup == 0 && prev.gap_lo >= prev.gap_hi;   // a unit without rows to zero
+          if (!whole && nvalid % kGroup) {
             if constexpr (kFp8) {
               constexpr int kRowC = kD / 16;   // 16-byte chunks of a kD-byte row
               for (int e = lane; e < (kGroup * ngroups - nvalid) * kRowC; e += 32)
@@ -1434,7 +1449,7 @@ __device__ __forceinline__ void decode_tc_body(const DecodeTcParams &tp, const C
             fence_async_smem();   // the zeroed rows (generic proxy) -> the MMAs' reads
             __syncwarp();
           }
-          if constexpr (kExt) {
+          if (kExt && !whole) {
             // the same for the keys outside the window: P is 0, their rows may hold anything
             const int z0 = max(prev.gap_lo - j * kKeys, 0), z1 = min(prev.gap_hi - j * kKeys, nvalid);
             if (z0 < z1) {
@@ -1451,7 +1466,7 @@ __device__ __forceinline__ void decode_tc_body(const DecodeTcParams &tp, const C
           }
           // P^T was fenced by the softmax warps before p_full; the tile came by bulk copy
           tc_fence_after();
-          if (leader) {
+          if (kLean || leader) {
             const uint64_t vd = vdesc0 + dofs(slot * GE::kSlotBytes), pd = pdesc0 + dofs((bp * kMaxTiles + j) * GE::kPBytes);
             const uint32_t dcol = col_o(bp), acc0 = j > 0 ? 1u : 0u;
             // unrolled over a whole tile's key groups, the tail's predicated off
@@ -1459,27 +1474,25 @@ __device__ __forceinline__ void decode_tc_body(const DecodeTcParams &tp, const C
               // V^T: one kD-element MN panel, 8-key groups 8 kD bytes apart, 32 keys per MMA
 #pragma unroll
               for (int kk = 0; kk < kKeys / 32; ++kk)
-                if (kk < ngroups) mma(dcol, vd + dofs(kk * 32 * kD), pd + dofs(kk * 32), idesc_o, kk > 0 ? 1u : acc0);
+                mma_if(kk < ngroups, dcol, vd + dofs(kk * 32 * kD), pd + dofs(kk * 32), idesc_o,
+                       kk > 0 ? 1u : acc0);
             } else {
               // M = 128 elements of V^T in two 64-element halves (LBO apart): panels 0 and 1,
               // or panel 0 twice with head_dim 64 (lanes 64..127 of O^T then repeat 0..63)
 #pragma unroll
               for (int kk = 0; kk < kKeys / 16; ++kk)
-                if (kk < ngroups)
-                  mma(dcol, vd + dofs(kk * 2 * kAtomB), pd + dofs((kk >> 2) * (kNO * 128) + (kk & 3) * 32), idesc_o,
-                      kk > 0 ? 1u : acc0);
+                mma_if(kk < ngroups, dcol, vd + dofs(kk * 2 * kAtomB),
+                       pd + dofs((kk >> 2) * (kNO * 128) + (kk & 3) * 32), idesc_o, kk > 0 ? 1u : acc0);
             }
-            umma_commit(&slot_free[slot]);
+            commit(&slot_free[slot]);
           }
-          __syncwarp();
+          if constexpr (!kLean) __syncwarp();
           issued = true;
           ++g_cons;
         }
         if (!ok) break;
-        if (leader) {
-          umma_commit(&o_full[bp]);
-          mbar_arrive(&info_free[(u - 1) % kInfo]);
-        }
+        if (kLean || leader) commit(&o_full[bp]);
+        if (leader) mbar_arrive(&info_free[(u - 1) % kInfo]);
         __syncwarp();
       }
       if (!cur.valid) break;

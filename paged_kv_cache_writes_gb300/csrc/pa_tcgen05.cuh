@@ -83,6 +83,24 @@ __device__ __forceinline__ void split3_e4m3(float2 x, uint32_t &hi, uint32_t &mi
   split2_e4m3(r, mid, lo);
 }
 
+// An MMA with 8-bit operands, and a commit, by the lane where `issue` is set, without a branch: executed by the whole
+// (converged) warp, so that the operands stay in uniform registers (in a divergent branch each is first moved there).
+__device__ __forceinline__ void umma_f8_if(bool issue, uint32_t tmem_d, uint64_t a, uint64_t b, uint32_t idesc,
+                                           uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem_d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"((uint32_t)issue)
+      : "memory");
+}
+__device__ __forceinline__ void umma_commit_if(bool issue, uint64_t *bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
+      "r"((uint32_t)issue)
+      : "memory");
+}
+
 // Arrive once on `bar` when every tcgen05 operation this thread issued so far is complete.
 __device__ __forceinline__ void umma_commit(uint64_t *bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
