@@ -127,7 +127,8 @@ __device__ __forceinline__ void move_tokens(const EvictParams &p, const Head &h,
   const int64_t o = (word % (kLanes / 2)) * 16;
   int64_t src = -1, dst = -1;              // row indexes
   if (lane < n) {
-    const int to = hole_list[i0 + lane], from = mover_list[i0 + lane];
+    // (within the sequence in any case: see where the lists are written)
+    const int to = min((uint32_t)hole_list[i0 + lane], h.L - 1u), from = min((uint32_t)mover_list[i0 + lane], h.L - 1u);
     const int32_t *table = p.block_tables + (int64_t)h.row * p.max_blocks_per_seq;
     const int bf = __ldg(table + from / bs), bt = __ldg(table + to / bs);
     const float x = p.weights[h.base + from];
@@ -156,10 +157,11 @@ __device__ __forceinline__ void move_tokens(const EvictParams &p, const Head &h,
   }
 }
 
-template <int kLanes>
-__global__ void __launch_bounds__(kThreads, 2) evict_kernel(const EvictParams p, int cluster, int cached, int smem_list, int split) {
+// kCached: the keys fit in shared memory; else they are computed again in each phase.
+template <int kLanes, bool kCached>
+__global__ void __launch_bounds__(kThreads, 2) evict_kernel(const EvictParams p, int cluster, int smem_list, int split) {
   __shared__ __align__(16) Shared sh;
-  extern __shared__ __align__(16) uint32_t dynamic[];   // cached: this CTA's keys; smem_list: its list of moves
+  extern __shared__ __align__(16) uint32_t dynamic[];   // kCached: this CTA's keys; smem_list: its list of moves
   // launched as a programmatic dependent: nothing is read before what precedes it is complete
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -207,7 +209,7 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const EvictParams p,
   const int lo = min((int64_t)L, (int64_t)rank * kWarps * per_warp), hi = min((int64_t)L, lo + (int64_t)kWarps * per_warp);
   const int wlo = min(hi, lo + warp * per_warp), whi = min(hi, wlo + per_warp);
   auto key_of = [&](float x, int t) { return t < p.num_sinks || t >= seen - p.num_recent ? kProtected : weight_key(x); };
-  if (cached) {
+  if constexpr (kCached) {
 #pragma unroll 1
     for (int s0 = wlo + lane; s0 < whi; s0 += 4 * 32) {   // four slots' loads in flight
       float x[4];
@@ -226,7 +228,7 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const EvictParams p,
   }
   // the keys of slots s .. s + 3 (s from lo on in steps of 4; slots past the warp's: 0, which `own` tells apart)
   auto four_keys = [&](int s, uint32_t (&k)[4]) {
-    if (cached) {
+    if constexpr (kCached) {
       const uint4 x = *reinterpret_cast<const uint4 *>(dynamic + (s - lo));   // (past the warp's: unused)
       k[0] = x.x;
       k[1] = x.y;
@@ -405,6 +407,10 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const EvictParams p,
   }   // one CTA: the barrier before the counts did
   int32_t *hole_list = smem_list ? reinterpret_cast<int32_t *>(dynamic) + smem_list : list + 4;
   int32_t *mover_list = hole_list + p.list_cap;
+  // As many tokens move as slots are freed, at most list_cap.  Where keys are computed again that holds only while nobody
+  // changes the weights under the kernel (two sequences of one weights row, in place), and the lists are not left even then.
+  if constexpr (!kCached) moves = min(moves, (int)p.list_cap);
+  auto listed = [&](int i) { return kCached ? i : min(i, (int)p.list_cap - 1); };
   {
     int ties = tie0;
 #pragma unroll 1
@@ -417,8 +423,8 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const EvictParams p,
       int hi0 = hole0 + ((end - own) & 0xffff), mi0 = mover0 + ((end - own) >> 16);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        if (hole >> j & 1u) hole_list[hi0++] = s + j;
-        if (mover >> j & 1u) mover_list[mi0++] = s + j;
+        if (hole >> j & 1u) hole_list[listed(hi0++)] = s + j;
+        if (mover >> j & 1u) mover_list[listed(mi0++)] = s + j;
       }
       const int all = __shfl_sync(0xffffffffu, end, 31);
       hole0 += all & 0xffff;
@@ -468,10 +474,9 @@ __global__ void __launch_bounds__(kMoveWarps * 32) evict_move_kernel(const Evict
   move_tokens<kLanes>(p, head, list + 4, list + 4 + p.list_cap, i0, min(32, moves - i0));
 }
 
-template <int kLanes>
-cudaError_t launch_one(const EvictParams &p, int cluster, int cached, int smem, int smem_list, bool split,
-                       cudaStream_t s) {
-  cudaError_t e = ensure_smem_limit<evict_kernel<kLanes>>(kCachedKeys * 4 + kSmemMoves * 8);
+template <int kLanes, bool kCached>
+cudaError_t launch_one(const EvictParams &p, int cluster, int smem, int smem_list, bool split, cudaStream_t s) {
+  cudaError_t e = ensure_smem_limit<evict_kernel<kLanes, kCached>>(kCachedKeys * 4 + kSmemMoves * 8);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)((int64_t)p.num_seqs * p.num_kv_heads * cluster));
@@ -487,7 +492,7 @@ cudaError_t launch_one(const EvictParams &p, int cluster, int cached, int smem, 
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  if ((e = cudaLaunchKernelEx(&cfg, evict_kernel<kLanes>, p, cluster, cached, smem_list, (int)split)) != cudaSuccess || !split)
+  if ((e = cudaLaunchKernelEx(&cfg, evict_kernel<kLanes, kCached>, p, cluster, smem_list, (int)split)) != cudaSuccess || !split)
     return e;
   const int chunks = (int)((p.list_cap + kMoveWarps * 32 - 1) / (kMoveWarps * 32));
   const int64_t grid = (int64_t)p.num_seqs * p.num_kv_heads * chunks;
@@ -513,13 +518,14 @@ cudaError_t launch_lanes(const EvictParams &p, cudaStream_t s) {
   if (heads * cluster > 2147483647ll) return cudaErrorInvalidValue;
   // a CTA's slots: per_warp rounded up to 128, times the warps
   const int64_t slots = (((int64_t)p.max_seq_len + cluster * kWarps - 1) / (cluster * kWarps) + 127) / 128 * 128 * kWarps;
-  const int cached = slots <= kCachedKeys;
+  const bool cached = slots <= kCachedKeys;
   // the list of moves: behind the keys, 16 words in (an offset of 0 stands for the workspace)
   const int keys = cached ? (int)slots : 16;
   const bool split = heads * p.list_cap > kFusedMoves;
   const int smem_list = !split && cluster == 1 && p.list_cap <= kSmemMoves ? keys : 0;
   const int smem = smem_list ? (keys + 2 * (int)p.list_cap) * 4 : cached ? keys * 4 : 0;
-  return launch_one<kLanes>(p, cluster, cached, smem, smem_list, split, s);
+  return cached ? launch_one<kLanes, true>(p, cluster, smem, smem_list, split, s)
+                : launch_one<kLanes, false>(p, cluster, smem, smem_list, split, s);
 }
 
 }  // namespace

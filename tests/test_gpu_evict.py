@@ -171,3 +171,22 @@ def test_bad_metadata_is_reported_and_skipped():
     tables[0, :3] = c.num_blocks           # destinations out of range: reported, those rows stay
     pa.pa_evict(k, v, desc, tables, i32([100, 0, 0, 0]), 100, i32([100] * 4), i32([0] * 4), 50, 0, 0, w, p, w, p, i32([0] * 4), None, ws)
     assert pa.pa_get_device_error() == 4
+
+
+def test_two_sequences_of_one_weights_row():
+    """Not a meaningful call (the rows have to be distinct): whatever stays, every access is in range, and nothing else changes."""
+    for n, most in ((700, 700), (900, 400000)):      # keys in shared memory, and read again in every phase
+        c = Cache([n, n, n], 1, 64, 16, "fp8", 15)
+        k, v, tables, desc = c.device(pa)
+        i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+        w = torch.rand((3, 1, most), device="cuda")
+        p = torch.zeros((3, 1, most), dtype=torch.int32, device="cuda")
+        before, nl = w.clone(), i32([0] * 3)
+        ws = torch.empty(pa.pa_evict_workspace_bytes(3, 1, most, 300), dtype=torch.uint8, device="cuda")
+        pa.pa_evict(k, v, desc, tables, i32([n, n, 100]), most, i32([n, n, 100]), i32([0] * 3), 300, 4, 10, w, p, w, p, nl,
+                    i32([1, 1, 0]), ws)
+        assert pa.pa_get_device_error() in (0, 4)
+        assert nl.tolist() == [300, 300, 100]
+        assert torch.equal(w[0], before[0]) and torch.equal(w[2], before[2])
+        third = c.tables[2, :-(-n // 16)].long()      # its blocks (the entries behind them are out of range), on the CPU
+        assert torch.equal(k.cpu()[third], c.k[third]) and torch.equal(v.cpu()[third], c.v[third])
