@@ -453,7 +453,8 @@ PA_API pa_status pa_prefill_chunk_window(const void *q_chunk, pa_dtype q_dtype, 
  *   fresh_from   device int32 [num_seqs], or NULL for L - 1: tokens from there
  *                on have no running weight yet, and what weights holds for them
  *                is not read (0: the first decode after a prompt)
- *   decay        finite; 1 adds up, 0 keeps only this step's weights
+ *   decay        finite; 1 adds up, 0 keeps only this step's weights (weights is
+ *                not read then, and may hold anything)
  *   workspace    >= pa_decode_weights_workspace_bytes(...) bytes (it holds one
  *                fp32 score per query head and token), else as for pa_decode
  *   all other arguments as for pa_decode, seq_lens[i] <= max_seq_len included.

@@ -163,7 +163,8 @@ __device__ __forceinline__ void weights_cta(const FinishParams &p, int64_t block
     }
   };
   load(0);
-  const int fresh = p.fresh_from ? __ldg(p.fresh_from + row) : L - 1;
+  // (a decay of 0 reads no running weight: whatever it is, NaN included, nothing of it is kept)
+  const int fresh = p.decay == 0.f ? 0 : p.fresh_from ? __ldg(p.fresh_from + row) : L - 1;
 #pragma unroll
   for (int k = 0; k < kTokens; ++k) {
     const int t = first + k * kThreads + threadIdx.x;

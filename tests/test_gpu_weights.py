@@ -60,6 +60,24 @@ def test_decay_and_partitions(decay, ps):
     weights_case(LENS, 8, 2, 128, 16, "bf16", "bf16", seed=ps, ps=ps, decay=decay)
 
 
+def test_no_decayed_weight_is_read():
+    """decay 0: whatever stands for the running weights (NaN, infinities) leaves nothing behind."""
+    c = Cache([700, 33], 2, 128, 16, "bf16", 14)
+    k, v, tables, desc = c.device(pa)
+    q = torch.randn((2, 8, 128), generator=torch.Generator().manual_seed(2)).bfloat16().cuda()
+    lens = torch.tensor([700, 33], dtype=torch.int32, device="cuda")
+    fresh = torch.tensor([650, 33], dtype=torch.int32, device="cuda")
+    ws = torch.empty(pa.pa_decode_weights_workspace_bytes(2, 8, 2, 128, 700), dtype=torch.uint8, device="cuda")
+    got = []
+    for stale in (0.0, float("nan"), float("inf")):
+        w = torch.full((2, 2, 700), stale, device="cuda")
+        pa.pa_decode_weights(q, k, v, desc, tables, lens, 700, 0.09, torch.empty_like(q), w, None, fresh, 0.0, ws)
+        got.append([w[0].cpu(), w[1, :, :33].cpu()])
+    assert pa.pa_get_device_error() == 0
+    for g in got[1:]:
+        assert all(torch.equal(x, y) for x, y in zip(g, got[0]))
+
+
 def test_fresh_tokens():
     weights_case([40, 700, 130, 5], 8, 2, 128, 16, "bf16", "bf16", seed=3, fresh=[0, 300, 130, 4])
 
