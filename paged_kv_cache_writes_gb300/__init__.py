@@ -332,8 +332,10 @@ class _Args:
         """What the library cannot see: pools that hold what the descriptor says, an output of the queries' shape, a
         table row per sequence."""
         size = cache.num_blocks * cache.num_kv_heads * cache.block_size * cache.head_dim
-        if k_cache.numel() < size or v_cache.numel() < size:
-            raise ValueError("k_cache and v_cache must have the descriptor's shape")
+        if cache.kv_dtype != PA_FP8_E4M3:
+            size *= 2
+        if k_cache.nbytes < size or v_cache.nbytes < size:
+            raise ValueError("k_cache and v_cache must have the descriptor's shape and type")
         if q is not None and (q.shape != out.shape or q.shape[2] != cache.head_dim):
             raise ValueError("q and out must be [rows, num_q_heads, head_dim]")
         if len(block_tables) != n:

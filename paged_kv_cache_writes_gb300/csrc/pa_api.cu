@@ -513,6 +513,7 @@ pa_status bounded_layout(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_h
   b->parts = (int)parts;
   b->w = decode_workspace_layout(num_seqs, num_q_heads, head_dim, parts);
   b->score_stride = parts * b->ps;
+  if ((double)num_seqs * units * b->score_stride * b->rows >= 1e15) return PA_ERR_UNSUPPORTED;   // no size_t wraps
   b->scores_off = b->w.total;
   b->row_ml_off = b->scores_off + (weights ? (size_t)num_seqs * units * b->score_stride * b->rows * 4 : 0);
   b->total = b->row_ml_off + (weights ? round256((size_t)num_seqs * num_q_heads * 8) : 0);

@@ -135,6 +135,7 @@ def test_workspace_sizes(pa):
                 (4, 64, 8, 128, 16, 100, 0, 0), (4, 64, 8, 128, 16, 100, 10, -1), (4, 64, 8, 128, 24, 100, 10, 0)):
         assert pa.pa_decode_window_workspace_bytes(*bad) == 0
     assert pa.pa_decode_weights_workspace_bytes(4, 30, 8, 128, 100) == 0
+    assert pa.pa_decode_weights_workspace_bytes(60000, 30000, 30000, 128, 2 ** 31 - 1, 2 ** 31 - 32) == 0   # past 2^64 bytes
     assert pa.pa_evict_workspace_bytes(4, 8, 100, 0) == 0 and pa.pa_evict_workspace_bytes(4, 0, 100, 5) == 0
     assert pa.pa_evict_workspace_bytes(4, 8, 100, 200) > 0
 
@@ -149,6 +150,8 @@ def test_binding_checks(pa, monkeypatch):
         pa._Args.shapes(None, None, k, k[:3], d, torch.zeros((1, 4)), 1)
     with pytest.raises(ValueError, match="descriptor"):
         pa._Args.shapes(None, None, k[:3], k[:3], d, torch.zeros((1, 4)), 1)
+    with pytest.raises(ValueError, match="descriptor"):
+        pa._Args.shapes(None, None, k.to(torch.uint8), k.to(torch.uint8), d, torch.zeros((1, 4)), 1)   # a smaller type
     with pytest.raises(ValueError, match="q and out"):
         pa._Args.shapes(torch.zeros((1, 4, 64)), torch.zeros((2, 4, 64)), k, k, d, torch.zeros((1, 4)), 1)
     with pytest.raises(ValueError, match="one row"):
