@@ -413,6 +413,10 @@ __device__ __forceinline__ void prefill_tc_body(const PrefillTcParams &p, int bx
         const int key0 = j * kN + grp * kOwn;
         const int nvis = lim - key0, g0 = p.num_sinks - key0, g1 = row_low - key0;
         const bool full_tile = __all_sync(0xffffffffu, nvis >= kOwn && (g0 >= g1 || g0 >= kOwn || g1 <= 0));
+        // The last tile may hold fewer chunks of keys: what the others' columns hold is never a score.  (8 chunks of
+        // 2048, whose rows see eight tiles and 32 keys: 699 -> 619 us, with S of the last tile cut short likewise.  The
+        // second pass of fp8 caches has no register for the test: it spills, 44.4 -> 48 us for 5 ragged chunks.)
+        const int nch = kTwice && kFp8 ? kChunks : min(kChunks, (kv_end - key0 + 31) >> 5);
         float mx[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) mx[i] = kNegInf;
@@ -441,7 +445,7 @@ __device__ __forceinline__ void prefill_tc_body(const PrefillTcParams &p, int bx
         } else {
           if (!full_tile) {   // mask in place: the second pass then finds -inf
 #pragma unroll 1
-            for (int ck = 0; ck < kChunks; ++ck) {
+            for (int ck = 0; ck < nch; ++ck) {
               tmem_ld32_start(sb + 32 * ck, sv[0]);
               tmem_ld32_finish(sv[0]);
               mask(ck, sv[0]);
@@ -506,38 +510,40 @@ __device__ __forceinline__ void prefill_tc_body(const PrefillTcParams &p, int bx
 #pragma unroll
         for (int ck = 0; ck < kChunks; ++ck) {
           float (&v)[32] = sv[ck % kHeld];
-          if constexpr (kTwice) {
-            tmem_ld32_finish(v);
-            if (ck + 1 < kChunks) tmem_ld32_start(sb + 32 * (ck + 1), sv[(ck + 1) & 1]);
-          }
-#pragma unroll
-          for (int hh = 0; hh < 2; ++hh) {   // keys 32ck + 16hh .. +15
-            uint32_t w[8], wl[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const int i0 = 16 * hh + 2 * k;
-              const float2 a = ffma2(make_float2(v[i0], v[i0 + 1]), cc, nm);
-              const float2 pk = make_float2(fast_exp2(a.x), fast_exp2(a.y));
-              if constexpr (kBf16 && !kFp8 && !kLo) {   // rounded to bf16, the sum that of the rounded P
-                uint32_t hw;
-                asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(hw) : "f"(pk.y), "f"(pk.x));
-                w[k] = hw;
-                lacc[k & 3] = ffma2(make_float2(__uint_as_float(hw << 16), __uint_as_float(hw & 0xffff0000u)), ones, lacc[k & 3]);
-              } else if constexpr (kSplit) {   // hi + lo, as in the other kernel
-                uint32_t hw, lw2;
-                asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(hw) : "f"(pk.y), "f"(pk.x));
-                w[k] = hw;
-                const float2 lo = ffma2(make_float2(__uint_as_float(hw << 16), __uint_as_float(hw & 0xffff0000u)),
-                                        make_float2(-1.f, -1.f), pk);
-                asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(lw2) : "f"(lo.y), "f"(lo.x));
-                wl[k] = lw2;
-                lacc[k & 3] = ffma2(pk, ones, lacc[k & 3]);
-              } else {
-                w[k] = f16x2_rn_add(pk.x, pk.y, lacc[k & 3]);
-              }
+          if (ck < nch) {
+            if constexpr (kTwice) {
+              tmem_ld32_finish(v);
+              if (ck + 1 < nch) tmem_ld32_start(sb + 32 * (ck + 1), sv[(ck + 1) & 1]);
             }
-            tmem_st8(sb + 32 * ck + 16 * hh, w);
-            if constexpr (kSplit) tmem_st8(sb + 32 * ck + 16 * hh + 8, wl);
+#pragma unroll
+            for (int hh = 0; hh < 2; ++hh) {   // keys 32ck + 16hh .. +15
+              uint32_t w[8], wl[8];
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                const int i0 = 16 * hh + 2 * k;
+                const float2 a = ffma2(make_float2(v[i0], v[i0 + 1]), cc, nm);
+                const float2 pk = make_float2(fast_exp2(a.x), fast_exp2(a.y));
+                if constexpr (kBf16 && !kFp8 && !kLo) {   // rounded to bf16, the sum that of the rounded P
+                  uint32_t hw;
+                  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(hw) : "f"(pk.y), "f"(pk.x));
+                  w[k] = hw;
+                  lacc[k & 3] = ffma2(make_float2(__uint_as_float(hw << 16), __uint_as_float(hw & 0xffff0000u)), ones, lacc[k & 3]);
+                } else if constexpr (kSplit) {   // hi + lo, as in the other kernel
+                  uint32_t hw, lw2;
+                  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(hw) : "f"(pk.y), "f"(pk.x));
+                  w[k] = hw;
+                  const float2 lo = ffma2(make_float2(__uint_as_float(hw << 16), __uint_as_float(hw & 0xffff0000u)),
+                                          make_float2(-1.f, -1.f), pk);
+                  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(lw2) : "f"(lo.y), "f"(lo.x));
+                  wl[k] = lw2;
+                  lacc[k & 3] = ffma2(pk, ones, lacc[k & 3]);
+                } else {
+                  w[k] = f16x2_rn_add(pk.x, pk.y, lacc[k & 3]);
+                }
+              }
+              tmem_st8(sb + 32 * ck + 16 * hh, w);
+              if constexpr (kSplit) tmem_st8(sb + 32 * ck + 16 * hh + 8, wl);
+            }
           }
           if (ck == kChunks - 1 || (kGroups == 1 && ck == 1)) {   // a half of the tile is written
             tmem_wait_st();
@@ -1068,6 +1074,7 @@ __device__ __forceinline__ void prefill_tc_body(const PrefillTcParams &p, int bx
       // in, once that P.V is complete.  Keys past kv_end take part up to the end of their group of 16.
       const bool leader = elect_one();
       const uint32_t idesc_s = umma_idesc(kAB, kN, false);
+      const uint32_t idesc_last = umma_idesc(kAB, (kv_end - (nkt - 1) * kN + 15) & ~15, false);   // the last tile's keys
       const uint32_t idesc_o = umma_idesc(kAB, kD, true);
       const uint32_t kv_k = smem_u32(smem + L::kOffK), kv_v = smem_u32(smem + L::kOffV);
       const uint64_t qdesc = umma_desc(smem_u32(smem + L::kOffQ), 16);
@@ -1081,11 +1088,12 @@ __device__ __forceinline__ void prefill_tc_body(const PrefillTcParams &p, int bx
       bool issued = false;
       auto issue_s = [&](int j) {   // S(j), its K tile waited for
         const uint64_t kd = kdesc0 + (((j % kStages) * kTileBytes) >> 4);
+        const uint32_t idesc = j == nkt - 1 ? idesc_last : idesc_s;
         if (leader) {
 #pragma unroll 1
           for (int k = 0; k < kD / 16; ++k)
             umma(sbuf(0, j % kBufs), qdesc + (((k >> 2) * (kM * 128) + (k & 3) * 32) >> 4),
-                 kd + (((k >> 2) * kKPanel + (k & 3) * 32) >> 4), idesc_s, k > 0 ? 1u : 0u);
+                 kd + (((k >> 2) * kKPanel + (k & 3) * 32) >> 4), idesc, k > 0 ? 1u : 0u);
           umma_commit(&s_full[j % kBufs]);
           umma_commit(&k_free[j % kStages]);
         }

@@ -176,6 +176,14 @@ def test_chunk_two_tiles_per_cta(qt, kv, d):
     chunk_case([(200, 900), (0, 1000), (37, 513)], 32, 8, d, 16, qt, kv, 250, 9, seed=d)
 
 
+@pytest.mark.parametrize("qt,kv,out", [("bf16", "bf16", "f32"), ("bf16", "bf16", "bf16"), ("f16", "f16", "f32"), ("bf16", "fp8", "f32")])
+@pytest.mark.parametrize("d,hkv", [(128, 2), (128, 8), (64, 8)])
+def test_chunk_last_tiles_of_every_length(qt, kv, out, d, hkv):
+    # the last tile's keys: 1 to 128, with few CTAs and with two per SM; what an earlier launch left behind them is no score
+    ends = [1, 15, 16, 17, 31, 32, 33, 47, 48, 63, 64, 65, 79, 80, 96, 97, 111, 112, 113, 127, 128, 129, 144, 161]
+    chunk_case([(max(0, n - 9), min(n, 9)) for n in ends], 2 * hkv, hkv, d, 16, qt, kv, 100, 3, seed=d + hkv, out=out)
+
+
 @pytest.mark.parametrize("out", ["bf16", "f32"])
 def test_chunk_output_types_and_negative_scale(out):
     chunk_case(CHUNKS, 8, 2, 128, 16, "bf16", "bf16", 64, 4, seed=3, out=out, scale=-0.05)
