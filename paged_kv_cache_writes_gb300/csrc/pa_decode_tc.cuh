@@ -44,7 +44,8 @@
 // 32 keys or elements per MMA), so a tile goes from the bulk copy to the
 // MMAs untouched.  The other operand is then e4m3 too, as a sum of terms:
 // 256 p is written as hi + lo / 16 (hi in rows 0..G-1 of P^T, lo in rows
-// G..2G-1), which holds it to 2^-8 of itself; the query rows, scaled by a
+// G..2G-1), which holds it to 2^-8 of itself (the bounded-cache decodes of
+// f16 queries add a third term, to 2^-12); the query rows, scaled by a
 // power of two 2^e per unit (|q| 2^e in [128, 256) at the unit's largest
 // element), likewise as hi + lo / 16 for bf16 queries and as hi + mid / 16 +
 // lo / 256 in rows 0..3G-1 for f16 queries: either holds every query element
@@ -244,6 +245,14 @@ struct QTerms {
   static constexpr int value = !std::is_same<KV, uint8_t>::value ? 1 : std::is_same<QT, __half>::value ? 3 : 2;
 };
 
+// e4m3 terms per probability with an fp8 cache: two hold 8 significant bits;
+// the bounded-cache decodes of f16 queries, whose output has 11, take three
+// (with two its error against 64 bits is 2.2 times that of its own rounding).
+template <typename QT, bool kExt>
+struct PTerms {
+  static constexpr int value = kExt && std::is_same<QT, __half>::value ? 3 : 2;
+};
+
 // Shared-memory and tensor-memory geometry.  16-bit caches: K/V tiles of
 // 32 KB (two 128-byte panels per 8-key atom), Q^T of 16 rows (the heads,
 // padded) and P^T of kNO rows, each in two 64-element panels.  fp8 caches:
@@ -251,16 +260,16 @@ struct QTerms {
 // KB of 64-byte rows with the 64-byte swizzle for head_dim 64: the layouts a
 // 2D bulk-tensor box writes), Q^T of head_dim-byte rows in the same swizzle
 // and P^T of one 128-key panel, holding the hi terms in rows 0..G-1, the lo
-// terms in rows G..2G-1 (and with three query terms, the last in rows
-// 2G..3G-1 of Q^T).
-template <int G, bool kSplit, bool kFp8, int kQTerms = 1, int D = 128>
+// terms in rows G..2G-1 (and with three terms, the last in rows 2G..3G-1 of
+// Q^T or P^T).
+template <int G, bool kSplit, bool kFp8, int kQTerms = 1, int D = 128, int kPTerms = 2>
 struct TcGeo {
   static_assert(G == 4 || G == 8 || G == 16, "4, 8 or 16 query heads per KV head");
   static_assert(D == 128 || D == 64, "head_dim 128 or 64");
   static constexpr int kPanels = D / 64;                            // 128-byte panels of a 16-bit row
   static constexpr int kAtom = 8 * 2 * D;                           // 8 keys of a 16-bit tile (all panels)
-  static constexpr int kPRows = (kSplit || kFp8) ? 2 * G : G;       // P^T rows in use
-  static constexpr int kNO = kPRows <= 16 ? 16 : 32;                // O^T columns (MMA N)
+  static constexpr int kPRows = kFp8 ? kPTerms * G : kSplit ? 2 * G : G;   // P^T rows in use
+  static constexpr int kNO = kPRows <= 16 ? 16 : (kPRows + 15) / 16 * 16;   // O^T columns (MMA N)
   static constexpr int kQRows = kQTerms * G;                        // Q^T rows in use
   static constexpr int kNS = kQRows <= 16 ? 16 : (kQRows + 15) / 16 * 16;   // S^T columns per tile (MMA N)
   static constexpr int kSCols = kFp8 ? kNS : G;                     // S^T columns read per tile
@@ -431,11 +440,12 @@ __device__ __forceinline__ void decode_tc_body(const DecodeTcParams &tp, const C
   constexpr int kThreads = Roles::threads_for(NL, kSepMerge), kLoadWarp1 = Roles::kLoadWarp1;
   constexpr int kMerge2Warp = Roles::merge2_warp(NL);   // with kSepMerge: merges only
   // MMA operands: the cache's type (bf16 / f16 with a 16-bit cache, the queries
-  // in the same type; e4m3 with an fp8 cache, the queries and P as two e4m3 terms)
+  // in the same type; e4m3 with an fp8 cache, the queries and P as two or three e4m3 terms)
   constexpr bool kBf16 = std::is_same<QT, __nv_bfloat16>::value && !kFp8;
   constexpr bool kSplit = split_p<KV, QT, kExt>();   // 16-bit caches: P as hi + lo
   constexpr int kQTerms = QTerms<KV, QT>::value;
-  using GE = TcGeo<G, kSplit, kFp8, kQTerms, D>;
+  constexpr int kPTerms = PTerms<QT, kExt>::value;
+  using GE = TcGeo<G, kSplit, kFp8, kQTerms, D, kPTerms>;
   // The MMA warp consumes the ring in order, so a loader's wait for the consumption of
   // position g - S is never two phases behind while it has NL <= S positions in hand.
   static_assert(GE::kSlots >= NL, "at least as many ring slots as loaders (parity waits stay within one phase)");
@@ -754,7 +764,7 @@ __device__ __forceinline__ void decode_tc_body(const DecodeTcParams &tp, const C
       // P^T of this unit (its buffer's previous reader, P.V of unit u-2, finished
       // before the epilogue of u-2, which ran in the previous iteration)
       if (cur.valid && kFp8) {
-        // 256 p = hi + lo / 16 in e4m3, key tid's byte of rows h and G + h
+        // 256 p = hi + lo / 16 (+ lo2 / 256) in e4m3, key tid's byte of rows h, G + h (and 2G + h)
 #pragma unroll
         for (int h = 0; h < G; ++h) l_part[h] = 0.f;
         uint8_t *pb = smem + GE::kOffP + b * kMaxTiles * GE::kPBytes + (tid & 15);
@@ -767,13 +777,18 @@ __device__ __forceinline__ void decode_tc_body(const DecodeTcParams &tp, const C
             const float msub0 = m_cur[h] == kNegInf ? 0.f : m_cur[h];
             const float msub1 = m_cur[h + 1] == kNegInf ? 0.f : m_cur[h + 1];
             const float p0 = fast_exp2(t[j][h] - msub0), p1 = fast_exp2(t[j][h + 1] - msub1);
-            uint32_t hi, lo;
-            split2_e4m3(make_float2(p0 * 256.f, p1 * 256.f), hi, lo);
+            uint32_t hi, lo, lo2 = 0;
+            if constexpr (kPTerms == 3) split3_e4m3(make_float2(p0 * 256.f, p1 * 256.f), hi, lo, lo2);
+            else split2_e4m3(make_float2(p0 * 256.f, p1 * 256.f), hi, lo);
             auto put = [&](int row, uint32_t code) { pt[row * 128 + (((tid >> 4) ^ (row & 7)) << 4)] = (uint8_t)code; };
             put(h, hi);
             put(h + 1, hi >> 8);
             put(G + h, lo);
             put(G + h + 1, lo >> 8);
+            if constexpr (kPTerms == 3) {
+              put(2 * G + h, lo2);
+              put(2 * G + h + 1, lo2 >> 8);
+            }
             l_part[h] += p0;
             l_part[h + 1] += p1;
           }
@@ -836,9 +851,12 @@ __device__ __forceinline__ void decode_tc_body(const DecodeTcParams &tp, const C
         const int gr = ph.n;
         const int64_t head0 = (int64_t)prev.row * hq + ph.h0;
         const int d = tid;            // with head_dim 64, lanes 64..127 repeat 0..63: not stored
-        // the two column halves of O^T: bf16 p = hi + lo; fp8 256 p = hi + lo / 16
+        // the two column halves of O^T (or three thirds): bf16 p = hi + lo; fp8 256 p = hi + lo / 16 (+ lo2 / 256)
         auto o_val = [&](int h) {
-          return kSplit ? o[h] + o[G + h] : kFp8 ? fmaf(o[G + h], 0.0625f, o[h]) * (1.f / 256.f) : o[h];
+          if constexpr (kFp8 && kPTerms == 3)
+            return fmaf(fmaf(o[2 * G + h], 0.0625f, o[G + h]), 0.0625f, o[h]) * (1.f / 256.f);
+          else
+            return kSplit ? o[h] + o[G + h] : kFp8 ? fmaf(o[G + h], 0.0625f, o[h]) * (1.f / 256.f) : o[h];
         };
         if (prev.nparts == 1) {
 #pragma unroll
@@ -1608,7 +1626,8 @@ cudaError_t launch_decode_tc_plan(const DecodeTcParams &tp, cudaStream_t s) {
 template <typename KV, typename QT, int G, int D, bool kPadRows, bool kExt = false>
 cudaError_t launch_decode_tc_one(const DecodeTcParams &p, const PoolMaps &m, cudaStream_t s) {
   constexpr int smem =
-      dtc::TcGeo<G, dtc::split_p<KV, QT, kExt>(), std::is_same<KV, uint8_t>::value, dtc::QTerms<KV, QT>::value, D>::kSmemBytes;
+      dtc::TcGeo<G, dtc::split_p<KV, QT, kExt>(), std::is_same<KV, uint8_t>::value, dtc::QTerms<KV, QT>::value, D,
+                 dtc::PTerms<QT, kExt>::value>::kSmemBytes;
   cudaError_t e = cudaSuccess;
   if (!(kExt && p.direct) && (e = launch_decode_tc_plan<kExt>(p, s)) != cudaSuccess) return e;
   if ((e = ensure_smem_limit<decode_tc_kernel<KV, QT, G, D, kPadRows, kExt>>(smem)) != cudaSuccess) return e;

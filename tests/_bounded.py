@@ -103,7 +103,7 @@ def visible(t, n, window, sinks):
     return (p <= t) & ((p < sinks) | (p > t - window))
 
 
-def attend(q, k, v, seen, scale, kv, out, prefill=False):
+def attend(q, k, v, seen, scale, kv, out, prefill=False, p_terms=2):
     """q [r, hq, d] (the stored values), k and v [hkv, n, d] in 64 bits, seen [r, n].  Returns (out [r, hq, d],
     bound on |kernel - out|, weights [r, hq, n], relative bound of the weights [r, hq])."""
     r, hq, d = q.shape
@@ -131,6 +131,8 @@ def attend(q, k, v, seen, scale, kv, out, prefill=False):
         rel, low = rel + (2.0 ** -15 if not prefill else 2.0 ** -7 if out == "bf16" else 2.0 ** -16), 0.0
     elif kv == "f16" or prefill:
         rel, low = rel + 2.0 ** -10, count * 2.0 ** -25 * vmax
+    elif p_terms == 3:   # 256 p in three e4m3 terms: within 2^-12 of it, or 2^-18 where it is small
+        rel, low = rel + 2.0 ** -12, count * 2.0 ** -26 * vmax
     else:
         rel, low = rel + 2.0 ** -8, count * 2.0 ** -22 * vmax
     bound = rel * big + low

@@ -36,7 +36,8 @@ def weights_case(lens, hq, hkv, d, bs, qt, kv, seed=0, out="f32", ps=0, decay=1.
         if m == 0:
             assert (o[i] == 0).all()
             continue
-        ref, bound, a, rel = attend(q[i:i + 1], c.rows("k", i, m), c.rows("v", i, m), torch.ones((1, m), dtype=bool), d ** -0.5, kv, out)
+        ref, bound, a, rel = attend(q[i:i + 1], c.rows("k", i, m), c.rows("v", i, m), torch.ones((1, m), dtype=bool), d ** -0.5, kv, out,
+                                     p_terms=3 if qt == "f16" else 2)
         check(o[i:i + 1], ref, bound, f"output of sequence {i}")
         a, rel = a[0].view(hkv, hq // hkv, m), rel[0].view(hkv, hq // hkv, 1)
         before = torch.where(torch.arange(m) < start[i], old[at[i], :, :m].double() * decay, 0.0)

@@ -35,7 +35,7 @@ def decode_case(lens, hq, hkv, d, bs, qt, kv, window, sinks, seed=0, out="f32", 
     want = []
     for i, n in enumerate(lens):
         seen = visible(n - 1, n, window, sinks)
-        want.append(attend(q[i:i + 1], c.rows("k", i, n), c.rows("v", i, n), seen[None], scale, kv, out))
+        want.append(attend(q[i:i + 1], c.rows("k", i, n), c.rows("v", i, n), seen[None], scale, kv, out, p_terms=3 if qt == "f16" else 2))
         c.poison(i, ~seen)
     o = decode(c, q, window, sinks, scale, out, ps)
     for i in range(len(lens)):
