@@ -1367,10 +1367,9 @@ cudaError_t launch_prefill_window_one(const PrefillTcParams &p0, const PoolMaps 
   const int64_t gx = (int64_t)num_chunks * p.row_blocks, gy = (int64_t)p.num_kv_heads * p.shares;
   if (gx > 2147483647ll || gy > 65535) return cudaErrorInvalidValue;
   const dim3 grid((unsigned)gx, (unsigned)gy);
-  // one CTA per SM while that is all there is
   constexpr bool kBf16Cache = std::is_same<KV, __nv_bfloat16>::value;
-  // One CTA per SM while that is all there is: a 512-token chunk of 32/8 heads (128 CTAs) 17.5 us, as pairs 21.9;
-  // beyond that pairs: 8 chunks of 2048, 64/8 heads (8192 CTAs), 0.70 ms, one CTA per SM 0.87.
+  // One CTA per SM while that is all there is: a 512-token chunk of 32/8 heads (128 CTAs) 17.2 us, as pairs 20.1;
+  // beyond that pairs: 8 chunks of 2048, 64/8 heads (8192 CTAs), 0.61 ms, one CTA per SM 0.86.
   const bool pair = gx * gy > num_sms;
   if (kBf16Cache && !p.out_f32)
     return pair ? launch_prefill_window_tiles<KV, QT, D, true, !kBf16Cache>(p, m, grid, s)
