@@ -178,6 +178,9 @@ pa_status pa_bm_append(pa_block_manager *bm, int32_t seq, int32_t num_tokens, co
     cow_pairs[0] = src;
     cow_pairs[1] = dst;
     *num_cow = 1;
+  } else if (off != 0 && num_tokens > 0) {
+    // a partly filled block still has a name if it was truncated while other sequences held it, and they are gone now
+    bm->forget(s.blocks.back());
   }
   int32_t t = 0;
   while (t < num_tokens) {
@@ -273,7 +276,7 @@ pa_status pa_bm_truncate(pa_block_manager *bm, int32_t seq, int32_t new_len) {
   s.blocks.resize(n);
   s.len = new_len;
   // the kept part of a full block will be written behind: it is no longer the block its hash names
-  // (a shared one is copied before that write, and keeps its name)
+  // (a shared one keeps its name: pa_bm_append copies it before that write or, if it is no longer shared by then, forgets it)
   if (new_len % bs && bm->ref[s.blocks[n - 1]] == 1) bm->forget(s.blocks[n - 1]);
   s.chain = 0;
   s.chain_known = new_len == 0;
