@@ -510,7 +510,9 @@ PA_API pa_status pa_decode_weights(const void *q, pa_dtype q_dtype, int32_t num_
  *   workspace    device, >= pa_evict_workspace_bytes(...) bytes, 256-byte
  *                aligned; its contents on entry are ignored
  * A sequence whose metadata is out of range sets PA_ERR_DEVICE_CHECK and is
- * left as it is; so is a move whose block id is out of range.
+ * left as it is (new_seq_lens[i] = L).  A move with a block id out of range, of
+ * its source or its destination, sets it too and is not made: the destination
+ * keeps its own token, with that token's weight and position in the new arrays.
  */
 PA_API size_t pa_evict_workspace_bytes(int32_t num_seqs, int32_t num_kv_heads, int32_t max_seq_len, int32_t budget);
 PA_API pa_status pa_evict(void *k_cache, void *v_cache, const pa_kv_cache *cache, int32_t num_seqs,

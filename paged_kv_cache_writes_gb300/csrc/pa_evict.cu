@@ -131,16 +131,20 @@ __device__ __forceinline__ void move_tokens(const EvictParams &p, const Head &h,
     const int to = min((uint32_t)hole_list[i0 + lane], h.L - 1u), from = min((uint32_t)mover_list[i0 + lane], h.L - 1u);
     const int32_t *table = p.block_tables + (int64_t)h.row * p.max_blocks_per_seq;
     const int bf = __ldg(table + from / bs), bt = __ldg(table + to / bs);
-    const float x = p.weights[h.base + from];
-    const int t = from < h.old ? p.positions[h.base + from] : h.seen - h.L + from;
-    p.new_weights[h.base + to] = x;
-    p.new_positions[h.base + to] = t;
+    float x = p.weights[h.base + from];
+    auto position = [&](int s) { return s < h.old ? p.positions[h.base + s] : h.seen - h.L + s; };
+    int t = position(from);
     if (bf < 0 || bt < 0 || bf >= p.num_blocks || bt >= p.num_blocks) {
+      // refused: the slot keeps its own token, and so that token's weight and position (in a slot that nothing else writes)
       record_error(p.err, PA_ERR_DEVICE_CHECK);
+      x = p.weights[h.base + to];
+      t = position(to);
     } else {
       src = ((int64_t)bf * p.num_kv_heads + h.g) * bs + from % bs;
       dst = ((int64_t)bt * p.num_kv_heads + h.g) * bs + to % bs;
     }
+    p.new_weights[h.base + to] = x;
+    p.new_positions[h.base + to] = t;
   }
   for (int j0 = 0; j0 < n; j0 += kPer * kDeep) {
     uint4 x[kDeep];
