@@ -205,8 +205,13 @@ __device__ __forceinline__ void weights_cta(const FinishParams &p, int64_t block
   }
 }
 
+// CTAs per SM that the registers allow.  A weights CTA is bound by its loads: more CTAs help a batch while the scores that
+// a thread holds (kTokens * G) fit.  Both launches, at 4 against 2 per SM: 64 sequences of 100 to 8192 tokens G = 4 204 /
+// 212 us, G = 8 230 / 234, G = 16 319 (it spills 376 bytes) / 299; 2 sequences of 8000 18.4 / 17.5, 22.3 / 20.2, 38 / 28.
+constexpr int finish_ctas(int g) { return g == 16 ? 2 : 4; }
+
 template <int G, int D>
-__global__ void __launch_bounds__(kThreads, 4) decode_finish_kernel(const FinishParams p) {
+__global__ void __launch_bounds__(kThreads, finish_ctas(G)) decode_finish_kernel(const FinishParams p) {
   extern __shared__ __align__(16) float smem[];
   // launched as the decode's programmatic dependent
   asm volatile("griddepcontrol.wait;" ::: "memory");
