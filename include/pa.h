@@ -384,6 +384,11 @@ PA_API pa_status pa_mixed_step(const pa_decode_part *decode, const pa_prefill_pa
  * Eviction by accumulated attention weight (pa_decode_weights, pa_evict): the
  * decode adds up what each cached token received, and from time to time the
  * cache goes back to a budget, keeping the tokens that received most.
+ *
+ * Precision.  Scores, softmax maxima and sums and all accumulations are fp32;
+ * the softmax weights meet V in the tensor cores' operand type.  The decodes
+ * hold a weight there to 2^-15 of itself with a bf16 cache and 2^-22 with an f16
+ * one; with an fp8 cache to 2^-8 for a bf16 output, 2^-12 for any other.
  */
 
 /*

@@ -44,8 +44,8 @@
 // 32 keys or elements per MMA), so a tile goes from the bulk copy to the
 // MMAs untouched.  The other operand is then e4m3 too, as a sum of terms:
 // 256 p is written as hi + lo / 16 (hi in rows 0..G-1 of P^T, lo in rows
-// G..2G-1), which holds it to 2^-8 of itself (the bounded-cache decodes of
-// f16 queries add a third term, to 2^-12); the query rows, scaled by a
+// G..2G-1), which holds it to 2^-8 of itself (the bounded-cache decodes add a
+// third term for an f16 or fp32 output, to 2^-12); the query rows, scaled by a
 // power of two 2^e per unit (|q| 2^e in [128, 256) at the unit's largest
 // element), likewise as hi + lo / 16 for bf16 queries and as hi + mid / 16 +
 // lo / 256 in rows 0..3G-1 for f16 queries: either holds every query element
@@ -245,13 +245,10 @@ struct QTerms {
   static constexpr int value = !std::is_same<KV, uint8_t>::value ? 1 : std::is_same<QT, __half>::value ? 3 : 2;
 };
 
-// e4m3 terms per probability with an fp8 cache: two hold 8 significant bits;
-// the bounded-cache decodes of f16 queries, whose output has 11, take three
-// (with two its error against 64 bits is 2.2 times that of its own rounding).
-template <typename QT, bool kExt>
-struct PTerms {
-  static constexpr int value = kExt && std::is_same<QT, __half>::value ? 3 : 2;
-};
+// e4m3 terms per probability with an fp8 cache (kPTerms of the kernels): two
+// hold 8 significant bits, as many as a bf16 output; the bounded-cache decodes
+// take three, 12 bits, for an f16 or fp32 output (with two the error of an f16
+// output against 64 bits is 2.2 times that of its own rounding).
 
 // Shared-memory and tensor-memory geometry.  16-bit caches: K/V tiles of
 // 32 KB (two 128-byte panels per 8-key atom), Q^T of 16 rows (the heads,
@@ -428,7 +425,7 @@ __device__ __forceinline__ int32_t query_scale_bits(float amax) {
 // kExt: a sliding window with first tokens that stay visible, groups cut into
 // shares, and the scores written out (the bounded-cache decodes).
 template <typename KV, typename QT, int G, int D = 128, int NL = 1, bool kSepMerge = false, bool kPadRows = false,
-          bool kExt = false>
+          bool kExt = false, int kPTerms = 2>
 __device__ __forceinline__ void decode_tc_body(const DecodeTcParams &tp, const CUtensorMap *tmap_k,
                                                const CUtensorMap *tmap_v) {
   using namespace tc;
@@ -444,7 +441,6 @@ __device__ __forceinline__ void decode_tc_body(const DecodeTcParams &tp, const C
   constexpr bool kBf16 = std::is_same<QT, __nv_bfloat16>::value && !kFp8;
   constexpr bool kSplit = split_p<KV, QT, kExt>();   // 16-bit caches: P as hi + lo
   constexpr int kQTerms = QTerms<KV, QT>::value;
-  constexpr int kPTerms = PTerms<QT, kExt>::value;
   using GE = TcGeo<G, kSplit, kFp8, kQTerms, D, kPTerms>;
   // The MMA warp consumes the ring in order, so a loader's wait for the consumption of
   // position g - S is never two phases behind while it has NL <= S positions in hand.
@@ -1534,11 +1530,12 @@ __device__ __forceinline__ void decode_tc_body(const DecodeTcParams &tp, const C
   }
 }
 
-template <typename KV, typename QT, int G, int D, bool kPadRows, bool kExt>
+template <typename KV, typename QT, int G, int D, bool kPadRows, bool kExt, int kPTerms>
 __global__ void __launch_bounds__(dtc::Roles::threads_for(dtc::Roles::loaders(G), dtc::Roles::sep_merge(G)), 1)
     decode_tc_kernel(const DecodeTcParams tp, const __grid_constant__ CUtensorMap tmap_k,
                      const __grid_constant__ CUtensorMap tmap_v) {
-  decode_tc_body<KV, QT, G, D, dtc::Roles::loaders(G), dtc::Roles::sep_merge(G), kPadRows, kExt>(tp, &tmap_k, &tmap_v);
+  decode_tc_body<KV, QT, G, D, dtc::Roles::loaders(G), dtc::Roles::sep_merge(G), kPadRows, kExt, kPTerms>(tp, &tmap_k,
+                                                                                                     &tmap_v);
 }
 
 // One CTA: count the split rows' merges and clear the merge list, and list
@@ -1623,14 +1620,14 @@ cudaError_t launch_decode_tc_plan(const DecodeTcParams &tp, cudaStream_t s) {
   return cudaLaunchKernelEx(&cfg, decode_tc_plan_kernel<kExt>, tp);
 }
 
-template <typename KV, typename QT, int G, int D, bool kPadRows, bool kExt = false>
+template <typename KV, typename QT, int G, int D, bool kPadRows, bool kExt = false, int kPTerms = 2>
 cudaError_t launch_decode_tc_one(const DecodeTcParams &p, const PoolMaps &m, cudaStream_t s) {
   constexpr int smem =
       dtc::TcGeo<G, dtc::split_p<KV, QT, kExt>(), std::is_same<KV, uint8_t>::value, dtc::QTerms<KV, QT>::value, D,
-                 dtc::PTerms<QT, kExt>::value>::kSmemBytes;
+                 kPTerms>::kSmemBytes;
   cudaError_t e = cudaSuccess;
   if (!(kExt && p.direct) && (e = launch_decode_tc_plan<kExt>(p, s)) != cudaSuccess) return e;
-  if ((e = ensure_smem_limit<decode_tc_kernel<KV, QT, G, D, kPadRows, kExt>>(smem)) != cudaSuccess) return e;
+  if ((e = ensure_smem_limit<decode_tc_kernel<KV, QT, G, D, kPadRows, kExt, kPTerms>>(smem)) != cudaSuccess) return e;
   int sms = 0;
   if ((e = current_sm_count(&sms)) != cudaSuccess) return e;
   if (kExt && p.direct) sms = (int)std::min<int64_t>(sms, (int64_t)p.d.num_seqs * p.d.max_partitions * p.d.num_kv_heads * p.shares);
@@ -1645,7 +1642,7 @@ cudaError_t launch_decode_tc_one(const DecodeTcParams &p, const PoolMaps &m, cud
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, decode_tc_kernel<KV, QT, G, D, kPadRows, kExt>, p, m.k, m.v);
+  return cudaLaunchKernelEx(&cfg, decode_tc_kernel<KV, QT, G, D, kPadRows, kExt, kPTerms>, p, m.k, m.v);
 }
 
 // m: tensor maps over the pools, one box per cache block of one KV head: 16-bit
@@ -1673,19 +1670,28 @@ cudaError_t launch_decode_tc(const DecodeTcParams &p, int gqa, int head_dim, con
 
 // The bounded-cache decodes (kExt): every group size, a share of at most 16
 // (head_dim 64: 8) query heads per unit, run padded to 4, 8 or 16 rows.
-template <typename KV, typename QT>
-cudaError_t launch_decode_ext(const DecodeTcParams &p, int head_dim, const PoolMaps &m, cudaStream_t s) {
+template <typename KV, typename QT, int kPTerms>
+cudaError_t launch_decode_ext_terms(const DecodeTcParams &p, int head_dim, const PoolMaps &m, cudaStream_t s) {
   switch (decode_ext_rows(p.share_heads)) {
     case 4:
-      return head_dim == 64 ? launch_decode_tc_one<KV, QT, 4, 64, true, true>(p, m, s)
-                            : launch_decode_tc_one<KV, QT, 4, 128, true, true>(p, m, s);
+      return head_dim == 64 ? launch_decode_tc_one<KV, QT, 4, 64, true, true, kPTerms>(p, m, s)
+                            : launch_decode_tc_one<KV, QT, 4, 128, true, true, kPTerms>(p, m, s);
     case 8:
-      return head_dim == 64 ? launch_decode_tc_one<KV, QT, 8, 64, true, true>(p, m, s)
-                            : launch_decode_tc_one<KV, QT, 8, 128, true, true>(p, m, s);
+      return head_dim == 64 ? launch_decode_tc_one<KV, QT, 8, 64, true, true, kPTerms>(p, m, s)
+                            : launch_decode_tc_one<KV, QT, 8, 128, true, true, kPTerms>(p, m, s);
     case 16:
-      if (head_dim == 128) return launch_decode_tc_one<KV, QT, 16, 128, true, true>(p, m, s);
+      if (head_dim == 128) return launch_decode_tc_one<KV, QT, 16, 128, true, true, kPTerms>(p, m, s);
   }
   return cudaErrorInvalidValue;
+}
+
+template <typename KV, typename QT>
+cudaError_t launch_decode_ext(const DecodeTcParams &p, int head_dim, const PoolMaps &m, cudaStream_t s) {
+  constexpr bool kFp8 = std::is_same<KV, uint8_t>::value;
+  if constexpr (kFp8 && std::is_same<QT, __nv_bfloat16>::value) {   // a bf16 output has no more than two terms' bits
+    if (!p.d.out_f32) return launch_decode_ext_terms<KV, QT, 2>(p, head_dim, m, s);
+  }
+  return launch_decode_ext_terms<KV, QT, kFp8 ? 3 : 2>(p, head_dim, m, s);
 }
 
 }  // namespace pa
