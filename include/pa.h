@@ -388,7 +388,11 @@ PA_API pa_status pa_mixed_step(const pa_decode_part *decode, const pa_prefill_pa
  * Precision.  Scores, softmax maxima and sums and all accumulations are fp32;
  * the softmax weights meet V in the tensor cores' operand type.  The decodes
  * hold a weight there to 2^-15 of itself with a bf16 cache and 2^-22 with an f16
- * one; with an fp8 cache to 2^-8 for a bf16 output, 2^-12 for any other.
+ * one; with an fp8 cache to 2^-8 for a bf16 output, 2^-12 for any other.  The
+ * chunks round it once for a 16-bit output, to the operands' type (bf16 with a
+ * bf16 cache: 2^-8; f16 with any other: 2^-11), numerator and sum alike, and
+ * hold it to 2^-16 or 2^-22 for an fp32 output: who wants more than the
+ * output's own rounding asks for that.
  */
 
 /*

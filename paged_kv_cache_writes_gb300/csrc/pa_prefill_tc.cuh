@@ -121,7 +121,20 @@ __device__ __forceinline__ uint32_t f16x2_rn_add(float p0, float p1, float2 &acc
   return w;
 }
 
-// The same in bf16 (8 chunks of 2048 at a window of 1024 + 4: 617 us with the halves widened by shifts, 608 so).
+// The two as f16x2 hi + lo: hi rounded to nearest, lo the rest (exact in fp32), rounded to nearest.
+__device__ __forceinline__ uint32_t f16x2_split(float p0, float p1, uint32_t &lo) {
+  uint32_t w;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(p1), "f"(p0));
+  unsigned short h0, h1;
+  asm("mov.b32 {%0, %1}, %2;" : "=h"(h0), "=h"(h1) : "r"(w));
+  const unsigned short minus = 0xbc00;   // f16 -1.0
+  asm("fma.rn.f32.f16 %0, %1, %2, %0;" : "+f"(p0) : "h"(h0), "h"(minus));
+  asm("fma.rn.f32.f16 %0, %1, %2, %0;" : "+f"(p1) : "h"(h1), "h"(minus));
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(lo) : "f"(p1), "f"(p0));
+  return w;
+}
+
+// f16x2_rn_add in bf16 (8 chunks of 2048 at a window of 1024 + 4: 617 us with the halves widened by shifts, 608 so).
 __device__ __forceinline__ uint32_t bf16x2_rn_add(float p0, float p1, float2 &acc) {
   uint32_t w;
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(p1), "f"(p0));
@@ -227,7 +240,7 @@ __device__ __forceinline__ void prefill_tc_body(const PrefillTcParams &p, int bx
   constexpr int kBufs = R::kBufs;
   constexpr bool kFp8 = std::is_same<KV, uint8_t>::value;
   constexpr bool kBf16 = std::is_same<QT, __nv_bfloat16>::value;
-  constexpr bool kSplit = kBf16 && !kFp8 && kLo;   // bf16 cache: P as hi + lo
+  constexpr bool kSplit = kWin ? kLo : kBf16 && !kFp8;   // P as hi + lo (kWin: for an fp32 output, else a bf16 cache)
   // K and V tiles come as bulk-tensor boxes of whole cache blocks, in atoms of 8 keys (all panels) of kAtom
   // bytes; else the loaders write panels of 128 keys
   constexpr bool kBoxes = kWin && !kFp8;
@@ -535,9 +548,13 @@ __device__ __forceinline__ void prefill_tc_body(const PrefillTcParams &p, int bx
                 const int i0 = 16 * hh + 2 * k;
                 const float2 a = ffma2(make_float2(v[i0], v[i0 + 1]), cc, nm);
                 const float2 pk = make_float2(fast_exp2(a.x), fast_exp2(a.y));
-                if constexpr (kBf16 && !kFp8 && !kLo) {   // rounded to bf16, the sum that of the rounded P
-                  w[k] = bf16x2_rn_add(pk.x, pk.y, lacc[k & 3]);
-                } else if constexpr (kSplit) {   // hi + lo, as in the other kernel
+                if constexpr (!kSplit) {   // rounded to the MMA's type, the sum that of the rounded P
+                  if constexpr (kF16Ops) w[k] = f16x2_rn_add(pk.x, pk.y, lacc[k & 3]);
+                  else w[k] = bf16x2_rn_add(pk.x, pk.y, lacc[k & 3]);
+                } else if constexpr (kF16Ops) {   // hi + lo: hi rounded to f16, lo = p - hi, exact in fp32, rounded too
+                  w[k] = f16x2_split(pk.x, pk.y, wl[k]);
+                  lacc[k & 3] = ffma2(pk, ones, lacc[k & 3]);
+                } else {   // the same in bf16, as in the other kernel
                   uint32_t hw, lw2;
                   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(hw) : "f"(pk.y), "f"(pk.x));
                   w[k] = hw;
@@ -546,8 +563,6 @@ __device__ __forceinline__ void prefill_tc_body(const PrefillTcParams &p, int bx
                   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(lw2) : "f"(lo.y), "f"(lo.x));
                   wl[k] = lw2;
                   lacc[k & 3] = ffma2(pk, ones, lacc[k & 3]);
-                } else {
-                  w[k] = f16x2_rn_add(pk.x, pk.y, lacc[k & 3]);
                 }
               }
               tmem_st8(sb + 32 * ck + 16 * hh, w);
@@ -1334,11 +1349,16 @@ cudaError_t launch_prefill_tc(const PrefillTcParams &p, const PoolMaps &m, int g
 // One kernel for every group size (the group is a run-time number: one
 // division per thread) and for head_dim 64 and 128.
 //
-// A bf16 cache's P: hi + lo for an fp32 output (kLo), rounded once to bf16 (to
-// nearest, the softmax sum that of the rounded P, so that the output stays a
-// convex combination of V rows) for a bf16 output, whose own rounding is as
-// large: the error against 64 bits goes from 1.7e-3 to 2.3e-3 of the output's
-// norm, and a third of the MMAs go away.
+// P for an fp32 output: hi + lo in the MMA's type (kLo; bf16 for a bf16 cache,
+// f16 for the others), within 2^-16 or 2^-22 of it.  For a 16-bit output it is
+// rounded once to that type (to nearest, the softmax sum that of the rounded P,
+// so that the output stays a convex combination of V rows), about as much as
+// the output's own rounding.  Measured for a bf16 cache: the error against 64 bits
+// goes from 1.7e-3 (the output's rounding alone) to 2.3e-3 of the output's
+// norm, and a third of the MMAs go away: 8 chunks of 2048, 64/8 heads 701 ->
+// 607 us, one of 512, 32/8 heads 19.3 -> 17.0, 4 of 1024, head_dim 64 54.8 -> 51.0,
+// 3 of 700, 40/8 heads 36.9 -> 33.2.  A caller that wants all bits of P asks for
+// an fp32 output.
 template <typename KV, typename QT, int D, bool kPair, bool kLo>
 __global__ void __launch_bounds__((tc::WinRoles<kPair, std::is_same<KV, uint8_t>::value>::kThreads), kPair ? 2 : 1)
     prefill_window_kernel(const PrefillTcParams p, const __grid_constant__ CUtensorMap tmap_k,
@@ -1367,13 +1387,12 @@ cudaError_t launch_prefill_window_one(const PrefillTcParams &p0, const PoolMaps 
   const int64_t gx = (int64_t)num_chunks * p.row_blocks, gy = (int64_t)p.num_kv_heads * p.shares;
   if (gx > 2147483647ll || gy > 65535) return cudaErrorInvalidValue;
   const dim3 grid((unsigned)gx, (unsigned)gy);
-  constexpr bool kBf16Cache = std::is_same<KV, __nv_bfloat16>::value;
   // One CTA per SM while that is all there is: a 512-token chunk of 32/8 heads (128 CTAs) 17.2 us, as pairs 20.1;
   // beyond that pairs: 8 chunks of 2048, 64/8 heads (8192 CTAs), 0.61 ms, one CTA per SM 0.86.
   const bool pair = gx * gy > num_sms;
-  if (kBf16Cache && !p.out_f32)
-    return pair ? launch_prefill_window_tiles<KV, QT, D, true, !kBf16Cache>(p, m, grid, s)
-                : launch_prefill_window_tiles<KV, QT, D, false, !kBf16Cache>(p, m, grid, s);
+  if (!p.out_f32)
+    return pair ? launch_prefill_window_tiles<KV, QT, D, true, false>(p, m, grid, s)
+                : launch_prefill_window_tiles<KV, QT, D, false, false>(p, m, grid, s);
   return pair ? launch_prefill_window_tiles<KV, QT, D, true, true>(p, m, grid, s)
               : launch_prefill_window_tiles<KV, QT, D, false, true>(p, m, grid, s);
 }
