@@ -407,7 +407,9 @@ PA_API pa_status pa_mixed_step(const pa_decode_part *decode, const pa_prefill_pa
  *   block_tables  as for pa_decode; the entries of blocks without a visible
  *               token are not read and may hold anything
  *   workspace   >= pa_decode_window_workspace_bytes(...) bytes for the same
- *               arguments, else as for pa_decode
+ *               arguments, or for larger num_seqs, max_seq_len, window or
+ *               num_sinks (one workspace may serve batches of every size);
+ *               else as for pa_decode
  *   all other arguments as for pa_decode.
  * Every shape of pa_decode is served, by the tensor-core decode whatever
  * pa_set_decode_kernel says: the kernel walks the visible blocks as one
@@ -465,7 +467,8 @@ PA_API pa_status pa_prefill_chunk_window(const void *q_chunk, pa_dtype q_dtype, 
  *   decay        finite; 1 adds up, 0 keeps only this step's weights (weights is
  *                not read then, and may hold anything)
  *   workspace    >= pa_decode_weights_workspace_bytes(...) bytes (it holds one
- *                fp32 score per query head and token), else as for pa_decode
+ *                fp32 score per query head and token) for the same arguments, or
+ *                for a larger num_seqs or max_seq_len; else as for pa_decode
  *   all other arguments as for pa_decode, seq_lens[i] <= max_seq_len included.
  * out equals pa_decode's within the decode tolerance.  A row of weight_rows
  * outside [0, num_weight_rows) sets PA_ERR_DEVICE_CHECK and is skipped.

@@ -520,6 +520,32 @@ pa_status bounded_layout(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_h
   return PA_OK;
 }
 
+// The workspace that the size calls promise: what bounded_layout needs for these arguments or for any smaller number of
+// rows and length (so also a smaller window), as a serving loop keeps one workspace for all its batches.  bounded_layout
+// alone does not grow with them: fewer rows are cut into more partitions, and a shorter length may be cut more finely.  A
+// row of `longest` tokens has at most ceil(longest / 64) partitions, and at most `most`, or those of full size.
+size_t bounded_workspace(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                         int32_t block_size, int32_t max_seq_len, int32_t window, int32_t num_sinks,
+                         int32_t partition_size, bool weights) {
+  BoundedLayout b;
+  if (bounded_layout(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, max_seq_len, window, num_sinks,
+                     partition_size, weights, &b) != PA_OK)
+    return 0;
+  size_t most_bytes = b.total;
+  if (partition_size != 0) return most_bytes;   // a size of partition that the caller gave stays: more of all is more
+  const int64_t longest = window_max_packed(max_seq_len, window, num_sinks, block_size);
+  const int64_t units = (int64_t)num_kv_heads * b.shares;
+  const int64_t full = (longest + kDefaultPartition - 1) / kDefaultPartition;
+  for (int64_t n = 1; n <= num_seqs && kPlanSms / (n * units) > 1; ++n) {
+    const int64_t parts = std::max<int64_t>({1, std::min<int64_t>(kPlanSms / (n * units), (longest + 63) / 64), full});
+    size_t bytes = decode_workspace_layout(n, num_q_heads, head_dim, parts).total;
+    if (weights)   // partitions times their size: less than one of them more than the row
+      bytes += (size_t)n * units * (longest + kDefaultPartition) * b.rows * 4 + round256((size_t)n * num_q_heads * 8);
+    most_bytes = std::max(most_bytes, bytes);
+  }
+  return most_bytes;
+}
+
 // Workspace of pa_evict: each head's list of moves (their number padded to 16
 // bytes, destinations, sources).
 struct EvictLayout {
@@ -638,11 +664,8 @@ extern "C" {
 size_t pa_decode_window_workspace_bytes(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
                                         int32_t block_size, int32_t max_seq_len, int32_t window, int32_t num_sinks,
                                         int32_t partition_size) {
-  BoundedLayout b;
-  return bounded_layout(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, max_seq_len, window, num_sinks,
-                        partition_size, false, &b) == PA_OK
-             ? b.total
-             : 0;
+  return bounded_workspace(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, max_seq_len, window, num_sinks,
+                           partition_size, false);
 }
 
 pa_status pa_decode_window(const void *q, pa_dtype q_dtype, int32_t num_seqs, int32_t num_q_heads, const void *k_cache,
@@ -725,11 +748,9 @@ pa_status pa_evict(void *k_cache, void *v_cache, const pa_kv_cache *cache, int32
 
 size_t pa_decode_weights_workspace_bytes(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
                                          int32_t max_seq_len, int32_t partition_size) {
-  BoundedLayout b;   // no window: the block size does not matter
-  return bounded_layout(num_seqs, num_q_heads, num_kv_heads, head_dim, 16, max_seq_len, INT32_MAX, 0, partition_size,
-                        true, &b) == PA_OK
-             ? b.total
-             : 0;
+  // no window: the block size does not matter
+  return bounded_workspace(num_seqs, num_q_heads, num_kv_heads, head_dim, 16, max_seq_len, INT32_MAX, 0, partition_size,
+                           true);
 }
 
 pa_status pa_decode_weights(const void *q, pa_dtype q_dtype, int32_t num_seqs, int32_t num_q_heads,
