@@ -470,6 +470,7 @@ PA_API pa_status pa_prefill_chunk_window(const void *q_chunk, pa_dtype q_dtype, 
  *                fp32 score per query head and token) for the same arguments, or
  *                for a larger num_seqs or max_seq_len; else as for pa_decode
  *   all other arguments as for pa_decode, seq_lens[i] <= max_seq_len included.
+ * At most 6144 query heads per KV head (PA_ERR_UNSUPPORTED, workspace 0).
  * out equals pa_decode's within the decode tolerance.  A row of weight_rows
  * outside [0, num_weight_rows) sets PA_ERR_DEVICE_CHECK and is skipped.
  */

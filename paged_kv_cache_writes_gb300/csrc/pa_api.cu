@@ -496,6 +496,7 @@ pa_status bounded_layout(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_h
     return PA_ERR_UNSUPPORTED;
   const int64_t longest = window_max_packed(max_seq_len, window, num_sinks, block_size);
   const int gqa = num_q_heads / num_kv_heads;
+  if (weights && gqa > kMaxWeightsGroup) return PA_ERR_UNSUPPORTED;
   b->shares = decode_ext_shares(head_dim, gqa);
   b->share_heads = (gqa + b->shares - 1) / b->shares;
   b->rows = decode_ext_rows(b->share_heads);

@@ -214,6 +214,9 @@ struct FinishParams {
   float decay;
   int32_t *err;
 };
+// Query heads per KV head that pa_decode_weights serves: the weights' CTAs hold each head's maximum and sum, 8 bytes, in the
+// 48 KB of shared memory that a launch has without asking for more.
+constexpr int kMaxWeightsGroup = 6144;
 cudaError_t launch_decode_finish(const FinishParams &p, int head_dim, cudaStream_t s);
 
 // Eviction by accumulated attention weight (pa_evict.cu).
