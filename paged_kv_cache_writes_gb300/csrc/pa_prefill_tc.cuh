@@ -665,10 +665,10 @@ __device__ __forceinline__ void prefill_tc_body(const PrefillTcParams &p, int bx
       if constexpr (kFp8 && kBf16) {
         // f16 operands: the row times 2^e (its largest element in [2^14, 2^15)), rounded to f16;
         // the scores are multiplied back by 2^-e
-        uint4 v[kD / 8];
+        uint4 v[16];
         float amax = 0.f;
 #pragma unroll
-        for (int ch = 0; ch < kD / 8; ++ch) {
+        for (int ch = 0; ch < 16; ++ch) {
           v[ch] = row_ok ? __ldg(reinterpret_cast<const uint4 *>(src) + ch) : make_uint4(0, 0, 0, 0);
           const uint32_t ws[4] = {v[ch].x, v[ch].y, v[ch].z, v[ch].w};
 #pragma unroll
@@ -681,7 +681,7 @@ __device__ __forceinline__ void prefill_tc_body(const PrefillTcParams &p, int bx
         const float sc = __uint_as_float((uint32_t)(e + 127) << 23);
         cmul *= __uint_as_float((uint32_t)(127 - e) << 23);
 #pragma unroll
-        for (int ch = 0; ch < kD / 8; ++ch) {
+        for (int ch = 0; ch < 16; ++ch) {
           const uint32_t ws[4] = {v[ch].x, v[ch].y, v[ch].z, v[ch].w};
           uint32_t o[4];
 #pragma unroll
@@ -695,7 +695,7 @@ __device__ __forceinline__ void prefill_tc_body(const PrefillTcParams &p, int bx
         }
       } else {
 #pragma unroll
-        for (int ch = 0; ch < kD / 8; ++ch) {
+        for (int ch = 0; ch < 16; ++ch) {
           uint4 v = row_ok ? __ldg(reinterpret_cast<const uint4 *>(src) + ch) : make_uint4(0, 0, 0, 0);
           v.x ^= qflip; v.y ^= qflip; v.z ^= qflip; v.w ^= qflip;
           *reinterpret_cast<uint4 *>(qt + (ch >> 3) * (kM * 128) + mr * 128 + (((ch & 7) ^ (mr & 7)) << 4)) = v;
@@ -937,9 +937,8 @@ __device__ __forceinline__ void prefill_tc_body(const PrefillTcParams &p, int bx
           for (int t = max(0, filled[which] - kStages); t < filled[which]; ++t)
             mbar_wait(which ? &v_full[t % kStages] : &k_full[t % kStages], (t / kStages) & 1, p.err);
     } else if constexpr (!kFp8) {
-      // 16-bit rows: per instruction 2 rows x 16 chunks of 16 B (head_dim 64: 4 rows x 8 chunks)
-      constexpr int kC = kD / 8, kRI = 32 / kC;   // chunks per row, rows per instruction
-      const int q = lane % kC, pn = q >> 3, cq = q & 7;
+      // 16-bit rows (256 B): per instruction 2 rows x 16 chunks of 16 B
+      const int q = lane & 15, pn = q >> 3, cq = q & 7;
       for (int j = 0; j < nkt && ok; ++j) {
         const int s = j % kStages;
         const uint32_t ph_prev = ((j / kStages) - 1) & 1;
@@ -955,10 +954,10 @@ __device__ __forceinline__ void prefill_tc_body(const PrefillTcParams &p, int bx
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
 #pragma unroll
-            for (int i = 0; i < 16 / kRI; ++i) {
-              const int rr = kRI * i + lane / kC;             // row among the run's 16
+            for (int i = 0; i < 8; ++i) {
+              const int rr = 2 * i + (lane >> 4);             // row among the run's 16
               const int row = 32 * lw + 16 * r + rr;           // row of the tile
-              const bool v = seen(j, r, rr, nval[r]);
+              const bool v = rr < nval[r];
               const char *src = v ? pool + (row0[r] + rr) * kRowBytes + q * 16 : pool;
               cp_async16(tile + row * 128 + ((cq ^ (row & 7)) << 4), src, v ? 16u : 0u);
             }
@@ -1035,7 +1034,8 @@ __device__ __forceinline__ void prefill_tc_body(const PrefillTcParams &p, int bx
         wait_or_abort(&cbar[jj % kCS], (jj / kCS) & 1, p.err, abort_flag);
     } else {
       // fp8 rows (128 B), two Q tiles: per instruction 4 rows x 8 words of 16
-      // codes (head_dim 64, any number of Q tiles: 8 rows x 4 words).  A tile is four quarters (K run 0, K run 1, V run 0, V run 1).
+      // codes; the windowed kernel, two CTAs per SM or head_dim 64 (8 rows x 4 words).
+      // A tile is four quarters (K run 0, K run 1, V run 0, V run 1).
       // The loads run kPf quarters (half a tile) ahead of the widening into
       // shared memory.
       constexpr int kPf = 2;
