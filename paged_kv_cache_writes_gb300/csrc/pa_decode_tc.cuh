@@ -450,8 +450,9 @@ __device__ __forceinline__ void decode_tc_body(const DecodeTcParams &tp, const C
   constexpr int S = GE::kSlots, kNO = GE::kNO, kNS = GE::kNS;
   constexpr uint32_t kAB = kBf16 ? 1u : 0u;   // instruction-descriptor format: bf16 1, f16 0, e4m3 0
   // small tiles (fp8) make the MMA warp's own instructions the bound: its MMAs and commits are predicated instead
-  // of branched around, its waits short.  33 sequences, head_dim 64, fp8: 23.8 -> 22.5 us; with a bf16 cache (one
-  // sequence, head_dim 128) 12.5 -> 13.1, so not there.
+  // of branched around, its waits short.  GPU time: 33 sequences, head_dim 64, fp8 23.8 -> 22.8 us, 64 of 32/8 heads 94.6
+  // -> 92.5, head_dim 128 and 64/8 heads 131.6 -> 129.7; with a bf16 cache (one sequence, head_dim 128) 12.5 -> 13.1, so
+  // not there.
   constexpr bool kLean = kExt && kFp8;
   const DecodeParams &p = tp.d;
   const float kNegInf = -__int_as_float(0x7f800000);
@@ -906,8 +907,12 @@ __device__ __forceinline__ void decode_tc_body(const DecodeTcParams &tp, const C
     const int bs = p.block_size;
     const int ldr = warp == kLoadWarp ? 0 : warp - kLoadWarp1 + 1;   // this warp's share: positions = ldr mod NL
     bool ok = true;
-    // K and V are read once: first to be evicted, so that they leave the L2 to what is read again (the scores, the
-    // partial results); 64 sequences of 64/8 heads and 4100 visible tokens: 178 -> 167 us
+    // K and V are first to be evicted, so that they leave the L2 to what is read again (the scores, the partial results).
+    // GPU time without and with the policy: 64 sequences of 64/8 heads, 4100 visible tokens 181 / 163 us, fp8 138 / 130,
+    // with weights 233 / 230.  Blocks that are read more than once (a group in shares, shared prefixes) gain too: 128/4
+    // heads 240 / 227 us, 32 prefixes of 2048 tokens with 4 branches each 158 / 153, with weights 175 / 168; but 64
+    // branches of one prefix of 8192 tokens, whose 34 MB would stay in the L2 beside 142 MB of scores: 306 / 304, with
+    // weights 358 / 390.  Which blocks are shared is not known here.
     const uint64_t policy = kExt ? l2_evict_first() : 0;
     auto issue_tile = [&](const UnitHdr &un, int info_idx, int j, bool is_k, int slot) {
       uint64_t *full_bar = &slot_full[slot];
