@@ -326,7 +326,7 @@ def _exact_append(st, c):
 
     found = [turn(st["q"])]
     scales = []
-    powers = torch.ldexp(torch.ones((), dtype=torch.float64, device=DEV), torch.arange(LEAST, MOST + 1, device=DEV))
+    powers = torch.tensor([2.0 ** e for e in range(LEAST, MOST + 1)], dtype=torch.float64, device=DEV)
     slots = st["slots"].tolist()
     for pool, old, x in ((st["k"], st["k_scales"], turn(st["k_new"])), (st["v"], st["v_scales"], st["v_new"].double())):
         if c["kv"] in TYPES:
