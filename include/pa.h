@@ -537,6 +537,113 @@ PA_API pa_status pa_evict(void *k_cache, void *v_cache, const pa_kv_cache *cache
                           pa_stream_t stream);
 
 /*
+ * pa_rope_and_cache -- a step's new tokens: rotate queries and keys by their
+ * positions and store keys and values in their cache slots, in one launch.
+ * (The pages store keys as they come; rotation and block scales are this
+ * library's extensions.)
+ *
+ * Token t has position positions[t] and slot slot_mapping[t]; with r = rope_dim
+ * and c, s the two halves of row cos_sin[positions[t]], elements (a, b) =
+ * (x[i], x[i + r/2]) of a query or key row (interleaved: (x[2i], x[2i + 1])),
+ * i < r/2, become
+ *     (a c[i] - b s[i],  b c[i] + a s[i]),
+ * two products and their sum each rounded to fp32; elements from r on stay.
+ * Queries go to q_out, rounded once to in_dtype.  Keys, rotated, and values,
+ * as they are, are stored as pa_reshape_and_cache stores them, each rounded
+ * once to the cache's type (fp8: e4m3(x / scale), saturating).
+ *
+ *   q, q_out      device [num_tokens][num_q_heads][head_dim], in_dtype; q has
+ *                 token stride q_stride (>= num_q_heads * head_dim, a multiple of
+ *                 8), q_out is contiguous.  q_out may be q if q is contiguous,
+ *                 and must not overlap q otherwise, nor k, v or the pools.
+ *                 num_q_heads 0: no queries (q and q_out are not used)
+ *   k, v, token_stride, slot_mapping  as for pa_reshape_and_cache (a negative
+ *                 slot: the token's K and V are not stored, its query is
+ *                 rotated)
+ *   positions     device int32 [num_tokens]; a negative one marks a padding
+ *                 token, nothing of which is read or written
+ *   cos_sin       device fp32 [num_positions][rope_dim], 16-byte aligned: cosines,
+ *                 then sines, of each position's rope_dim / 2 angles
+ *   rope_dim      a multiple of 16, at most head_dim; 0: keys are stored as they
+ *                 come (num_q_heads must be 0; positions and cos_sin are not used)
+ *   k_block_scales, v_block_scales  NULL, or device fp32 [num_blocks]
+ *                 [num_kv_heads] of a block-scaled cache (below); both or neither
+ * A position >= num_positions or a slot past the pool sets PA_ERR_DEVICE_CHECK:
+ * the token is skipped (the slot: its K and V).
+ *
+ * The block-scaled cache.  An fp8 pool in which a code of block b and KV head h
+ * means code * scales[b][h], one fp32 scale per block and head and pool; the
+ * descriptor's k_scale and v_scale are not used and its per-head scales must be
+ * NULL.  Scales are in [2^-64, 2^32].  This call chooses them: powers of two, so
+ * that changing one later only moves the codes' exponents.  For a block whose
+ * first slot is among the call's new tokens: the smallest 2^e with
+ * |x| <= 448 * 2^e for every finite new x (2^-64 at least; 2^32 at most, larger
+ * values saturate).  For a block that holds tokens, the slots in front of the
+ * first new one: the scale it has, if the new elements fit in 448 times it; else
+ * the power of two as above, and the codes of the held tokens become
+ * e4m3(code * old / new), exact but for codes that fall below e4m3's normal
+ * range.  The new codes are e4m3(x / scale); slots behind the new ones are not
+ * touched.  New tokens of one block are expected within block_size consecutive
+ * tokens of the call (as sequences' tokens in order are).  A block to be added
+ * to whose scale is out of range sets PA_ERR_DEVICE_CHECK and keeps its tokens;
+ * the new ones are not stored.  A block shared with another sequence is copied
+ * first (pa_bm_append's pairs, pa_copy_blocks_scaled).
+ * pa_evict does not take a block-scaled cache: it moves rows between blocks.
+ */
+PA_API pa_status pa_rope_and_cache(const void *q, int64_t q_stride, void *q_out, int32_t num_q_heads, const void *k,
+                                   const void *v, pa_dtype in_dtype, int32_t num_tokens, int64_t token_stride,
+                                   const int32_t *positions, const float *cos_sin, int32_t num_positions,
+                                   int32_t rope_dim, int32_t interleaved, const int64_t *slot_mapping, void *k_cache,
+                                   void *v_cache, const pa_kv_cache *cache, float *k_block_scales,
+                                   float *v_block_scales, pa_stream_t stream);
+
+/*
+ * pa_copy_blocks_scaled -- pa_copy_blocks for a block-scaled cache: the blocks
+ * and their scales.  Scales as for pa_rope_and_cache, neither NULL.
+ */
+PA_API pa_status pa_copy_blocks_scaled(void *k_cache, void *v_cache, const pa_kv_cache *cache, float *k_block_scales,
+                                       float *v_block_scales, const int32_t *src_dst_pairs, int32_t num_pairs,
+                                       pa_stream_t stream);
+
+/*
+ * pa_decode_scaled -- pa_decode over a block-scaled cache: K_i[p] is code *
+ * k_block_scales[b][g] and V_i[p] code * v_block_scales[b][g], b the block of
+ * position p.  Scales need not be powers of two; one out of [2^-64, 2^32] sets
+ * PA_ERR_DEVICE_CHECK (the rows that read it are then undefined).  The tensor
+ * cores multiply the codes as stored: K's scales meet the scores, V's the softmax
+ * weights, whose sum stays that of the weights without them, in fp32.  A weight
+ * times V's scale is held to 2^-8 of itself for a bf16 output, to 2^-12 for any
+ * other.
+ *   workspace   device, >= pa_decode_scaled_workspace_bytes(...) bytes for the
+ *               same arguments or for a larger num_seqs or max_seq_len; else as
+ *               for pa_decode
+ *   all other arguments as for pa_decode.  Every shape of pa_decode is served by
+ *   the tensor-core decode, whatever pa_set_decode_kernel says.
+ */
+PA_API size_t pa_decode_scaled_workspace_bytes(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
+                                               int32_t head_dim, int32_t max_seq_len, int32_t partition_size);
+PA_API pa_status pa_decode_scaled(const void *q, pa_dtype q_dtype, int32_t num_seqs, int32_t num_q_heads,
+                                  const void *k_cache, const void *v_cache, const pa_kv_cache *cache,
+                                  const float *k_block_scales, const float *v_block_scales,
+                                  const int32_t *block_tables, int32_t max_blocks_per_seq, const int32_t *seq_lens,
+                                  int32_t max_seq_len, float scale, int32_t partition_size, void *workspace,
+                                  size_t workspace_bytes, void *out, pa_dtype out_dtype, pa_stream_t stream);
+
+/*
+ * pa_prefill_chunk_scaled -- pa_prefill_chunk over a block-scaled cache (K, V
+ * and scales as for pa_decode_scaled).  A softmax weight times V's scale is
+ * rounded once to f16 for a 16-bit output and held to 2^-22 for an fp32 one.
+ * Every shape of pa_prefill_chunk is served on the tensor cores.
+ */
+PA_API pa_status pa_prefill_chunk_scaled(const void *q_chunk, pa_dtype q_dtype, const int32_t *cu_q_lens,
+                                         const int32_t *q_start, int32_t num_chunks, int32_t max_q_len,
+                                         int32_t num_q_heads, const void *k_cache, const void *v_cache,
+                                         const pa_kv_cache *cache, const float *k_block_scales,
+                                         const float *v_block_scales, const int32_t *block_tables,
+                                         int32_t max_blocks_per_seq, const int32_t *seq_lens, int32_t max_seq_len,
+                                         float scale, void *out, pa_dtype out_dtype, pa_stream_t stream);
+
+/*
  * pa_get_device_error -- read and clear the current device's error word.
  * Synchronises `stream`, then stores into *code the first device-side status
  * recorded since the last clear (PA_OK if none): PA_ERR_DEVICE_CHECK for

@@ -23,6 +23,8 @@ __all__ = [
     "pa_mixed_step", "PaDecodePart", "PaPrefillPart",
     "pa_decode_window_workspace_bytes", "pa_decode_window", "pa_prefill_chunk_window",
     "pa_decode_weights_workspace_bytes", "pa_decode_weights", "pa_evict_workspace_bytes", "pa_evict",
+    "pa_rope_and_cache", "pa_copy_blocks_scaled", "pa_decode_scaled_workspace_bytes", "pa_decode_scaled",
+    "pa_prefill_chunk_scaled",
 ]
 
 PA_F16, PA_BF16, PA_FP8_E4M3, PA_F32 = 0, 1, 2, 3
@@ -110,6 +112,15 @@ def lib() -> ctypes.CDLL:
         L.pa_evict_workspace_bytes.restype = SZ
         L.pa_evict.argtypes = [P, P, CACHE, I32, P, I32, P, I32, P, P, I32, I32, I32, P, P, P, P, I64, I32, P, P, P, SZ,
                                P]
+        L.pa_rope_and_cache.argtypes = [P, I64, P, I32, P, P, ctypes.c_int, I32, I64, P, P, I32, I32, I32, P, P, P, CACHE, P,
+                                        P, P]
+        L.pa_copy_blocks_scaled.argtypes = [P, P, CACHE, P, P, P, I32, P]
+        L.pa_decode_scaled_workspace_bytes.argtypes = [I32] * 6
+        L.pa_decode_scaled_workspace_bytes.restype = SZ
+        L.pa_decode_scaled.argtypes = [P, ctypes.c_int, I32, I32, P, P, CACHE, P, P, P, I32, P, I32, F, I32, P, SZ, P,
+                                       ctypes.c_int, P]
+        L.pa_prefill_chunk_scaled.argtypes = [P, ctypes.c_int, P, P, I32, I32, I32, P, P, CACHE, P, P, P, I32, P, I32, F, P,
+                                              ctypes.c_int, P]
         L.pa_get_device_error.argtypes = [P, ctypes.POINTER(I32)]
         L.pa_set_decode_kernel.argtypes = [I32]
         L.pa_selftest_wait_timeout.argtypes = [P]
@@ -133,7 +144,8 @@ def lib() -> ctypes.CDLL:
                      "pa_get_device_error", "pa_selftest_wait_timeout", "pa_bm_create", "pa_bm_new_sequence",
                      "pa_bm_fork", "pa_bm_append", "pa_bm_free", "pa_bm_block_table", "pa_bm_get_stats",
                      "pa_decode_window", "pa_prefill_chunk_window", "pa_decode_weights", "pa_evict", "pa_bm_unshare",
-                     "pa_bm_truncate", "pa_bm_release_window"):
+                     "pa_bm_truncate", "pa_bm_release_window", "pa_rope_and_cache", "pa_copy_blocks_scaled",
+                     "pa_decode_scaled", "pa_prefill_chunk_scaled"):
             getattr(L, name).restype = ctypes.c_int
         _lib = L
     return _lib
@@ -331,15 +343,19 @@ class _Args:
                block_tables: torch.Tensor, n: int) -> None:
         """What the library cannot see: pools that hold what the descriptor says, an output of the queries' shape, a
         table row per sequence."""
+        _Args.pools(k_cache, v_cache, cache)
+        if q is not None and (q.shape != out.shape or q.shape[2] != cache.head_dim):
+            raise ValueError("q and out must be [rows, num_q_heads, head_dim]")
+        if len(block_tables) != n:
+            raise ValueError("block_tables must have one row per sequence")
+
+    @staticmethod
+    def pools(k_cache: torch.Tensor, v_cache: torch.Tensor, cache: PaKvCache) -> None:
         size = cache.num_blocks * cache.num_kv_heads * cache.block_size * cache.head_dim
         if cache.kv_dtype != PA_FP8_E4M3:
             size *= 2
         if k_cache.nbytes < size or v_cache.nbytes < size:
             raise ValueError("k_cache and v_cache must have the descriptor's shape and type")
-        if q is not None and (q.shape != out.shape or q.shape[2] != cache.head_dim):
-            raise ValueError("q and out must be [rows, num_q_heads, head_dim]")
-        if len(block_tables) != n:
-            raise ValueError("block_tables must have one row per sequence")
 
     def stream(self, stream) -> int:
         return torch._C._cuda_getCurrentRawStream(self.device) if stream is None else _stream(stream)
@@ -459,6 +475,138 @@ def pa_evict(k_cache: torch.Tensor, v_cache: torch.Tensor, cache: PaKvCache, blo
         0 if workspace is None else workspace.nbytes, a.stream(stream))
     if status:
         raise PaError(status, "pa_evict")
+
+
+def _heads_rows(a: _Args, t: torch.Tensor, name: str, tokens: int, d: int, dtype: torch.dtype):
+    """(pointer, token stride) of [tokens, heads, head_dim] rows with unit inner strides."""
+    if t.dim() != 3 or t.shape[0] != tokens or t.shape[2] != d:
+        raise ValueError(f"{name} must be [tokens, heads, head_dim]")
+    if t.get_device() != a.device:
+        raise ValueError(f"{name} must be a CUDA tensor on the current device")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}")
+    stride = t.stride()
+    if stride[2] != 1 or stride[1] != d:
+        raise ValueError(f"{name} must have unit inner strides")
+    return t.data_ptr(), stride[0]
+
+
+def _block_scales(a: _Args, k_scales: torch.Tensor, v_scales: torch.Tensor, cache: PaKvCache):
+    shape = (cache.num_blocks, cache.num_kv_heads)
+    if k_scales.shape != shape or v_scales.shape != shape:
+        raise ValueError("k_scales and v_scales must be [num_blocks, num_kv_heads]")
+    return a(k_scales, "k_scales", _F32), a(v_scales, "v_scales", _F32)
+
+
+def pa_rope_and_cache(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor | None,
+                      cos_sin: torch.Tensor | None, slot_mapping: torch.Tensor, k_cache: torch.Tensor,
+                      v_cache: torch.Tensor, cache: PaKvCache, q_out: torch.Tensor | None = None,
+                      interleaved: bool = False, k_scales: torch.Tensor | None = None,
+                      v_scales: torch.Tensor | None = None, stream=None) -> None:
+    """Rotate q [T, Hq, D] into q_out (which may be q) and k [T, Hkv, D] by ``positions`` (int32 [T]; negative: padding), and
+    store k and v in their slots (int64 [T]).  ``cos_sin``: float32 [num_positions, rope_dim], cosines then sines; None: k is
+    stored as it comes (q must be None).  q, k and v may be views into one QKV tensor.  ``k_scales``, ``v_scales``: float32
+    [num_blocks, Hkv] of a block-scaled fp8 cache, which this call chooses and raises."""
+    a = _Args()
+    if k.dim() != 3:
+        raise ValueError("k must be [tokens, heads, head_dim]")
+    T, hkv, d = k.shape
+    if hkv != cache.num_kv_heads or d != cache.head_dim or v.shape != k.shape:
+        raise ValueError("k and v must be [tokens, num_kv_heads, head_dim]")
+    kp, stride = _heads_rows(a, k, "k", T, d, k.dtype)
+    vp, v_stride = _heads_rows(a, v, "v", T, d, k.dtype)
+    if T <= 1:
+        stride = v_stride = hkv * d
+    if v_stride != stride:
+        raise ValueError("k and v must have equal token strides")
+    a.pools(k_cache, v_cache, cache)
+    if slot_mapping.shape != (T,):
+        raise ValueError("slot_mapping must have one entry per token")
+    qp, q_stride, qo, hq = None, 0, None, 0
+    if q is not None:
+        qp, q_stride = _heads_rows(a, q, "q", T, d, k.dtype)
+        hq = q.shape[1]
+        if T <= 1:
+            q_stride = hq * d
+        if q_out is None or q_out.shape != q.shape:
+            raise ValueError("q_out must have q's shape")
+        qo = a(q_out, "q_out", k.dtype)
+    pos, table, num_pos, rope = None, None, 0, 0
+    if cos_sin is not None:
+        if cos_sin.dim() != 2 or positions is None or positions.shape != (T,):
+            raise ValueError("cos_sin must be [num_positions, rope_dim], positions one per token")
+        pos, table = a(positions, "positions", _I32), a(cos_sin, "cos_sin", _F32)
+        num_pos, rope = cos_sin.shape
+    elif q is not None:
+        raise ValueError("q needs positions and cos_sin")
+    ks = vs = None
+    if k_scales is not None or v_scales is not None:
+        if k_scales is None or v_scales is None:
+            raise ValueError("k_scales and v_scales go together")
+        ks, vs = _block_scales(a, k_scales, v_scales, cache)
+    status = lib().pa_rope_and_cache(qp, q_stride, qo, hq, kp, vp, _dtype_code(k.dtype), T, stride, pos, table, num_pos, rope,
+                                     interleaved, a(slot_mapping, "slot_mapping", torch.int64), a(k_cache, "k_cache"),
+                                     a(v_cache, "v_cache"), ctypes.byref(cache), ks, vs, a.stream(stream))
+    if status:
+        raise PaError(status, "pa_rope_and_cache")
+
+
+def pa_copy_blocks_scaled(k_cache: torch.Tensor, v_cache: torch.Tensor, cache: PaKvCache, k_scales: torch.Tensor,
+                          v_scales: torch.Tensor, src_dst_pairs: torch.Tensor, stream=None) -> None:
+    """pa_copy_blocks for a block-scaled cache: the blocks and their scales.  src_dst_pairs: int32 [n, 2]."""
+    a = _Args()
+    a.pools(k_cache, v_cache, cache)
+    if src_dst_pairs.dim() != 2 or src_dst_pairs.shape[1] != 2:
+        raise ValueError("src_dst_pairs must be [n, 2]")
+    ks, vs = _block_scales(a, k_scales, v_scales, cache)
+    status = lib().pa_copy_blocks_scaled(a(k_cache, "k_cache"), a(v_cache, "v_cache"), ctypes.byref(cache), ks, vs,
+                                         a(src_dst_pairs, "src_dst_pairs", _I32), src_dst_pairs.shape[0], a.stream(stream))
+    if status:
+        raise PaError(status, "pa_copy_blocks_scaled")
+
+
+def pa_decode_scaled_workspace_bytes(num_seqs: int, num_q_heads: int, num_kv_heads: int, head_dim: int,
+                                     max_seq_len: int, partition_size: int = 0) -> int:
+    return int(lib().pa_decode_scaled_workspace_bytes(num_seqs, num_q_heads, num_kv_heads, head_dim, max_seq_len,
+                                                      partition_size))
+
+
+def pa_decode_scaled(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, cache: PaKvCache,
+                     k_scales: torch.Tensor, v_scales: torch.Tensor, block_tables: torch.Tensor, seq_lens: torch.Tensor,
+                     max_seq_len: int, scale: float, out: torch.Tensor, workspace: torch.Tensor | None = None,
+                     partition_size: int = 0, stream=None) -> None:
+    """pa_decode over a block-scaled fp8 cache (``k_scales``, ``v_scales``: float32 [num_blocks, Hkv]).
+    ``workspace``: uint8 tensor of >= pa_decode_scaled_workspace_bytes(...) bytes."""
+    a = _Args()
+    B, hq, _ = q.shape
+    a.shapes(q, out, k_cache, v_cache, cache, block_tables, B)
+    ks, vs = _block_scales(a, k_scales, v_scales, cache)
+    status = lib().pa_decode_scaled(
+        a(q, "q"), _dtype_code(q.dtype), B, hq, a(k_cache, "k_cache"), a(v_cache, "v_cache"), ctypes.byref(cache), ks, vs,
+        a(block_tables, "block_tables", _I32), block_tables.shape[1], a.of_sequences(seq_lens, "seq_lens", B), max_seq_len,
+        scale, partition_size, a.maybe(workspace, "workspace"), 0 if workspace is None else workspace.nbytes,
+        a(out, "out"), _dtype_code(out.dtype), a.stream(stream))
+    if status:
+        raise PaError(status, "pa_decode_scaled")
+
+
+def pa_prefill_chunk_scaled(q_chunk: torch.Tensor, cu_q_lens: torch.Tensor, q_start: torch.Tensor, max_q_len: int,
+                            k_cache: torch.Tensor, v_cache: torch.Tensor, cache: PaKvCache, k_scales: torch.Tensor,
+                            v_scales: torch.Tensor, block_tables: torch.Tensor, seq_lens: torch.Tensor, max_seq_len: int,
+                            scale: float, out: torch.Tensor, stream=None) -> None:
+    """pa_prefill_chunk over a block-scaled fp8 cache (``k_scales``, ``v_scales``: float32 [num_blocks, Hkv])."""
+    a = _Args()
+    n = q_start.shape[0]
+    a.shapes(q_chunk, out, k_cache, v_cache, cache, block_tables, n)
+    ks, vs = _block_scales(a, k_scales, v_scales, cache)
+    status = lib().pa_prefill_chunk_scaled(
+        a(q_chunk, "q_chunk"), _dtype_code(q_chunk.dtype), a.of_sequences(cu_q_lens, "cu_q_lens", n + 1),
+        a.of_sequences(q_start, "q_start", n), n, max_q_len, q_chunk.shape[1], a(k_cache, "k_cache"),
+        a(v_cache, "v_cache"), ctypes.byref(cache), ks, vs, a(block_tables, "block_tables", _I32), block_tables.shape[1],
+        a.of_sequences(seq_lens, "seq_lens", n), max_seq_len, scale, a(out, "out"), _dtype_code(out.dtype),
+        a.stream(stream))
+    if status:
+        raise PaError(status, "pa_prefill_chunk_scaled")
 
 
 def pa_get_device_error(stream=None) -> int:

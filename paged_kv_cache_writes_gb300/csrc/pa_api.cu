@@ -77,6 +77,25 @@ pa_status check_pools(const void *k_cache, const void *v_cache) {
   return PA_OK;
 }
 
+bool overlap(const void *p, double p_bytes, const void *q, double q_bytes) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+  return a < b ? (double)(b - a) < p_bytes : (double)(a - b) < q_bytes;
+}
+
+// A block-scaled cache: an fp8 pool without per-head scales, and two arrays of scales.  *c is its descriptor with scales of 1
+// in the place of the unused ones.
+pa_status check_scaled_cache(const pa_kv_cache *cache, const float *k_scales, const float *v_scales, pa_kv_cache *c) {
+  if (!cache) return PA_ERR_INVALID_ARG;
+  *c = *cache;
+  c->k_scale = c->v_scale = 1.f;
+  const pa_status st = check_cache(c);
+  if (st != PA_OK) return st;
+  if (c->kv_dtype != PA_FP8_E4M3) return PA_ERR_UNSUPPORTED;
+  if (!k_scales || !v_scales || !aligned(k_scales, 4) || !aligned(v_scales, 4) || c->k_head_scales) return PA_ERR_INVALID_ARG;
+  const double bytes = 4. * c->num_blocks * c->num_kv_heads;
+  return overlap(k_scales, bytes, v_scales, bytes) ? PA_ERR_INVALID_ARG : PA_OK;
+}
+
 // q dtype must equal the cache dtype, except that an fp8 cache takes f16/bf16 queries.
 pa_status check_q_dtype(pa_dtype q, const pa_kv_cache &c) {
   if (q != PA_F16 && q != PA_BF16) return PA_ERR_UNSUPPORTED;
@@ -241,6 +260,91 @@ pa_status pa_reshape_and_cache(const void *k, const void *v, pa_dtype in_dtype, 
   return launch_reshape_and_cache(k, v, in_dtype, num_tokens, token_stride, slot_mapping, k_cache,
                                   v_cache, *cache, err, reinterpret_cast<cudaStream_t>(stream)) ==
                  cudaSuccess
+             ? PA_OK
+             : PA_ERR_CUDA;
+}
+
+pa_status pa_rope_and_cache(const void *q, int64_t q_stride, void *q_out, int32_t num_q_heads, const void *k,
+                            const void *v, pa_dtype in_dtype, int32_t num_tokens, int64_t token_stride,
+                            const int32_t *positions, const float *cos_sin, int32_t num_positions, int32_t rope_dim,
+                            int32_t interleaved, const int64_t *slot_mapping, void *k_cache, void *v_cache,
+                            const pa_kv_cache *cache, float *k_block_scales, float *v_block_scales,
+                            pa_stream_t stream) {
+  const bool scaled = k_block_scales || v_block_scales;
+  pa_kv_cache c;
+  pa_status st = scaled ? check_scaled_cache(cache, k_block_scales, v_block_scales, &c) : check_cache(cache);
+  if (st != PA_OK) return st;
+  if (!scaled) c = *cache;
+  if (num_tokens < 0 || num_q_heads < 0 || rope_dim < 0) return PA_ERR_INVALID_ARG;
+  if (in_dtype != PA_F16 && in_dtype != PA_BF16) return PA_ERR_UNSUPPORTED;
+  if (c.kv_dtype != PA_FP8_E4M3 && c.kv_dtype != in_dtype) return PA_ERR_UNSUPPORTED;
+  if (rope_dim % 16 || rope_dim > c.head_dim) return PA_ERR_UNSUPPORTED;
+  if ((rope_dim == 0 && num_q_heads > 0) || (rope_dim > 0 && num_positions <= 0)) return PA_ERR_INVALID_ARG;
+  const int64_t q_row = (int64_t)num_q_heads * c.head_dim, kv_row = (int64_t)c.num_kv_heads * c.head_dim;
+  if (token_stride < kv_row || token_stride % 8 || (num_q_heads > 0 && (q_stride < q_row || q_stride % 8)))
+    return PA_ERR_INVALID_ARG;
+  if (num_tokens == 0) return PA_OK;
+  if (!k || !v || !slot_mapping || !aligned(k, 16) || !aligned(v, 16) || !aligned(slot_mapping, 8)) return PA_ERR_INVALID_ARG;
+  if (rope_dim > 0 && (!positions || !cos_sin || !aligned(positions, 4) || !aligned(cos_sin, 16))) return PA_ERR_INVALID_ARG;
+  if ((st = check_pools(k_cache, v_cache)) != PA_OK) return st;
+  if (num_q_heads > 0) {
+    if (!q || !q_out || !aligned(q, 16) || !aligned(q_out, 16)) return PA_ERR_INVALID_ARG;
+    const double out_bytes = 2. * num_tokens * q_row, pool = (double)c.num_blocks * kv_row * c.block_size * dtype_bytes(c.kv_dtype);
+    const double q_bytes = 2. * ((double)(num_tokens - 1) * q_stride + q_row);
+    const double kv_bytes = 2. * ((double)(num_tokens - 1) * token_stride + kv_row);
+    const bool in_place = q == q_out && (q_stride == q_row || num_tokens == 1);
+    if ((!in_place && overlap(q_out, out_bytes, q, q_bytes)) || overlap(q_out, out_bytes, k, kv_bytes) ||
+        overlap(q_out, out_bytes, v, kv_bytes) || overlap(q_out, out_bytes, k_cache, pool) ||
+        overlap(q_out, out_bytes, v_cache, pool))
+      return PA_ERR_INVALID_ARG;
+  }
+  RopeParams p{};
+  p.q = q;
+  p.q_stride = q_stride;
+  p.q_out = q_out;
+  p.num_q_heads = num_q_heads;
+  p.k = k;
+  p.v = v;
+  p.stride = token_stride;
+  p.num_tokens = num_tokens;
+  p.positions = positions;
+  p.table = cos_sin;
+  p.num_positions = num_positions;
+  p.rope = rope_dim;
+  p.interleaved = interleaved != 0;
+  p.slots = slot_mapping;
+  p.k_cache = k_cache;
+  p.v_cache = v_cache;
+  p.num_blocks = c.num_blocks;
+  p.block_size = c.block_size;
+  p.num_kv_heads = c.num_kv_heads;
+  p.head_dim = c.head_dim;
+  p.fp8 = c.kv_dtype == PA_FP8_E4M3;
+  p.k_scale = c.k_scale;
+  p.v_scale = c.v_scale;
+  p.k_hs = c.k_head_scales;
+  p.v_hs = c.v_head_scales;
+  p.k_scales = k_block_scales;
+  p.v_scales = v_block_scales;
+  p.err = device_error_word();
+  if (!p.err) return PA_ERR_CUDA;
+  return launch_rope_and_cache(p, in_dtype, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+pa_status pa_copy_blocks_scaled(void *k_cache, void *v_cache, const pa_kv_cache *cache, float *k_block_scales,
+                                float *v_block_scales, const int32_t *src_dst_pairs, int32_t num_pairs,
+                                pa_stream_t stream) {
+  pa_kv_cache c;
+  pa_status st = check_scaled_cache(cache, k_block_scales, v_block_scales, &c);
+  if (st != PA_OK) return st;
+  if (num_pairs < 0) return PA_ERR_INVALID_ARG;
+  if (num_pairs == 0) return PA_OK;
+  if (!src_dst_pairs || !aligned(src_dst_pairs, 8)) return PA_ERR_INVALID_ARG;
+  if ((st = check_pools(k_cache, v_cache)) != PA_OK) return st;
+  int32_t *err = device_error_word();
+  if (!err) return PA_ERR_CUDA;
+  return launch_copy_blocks_scaled(k_cache, v_cache, c, k_block_scales, v_block_scales, src_dst_pairs, num_pairs, err,
+                                   reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
              ? PA_OK
              : PA_ERR_CUDA;
 }
@@ -574,11 +678,18 @@ struct Weights {
   float decay;
 };
 
+// The scales of a block-scaled cache.
+struct BlockScales {
+  const float *k, *v;
+};
+
+// bs: over a block-scaled cache.
 pa_status bounded_decode(const void *q, pa_dtype q_dtype, int32_t num_seqs, int32_t num_q_heads, const void *k_cache,
                          const void *v_cache, const pa_kv_cache *cache, const int32_t *block_tables,
                          int32_t max_blocks_per_seq, const int32_t *seq_lens, int32_t max_seq_len, int32_t window,
                          int32_t num_sinks, float scale, int32_t partition_size, void *workspace,
-                         size_t workspace_bytes, void *out, pa_dtype out_dtype, const Weights *wt, pa_stream_t stream) {
+                         size_t workspace_bytes, void *out, pa_dtype out_dtype, const Weights *wt,
+                         const BlockScales *bs, pa_stream_t stream) {
   pa_status st = check_decode(q, q_dtype, num_seqs, num_q_heads, k_cache, v_cache, cache, block_tables,
                               max_blocks_per_seq, seq_lens, max_seq_len, scale, partition_size, out, out_dtype);
   if (st != PA_OK) return st;
@@ -606,6 +717,10 @@ pa_status bounded_decode(const void *q, pa_dtype q_dtype, int32_t num_seqs, int3
   tp.shares = b.shares;
   tp.share_heads = b.share_heads;
   tp.direct = b.direct;
+  if (bs) {
+    tp.k_scales = bs->k;
+    tp.v_scales = bs->v;
+  }
   if (wt) {
     tp.scores = reinterpret_cast<float *>(ws + b.scores_off);
     tp.score_stride = b.score_stride;
@@ -615,7 +730,8 @@ pa_status bounded_decode(const void *q, pa_dtype q_dtype, int32_t num_seqs, int3
   if (!encode_decode_tc_maps(&maps, k_cache, v_cache, c)) return PA_ERR_CUDA;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e;
-  if (c.kv_dtype == PA_BF16) e = launch_decode_ext_bf16(tp, c.head_dim, maps, s);
+  if (bs) e = q_dtype == PA_BF16 ? launch_decode_scaled_bf16q(tp, c.head_dim, maps, s) : launch_decode_scaled_f16q(tp, c.head_dim, maps, s);
+  else if (c.kv_dtype == PA_BF16) e = launch_decode_ext_bf16(tp, c.head_dim, maps, s);
   else if (c.kv_dtype == PA_F16) e = launch_decode_ext_f16(tp, c.head_dim, maps, s);
   else if (q_dtype == PA_BF16) e = launch_decode_ext_fp8_bf16q(tp, c.head_dim, maps, s);
   else e = launch_decode_ext_fp8_f16q(tp, c.head_dim, maps, s);
@@ -676,7 +792,28 @@ pa_status pa_decode_window(const void *q, pa_dtype q_dtype, int32_t num_seqs, in
                            size_t workspace_bytes, void *out, pa_dtype out_dtype, pa_stream_t stream) {
   return bounded_decode(q, q_dtype, num_seqs, num_q_heads, k_cache, v_cache, cache, block_tables, max_blocks_per_seq,
                         seq_lens, max_seq_len, window, num_sinks, scale, partition_size, workspace, workspace_bytes,
-                        out, out_dtype, nullptr, stream);
+                        out, out_dtype, nullptr, nullptr, stream);
+}
+
+// no window: the block size does not matter
+size_t pa_decode_scaled_workspace_bytes(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                                        int32_t max_seq_len, int32_t partition_size) {
+  return bounded_workspace(num_seqs, num_q_heads, num_kv_heads, head_dim, 16, max_seq_len, INT32_MAX, 0, partition_size,
+                           false);
+}
+
+pa_status pa_decode_scaled(const void *q, pa_dtype q_dtype, int32_t num_seqs, int32_t num_q_heads, const void *k_cache,
+                           const void *v_cache, const pa_kv_cache *cache, const float *k_block_scales,
+                           const float *v_block_scales, const int32_t *block_tables, int32_t max_blocks_per_seq,
+                           const int32_t *seq_lens, int32_t max_seq_len, float scale, int32_t partition_size,
+                           void *workspace, size_t workspace_bytes, void *out, pa_dtype out_dtype, pa_stream_t stream) {
+  pa_kv_cache c;
+  const pa_status st = check_scaled_cache(cache, k_block_scales, v_block_scales, &c);
+  if (st != PA_OK) return st;
+  const BlockScales bs{k_block_scales, v_block_scales};
+  return bounded_decode(q, q_dtype, num_seqs, num_q_heads, k_cache, v_cache, &c, block_tables, max_blocks_per_seq,
+                        seq_lens, max_seq_len, INT32_MAX, 0, scale, partition_size, workspace, workspace_bytes, out,
+                        out_dtype, nullptr, &bs, stream);
 }
 
 size_t pa_evict_workspace_bytes(int32_t num_seqs, int32_t num_kv_heads, int32_t max_seq_len, int32_t budget) {
@@ -764,7 +901,7 @@ pa_status pa_decode_weights(const void *q, pa_dtype q_dtype, int32_t num_seqs, i
   const Weights wt{weights, weights_stride, num_weight_rows, weight_rows, fresh_from, decay};
   return bounded_decode(q, q_dtype, num_seqs, num_q_heads, k_cache, v_cache, cache, block_tables, max_blocks_per_seq,
                         seq_lens, max_seq_len, INT32_MAX, 0, scale, partition_size, workspace, workspace_bytes, out,
-                        out_dtype, &wt, stream);
+                        out_dtype, &wt, nullptr, stream);
 }
 
 }  // extern "C"
@@ -930,6 +1067,37 @@ pa_status pa_prefill_chunk_window(const void *q_chunk, pa_dtype q_dtype, const i
   else if (c.kv_dtype == PA_F16) e = launch_prefill_window_f16(t, maps, c.head_dim, num_chunks, s);
   else if (q_dtype == PA_BF16) e = launch_prefill_window_fp8_bf16q(t, maps, c.head_dim, num_chunks, s);
   else e = launch_prefill_window_fp8_f16q(t, maps, c.head_dim, num_chunks, s);
+  return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+pa_status pa_prefill_chunk_scaled(const void *q_chunk, pa_dtype q_dtype, const int32_t *cu_q_lens,
+                                  const int32_t *q_start, int32_t num_chunks, int32_t max_q_len, int32_t num_q_heads,
+                                  const void *k_cache, const void *v_cache, const pa_kv_cache *cache,
+                                  const float *k_block_scales, const float *v_block_scales,
+                                  const int32_t *block_tables, int32_t max_blocks_per_seq, const int32_t *seq_lens,
+                                  int32_t max_seq_len, float scale, void *out, pa_dtype out_dtype, pa_stream_t stream) {
+  pa_kv_cache c;
+  pa_status st = check_scaled_cache(cache, k_block_scales, v_block_scales, &c);
+  if (st != PA_OK) return st;
+  bool empty = false, use_tc = false;
+  PrefillTcParams t{};
+  st = prefill_prepare(q_chunk, q_dtype, cu_q_lens, q_start, num_chunks, max_q_len, num_q_heads, k_cache, v_cache, &c,
+                       block_tables, max_blocks_per_seq, seq_lens, max_seq_len, scale, out, out_dtype, &empty, &use_tc,
+                       &t, true);
+  if (st != PA_OK || empty) return st;
+  const int gqa = num_q_heads / c.num_kv_heads;
+  t.window = INT32_MAX;
+  t.shares = (gqa + kPrefillWindowHeads - 1) / kPrefillWindowHeads;
+  t.share_heads = (gqa + t.shares - 1) / t.shares;
+  t.k_scales = k_block_scales;
+  t.v_scales = v_block_scales;
+  t.err = device_error_word();
+  if (!t.err) return PA_ERR_CUDA;
+  PoolMaps maps{};
+  if (!encode_decode_tc_maps(&maps, k_cache, v_cache, c)) return PA_ERR_CUDA;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const cudaError_t e = q_dtype == PA_BF16 ? launch_prefill_scaled_bf16q(t, maps, c.head_dim, num_chunks, s)
+                                           : launch_prefill_scaled_f16q(t, maps, c.head_dim, num_chunks, s);
   return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 

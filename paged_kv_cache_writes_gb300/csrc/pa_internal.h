@@ -171,6 +171,10 @@ cudaError_t launch_decode_ext_f16(const DecodeTcParams &p, int head_dim, const P
 cudaError_t launch_decode_ext_fp8_bf16q(const DecodeTcParams &p, int head_dim, const PoolMaps &m, cudaStream_t s);
 cudaError_t launch_decode_ext_fp8_f16q(const DecodeTcParams &p, int head_dim, const PoolMaps &m, cudaStream_t s);
 
+// The same over a block-scaled cache (pa_decode_scaled).
+cudaError_t launch_decode_scaled_bf16q(const DecodeTcParams &p, int head_dim, const PoolMaps &m, cudaStream_t s);
+cudaError_t launch_decode_scaled_f16q(const DecodeTcParams &p, int head_dim, const PoolMaps &m, cudaStream_t s);
+
 // Bounded-cache decodes of at most kDirectRows rows and kDirectUnits units (row,
 // partition, KV head share), counted at the longest row, run without the plan kernel and its
 // scheduling (pa_decode_tc.cuh, `direct`).  Measured, plan against direct: one
@@ -246,6 +250,41 @@ struct EvictParams {
 };
 cudaError_t launch_evict(const EvictParams &p, cudaStream_t s);
 
+// Block-scaled fp8 caches: one fp32 scale per block and KV head, in [2^-64, 2^32].  The attention kernels weight V's codes by
+// 2^(score + log2 scale - maximum) and sum 2^(...) / scale: with scales at most 2^96 apart a weight of 2^-30 of the softmax's
+// largest is still a normal fp32 number.
+constexpr int kMinScaleExp = -64, kMaxScaleExp = 32;
+__host__ __device__ __forceinline__ bool block_scale_ok(float s) {
+  return s >= 5.421010862427522e-20f && s <= 4294967296.f;   // 2^-64, 2^32 (false for NaN)
+}
+
+// Rotation and cache write of a step's new tokens (pa_rope.cu).
+struct RopeParams {
+  const void *q;              // [num_tokens] rows of q_stride elements
+  int64_t q_stride;
+  void *q_out;                // [num_tokens][num_q_heads][head_dim]
+  int32_t num_q_heads;        // 0: none
+  const void *k, *v;          // rows of `stride` elements
+  int64_t stride;
+  int32_t num_tokens;
+  const int32_t *positions;
+  const float *table;         // [num_positions][rope]: cosines, sines
+  int32_t num_positions, rope;
+  bool interleaved;
+  const int64_t *slots;
+  void *k_cache, *v_cache;
+  int64_t num_blocks;
+  int32_t block_size, num_kv_heads, head_dim;
+  bool fp8;
+  float k_scale, v_scale;     // fp8: fixed scales, or per head, or per block and head
+  const float *k_hs, *v_hs;
+  float *k_scales, *v_scales;
+  int32_t *err;
+};
+cudaError_t launch_rope_and_cache(const RopeParams &p, pa_dtype in_dtype, cudaStream_t s);
+cudaError_t launch_copy_blocks_scaled(void *k_cache, void *v_cache, const pa_kv_cache &c, float *k_scales, float *v_scales,
+                                      const int32_t *pairs, int32_t num_pairs, int32_t *err, cudaStream_t s);
+
 // One launch for a prefill chunk batch and a decode batch (pa_mixed_tc.cuh):
 // both on the tensor cores, head_dim 128, 4 or 8 query heads per KV head.
 constexpr bool mixed_tc_supported(int head_dim, int gqa) { return head_dim == 128 && (gqa == 4 || gqa == 8); }
@@ -281,5 +320,10 @@ cudaError_t launch_prefill_window_fp8_bf16q(const PrefillTcParams &p, const Pool
                                             cudaStream_t s);
 cudaError_t launch_prefill_window_fp8_f16q(const PrefillTcParams &p, const PoolMaps &m, int head_dim, int num_chunks,
                                            cudaStream_t s);
+// The same over a block-scaled cache (pa_prefill_chunk_scaled).
+cudaError_t launch_prefill_scaled_bf16q(const PrefillTcParams &p, const PoolMaps &m, int head_dim, int num_chunks,
+                                        cudaStream_t s);
+cudaError_t launch_prefill_scaled_f16q(const PrefillTcParams &p, const PoolMaps &m, int head_dim, int num_chunks,
+                                       cudaStream_t s);
 
 }  // namespace pa
