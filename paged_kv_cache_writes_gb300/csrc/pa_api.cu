@@ -1086,18 +1086,17 @@ pa_status pa_prefill_chunk_scaled(const void *q_chunk, pa_dtype q_dtype, const i
                        &t, true);
   if (st != PA_OK || empty) return st;
   const int gqa = num_q_heads / c.num_kv_heads;
-  t.window = INT32_MAX;
   t.shares = (gqa + kPrefillWindowHeads - 1) / kPrefillWindowHeads;
   t.share_heads = (gqa + t.shares - 1) / t.shares;
   t.k_scales = k_block_scales;
   t.v_scales = v_block_scales;
   t.err = device_error_word();
   if (!t.err) return PA_ERR_CUDA;
-  PoolMaps maps{};
-  if (!encode_decode_tc_maps(&maps, k_cache, v_cache, c)) return PA_ERR_CUDA;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const cudaError_t e = q_dtype == PA_BF16 ? launch_prefill_scaled_bf16q(t, maps, c.head_dim, num_chunks, s)
-                                           : launch_prefill_scaled_f16q(t, maps, c.head_dim, num_chunks, s);
+  CUtensorMap k{};
+  if (!encode_pool_map_fp8_blocks(&k, k_cache, c)) return PA_ERR_CUDA;
+  const cudaError_t e = q_dtype == PA_BF16 ? launch_prefill_scaled_bf16q(t, k, c.head_dim, num_chunks, s)
+                                           : launch_prefill_scaled_f16q(t, k, c.head_dim, num_chunks, s);
   return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 

@@ -320,10 +320,10 @@ cudaError_t launch_prefill_window_fp8_bf16q(const PrefillTcParams &p, const Pool
                                             cudaStream_t s);
 cudaError_t launch_prefill_window_fp8_f16q(const PrefillTcParams &p, const PoolMaps &m, int head_dim, int num_chunks,
                                            cudaStream_t s);
-// The same over a block-scaled cache (pa_prefill_chunk_scaled).
-cudaError_t launch_prefill_scaled_bf16q(const PrefillTcParams &p, const PoolMaps &m, int head_dim, int num_chunks,
+// Chunked prefill over a block-scaled cache (pa_prefill_scaled.cuh), groups in shares as for the window.
+cudaError_t launch_prefill_scaled_bf16q(const PrefillTcParams &p, const CUtensorMap &k, int head_dim, int num_chunks,
                                         cudaStream_t s);
-cudaError_t launch_prefill_scaled_f16q(const PrefillTcParams &p, const PoolMaps &m, int head_dim, int num_chunks,
+cudaError_t launch_prefill_scaled_f16q(const PrefillTcParams &p, const CUtensorMap &k, int head_dim, int num_chunks,
                                        cudaStream_t s);
 
 }  // namespace pa

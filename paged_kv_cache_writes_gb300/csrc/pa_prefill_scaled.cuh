@@ -1,0 +1,744 @@
+// pa_prefill_scaled.cuh -- chunked-prefill attention over a block-scaled fp8
+// cache (pa_prefill_chunk_scaled) on the 5th-generation tensor cores.
+//
+// Row r of chunk c, at position t = q_start[c] + r, query head h of KV head g:
+//   out = sum_p w_p v_p / sum_p w_p / sv_p  over p <= t,
+//   w_p = 2^(a_p + log2 sv_p - m),  a_p = scale log2(e) (q . k_p) sk_p,
+// k_p, v_p the codes' values, sk_p, sv_p the scales of their block and head, m a
+// running maximum of a_p + log2 sv_p.  K's scale multiplies the scores and V's is
+// an addend of the exponent, so that both products take the codes as they are;
+// the sum takes 1 / sv_p, in fp32, from unrounded w: a token whose values are
+// tiny may hold most of the softmax.  A run of 16 keys lies in one block.
+//
+// Operands.  V's codes are widened to f16, exactly, on their way into shared memory, and w is rounded once to f16 for a
+// 16-bit output (kLo false), else taken as hi + lo.  K, for bf16 queries and a bf16 output (raw_k): the codes as stored
+// (kind::f8f6f4), a query row being two e4m3 terms of its elements times a power of two that puts the largest in [128,
+// 256): elements down to 2^-9 of it are exact, smaller ones off by 2^-17 of it at most.  Otherwise K is widened too, and
+// bf16 query rows are multiplied by a power of two that puts their largest element in [2^14, 2^15) and rounded to f16,
+// exact for every element above 2^-28 of it.  (Raw K tiles come by bulk copies and cost no warp anything; widening takes
+// a warp some 200 instructions per tile.)
+//
+// One CTA per SM, two teams.  A team is 128 softmax threads (thread m owns packed
+// row m: token m / heads, head m % heads), a score buffer and an O accumulator in
+// tensor memory (2 x 128 + 2 x head_dim columns): while one team's softmax works,
+// the tensor cores have the other team's P.V and Q.K^T.
+//  * kSplitKeys false: the teams have two Q tiles of 128 packed rows and walk the
+//    same key tiles (128 keys), each of which is widened once for both.
+//  * kSplitKeys true (few rows: two Q tiles per CTA would leave SMs idle): both
+//    teams have the same Q tile, team 0 the even key tiles and team 1 the odd
+//    ones; their results are joined by their maxima through shared memory.
+//
+// P (f16 pairs) goes over the score buffer's first 64 columns (hi + lo: over all of it), keys 0..63 first, whose P.V starts
+// when they are there; the next tile's scores wait for the P.V that reads P.
+//
+// Registers: launched with 128 a thread, of which the loaders and the MMA warp's group give to the softmax (184), whose
+// threads hold their row's 128 scores: one pass over tensor memory instead of two.
+//
+// Loaders: four warps, 32 keys of a tile each, a key tile ahead in registers (8-byte loads, a row of codes per 8 lanes),
+// widened into the MMAs' 128-byte-swizzled panels.  Codes staged by bulk copies instead would cost shared memory's
+// bandwidth twice more, and that is what the MMAs are short of: an SS MMA of 128 x 128 x 16 reads 8 KB in 64 clocks.
+// Raw K tiles: one bulk-tensor box per cache block, by a warp of its own.
+//
+// Every mbarrier wait is bounded (PA_ERR_TIMEOUT, then the CTA abandons its work).
+#pragma once
+
+#include <type_traits>
+
+#include "pa_common.cuh"
+#include "pa_internal.h"
+#include "pa_prefill_tc.cuh"
+#include "pa_tcgen05.cuh"
+
+namespace pa {
+namespace psc {
+
+constexpr int kM = 128, kN = 128;              // packed rows per Q tile, keys per tile
+constexpr int kTeams = 2, kSoftmax = kTeams * 128;
+constexpr int kLoadWarp0 = kSoftmax / 32, kLoaders = 128, kMmaWarp = kLoadWarp0 + 4, kKWarp = kMmaWarp + 1;
+constexpr int kThreads = 512;                  // four warpgroups: a team's softmax each, the loaders, the MMA warp
+constexpr int kSoftmaxRegs = 168, kLoadRegs = 112, kMmaRegs = 64;
+static_assert(2 * kSoftmaxRegs + kLoadRegs + kMmaRegs == 4 * 128, "the launch's registers");
+constexpr int kPanel = kN * 128;               // 64 elements of 128 rows
+constexpr float kRescaleLog2 = 8.f;            // O is rescaled when the maximum exceeds its reference by 2^8
+
+// K as stored for bf16 queries and outputs.
+template <typename QT, bool kLo>
+constexpr bool raw_k() {
+  return std::is_same<QT, __nv_bfloat16>::value && !kLo;
+}
+
+template <int D, bool kSplitKeys, bool kRaw>
+struct Layout {
+  static constexpr int kTile = kN * D * 2;                     // a Q or V tile (Q: f16, or two terms of codes)
+  static constexpr int kKTile = kRaw ? kN * D : kTile;
+  static constexpr int kStages = 2, kKStages = kRaw ? 3 : 2;   // V, K tiles in flight
+  static constexpr int kOffQ = 0;
+  static constexpr int kOffK = kOffQ + (kSplitKeys ? 1 : 2) * kTile;
+  static constexpr int kOffV = kOffK + kKStages * kKTile;
+  static constexpr int kOffBar = kOffV + kStages * kTile;
+  static constexpr int kNumBars = 2 * kStages + 2 * kKStages + 4 * kTeams + 2;
+  static constexpr int kOffMisc = kOffBar + kNumBars * 8;
+  static constexpr int kOffRow = kOffMisc + 16;                // float2 [kTeams][128]
+  static constexpr int kOffRuns = kOffRow + kTeams * 128 * 8;  // float4 [softmax warp][2][8 runs]
+  static constexpr int kBytes = kOffRuns + kSoftmax / 32 * 2 * 8 * 16 + 1024;   // + alignment slack
+  static_assert(kBytes <= 227 * 1024 && kOffRow % 8 == 0 && kOffRuns % 16 == 0, "shared memory");
+  static constexpr int kStage = kOffBar - kSoftmax / 32 * 4096;   // kSplitKeys: 4 KB per softmax warp for the output's way
+  static_assert(kOffV % 1024 == 0 && (!kSplitKeys || kStage >= 128 * D * 4), "room for the teams' halves of O before it");
+};
+
+__device__ __forceinline__ uint2 ld_nc8(const void *p) {
+  uint2 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+  return v;
+}
+// 8 e4m3 codes -> 8 f16 values, exactly.
+__device__ __forceinline__ uint4 widen8(uint2 w) {
+  auto two = [](uint32_t x) {
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(x & 0xffffu), __NV_E4M3);
+    return *reinterpret_cast<const uint32_t *>(&h);
+  };
+  return make_uint4(two(w.x), two(w.x >> 16), two(w.y), two(w.y >> 16));
+}
+
+template <typename QT, int D, bool kSplitKeys, bool kLo>
+__global__ void __launch_bounds__(kThreads, 1)
+    prefill_scaled_kernel(const PrefillTcParams p, int num_chunks, const __grid_constant__ CUtensorMap tmap_k) {
+  using namespace tc;
+  constexpr bool kRaw = raw_k<QT, kLo>();
+  using L = Layout<D, kSplitKeys, kRaw>;
+  constexpr int kStages = L::kStages, kKStages = L::kKStages, kTile = L::kTile, kKTile = L::kKTile;
+  constexpr bool kBf16 = std::is_same<QT, __nv_bfloat16>::value;
+  const float kNegInf = -__int_as_float(0x7f800000);
+
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L::kOffBar);
+  uint64_t *v_full = bars;                       // [kStages] a tile is widened (128 loader arrivals)
+  uint64_t *v_free = v_full + kStages;           // [kStages] the MMAs that read it are complete
+  uint64_t *k_full = v_free + kStages;           // [kKStages] the same of K (raw: one expect-tx arrival)
+  uint64_t *k_free = k_full + kKStages;
+  uint64_t *s_full = k_free + kKStages;          // [team] scores of its step i (phase i)
+  uint64_t *p_full = s_full + kTeams;            // [half][team] P of keys 0..63, of keys 64..127 written (128 arrivals)
+  uint64_t *o_done = p_full + 2 * kTeams;        // [team] P.V of step i complete
+  uint64_t *q_ready = o_done + kTeams;
+  uint64_t *fin = q_ready + 1;                   // every MMA of the CTA complete
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::kOffMisc);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::kOffMisc + 8);
+  float2 *row_info = reinterpret_cast<float2 *>(smem + L::kOffRow);
+
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  // work item: KV head share fastest, then chunk, then row block from the last (longest) one down
+  const int gy = p.num_kv_heads * p.shares, by = blockIdx.x % gy, rest = blockIdx.x / gy;
+  const int c = rest % num_chunks, rb = p.row_blocks - 1 - rest / num_chunks;
+  const int g = by / p.shares, gr = p.share_heads, h_first = (by - g * p.shares) * gr;
+  const int gqa = p.num_q_heads / p.num_kv_heads;
+  const int BR = kM / gr;                        // token rows per Q tile
+  const int cu0 = __ldg(p.cu_q_lens + c), nrows = __ldg(p.cu_q_lens + c + 1) - cu0, qs = __ldg(p.q_start + c);
+  if (tid == 0 && by == 0 && rb == 0) {
+    const int64_t len = (int64_t)qs + nrows;
+    if (nrows < 0 || nrows > p.max_q_len || qs < 0 || __ldg(p.seq_lens + c) != len ||
+        len > (int64_t)p.max_blocks_per_seq * p.block_size)
+      record_error(p.err, PA_ERR_DEVICE_CHECK);
+  }
+  const int r0 = rb * BR * (kSplitKeys ? 1 : kTeams);
+  if (r0 >= nrows) return;   // whole CTA, before any barrier or tensor memory
+  const int64_t cap = (int64_t)p.max_blocks_per_seq * p.block_size, len64 = (int64_t)qs + nrows;
+  const int seq_eff = len64 <= 0 ? 0 : (int)(len64 < cap ? len64 : cap);
+  const int bs_log2 = p.block_size == 32 ? 5 : 4;
+  const int32_t *table = p.block_tables + (int64_t)c * p.max_blocks_per_seq;
+  // key tiles of a team's Q tile, of the CTA, and a team's steps: step i of team t is key tile tile_of(t, i)
+  auto key_tiles = [&](int t) {
+    const int first = r0 + (kSplitKeys ? 0 : t * BR);
+    if (first >= nrows) return 0;
+    return (min(seq_eff, max(0, qs + min(first + BR, nrows))) + kN - 1) / kN;
+  };
+  const int n0 = key_tiles(0), n1 = key_tiles(1), nkt = max(n0, n1);
+  auto steps = [&](int t) { return kSplitKeys ? (n0 + 1 - t) / 2 : t ? n1 : n0; };
+  auto tile_of = [&](int t, int i) { return kSplitKeys ? 2 * i + t : i; };
+
+  if (tid == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&v_full[s], kLoaders);
+      mbar_init(&v_free[s], 1);
+    }
+    for (int s = 0; s < kKStages; ++s) {
+      mbar_init(&k_full[s], kRaw ? 1 : kLoaders);
+      mbar_init(&k_free[s], 1);
+    }
+    for (int t = 0; t < kTeams; ++t) {
+      mbar_init(&s_full[t], 1);
+      mbar_init(&p_full[t], 128);
+      mbar_init(&p_full[kTeams + t], 128);
+      mbar_init(&o_done[t], 1);
+    }
+    mbar_init(q_ready, kSplitKeys ? 128 : kSoftmax);
+    mbar_init(fin, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == kMmaWarp) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(tmem_slot)));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  auto sbuf = [&](int t) { return tmem + (uint32_t)(t * kN); };
+  auto obuf = [&](int t) { return tmem + (uint32_t)(kTeams * kN + t * D); };
+  auto wait_all = [&](uint64_t *bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, mbar_try_wait(bar, parity) || wait_or_abort(bar, parity, p.err, abort_flag));
+  };
+
+  if (warp < kLoadWarp0) {
+    // ===================================================== softmax
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+    const int team = warp >> 2, quad = warp & 3, m = tid & 127;
+    const int tile0 = r0 + (kSplitKeys ? 0 : team * BR);         // the Q tile's first token row
+    const int rl = m / gr, hq = m - rl * gr;
+    const bool row_ok = tile0 + rl < nrows && rl < BR && h_first + hq < gqa;
+    const int64_t row_elem = row_ok ? ((int64_t)(cu0 + tile0 + rl) * p.num_q_heads + g * gqa + h_first + hq) * D : -1;
+    // the row sees keys < lim (idle rows, with q = 0, all of them: they are not stored)
+    const int lim = row_ok ? min(seq_eff, max(0, qs + tile0 + rl + 1)) : 1 << 30;
+    const uint32_t lane_base = (uint32_t)(quad * 32) << 16;
+    // scores are scaled by |s_mult| in the exponent; a negative scale flips q's sign instead.  A masked score of
+    // -inf has to stay -inf whatever the scale (a scale of 0 gives scores of about 0).
+    float cmul = fmaxf(fabsf(p.s_mult), 1e-30f);
+    const uint32_t qflip = p.s_mult < 0.f ? 0x80008000u : 0u;
+    auto both_sync = [&]() { asm volatile("bar.sync 1, %0;" ::"n"(kSoftmax) : "memory"); };
+    {
+      // Stage Q: a warp brings its own 32 rows, kC lanes of 16 bytes per row (kSplitKeys: team 0 for both)
+      constexpr int kC = D / 8, kRI = 32 / kC;
+      if (!kSplitKeys || team == 0) {
+        uint4 v[kC];
+#pragma unroll
+        for (int i = 0; i < kC; ++i) {
+          const int64_t e = __shfl_sync(0xffffffffu, row_elem, i * kRI + lane / kC);
+          // (idle rows read row 0, and are zeroed: a branch around each load would wait for it)
+          v[i] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const QT *>(p.q) + max(e, (int64_t)0)) + lane % kC);
+        }
+#pragma unroll
+        for (int i = 0; i < kC; ++i)
+          if (__shfl_sync(0xffffffffu, (int)row_ok, i * kRI + lane / kC) == 0) v[i] = make_uint4(0, 0, 0, 0);
+        uint8_t *qt = smem + L::kOffQ + (kSplitKeys ? 0 : team * kTile);
+#pragma unroll
+        for (int i = 0; i < kC; ++i) {
+          const int mr = quad * 32 + i * kRI + lane / kC, ch = lane % kC;
+          uint32_t ws[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+          float back = 1.f;
+          if constexpr (kBf16) {
+            // the row times 2^e: its largest element in [128, 256), or [2^14, 2^15)
+            float amax = 0.f;
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              amax = fmaxf(amax, fmaxf(__uint_as_float((ws[k] << 16) & 0x7fffffffu), __uint_as_float(ws[k] & 0x7fff0000u)));
+#pragma unroll
+            for (int off = kC / 2; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
+            const int eb = max(1, (int)((__float_as_uint(amax) >> 23) & 0xff));
+            const int e = amax > 0.f ? max(-126, min(126, (kRaw ? 134 : 141) - eb)) : 0;
+            const float sc = __uint_as_float((uint32_t)(e + 127) << 23);
+            back = __uint_as_float((uint32_t)(127 - e) << 23);   // 2^-e
+            if constexpr (kRaw) {
+              const float sign = p.s_mult < 0.f ? -sc : sc;
+              uint32_t hi[4], lo[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const float2 f = unpack2(ws[k], __nv_bfloat16{});
+                const float2 x = make_float2(f.x * sign, f.y * sign);
+                hi[k] = __nv_cvt_float2_to_fp8x2(x, __NV_SATFINITE, __NV_E4M3);
+                const float2 h = unpack2_e4m3(hi[k]);
+                lo[k] = __nv_cvt_float2_to_fp8x2(make_float2(x.x - h.x, x.y - h.y), __NV_SATFINITE, __NV_E4M3);
+              }
+              // 8 bytes of a D-byte row, in the 128- or 64-byte swizzle
+              const int at = mr * D + (((ch >> 1) ^ (D == 128 ? mr & 7 : (mr >> 1) & 3)) << 4) + (ch & 1) * 8;
+              *reinterpret_cast<uint2 *>(qt + at) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
+              *reinterpret_cast<uint2 *>(qt + kM * D + at) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
+            } else {
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const float2 f = unpack2(ws[k], __nv_bfloat16{});
+                const __half2 h = __floats2half2_rn(f.x * sc, f.y * sc);
+                ws[k] = *reinterpret_cast<const uint32_t *>(&h);
+              }
+            }
+          }
+          if (ch == 0) {
+            row_info[(kSplitKeys ? 0 : team * 128) + mr].x = back;
+            if (kSplitKeys) row_info[128 + mr].x = back;
+          }
+          if constexpr (!kRaw)
+            *reinterpret_cast<uint4 *>(qt + (ch >> 3) * kPanel + mr * 128 + (((ch & 7) ^ (mr & 7)) << 4)) =
+                make_uint4(ws[0] ^ qflip, ws[1] ^ qflip, ws[2] ^ qflip, ws[3] ^ qflip);
+        }
+        fence_async_smem();
+        mbar_arrive(q_ready);
+      }
+      if (kSplitKeys) both_sync();
+      else __syncwarp();   // a warp's rows are staged by itself
+      cmul = fmaxf(cmul * row_info[team * 128 + m].x, 1e-30f);
+    }
+
+    // scales of this team's steps: lane i < 8 has those of run i (16 keys) of the next tile in flight (their block ids a
+    // step before that), and leaves them in shared memory for the warp when the tile is at hand
+    const int n = steps(team);
+    float next_k = 1.f, next_v = 1.f;
+    int32_t next_blk = -1;
+    auto run_block = [&](int i) -> int32_t {   // (an id out of range is reported by the loaders)
+      const int key = tile_of(team, i) * kN + 16 * lane;
+      if (lane >= 8 || i >= n || key >= seq_eff) return -1;
+      const int32_t bi = __ldg(table + (key >> bs_log2));
+      return bi >= 0 && bi < p.num_blocks ? bi : -1;
+    };
+    auto read_scales = [&](int32_t bi) {
+      next_k = next_v = 1.f;
+      if (bi >= 0) {
+        next_k = __ldg(p.k_scales + (int64_t)bi * p.num_kv_heads + g);
+        next_v = __ldg(p.v_scales + (int64_t)bi * p.num_kv_heads + g);
+      }
+    };
+    read_scales(run_block(0));
+    next_blk = run_block(1);
+    float4 *runs = reinterpret_cast<float4 *>(smem + L::kOffRuns) + warp * 16;
+
+    float m_ref = kNegInf;                       // reference maximum, log2 units
+    float2 lacc = make_float2(0.f, 0.f);         // row sum in two parts
+    const float2 ones = make_float2(1.f, 1.f);
+    bool ok = true;
+    const uint32_t sb = sbuf(team) + lane_base, ob = obuf(team) + lane_base;
+    for (int i = 0; i < n; ++i) {
+      if (lane < 8) {
+        const bool good = block_scale_ok(next_k) && block_scale_ok(next_v);
+        if (!good) record_error(p.err, PA_ERR_DEVICE_CHECK);
+        runs[(i & 1) * 8 + lane] = good ? make_float4(next_k, __log2f(next_v), __frcp_rn(next_v), 0.f) : make_float4(1.f, 0.f, 1.f, 0.f);
+      }
+      __syncwarp();
+      read_scales(next_blk);
+      next_blk = run_block(i + 2);
+      ok = wait_all(&s_full[team], i & 1);
+      if (!ok) break;
+      tc_fence_after();
+      float v[4][32];
+#pragma unroll
+      for (int ck = 0; ck < 4; ++ck) tmem_ld32_start(sb + 32 * ck, v[ck]);
+      // run r's score factor, log2 units (not 0: a masked score stays -inf), log2 of V's scale and 1 / V's scale; read
+      // for each pass, which has no registers to spare
+      const float4 *run = runs + (i & 1) * 8;
+      auto factor_of = [&](const float4 &x) { return fmaxf(cmul * x.x, 1e-37f); };
+#pragma unroll
+      for (int ck = 0; ck < 4; ++ck) tmem_ld32_finish(v[ck]);
+      const int nvis = lim - tile_of(team, i) * kN;
+      if (!__all_sync(0xffffffffu, nvis >= kN)) {
+#pragma unroll
+        for (int ck = 0; ck < 4; ++ck)
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            if (32 * ck + e >= nvis) v[ck][e] = kNegInf;
+      }
+      // maximum of a + log2 sv over the tile
+      float mt = kNegInf;
+#pragma unroll
+      for (int r = 0; r < 8; ++r) {
+        const float *x = &v[r >> 1][16 * (r & 1)];
+        float a = fmax3(x[0], x[1], x[2]), b = fmax3(x[3], x[4], x[5]);
+        a = fmax3(a, x[6], x[7]), b = fmax3(b, x[8], x[9]);
+        a = fmax3(a, x[10], x[11]), b = fmax3(b, x[12], x[13]);
+        const float4 sc = run[r];
+        mt = fmaxf(mt, fmaf(fmax3(fmaxf(a, b), x[14], x[15]), factor_of(sc), sc.y));
+      }
+      const bool rescale = mt > m_ref + kRescaleLog2;
+      if (__any_sync(0xffffffffu, rescale)) {
+        const float alpha = rescale ? fast_exp2(m_ref - mt) : 1.f;
+        if (i > 0) {   // (these scores came after the P.V of step i - 1 was complete)
+#pragma unroll 1
+          for (int c0 = 0; c0 < D; c0 += 16) {
+            float o[16];
+            uint32_t ow[16];
+            tmem_ld16(ob + c0, o);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) ow[e] = __float_as_uint(o[e] * alpha);
+            tmem_st16(ob + c0, ow);
+          }
+        }
+        if (rescale) {
+          lacc = make_float2(lacc.x * alpha, lacc.y * alpha);
+          m_ref = mt;
+        }
+      }
+      const float msub = m_ref == kNegInf ? 0.f : m_ref;
+      // w = 2^(a + log2 sv - m_ref), rounded to f16, and the sum of w / sv
+#pragma unroll
+      for (int r = 0; r < 8; ++r) {
+        const float *x = &v[r >> 1][16 * (r & 1)];
+        const float4 sc = run[r];
+        const float cr = factor_of(sc), nr = sc.y - msub, iv = sc.z;
+        const float2 cc = make_float2(cr, cr), nm = make_float2(nr, nr);
+        float2 sum[2] = {{0.f, 0.f}, {0.f, 0.f}};
+        uint32_t w[8], wl[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const float2 a = ffma2(make_float2(x[2 * k], x[2 * k + 1]), cc, nm);
+          const float2 pk = make_float2(fast_exp2(a.x), fast_exp2(a.y));
+          if constexpr (kLo) w[k] = f16x2_split(pk.x, pk.y, wl[k]);
+          else asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w[k]) : "f"(pk.y), "f"(pk.x));
+          sum[k & 1] = ffma2(pk, ones, sum[k & 1]);
+        }
+        lacc = ffma2(make_float2(sum[0].x + sum[1].x, sum[0].y + sum[1].y), make_float2(iv, iv), lacc);
+        if constexpr (kLo) {   // hi, lo of 16 keys over their own 16 columns
+          tmem_st8(sb + 16 * r, w);
+          tmem_st8(sb + 16 * r + 8, wl);
+        } else {
+          tmem_st8(sb + 8 * r, w);
+        }
+        if (r == 3 || r == 7) {
+          tmem_wait_st();
+          tc_fence_before();
+          mbar_arrive(&p_full[(r >> 2) * kTeams + team]);
+        }
+      }
+    }
+    float l = lacc.x + lacc.y;
+    if (ok && n > 0) ok = wait_all(&o_done[team], (n - 1) & 1);
+    tc_fence_after();
+    // Columns [c0, c1) of the row, kCols at a time through `value`, normalised by inv and stored by 8 (or 4) lanes per
+    // row: the threads write 128 bytes of their rows into the warp's 4 KB (16-byte chunk c of row r at chunk c ^ (r & 7))
+    auto emit = [&](auto f32, uint8_t *stage, int c0, int c1, float inv, auto &&value) {
+      constexpr bool kF32 = decltype(f32)::value;
+      constexpr int kCols = 32, kCh = kCols * (kF32 ? 4 : 2) / 16, kRI = 32 / kCh;
+      int64_t e[kCh];
+#pragma unroll
+      for (int i = 0; i < kCh; ++i) e[i] = __shfl_sync(0xffffffffu, row_elem, i * kRI + lane / kCh);
+#pragma unroll 1
+      for (int at = c0; at < c1; at += kCols) {
+        float o[32];
+        value(at, o);
+#pragma unroll
+        for (int i = 0; i < kCh; ++i) {
+          uint4 x;
+          if constexpr (kF32) {
+            x = make_uint4(__float_as_uint(o[4 * i] * inv), __float_as_uint(o[4 * i + 1] * inv),
+                           __float_as_uint(o[4 * i + 2] * inv), __float_as_uint(o[4 * i + 3] * inv));
+          } else {
+            const float *v = o + 8 * i;
+            x = make_uint4(pack2(v[0] * inv, v[1] * inv, QT{}), pack2(v[2] * inv, v[3] * inv, QT{}),
+                           pack2(v[4] * inv, v[5] * inv, QT{}), pack2(v[6] * inv, v[7] * inv, QT{}));
+          }
+          *reinterpret_cast<uint4 *>(stage + lane * 128 + ((i ^ (lane & 7)) << 4)) = x;
+        }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < kCh; ++i) {
+          const int r = i * kRI + lane / kCh, ch = lane % kCh;
+          const uint4 x = *reinterpret_cast<const uint4 *>(stage + r * 128 + ((ch ^ (r & 7)) << 4));
+          if (e[i] >= 0)
+            *reinterpret_cast<uint4 *>(static_cast<char *>(p.out) + (e[i] + at) * (kF32 ? 4 : 2) + ch * 16) = x;
+        }
+        __syncwarp();
+      }
+    };
+    auto load_o = [&](int at, float (&o)[32]) {
+      if (n > 0) {
+        tmem_ld32_start(ob + at, o);
+        tmem_ld32_finish(o);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 32; ++e) o[e] = 0.f;
+      }
+    };
+    if constexpr (!kSplitKeys) {
+      if (ok) {
+        // every MMA of this Q tile is complete: its place takes the output on its way
+        uint8_t *stage = smem + L::kOffQ + team * kTile + quad * 4096;
+        const float inv = l > 0.f ? 1.f / l : 0.f;
+        if (p.out_f32) emit(std::true_type{}, stage, 0, D, inv, load_o);
+        else emit(std::false_type{}, stage, 0, D, inv, load_o);
+      }
+    } else {
+      // Join the teams: each takes half of the columns and hands the other half to the other one, through the place of the
+      // Q, K and V tiles (every MMA is complete for both)
+      ok = __all_sync(0xffffffffu, ok);
+      row_info[team * 128 + m] = make_float2(m_ref, l);
+      both_sync();
+      const float2 other = row_info[(team ^ 1) * 128 + m];
+      const bool live = !*abort_flag;
+      const float top = fmaxf(m_ref, other.x), ref = top == kNegInf ? 0.f : top;
+      const float mine = fast_exp2(m_ref - ref), theirs = fast_exp2(other.x - ref);
+      l = l * mine + other.y * theirs;
+      float4 *box = reinterpret_cast<float4 *>(smem);   // [team][column / 4 of the half][row]
+      constexpr int kHalf = D / 2;
+      if (live && ok) {
+#pragma unroll 1
+        for (int at = 0; at < kHalf; at += 32) {
+          float o[32];
+          load_o((team ^ 1) * kHalf + at, o);
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            box[(team * (kHalf / 4) + at / 4 + k) * 128 + m] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+        }
+      }
+      both_sync();
+      if (live && ok) {
+        auto joined = [&](int at, float (&o)[32]) {
+          load_o(at, o);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const float4 x = box[((team ^ 1) * (kHalf / 4) + (at - team * kHalf) / 4 + k) * 128 + m];
+            o[4 * k] = o[4 * k] * mine + x.x * theirs;
+            o[4 * k + 1] = o[4 * k + 1] * mine + x.y * theirs;
+            o[4 * k + 2] = o[4 * k + 2] * mine + x.z * theirs;
+            o[4 * k + 3] = o[4 * k + 3] * mine + x.w * theirs;
+          }
+        };
+        uint8_t *stage = smem + L::kStage + warp * 4096;
+        const float inv = l > 0.f ? 1.f / l : 0.f;
+        if (p.out_f32) emit(std::true_type{}, stage, team * kHalf, (team + 1) * kHalf, inv, joined);
+        else emit(std::false_type{}, stage, team * kHalf, (team + 1) * kHalf, inv, joined);
+      }
+    }
+  } else if (warp < kMmaWarp) {
+    // ===================================================== loaders
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLoadRegs));
+    const int lw = warp - kLoadWarp0;
+    constexpr int kPanels = D / 64;
+    const char *kpool = static_cast<const char *>(p.k_cache), *vpool = static_cast<const char *>(p.v_cache);
+    const int q = lane & 7, rr0 = lane >> 3;     // 8 bytes q of each 64-byte half of rows rr0, rr0 + 4, ...
+    int32_t win = -1;                            // lane l: block id of run (l & 1) of tile win_base + (l >> 1)
+    int win_base = -16;
+    auto block_of = [&](int j, int r) -> int32_t {
+      if (j - win_base >= 16) {
+        win_base = j;
+        const int jt = j + (lane >> 1), key = jt * kN + 32 * lw + 16 * (lane & 1);
+        win = -1;
+        if (jt < nkt && key < seq_eff) {
+          const int32_t bi = __ldg(table + (key >> bs_log2));
+          if (bi < 0 || bi >= p.num_blocks) record_error(p.err, PA_ERR_DEVICE_CHECK);
+          else win = bi;
+        }
+      }
+      return __shfl_sync(0xffffffffu, win, 2 * (j - win_base) + r);
+    };
+    // Where this lane's words of the warp's two runs of tile j begin, and how many rows of each hold tokens.  A run without
+    // any (past the sequence's end, or in a bad block) is read from the pool's first rows; what is read of rows past the
+    // end is replaced by zeros.
+    struct Rows {
+      int64_t at[2];
+      int n[2];
+    };
+    auto rows_of = [&](int j) {
+      Rows x;
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const int key0 = j * kN + 32 * lw + 16 * r;
+        const int32_t b = block_of(j, r);
+        x.n[r] = b < 0 ? 0 : min(16, seq_eff - key0);
+        x.at[r] = (((int64_t)max(b, 0) * p.num_kv_heads + (b < 0 ? 0 : g)) * p.block_size + (b < 0 ? 0 : key0 & (p.block_size - 1)) + rr0) * D + q * 8;
+      }
+      return x;
+    };
+    using Words = uint2[kPanels][8];
+    auto load = [&](const Rows &x, const char *pool, Words &w) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int pn = 0; pn < kPanels; ++pn) w[pn][i] = ld_nc8(pool + x.at[i >> 2] + ((4 * i) & 15) * D + pn * 64);
+    };
+    const uint32_t to0 = (32 * lw + rr0) * 128 + ((q ^ rr0) << 4), to1 = to0 ^ 64;   // row 4 i + rr0: its chunk q ^ (row & 7)
+    auto widen = [&](Words &w, const Rows &x, uint8_t *tile) {
+      if (x.n[0] + x.n[1] < 32) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (((4 * i) & 15) + rr0 >= x.n[i >> 2])
+#pragma unroll
+            for (int pn = 0; pn < kPanels; ++pn) w[pn][i] = make_uint2(0, 0);
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int pn = 0; pn < kPanels; ++pn)
+          *reinterpret_cast<uint4 *>(tile + (i & 1 ? to1 : to0) + i * 512 + pn * kPanel) = widen8(w[pn][i]);
+      fence_async_smem();
+    };
+    Words kw, vw;
+    Rows now = rows_of(0), next = now;
+    if (nkt > 0) {
+      if constexpr (!kRaw) load(now, kpool, kw);
+      load(now, vpool, vw);
+    }
+    for (int j = 0; j < nkt; ++j) {
+      const int s = j % kStages;
+      if (j + 1 < nkt) next = rows_of(j + 1);
+      if constexpr (!kRaw) {
+        if (j >= kStages && !wait_all(&k_free[s], ((j / kStages) - 1) & 1)) break;
+        widen(kw, now, smem + L::kOffK + s * kTile);
+        mbar_arrive(&k_full[s]);
+        if (j + 1 < nkt) load(next, kpool, kw);
+      }
+      if (j >= kStages && !wait_all(&v_free[s], ((j / kStages) - 1) & 1)) break;
+      widen(vw, now, smem + L::kOffV + s * kTile);
+      mbar_arrive(&v_full[s]);
+      if (j + 1 < nkt) load(next, vpool, vw);
+      now = next;
+    }
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kMmaRegs));
+  }
+  if (kRaw && warp == kKWarp) {
+    // ===================================================== K tiles as stored
+    // one box per cache block that holds a key; what the tile's other rows hold is masked in the scores
+    const int bs = p.block_size, per_tile = kN / bs;
+    auto block = [&](int j) -> int32_t {   // lane i: the id of block i of tile j (-1: none; out of range: the loaders report it)
+      const int key = j * kN + lane * bs;
+      if (lane >= per_tile || j >= nkt || key >= seq_eff) return -1;
+      const int32_t bi = __ldg(table + (key >> bs_log2));
+      return bi >= 0 && bi < p.num_blocks ? bi : -1;
+    };
+    int32_t next = block(0);
+    int issued = 0;
+    for (int j = 0; j < nkt; ++j) {
+      const int s = j % kKStages;
+      const int32_t bi = next;
+      next = block(j + 1);
+      const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, bi >= 0));
+      if (j >= kKStages && !wait_all(&k_free[s], ((j / kKStages) - 1) & 1)) break;
+      if (lane == 0) mbar_arrive_expect_tx(&k_full[s], boxes * bs * D);
+      __syncwarp();
+      if (bi >= 0)
+        tma_load_2d(smem + L::kOffK + s * kKTile + lane * bs * D, &tmap_k, &k_full[s], 0,
+                    (int32_t)(((int64_t)bi * p.num_kv_heads + g) * bs));
+      ++issued;
+    }
+    // no box in flight at exit
+    for (int j = max(0, issued - kKStages); j < issued; ++j) mbar_wait(&k_full[j % kKStages], (j / kKStages) & 1, p.err);
+  } else if (warp == kMmaWarp) {
+    // ===================================================== MMA issue
+    // (the whole warp runs the schedule, the elected lane's predicate issues: operands stay in uniform registers)
+    const bool leader = elect_one();
+    const uint32_t idesc_s = umma_idesc(0, kN, false), idesc_o = umma_idesc(0, D, true);
+    constexpr bool kSw64 = kRaw && D == 64;     // rows of 64 bytes
+    const uint32_t q_at = smem_u32(smem + L::kOffQ), k_at = smem_u32(smem + L::kOffK);
+    const uint64_t qdesc0 = kSw64 ? umma_desc_sw64(q_at, 16, 512) : umma_desc(q_at, 16);
+    const uint64_t kdesc0 = kSw64 ? umma_desc_sw64(k_at, 16, 512) : umma_desc(k_at, 16);
+    const uint64_t vdesc0 = umma_desc(smem_u32(smem + L::kOffV), kPanel);
+    bool ok = nkt == 0 || wait_all(q_ready, 0), issued = false;
+    const int steps0 = steps(0), steps1 = steps(1);
+    // the last team to use key tile j
+    auto last_user = [&](int j) { return kSplitKeys ? j & 1 : j < n1 ? 1 : 0; };
+    auto issue_s = [&](int t, int j) {   // S of team t over key tile j
+      const uint64_t qd = qdesc0 + ((kSplitKeys ? 0 : t * kTile) >> 4), kd = kdesc0 + (((j % kKStages) * kKTile) >> 4);
+      if constexpr (kRaw) {
+#pragma unroll 1
+        for (int term = 0; term < 2; ++term)
+#pragma unroll
+          for (int k = 0; k < D / 32; ++k)
+            umma_f8_if(leader, sbuf(t), qd + term * ((kM * D) >> 4) + k * 2, kd + k * 2, idesc_s, term + k > 0 ? 1u : 0u);
+      } else {
+#pragma unroll 1
+        for (int h = 0; h < D / 64; ++h)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            umma_if(leader, sbuf(t), qd + h * (kPanel >> 4) + k * 2, kd + h * (kPanel >> 4) + k * 2, idesc_s, h + k > 0 ? 1u : 0u);
+      }
+      umma_commit_if(leader, &s_full[t]);
+      if (t == last_user(j)) umma_commit_if(leader, &k_free[j % kKStages]);
+      issued = true;
+    };
+    for (int t = 0; t < kTeams && ok; ++t) {
+      if ((t ? steps1 : steps0) == 0) continue;
+      const int j = tile_of(t, 0);
+      ok = wait_all(&k_full[j % kKStages], (j / kKStages) & 1);
+      if (!ok) break;
+      tc_fence_after();
+      issue_s(t, j);
+    }
+    for (int i = 0; i < max(steps0, steps1) && ok; ++i) {
+#pragma unroll 1
+      for (int t = 0; t < kTeams && ok; ++t) {
+        const int n = t ? steps1 : steps0;
+        if (i >= n) continue;
+        const int j = tile_of(t, i), s = j % kStages;
+        ok = wait_all(&v_full[s], (j / kStages) & 1);
+        if (!ok) break;
+        const uint64_t vd = vdesc0 + ((s * kTile) >> 4);
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {   // keys 0..63, then 64..127
+          ok = ok && wait_all(&p_full[h * kTeams + t], i & 1);
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) {
+            constexpr int kStep = (16 * 128) >> 4;
+            const uint32_t acc = i + h + kk > 0 ? 1u : 0u;
+            if constexpr (kLo) {
+              umma_ts_if(leader, obuf(t), sbuf(t) + 64 * h + 16 * kk, vd + (4 * h + kk) * kStep, idesc_o, acc);
+              umma_ts_if(leader, obuf(t), sbuf(t) + 64 * h + 16 * kk + 8, vd + (4 * h + kk) * kStep, idesc_o, 1u);
+            } else {
+              umma_ts_if(leader, obuf(t), sbuf(t) + 32 * h + 8 * kk, vd + (4 * h + kk) * kStep, idesc_o, acc);
+            }
+          }
+          issued = true;
+        }
+        if (!ok) break;
+        umma_commit_if(leader, &o_done[t]);
+        if (t == last_user(j)) umma_commit_if(leader, &v_free[s]);
+        if (i + 1 < n) {
+          const int jn = tile_of(t, i + 1);
+          ok = wait_all(&k_full[jn % kKStages], (jn / kKStages) & 1) && wait_all(&o_done[t], i & 1);
+          if (!ok) break;
+          tc_fence_after();
+          issue_s(t, jn);
+        }
+      }
+    }
+    // every MMA issued above is complete before tensor memory is freed
+    if (issued) {
+      if (leader) umma_commit(fin);
+      __syncwarp();
+      mbar_wait(fin, 0, p.err);
+    }
+  }
+
+  // ===================================================== teardown
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+  }
+}
+
+template <typename QT, int D, bool kSplitKeys, bool kLo>
+cudaError_t launch_tiles(const PrefillTcParams &p0, const CUtensorMap &k, int num_chunks, cudaStream_t s) {
+  PrefillTcParams p = p0;
+  const int rows = kM / p.share_heads * (kSplitKeys ? 1 : kTeams);
+  p.row_blocks = (p.max_q_len + rows - 1) / rows;
+  const int64_t grid = (int64_t)num_chunks * p.row_blocks * p.num_kv_heads * p.shares;
+  if (grid > 2147483647ll) return cudaErrorInvalidValue;
+  constexpr int smem = Layout<D, kSplitKeys, raw_k<QT, kLo>()>::kBytes;
+  cudaError_t e = ensure_smem_limit<prefill_scaled_kernel<QT, D, kSplitKeys, kLo>>(smem);
+  if (e != cudaSuccess) return e;
+  prefill_scaled_kernel<QT, D, kSplitKeys, kLo><<<(unsigned)grid, kThreads, smem, s>>>(p, num_chunks, k);
+  return cudaGetLastError();
+}
+
+template <typename QT, int D>
+cudaError_t launch_dim(const PrefillTcParams &p, const CUtensorMap &k, int num_chunks, cudaStream_t s) {
+  int sms = 0;
+  cudaError_t e = current_sm_count(&sms);
+  if (e != cudaSuccess) return e;
+  const int rows = kTeams * (kM / p.share_heads);
+  const int64_t pairs = (int64_t)num_chunks * ((p.max_q_len + rows - 1) / rows) * p.num_kv_heads * p.shares;
+  const bool split = pairs < sms;
+  if (p.out_f32) return split ? launch_tiles<QT, D, true, true>(p, k, num_chunks, s) : launch_tiles<QT, D, false, true>(p, k, num_chunks, s);
+  return split ? launch_tiles<QT, D, true, false>(p, k, num_chunks, s) : launch_tiles<QT, D, false, false>(p, k, num_chunks, s);
+}
+
+}  // namespace psc
+
+// k: K's pool as [rows][head_dim codes], one cache block per box.
+template <typename QT>
+cudaError_t launch_prefill_scaled(const PrefillTcParams &p, const CUtensorMap &k, int head_dim, int num_chunks, cudaStream_t s) {
+  if (head_dim == 64) return psc::launch_dim<QT, 64>(p, k, num_chunks, s);
+  if (head_dim == 128) return psc::launch_dim<QT, 128>(p, k, num_chunks, s);
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace pa

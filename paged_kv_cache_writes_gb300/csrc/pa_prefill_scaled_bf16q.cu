@@ -1,10 +1,10 @@
 // pa_prefill_scaled_bf16q.cu -- chunked-prefill instantiations for a block-scaled
 // fp8-e4m3 cache with bf16 queries.
-#include "pa_prefill_tc.cuh"
+#include "pa_prefill_scaled.cuh"
 
 namespace pa {
-cudaError_t launch_prefill_scaled_bf16q(const PrefillTcParams &p, const PoolMaps &m, int head_dim, int num_chunks,
-                                      cudaStream_t s) {
-  return launch_prefill_scaled<__nv_bfloat16>(p, m, head_dim, num_chunks, s);
+cudaError_t launch_prefill_scaled_bf16q(const PrefillTcParams &p, const CUtensorMap &k, int head_dim, int num_chunks,
+                                        cudaStream_t s) {
+  return launch_prefill_scaled<__nv_bfloat16>(p, k, head_dim, num_chunks, s);
 }
 }  // namespace pa

@@ -101,7 +101,7 @@ struct PrefillTcParams {
   int32_t window;
   int32_t num_sinks;
   int32_t shares, share_heads;
-  // kernels built with kBlk: scales of K and V of a block-scaled fp8 cache, [num_blocks][num_kv_heads]
+  // pa_prefill_scaled.cuh: scales of K and V of a block-scaled fp8 cache, [num_blocks][num_kv_heads]
   const float *k_scales, *v_scales;
 };
 
@@ -225,7 +225,7 @@ struct Layout {
 // G: query heads per KV head; with kWin 0, the group then being p.share_heads
 // heads, rows past the last whole token of the CTA's tiles left idle.
 template <typename KV, typename QT, int G, int kQTiles, int D = 128, bool kWin = false, bool kPair = false,
-          bool kLo = true, bool kBlk = false>
+          bool kLo = true>
 __device__ __forceinline__ void prefill_tc_body(const PrefillTcParams &p, int bx, int by, const CUtensorMap *tmap_k,
                                                 const CUtensorMap *tmap_v) {
   using namespace tc;
@@ -233,7 +233,6 @@ __device__ __forceinline__ void prefill_tc_body(const PrefillTcParams &p, int bx
   static_assert(kWin == (G == 0) && (kWin || D == 128), "any group and head_dim 64 with kWin only");
   constexpr int kD = D;                       // head_dim (hides tc::kD)
   static_assert(!kWin || kQTiles == 1, "the windowed kernel has one Q tile per CTA");
-  static_assert(!kBlk || (kWin && std::is_same<KV, uint8_t>::value), "block scales: fp8 caches, in the windowed kernel");
   using R = std::conditional_t<kWin, WinRoles<kPair, std::is_same<KV, uint8_t>::value>, Roles<kQTiles>>;
   constexpr int kStages = R::kStages;         // (hides tc::kStages)
   using L = Layout<kQTiles, std::is_same<KV, uint8_t>::value, D, kStages, kWin>;
@@ -425,31 +424,6 @@ __device__ __forceinline__ void prefill_tc_body(const PrefillTcParams &p, int bx
       auto wait_all = [&](uint64_t *bar, uint32_t parity) {
         return __all_sync(0xffffffffu, mbar_try_wait(bar, parity) || wait_or_abort(bar, parity, p.err, abort_flag));
       };
-      // kBlk: lane i < 8 holds the scales of run i (16 keys) of this tile, and the block id of run i of the next one
-      struct {
-        float k, log2_v, inv_v;
-      } run{1.f, 0.f, 1.f};
-      int32_t next_blk = -1;
-      auto run_block = [&](int j) -> int32_t {   // (an id out of range is reported by the loaders)
-        const int key = j * kN + 16 * lane;
-        if (lane >= 8 || j >= nkt || key >= kv_end) return -1;
-        int lb = key >> bs_log2;
-        if (lb >= span.head_blocks) lb += span.skip_blocks;
-        const int32_t bi = __ldg(table + lb);
-        return bi >= 0 && bi < p.num_blocks ? bi : -1;
-      };
-      float next_k = 1.f, next_v = 1.f;   // the scales as read, of the next tile
-      auto read_scales = [&](int32_t bi) {
-        next_k = next_v = 1.f;
-        if (bi >= 0) {
-          next_k = __ldg(p.k_scales + (int64_t)bi * p.num_kv_heads + g);
-          next_v = __ldg(p.v_scales + (int64_t)bi * p.num_kv_heads + g);
-        }
-      };
-      if constexpr (kBlk) {
-        read_scales(run_block(0));
-        next_blk = run_block(1);
-      }
       // The scores are read from tensor memory once into registers, but for fp8 caches with two CTAs per SM (whose four
       // loader warps leave 96 registers per thread): those in chunks of 32, twice (maximum, then probabilities), each
       // read while the one before is worked on.
@@ -457,13 +431,6 @@ __device__ __forceinline__ void prefill_tc_body(const PrefillTcParams &p, int bx
       constexpr int kChunks = kOwn / 32, kHeld = kTwice ? 2 : kChunks;   // chunks of 32 scores, and how many in registers
       for (int j = 0; j < nkt; ++j) {
         const int b = j % kBufs;
-        if constexpr (kBlk) {
-          bool good = block_scale_ok(next_k) && block_scale_ok(next_v);
-          if (!good) record_error(p.err, PA_ERR_DEVICE_CHECK);
-          run = {good ? next_k : 1.f, good ? __log2f(next_v) : 0.f, good ? __frcp_rn(next_v) : 1.f};
-          read_scales(next_blk);
-          next_blk = run_block(j + 2);
-        }
         ok = wait_all(&s_full[b], (j / kBufs) & 1) && ok;
         if (kGroups == 1 && !ok) break;   // two groups: the partner may be at a barrier; go through them without work to do
         const uint32_t sb = sbuf(0, b) + lane_base + grp * kOwn;
@@ -482,27 +449,9 @@ __device__ __forceinline__ void prefill_tc_body(const PrefillTcParams &p, int bx
 #pragma unroll
         for (int i = 0; i < 8; ++i) mx[i] = kNegInf;
         float sv[kHeld][32];
-        // kBlk: run r of this group's keys (r = 2 ck + hh); its score factor, log2 units, and log2 of V's scale.  (A masked
-        // score has to stay -inf: the factor is not 0.)
-        constexpr int kRuns = kOwn / 16;
-        auto run_factor = [&](int r) { return fmaxf(cmul * __shfl_sync(0xffffffffu, run.k, grp * kRuns + r), 1e-37f); };
-        auto run_log2v = [&](int r) { return __shfl_sync(0xffffffffu, run.log2_v, grp * kRuns + r); };
-        auto take_max = [&](int ck, float (&v)[32]) {
-          if constexpr (kBlk) {   // in log2 units
+        auto take_max = [&](float (&v)[32]) {
 #pragma unroll
-            for (int hh = 0; hh < 2; ++hh) {
-              float a = kNegInf, b2 = kNegInf;
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                a = fmax3(a, v[16 * hh + 4 * i], v[16 * hh + 4 * i + 1]);
-                b2 = fmax3(b2, v[16 * hh + 4 * i + 2], v[16 * hh + 4 * i + 3]);
-              }
-              mx[hh] = fmaxf(mx[hh], fmaf(fmaxf(a, b2), run_factor(2 * ck + hh), run_log2v(2 * ck + hh)));
-            }
-          } else {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) mx[i & 7] = fmax3(mx[i & 7], v[2 * i], v[2 * i + 1]);
-          }
+          for (int i = 0; i < 16; ++i) mx[i & 7] = fmax3(mx[i & 7], v[2 * i], v[2 * i + 1]);
         };
         // bits [0, n) of a word
         auto below = [](int n) { return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u; };
@@ -519,7 +468,7 @@ __device__ __forceinline__ void prefill_tc_body(const PrefillTcParams &p, int bx
           for (int ck = 0; ck < kChunks; ++ck) {
             tmem_ld32_finish(sv[ck]);   // (the first one waits for all)
             if (!full_tile) mask(ck, sv[ck]);
-            take_max(ck, sv[ck]);
+            take_max(sv[ck]);
           }
         } else {
           if (!full_tile) {   // mask in place: the second pass then finds -inf
@@ -528,7 +477,7 @@ __device__ __forceinline__ void prefill_tc_body(const PrefillTcParams &p, int bx
               tmem_ld32_start(sb + 32 * ck, sv[0]);
               tmem_ld32_finish(sv[0]);
               mask(ck, sv[0]);
-              take_max(ck, sv[0]);
+              take_max(sv[0]);
               tmem_st32(sb + 32 * ck, sv[0]);
             }
           } else {
@@ -537,7 +486,7 @@ __device__ __forceinline__ void prefill_tc_body(const PrefillTcParams &p, int bx
             for (int ck = 0; ck < kChunks; ++ck) {
               tmem_ld32_finish(sv[ck & 1]);
               if (ck + 1 < kChunks) tmem_ld32_start(sb + 32 * (ck + 1), sv[(ck + 1) & 1]);
-              take_max(ck, sv[ck & 1]);
+              take_max(sv[ck & 1]);
             }
           }
           tmem_ld32_start(sb, sv[0]);   // for the second pass
@@ -550,7 +499,7 @@ __device__ __forceinline__ void prefill_tc_body(const PrefillTcParams &p, int bx
           mr = fmaxf(mr, exch[(grp ^ 1) * 128 + m]);
           pair_sync();
         }
-        const float mt = kBlk || mr == kNegInf ? mr : mr * cmul;   // tile maximum, log2 units
+        const float mt = mr == kNegInf ? kNegInf : mr * cmul;   // tile maximum, log2 units
         const bool rescale = mt > m_ref + tc::kRescaleLog2;
         if (__any_sync(0xffffffffu, rescale)) {
           const float alpha = rescale ? fast_exp2(m_ref - mt) : 1.f;
@@ -585,7 +534,7 @@ __device__ __forceinline__ void prefill_tc_body(const PrefillTcParams &p, int bx
         // p = 2^(s * |s_mult| - m_ref), 16 keys at a time, written over those keys' own 16 score columns; the P.V MMAs
         // of a half of the tile (64 keys) start when it is written
         const float msub = m_ref == kNegInf ? 0.f : m_ref;
-        float2 cc = make_float2(cmul, cmul), nm = make_float2(-msub, -msub);
+        const float2 cc = make_float2(cmul, cmul), nm = make_float2(-msub, -msub);
 #pragma unroll
         for (int ck = 0; ck < kChunks; ++ck) {
           float (&v)[32] = sv[ck % kHeld];
@@ -597,24 +546,12 @@ __device__ __forceinline__ void prefill_tc_body(const PrefillTcParams &p, int bx
 #pragma unroll
             for (int hh = 0; hh < 2; ++hh) {   // keys 32ck + 16hh .. +15
               uint32_t w[8], wl[8];
-              // kBlk: p times V's scale; the sum is that of p, unrounded: a weight may be large where V's scale is so small
-              // that its f16 product with it is not
-              float2 run_sum[2] = {{0.f, 0.f}, {0.f, 0.f}};
-              if constexpr (kBlk) {
-                const float cr = run_factor(2 * ck + hh), nr = run_log2v(2 * ck + hh) - msub;
-                cc = make_float2(cr, cr);
-                nm = make_float2(nr, nr);
-              }
 #pragma unroll
               for (int k = 0; k < 8; ++k) {
                 const int i0 = 16 * hh + 2 * k;
                 const float2 a = ffma2(make_float2(v[i0], v[i0 + 1]), cc, nm);
                 const float2 pk = make_float2(fast_exp2(a.x), fast_exp2(a.y));
-                if constexpr (kBlk) {
-                  if constexpr (kSplit) w[k] = f16x2_split(pk.x, pk.y, wl[k]);
-                  else asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w[k]) : "f"(pk.y), "f"(pk.x));
-                  run_sum[k & 1] = ffma2(pk, ones, run_sum[k & 1]);
-                } else if constexpr (!kSplit) {   // rounded to the MMA's type, the sum that of the rounded P
+                if constexpr (!kSplit) {   // rounded to the MMA's type, the sum that of the rounded P
                   if constexpr (kF16Ops) w[k] = f16x2_rn_add(pk.x, pk.y, lacc[k & 3]);
                   else w[k] = bf16x2_rn_add(pk.x, pk.y, lacc[k & 3]);
                 } else if constexpr (kF16Ops) {   // hi + lo: hi rounded to f16, lo = p - hi, exact in fp32, rounded too
@@ -630,11 +567,6 @@ __device__ __forceinline__ void prefill_tc_body(const PrefillTcParams &p, int bx
                   wl[k] = lw2;
                   lacc[k & 3] = ffma2(pk, ones, lacc[k & 3]);
                 }
-              }
-              if constexpr (kBlk) {
-                const float iv = __shfl_sync(0xffffffffu, run.inv_v, grp * kRuns + 2 * ck + hh);
-                lacc[0] = ffma2(run_sum[0], make_float2(iv, iv), lacc[0]);
-                lacc[1] = ffma2(run_sum[1], make_float2(iv, iv), lacc[1]);
               }
               tmem_st8(sb + 32 * ck + 16 * hh, w);
               if constexpr (kSplit) tmem_st8(sb + 32 * ck + 16 * hh + 8, wl);
@@ -1430,25 +1362,25 @@ cudaError_t launch_prefill_tc(const PrefillTcParams &p, const PoolMaps &m, int g
 // 607 us, one of 512, 32/8 heads 19.3 -> 17.0, 4 of 1024, head_dim 64 54.8 -> 51.0,
 // 3 of 700, 40/8 heads 36.9 -> 33.2.  A caller that wants all bits of P asks for
 // an fp32 output.
-template <typename KV, typename QT, int D, bool kPair, bool kLo, bool kBlk>
+template <typename KV, typename QT, int D, bool kPair, bool kLo>
 __global__ void __launch_bounds__((tc::WinRoles<kPair, std::is_same<KV, uint8_t>::value>::kThreads), kPair ? 2 : 1)
     prefill_window_kernel(const PrefillTcParams p, const __grid_constant__ CUtensorMap tmap_k,
                           const __grid_constant__ CUtensorMap tmap_v) {
-  prefill_tc_body<KV, QT, 0, 1, D, true, kPair, kLo, kBlk>(p, blockIdx.x, blockIdx.y, &tmap_k, &tmap_v);
+  prefill_tc_body<KV, QT, 0, 1, D, true, kPair, kLo>(p, blockIdx.x, blockIdx.y, &tmap_k, &tmap_v);
 }
 
-template <typename KV, typename QT, int D, bool kPair, bool kLo, bool kBlk>
+template <typename KV, typename QT, int D, bool kPair, bool kLo>
 cudaError_t launch_prefill_window_tiles(const PrefillTcParams &p, const PoolMaps &m, dim3 grid, cudaStream_t s) {
   using R = tc::WinRoles<kPair, std::is_same<KV, uint8_t>::value>;
   constexpr int smem = tc::Layout<1, std::is_same<KV, uint8_t>::value, D, R::kStages, true>::kSmemBytes;
   static_assert(!kPair || 2 * (smem + 1024) <= 228 * 1024, "two CTAs per SM");
-  cudaError_t e = ensure_smem_limit<prefill_window_kernel<KV, QT, D, kPair, kLo, kBlk>>(smem);
+  cudaError_t e = ensure_smem_limit<prefill_window_kernel<KV, QT, D, kPair, kLo>>(smem);
   if (e != cudaSuccess) return e;
-  prefill_window_kernel<KV, QT, D, kPair, kLo, kBlk><<<grid, R::kThreads, smem, s>>>(p, m.k, m.v);
+  prefill_window_kernel<KV, QT, D, kPair, kLo><<<grid, R::kThreads, smem, s>>>(p, m.k, m.v);
   return cudaGetLastError();
 }
 
-template <typename KV, typename QT, int D, bool kBlk = false>
+template <typename KV, typename QT, int D>
 cudaError_t launch_prefill_window_one(const PrefillTcParams &p0, const PoolMaps &m, int num_chunks, cudaStream_t s) {
   int num_sms = 0;
   if (current_sm_count(&num_sms) != cudaSuccess) return cudaErrorUnknown;
@@ -1462,10 +1394,10 @@ cudaError_t launch_prefill_window_one(const PrefillTcParams &p0, const PoolMaps 
   // beyond that pairs: 8 chunks of 2048, 64/8 heads (8192 CTAs), 0.61 ms, one CTA per SM 0.86.
   const bool pair = gx * gy > num_sms;
   if (!p.out_f32)
-    return pair ? launch_prefill_window_tiles<KV, QT, D, true, false, kBlk>(p, m, grid, s)
-                : launch_prefill_window_tiles<KV, QT, D, false, false, kBlk>(p, m, grid, s);
-  return pair ? launch_prefill_window_tiles<KV, QT, D, true, true, kBlk>(p, m, grid, s)
-              : launch_prefill_window_tiles<KV, QT, D, false, true, kBlk>(p, m, grid, s);
+    return pair ? launch_prefill_window_tiles<KV, QT, D, true, false>(p, m, grid, s)
+                : launch_prefill_window_tiles<KV, QT, D, false, false>(p, m, grid, s);
+  return pair ? launch_prefill_window_tiles<KV, QT, D, true, true>(p, m, grid, s)
+              : launch_prefill_window_tiles<KV, QT, D, false, true>(p, m, grid, s);
 }
 
 template <typename KV, typename QT>
@@ -1473,19 +1405,6 @@ cudaError_t launch_prefill_window(const PrefillTcParams &p, const PoolMaps &m, i
                                   cudaStream_t s) {
   if (head_dim == 64) return launch_prefill_window_one<KV, QT, 64>(p, m, num_chunks, s);
   if (head_dim == 128) return launch_prefill_window_one<KV, QT, 128>(p, m, num_chunks, s);
-  return cudaErrorInvalidValue;
-}
-
-// pa_prefill_chunk_scaled: the windowed kernel with a window that reaches back
-// to the start, over a block-scaled fp8 cache.  K's scale of a run of 16 keys
-// multiplies their scores, V's their probabilities (as an addend of the exponent),
-// so that K and V are staged as the codes' values; each softmax warp reads the
-// scales itself, two tiles ahead.
-template <typename QT>
-cudaError_t launch_prefill_scaled(const PrefillTcParams &p, const PoolMaps &m, int head_dim, int num_chunks,
-                                  cudaStream_t s) {
-  if (head_dim == 64) return launch_prefill_window_one<uint8_t, QT, 64, true>(p, m, num_chunks, s);
-  if (head_dim == 128) return launch_prefill_window_one<uint8_t, QT, 128, true>(p, m, num_chunks, s);
   return cudaErrorInvalidValue;
 }
 

@@ -93,6 +93,22 @@ __device__ __forceinline__ void umma_f8_if(bool issue, uint32_t tmem_d, uint64_t
       "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"((uint32_t)issue)
       : "memory");
 }
+// The same with 16-bit operands, A in shared memory or (ts) in tensor memory.
+__device__ __forceinline__ void umma_if(bool issue, uint32_t tmem_d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem_d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"((uint32_t)issue)
+      : "memory");
+}
+__device__ __forceinline__ void umma_ts_if(bool issue, uint32_t tmem_d, uint32_t tmem_a, uint64_t b, uint32_t idesc,
+                                           uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(tmem_d),
+      "r"(tmem_a), "l"(b), "r"(idesc), "r"(acc), "r"((uint32_t)issue)
+      : "memory");
+}
 __device__ __forceinline__ void umma_commit_if(bool issue, uint64_t *bar) {
   asm volatile(
       "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"

@@ -7,6 +7,9 @@ rounded to nearest even.  So codes, scales and 16-bit rows are compared for equa
 
 Bounds of the attention, per output element (u = 2^-24; scores and their bound e as in tests/_bounded.py, K being code
 times scale):
+* chunks with bf16 queries and output take a query row, its largest element at 2^e in [128, 256), as hi + lo, e4m3 both:
+  exact where the element's last bit, 2^-7 of its power of two, is e4m3's smallest step 2^-9 or more, else off by half of
+  that step, 2^-10: 2^-17 of the largest element, in the place of 2^-21.
 * the exponent of a weight is t = s + log2 vs - max: log2 vs is within 2 ulp of its value and t is rounded, so e grows
   by 2^-21 (1 + |log2 vs|); the same factor meets numerator and sum.
 * the second product takes w = p vs.  Decode: 256 w in e4m3 terms, w <= 1 at the row's largest: two hold it to 2^-8 of
@@ -169,7 +172,8 @@ def attend(q, k, v, seen, scale, out, chunk):
     kk = kc * ks[..., None]
     s = torch.einsum("rhgd,hnd->rhgn", x, kk) * scale
     e = torch.einsum("rhgd,hnd->rhgn", x.abs(), kk.abs()) * abs(scale) * 24 * 2.0 ** -23
-    e = e + abs(scale) * 2.0 ** -21 * x.abs().amax(-1, keepdim=True) * kk.abs().sum(-1)[None, :, None, :]
+    terms = 2.0 ** -17 if chunk and out == "bf16" else 2.0 ** -21
+    e = e + abs(scale) * terms * x.abs().amax(-1, keepdim=True) * kk.abs().sum(-1)[None, :, None, :]
     lv = torch.log2(vs)[None, :, None, :]
     e = e + 4 * 2.0 ** -24 * s.abs() + 2.0 ** -22 + 2.0 ** -21 * (1 + lv.abs())
     m = seen[:, None, None, :]
