@@ -28,11 +28,10 @@
 //    teams have the same Q tile, team 0 the even key tiles and team 1 the odd
 //    ones; their results are joined by their maxima through shared memory.
 //
-// P (f16 pairs) goes over the score buffer's first 64 columns (hi + lo: over all of it), keys 0..63 first, whose P.V starts
-// when they are there; the next tile's scores wait for the P.V that reads P.
-//
-// Registers: launched with 128 a thread, of which the loaders and the MMA warp's group give to the softmax (184), whose
-// threads hold their row's 128 scores: one pass over tensor memory instead of two.
+// A team's score buffer is two halves of 64 keys, each with its own softmax step: while a team's threads work on one half,
+// the tensor cores compute the other half's scores and the P.V of the one before.  P (f16 pairs; hi + lo) goes over its own
+// half.  (With one buffer of 128 keys a team waited for P.V and the next Q.K^T in turn: 821 us against XXX for 4 chunks of
+// 2048 at 2048, 64/8 heads.)
 //
 // Loaders: four warps, 32 keys of a tile each, a key tile ahead in registers (8-byte loads, a row of codes per 8 lanes),
 // widened into the MMAs' 128-byte-swizzled panels.  Codes staged by bulk copies instead would cost shared memory's
@@ -54,10 +53,9 @@ namespace psc {
 
 constexpr int kM = 128, kN = 128;              // packed rows per Q tile, keys per tile
 constexpr int kTeams = 2, kSoftmax = kTeams * 128;
-constexpr int kLoadWarp0 = kSoftmax / 32, kLoaders = 128, kMmaWarp = kLoadWarp0 + 4, kKWarp = kMmaWarp + 1;
-constexpr int kThreads = 512;                  // four warpgroups: a team's softmax each, the loaders, the MMA warp
-constexpr int kSoftmaxRegs = 168, kLoadRegs = 112, kMmaRegs = 64;
-static_assert(2 * kSoftmaxRegs + kLoadRegs + kMmaRegs == 4 * 128, "the launch's registers");
+constexpr int kLoadWarp0 = kSoftmax / 32, kLoaders = 128, kMmaWarp = kLoadWarp0 + 4, kKWarp = kMmaWarp + kTeams;
+constexpr int kThreads = (kKWarp + 1) * 32;
+constexpr int kHalf = 64;                      // keys per softmax step
 constexpr int kPanel = kN * 128;               // 64 elements of 128 rows
 constexpr float kRescaleLog2 = 8.f;            // O is rescaled when the maximum exceeds its reference by 2^8
 
@@ -76,7 +74,7 @@ struct Layout {
   static constexpr int kOffK = kOffQ + (kSplitKeys ? 1 : 2) * kTile;
   static constexpr int kOffV = kOffK + kKStages * kKTile;
   static constexpr int kOffBar = kOffV + kStages * kTile;
-  static constexpr int kNumBars = 2 * kStages + 2 * kKStages + 4 * kTeams + 2;
+  static constexpr int kNumBars = 2 * kStages + 2 * kKStages + 3 * 2 * kTeams + 2 + kTeams;   // (even: 16-byte alignment behind them)
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;
   static constexpr int kOffRow = kOffMisc + 16;                // float2 [kTeams][128]
   static constexpr int kOffRuns = kOffRow + kTeams * 128 * 8;  // float4 [softmax warp][2][8 runs]
@@ -114,14 +112,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L::kOffBar);
   uint64_t *v_full = bars;                       // [kStages] a tile is widened (128 loader arrivals)
-  uint64_t *v_free = v_full + kStages;           // [kStages] the MMAs that read it are complete
+  uint64_t *v_free = v_full + kStages;           // [kStages] the MMAs that read it are complete (every team's that walks the tile)
   uint64_t *k_full = v_free + kStages;           // [kKStages] the same of K (raw: one expect-tx arrival)
   uint64_t *k_free = k_full + kKStages;
-  uint64_t *s_full = k_free + kKStages;          // [team] scores of its step i (phase i)
-  uint64_t *p_full = s_full + kTeams;            // [half][team] P of keys 0..63, of keys 64..127 written (128 arrivals)
-  uint64_t *o_done = p_full + 2 * kTeams;        // [team] P.V of step i complete
-  uint64_t *q_ready = o_done + kTeams;
-  uint64_t *fin = q_ready + 1;                   // every MMA of the CTA complete
+  uint64_t *s_full = k_free + kKStages;          // [team][half] scores of its step h (half h & 1, phase h >> 1)
+  uint64_t *p_full = s_full + 2 * kTeams;        // [team][half] P written over them (128 arrivals)
+  uint64_t *o_done = p_full + 2 * kTeams;        // [team][half] P.V complete
+  uint64_t *q_ready = o_done + 2 * kTeams;
+  uint64_t *fin = q_ready + 1;                   // [team] every MMA of the team complete
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::kOffMisc);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::kOffMisc + 8);
   float2 *row_info = reinterpret_cast<float2 *>(smem + L::kOffRow);
@@ -146,33 +144,37 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int seq_eff = len64 <= 0 ? 0 : (int)(len64 < cap ? len64 : cap);
   const int bs_log2 = p.block_size == 32 ? 5 : 4;
   const int32_t *table = p.block_tables + (int64_t)c * p.max_blocks_per_seq;
-  // key tiles of a team's Q tile, of the CTA, and a team's steps: step i of team t is key tile tile_of(t, i)
-  auto key_tiles = [&](int t) {
+  // keys that a team's Q tile sees, the CTA's key tiles, and a team's steps of 64 keys: step h of team t is half h & 1 of key
+  // tile tile_of(t, h)
+  auto keys_of = [&](int t) {
     const int first = r0 + (kSplitKeys ? 0 : t * BR);
-    if (first >= nrows) return 0;
-    return (min(seq_eff, max(0, qs + min(first + BR, nrows))) + kN - 1) / kN;
+    return first >= nrows ? 0 : min(seq_eff, max(0, qs + min(first + BR, nrows)));
   };
-  const int n0 = key_tiles(0), n1 = key_tiles(1), nkt = max(n0, n1);
-  auto steps = [&](int t) { return kSplitKeys ? (n0 + 1 - t) / 2 : t ? n1 : n0; };
-  auto tile_of = [&](int t, int i) { return kSplitKeys ? 2 * i + t : i; };
+  const int keys0 = keys_of(0), keys1 = keys_of(1), nkt = (max(keys0, keys1) + kN - 1) / kN;
+  auto steps = [&](int t) {
+    if (!kSplitKeys) return ((t ? keys1 : keys0) + kHalf - 1) / kHalf;
+    const int tiles = (nkt + 1 - t) / 2, last = keys0 - (nkt - 1) * kN;   // last: keys of the last tile
+    return 2 * tiles - (tiles > 0 && ((nkt - 1) & 1) == t && last <= kHalf ? 1 : 0);
+  };
+  auto tile_of = [&](int t, int h) { return kSplitKeys ? (h & ~1) + t : h >> 1; };
 
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&v_full[s], kLoaders);
-      mbar_init(&v_free[s], 1);
+      mbar_init(&v_free[s], kSplitKeys ? 1 : kTeams);
     }
     for (int s = 0; s < kKStages; ++s) {
       mbar_init(&k_full[s], kRaw ? 1 : kLoaders);
-      mbar_init(&k_free[s], 1);
+      mbar_init(&k_free[s], kSplitKeys ? 1 : kTeams);
     }
-    for (int t = 0; t < kTeams; ++t) {
+    for (int t = 0; t < 2 * kTeams; ++t) {
       mbar_init(&s_full[t], 1);
       mbar_init(&p_full[t], 128);
-      mbar_init(&p_full[kTeams + t], 128);
       mbar_init(&o_done[t], 1);
     }
     mbar_init(q_ready, kSplitKeys ? 128 : kSoftmax);
-    mbar_init(fin, 1);
+    mbar_init(&fin[0], 1);
+    mbar_init(&fin[1], 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -192,7 +194,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp < kLoadWarp0) {
     // ===================================================== softmax
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     const int team = warp >> 2, quad = warp & 3, m = tid & 127;
     const int tile0 = r0 + (kSplitKeys ? 0 : team * BR);         // the Q tile's first token row
     const int rl = m / gr, hq = m - rl * gr;
@@ -283,21 +284,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int n = steps(team);
     float next_k = 1.f, next_v = 1.f;
     int32_t next_blk = -1;
-    auto run_block = [&](int i) -> int32_t {   // (an id out of range is reported by the loaders)
-      const int key = tile_of(team, i) * kN + 16 * lane;
-      if (lane >= 8 || i >= n || key >= seq_eff) return -1;
+    auto run_block = [&](int h) -> int32_t {   // of the tile of step h (an id out of range is reported by the loaders)
+      const int key = tile_of(team, h) * kN + 16 * lane;
+      if (lane >= 8 || h >= n || key >= seq_eff) return -1;
       const int32_t bi = __ldg(table + (key >> bs_log2));
       return bi >= 0 && bi < p.num_blocks ? bi : -1;
     };
     auto read_scales = [&](int32_t bi) {
       next_k = next_v = 1.f;
       if (bi >= 0) {
-        next_k = __ldg(p.k_scales + (int64_t)bi * p.num_kv_heads + g);
-        next_v = __ldg(p.v_scales + (int64_t)bi * p.num_kv_heads + g);
+        const int64_t at = (int64_t)bi * p.num_kv_heads + g;
+        next_k = __ldg(p.k_scales + at);
+        next_v = __ldg(p.v_scales + at);
       }
     };
     read_scales(run_block(0));
-    next_blk = run_block(1);
+    next_blk = run_block(2);
     float4 *runs = reinterpret_cast<float4 *>(smem + L::kOffRuns) + warp * 16;
 
     float m_ref = kNegInf;                       // reference maximum, log2 units
@@ -305,50 +307,59 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float2 ones = make_float2(1.f, 1.f);
     bool ok = true;
     const uint32_t sb = sbuf(team) + lane_base, ob = obuf(team) + lane_base;
-    for (int i = 0; i < n; ++i) {
-      if (lane < 8) {
-        const bool good = block_scale_ok(next_k) && block_scale_ok(next_v);
-        if (!good) record_error(p.err, PA_ERR_DEVICE_CHECK);
-        runs[(i & 1) * 8 + lane] = good ? make_float4(next_k, __log2f(next_v), __frcp_rn(next_v), 0.f) : make_float4(1.f, 0.f, 1.f, 0.f);
+    for (int h = 0; h < n; ++h) {
+      const int b = h & 1, tb = team * 2 + b;
+      if (b == 0) {
+        if (lane < 8) {
+          const bool good = block_scale_ok(next_k) && block_scale_ok(next_v);
+          if (!good) record_error(p.err, PA_ERR_DEVICE_CHECK);
+          runs[(h & 2) * 4 + lane] = good ? make_float4(next_k, __log2f(next_v), __fdividef(1.f, next_v), 0.f) : make_float4(1.f, 0.f, 1.f, 0.f);
+        }
+        __syncwarp();
+        read_scales(next_blk);
+        next_blk = run_block(h + 4);
       }
-      __syncwarp();
-      read_scales(next_blk);
-      next_blk = run_block(i + 2);
-      ok = wait_all(&s_full[team], i & 1);
+      const float4 *run = runs + (h & 2) * 4 + 4 * b;   // the half's four runs
+      ok = wait_all(&s_full[tb], (h >> 1) & 1);
       if (!ok) break;
       tc_fence_after();
-      float v[4][32];
+      const uint32_t sh = sb + kHalf * b;
+      float v[2][32];
+      tmem_ld32_start(sh, v[0]);
+      tmem_ld32_start(sh + 32, v[1]);
+      // run r's score factor, log2 units (not 0: a masked score stays -inf), and log2 of V's scale
+      float factor[4], add[4];
 #pragma unroll
-      for (int ck = 0; ck < 4; ++ck) tmem_ld32_start(sb + 32 * ck, v[ck]);
-      // run r's score factor, log2 units (not 0: a masked score stays -inf), log2 of V's scale and 1 / V's scale; read
-      // for each pass, which has no registers to spare
-      const float4 *run = runs + (i & 1) * 8;
-      auto factor_of = [&](const float4 &x) { return fmaxf(cmul * x.x, 1e-37f); };
-#pragma unroll
-      for (int ck = 0; ck < 4; ++ck) tmem_ld32_finish(v[ck]);
-      const int nvis = lim - tile_of(team, i) * kN;
-      if (!__all_sync(0xffffffffu, nvis >= kN)) {
-#pragma unroll
-        for (int ck = 0; ck < 4; ++ck)
-#pragma unroll
-          for (int e = 0; e < 32; ++e)
-            if (32 * ck + e >= nvis) v[ck][e] = kNegInf;
+      for (int r = 0; r < 4; ++r) {
+        const float4 x = run[r];
+        factor[r] = fmaxf(cmul * x.x, 1e-37f);
+        add[r] = x.y;
       }
-      // maximum of a + log2 sv over the tile
+      tmem_ld32_finish(v[0]);
+      tmem_ld32_finish(v[1]);
+      const int nvis = lim - tile_of(team, h) * kN - kHalf * b;
+      if (!__all_sync(0xffffffffu, nvis >= kHalf)) {
+#pragma unroll
+        for (int e = 0; e < kHalf; ++e)
+          if (e >= nvis) v[e >> 5][e & 31] = kNegInf;
+      }
+      // maximum of a + log2 sv
       float mt = kNegInf;
 #pragma unroll
-      for (int r = 0; r < 8; ++r) {
+      for (int r = 0; r < 4; ++r) {
         const float *x = &v[r >> 1][16 * (r & 1)];
-        float a = fmax3(x[0], x[1], x[2]), b = fmax3(x[3], x[4], x[5]);
-        a = fmax3(a, x[6], x[7]), b = fmax3(b, x[8], x[9]);
-        a = fmax3(a, x[10], x[11]), b = fmax3(b, x[12], x[13]);
-        const float4 sc = run[r];
-        mt = fmaxf(mt, fmaf(fmax3(fmaxf(a, b), x[14], x[15]), factor_of(sc), sc.y));
+        float c0 = fmax3(x[0], x[1], x[2]), c1 = fmax3(x[3], x[4], x[5]);
+        c0 = fmax3(c0, x[6], x[7]), c1 = fmax3(c1, x[8], x[9]);
+        c0 = fmax3(c0, x[10], x[11]), c1 = fmax3(c1, x[12], x[13]);
+        mt = fmaxf(mt, fmaf(fmax3(fmaxf(c0, c1), x[14], x[15]), factor[r], add[r]));
       }
       const bool rescale = mt > m_ref + kRescaleLog2;
       if (__any_sync(0xffffffffu, rescale)) {
         const float alpha = rescale ? fast_exp2(m_ref - mt) : 1.f;
-        if (i > 0) {   // (these scores came after the P.V of step i - 1 was complete)
+        if (h > 0) {   // O holds the P.V of steps 0 .. h - 1: the last of them has to be complete
+          ok = wait_all(&o_done[tb ^ 1], ((h - 1) >> 1) & 1);
+          if (!ok) break;
+          tc_fence_after();
 #pragma unroll 1
           for (int c0 = 0; c0 < D; c0 += 16) {
             float o[16];
@@ -367,11 +378,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float msub = m_ref == kNegInf ? 0.f : m_ref;
       // w = 2^(a + log2 sv - m_ref), rounded to f16, and the sum of w / sv
 #pragma unroll
-      for (int r = 0; r < 8; ++r) {
+      for (int r = 0; r < 4; ++r) {
         const float *x = &v[r >> 1][16 * (r & 1)];
-        const float4 sc = run[r];
-        const float cr = factor_of(sc), nr = sc.y - msub, iv = sc.z;
-        const float2 cc = make_float2(cr, cr), nm = make_float2(nr, nr);
+        const float nr = add[r] - msub, iv = run[r].z;
+        const float2 cc = make_float2(factor[r], factor[r]), nm = make_float2(nr, nr);
         float2 sum[2] = {{0.f, 0.f}, {0.f, 0.f}};
         uint32_t w[8], wl[8];
 #pragma unroll
@@ -384,20 +394,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         lacc = ffma2(make_float2(sum[0].x + sum[1].x, sum[0].y + sum[1].y), make_float2(iv, iv), lacc);
         if constexpr (kLo) {   // hi, lo of 16 keys over their own 16 columns
-          tmem_st8(sb + 16 * r, w);
-          tmem_st8(sb + 16 * r + 8, wl);
+          tmem_st8(sh + 16 * r, w);
+          tmem_st8(sh + 16 * r + 8, wl);
         } else {
-          tmem_st8(sb + 8 * r, w);
-        }
-        if (r == 3 || r == 7) {
-          tmem_wait_st();
-          tc_fence_before();
-          mbar_arrive(&p_full[(r >> 2) * kTeams + team]);
+          tmem_st8(sh + 8 * r, w);
         }
       }
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(&p_full[tb]);
     }
     float l = lacc.x + lacc.y;
-    if (ok && n > 0) ok = wait_all(&o_done[team], (n - 1) & 1);
+    if (ok && n > 0) ok = wait_all(&o_done[team * 2 + ((n - 1) & 1)], ((n - 1) >> 1) & 1);
     tc_fence_after();
     // Columns [c0, c1) of the row, kCols at a time through `value`, normalised by inv and stored by 8 (or 4) lanes per
     // row: the threads write 128 bytes of their rows into the warp's 4 KB (16-byte chunk c of row r at chunk c ^ (r & 7))
@@ -464,15 +472,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float mine = fast_exp2(m_ref - ref), theirs = fast_exp2(other.x - ref);
       l = l * mine + other.y * theirs;
       float4 *box = reinterpret_cast<float4 *>(smem);   // [team][column / 4 of the half][row]
-      constexpr int kHalf = D / 2;
+      constexpr int kCols = D / 2;
       if (live && ok) {
 #pragma unroll 1
-        for (int at = 0; at < kHalf; at += 32) {
+        for (int at = 0; at < kCols; at += 32) {
           float o[32];
-          load_o((team ^ 1) * kHalf + at, o);
+          load_o((team ^ 1) * kCols + at, o);
 #pragma unroll
           for (int k = 0; k < 8; ++k)
-            box[(team * (kHalf / 4) + at / 4 + k) * 128 + m] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+            box[(team * (kCols / 4) + at / 4 + k) * 128 + m] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
         }
       }
       both_sync();
@@ -481,7 +489,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           load_o(at, o);
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
-            const float4 x = box[((team ^ 1) * (kHalf / 4) + (at - team * kHalf) / 4 + k) * 128 + m];
+            const float4 x = box[((team ^ 1) * (kCols / 4) + (at - team * kCols) / 4 + k) * 128 + m];
             o[4 * k] = o[4 * k] * mine + x.x * theirs;
             o[4 * k + 1] = o[4 * k + 1] * mine + x.y * theirs;
             o[4 * k + 2] = o[4 * k + 2] * mine + x.z * theirs;
@@ -490,13 +498,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         uint8_t *stage = smem + L::kStage + warp * 4096;
         const float inv = l > 0.f ? 1.f / l : 0.f;
-        if (p.out_f32) emit(std::true_type{}, stage, team * kHalf, (team + 1) * kHalf, inv, joined);
-        else emit(std::false_type{}, stage, team * kHalf, (team + 1) * kHalf, inv, joined);
+        if (p.out_f32) emit(std::true_type{}, stage, team * kCols, (team + 1) * kCols, inv, joined);
+        else emit(std::false_type{}, stage, team * kCols, (team + 1) * kCols, inv, joined);
       }
     }
   } else if (warp < kMmaWarp) {
     // ===================================================== loaders
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLoadRegs));
     const int lw = warp - kLoadWarp0;
     constexpr int kPanels = D / 64;
     const char *kpool = static_cast<const char *>(p.k_cache), *vpool = static_cast<const char *>(p.v_cache);
@@ -578,10 +585,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (j + 1 < nkt) load(next, vpool, vw);
       now = next;
     }
-  } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kMmaRegs));
-  }
-  if (kRaw && warp == kKWarp) {
+  } else if (kRaw && warp == kKWarp) {
     // ===================================================== K tiles as stored
     // one box per cache block that holds a key; what the tile's other rows hold is masked in the scores
     const int bs = p.block_size, per_tile = kN / bs;
@@ -608,91 +612,81 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     // no box in flight at exit
     for (int j = max(0, issued - kKStages); j < issued; ++j) mbar_wait(&k_full[j % kKStages], (j / kKStages) & 1, p.err);
-  } else if (warp == kMmaWarp) {
-    // ===================================================== MMA issue
-    // (the whole warp runs the schedule, the elected lane's predicate issues: operands stay in uniform registers)
+  } else if (warp >= kMmaWarp && warp < kMmaWarp + kTeams) {
+    // ===================================================== MMA issue, a warp per team
+    // (one warp for both had its own instructions as the bound: 16 waits per key tile at some 100 clocks.  The whole warp
+    // runs the schedule, the elected lane's predicate issues: operands stay in uniform registers)
     const bool leader = elect_one();
-    const uint32_t idesc_s = umma_idesc(0, kN, false), idesc_o = umma_idesc(0, D, true);
+    const int team = warp - kMmaWarp, n = steps(team);
+    const uint32_t idesc_s = umma_idesc(0, kHalf, false), idesc_o = umma_idesc(0, D, true);
     constexpr bool kSw64 = kRaw && D == 64;     // rows of 64 bytes
-    const uint32_t q_at = smem_u32(smem + L::kOffQ), k_at = smem_u32(smem + L::kOffK);
-    const uint64_t qdesc0 = kSw64 ? umma_desc_sw64(q_at, 16, 512) : umma_desc(q_at, 16);
+    const uint32_t q_at = smem_u32(smem + L::kOffQ) + (kSplitKeys ? 0 : team * kTile), k_at = smem_u32(smem + L::kOffK);
+    const uint64_t qdesc = kSw64 ? umma_desc_sw64(q_at, 16, 512) : umma_desc(q_at, 16);
     const uint64_t kdesc0 = kSw64 ? umma_desc_sw64(k_at, 16, 512) : umma_desc(k_at, 16);
     const uint64_t vdesc0 = umma_desc(smem_u32(smem + L::kOffV), kPanel);
-    bool ok = nkt == 0 || wait_all(q_ready, 0), issued = false;
-    const int steps0 = steps(0), steps1 = steps(1);
-    // the last team to use key tile j
-    auto last_user = [&](int j) { return kSplitKeys ? j & 1 : j < n1 ? 1 : 0; };
-    auto issue_s = [&](int t, int j) {   // S of team t over key tile j
-      const uint64_t qd = qdesc0 + ((kSplitKeys ? 0 : t * kTile) >> 4), kd = kdesc0 + (((j % kKStages) * kKTile) >> 4);
+    const uint32_t s_at = sbuf(team), o_at = obuf(team);
+    uint64_t *s_bar = s_full + 2 * team, *p_bar = p_full + 2 * team, *o_bar = o_done + 2 * team;
+    bool ok = nkt == 0 || wait_all(q_ready, 0);
+    // S of step h, its buffer's last P.V (step h - 2) complete
+    auto issue_s = [&](int h) {
+      const int j = tile_of(team, h), b = h & 1, slot = j % kKStages;
+      if (b == 0) ok = wait_all(&k_full[slot], (j / kKStages) & 1);
+      if (h >= 2) ok = ok && wait_all(&o_bar[b], ((h >> 1) - 1) & 1);
+      if (!ok) return;
+      tc_fence_after();
+      const uint32_t d = s_at + kHalf * b;
+      const uint64_t kd = kdesc0 + ((slot * kKTile + b * (kRaw ? kHalf * D : kHalf * 128)) >> 4);
       if constexpr (kRaw) {
-#pragma unroll 1
-        for (int term = 0; term < 2; ++term)
 #pragma unroll
-          for (int k = 0; k < D / 32; ++k)
-            umma_f8_if(leader, sbuf(t), qd + term * ((kM * D) >> 4) + k * 2, kd + k * 2, idesc_s, term + k > 0 ? 1u : 0u);
+        for (int k = 0; k < 2 * (D / 32); ++k)
+          umma_f8_if(leader, d, qdesc + (k / (D / 32)) * ((kM * D) >> 4) + (k % (D / 32)) * 2, kd + (k % (D / 32)) * 2, idesc_s, k > 0 ? 1u : 0u);
       } else {
-#pragma unroll 1
-        for (int h = 0; h < D / 64; ++h)
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            umma_if(leader, sbuf(t), qd + h * (kPanel >> 4) + k * 2, kd + h * (kPanel >> 4) + k * 2, idesc_s, h + k > 0 ? 1u : 0u);
+        for (int k = 0; k < D / 16; ++k)
+          umma_if(leader, d, qdesc + (k >> 2) * (kPanel >> 4) + (k & 3) * 2, kd + (k >> 2) * (kPanel >> 4) + (k & 3) * 2, idesc_s, k > 0 ? 1u : 0u);
       }
-      umma_commit_if(leader, &s_full[t]);
-      if (t == last_user(j)) umma_commit_if(leader, &k_free[j % kKStages]);
-      issued = true;
+      umma_commit_if(leader, &s_bar[b]);
+      if (b || h + 1 == n) umma_commit_if(leader, &k_free[slot]);
     };
-    for (int t = 0; t < kTeams && ok; ++t) {
-      if ((t ? steps1 : steps0) == 0) continue;
-      const int j = tile_of(t, 0);
-      ok = wait_all(&k_full[j % kKStages], (j / kKStages) & 1);
+    if (n > 0) issue_s(0);
+    if (n > 1 && ok) issue_s(1);
+    for (int h = 0; h < n && ok; ++h) {
+      const int j = tile_of(team, h), b = h & 1, slot = j % kStages;
+      if (b == 0) ok = wait_all(&v_full[slot], (j / kStages) & 1);
+      ok = ok && wait_all(&p_bar[b], (h >> 1) & 1);
       if (!ok) break;
       tc_fence_after();
-      issue_s(t, j);
-    }
-    for (int i = 0; i < max(steps0, steps1) && ok; ++i) {
-#pragma unroll 1
-      for (int t = 0; t < kTeams && ok; ++t) {
-        const int n = t ? steps1 : steps0;
-        if (i >= n) continue;
-        const int j = tile_of(t, i), s = j % kStages;
-        ok = wait_all(&v_full[s], (j / kStages) & 1);
-        if (!ok) break;
-        const uint64_t vd = vdesc0 + ((s * kTile) >> 4);
-#pragma unroll 1
-        for (int h = 0; h < 2; ++h) {   // keys 0..63, then 64..127
-          ok = ok && wait_all(&p_full[h * kTeams + t], i & 1);
-          if (!ok) break;
-          tc_fence_after();
+      const uint64_t vd = vdesc0 + ((slot * kTile + b * kHalf * 128) >> 4);
+      const uint32_t pa = s_at + kHalf * b;
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk) {
-            constexpr int kStep = (16 * 128) >> 4;
-            const uint32_t acc = i + h + kk > 0 ? 1u : 0u;
-            if constexpr (kLo) {
-              umma_ts_if(leader, obuf(t), sbuf(t) + 64 * h + 16 * kk, vd + (4 * h + kk) * kStep, idesc_o, acc);
-              umma_ts_if(leader, obuf(t), sbuf(t) + 64 * h + 16 * kk + 8, vd + (4 * h + kk) * kStep, idesc_o, 1u);
-            } else {
-              umma_ts_if(leader, obuf(t), sbuf(t) + 32 * h + 8 * kk, vd + (4 * h + kk) * kStep, idesc_o, acc);
-            }
-          }
-          issued = true;
-        }
-        if (!ok) break;
-        umma_commit_if(leader, &o_done[t]);
-        if (t == last_user(j)) umma_commit_if(leader, &v_free[s]);
-        if (i + 1 < n) {
-          const int jn = tile_of(t, i + 1);
-          ok = wait_all(&k_full[jn % kKStages], (jn / kKStages) & 1) && wait_all(&o_done[t], i & 1);
-          if (!ok) break;
-          tc_fence_after();
-          issue_s(t, jn);
+      for (int kk = 0; kk < 4; ++kk) {
+        constexpr int kStep = (16 * 128) >> 4;
+        const uint32_t acc = h + kk > 0 ? 1u : 0u;
+        if constexpr (kLo) {
+          umma_ts_if(leader, o_at, pa + 16 * kk, vd + kk * kStep, idesc_o, acc);
+          umma_ts_if(leader, o_at, pa + 16 * kk + 8, vd + kk * kStep, idesc_o, 1u);
+        } else {
+          umma_ts_if(leader, o_at, pa + 8 * kk, vd + kk * kStep, idesc_o, acc);
         }
       }
+      umma_commit_if(leader, &o_bar[b]);
+      if (b || h + 1 == n) umma_commit_if(leader, &v_free[slot]);
+      if (h + 2 < n) issue_s(h + 2);
     }
+    // key tiles that only the other team walks
+    if constexpr (!kSplitKeys)
+      for (int j = (n + 1) / 2; j < nkt && ok; ++j) {
+        ok = wait_all(&k_full[j % kKStages], (j / kKStages) & 1);
+        if (ok && leader) mbar_arrive(&k_free[j % kKStages]);
+        ok = ok && wait_all(&v_full[j % kStages], (j / kStages) & 1);
+        if (ok && leader) mbar_arrive(&v_free[j % kStages]);
+        __syncwarp();
+      }
     // every MMA issued above is complete before tensor memory is freed
-    if (issued) {
-      if (leader) umma_commit(fin);
+    if (n > 0) {
+      umma_commit_if(leader, &fin[team]);
       __syncwarp();
-      mbar_wait(fin, 0, p.err);
+      mbar_wait(&fin[team], 0, p.err);
     }
   }
 
