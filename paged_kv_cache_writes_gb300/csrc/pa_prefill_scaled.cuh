@@ -30,7 +30,7 @@
 //
 // A team's score buffer is two halves of 64 keys, each with its own softmax step: while a team's threads work on one half,
 // the tensor cores compute the other half's scores and the P.V of the one before.  P (f16 pairs; hi + lo) goes over its own
-// half.  (With one buffer of 128 keys a team waited for P.V and the next Q.K^T in turn: 821 us against XXX for 4 chunks of
+// half.  (With one buffer of 128 keys a team waited for P.V and the next Q.K^T in turn: 821 us against 721 for 4 chunks of
 // 2048 at 2048, 64/8 heads.)
 //
 // Loaders: four warps, 32 keys of a tile each, a key tile ahead in registers (8-byte loads, a row of codes per 8 lanes),
@@ -70,15 +70,16 @@ struct Layout {
   static constexpr int kTile = kN * D * 2;                     // a Q or V tile (Q: f16, or two terms of codes)
   static constexpr int kKTile = kRaw ? kN * D : kTile;
   static constexpr int kStages = 2, kKStages = kRaw ? 3 : 2;   // V, K tiles in flight
+  static constexpr int kScaleSlots = kStages + 2;              // key tiles whose scales are at hand
   static constexpr int kOffQ = 0;
   static constexpr int kOffK = kOffQ + (kSplitKeys ? 1 : 2) * kTile;
   static constexpr int kOffV = kOffK + kKStages * kKTile;
   static constexpr int kOffBar = kOffV + kStages * kTile;
-  static constexpr int kNumBars = 2 * kStages + 2 * kKStages + 3 * 2 * kTeams + 2 + kTeams;   // (even: 16-byte alignment behind them)
+  static constexpr int kNumBars = 2 * kStages + 2 * kKStages + 3 * 2 * kTeams + kScaleSlots + 2 + kTeams;   // (even: 16-byte alignment behind them)
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;
   static constexpr int kOffRow = kOffMisc + 16;                // float2 [kTeams][128]
-  static constexpr int kOffRuns = kOffRow + kTeams * 128 * 8;  // float4 [softmax warp][2][8 runs]
-  static constexpr int kBytes = kOffRuns + kSoftmax / 32 * 2 * 8 * 16 + 1024;   // + alignment slack
+  static constexpr int kOffRuns = (kOffRow + kTeams * 128 * 8 + 15) / 16 * 16;  // float4 [kScaleSlots][8 runs]
+  static constexpr int kBytes = kOffRuns + kScaleSlots * 8 * 16 + 1024;   // + alignment slack
   static_assert(kBytes <= 227 * 1024 && kOffRow % 8 == 0 && kOffRuns % 16 == 0, "shared memory");
   static constexpr int kStage = kOffBar - kSoftmax / 32 * 4096;   // kSplitKeys: 4 KB per softmax warp for the output's way
   static_assert(kOffV % 1024 == 0 && (!kSplitKeys || kStage >= 128 * D * 4), "room for the teams' halves of O before it");
@@ -118,11 +119,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t *s_full = k_free + kKStages;          // [team][half] scores of its step h (half h & 1, phase h >> 1)
   uint64_t *p_full = s_full + 2 * kTeams;        // [team][half] P written over them (128 arrivals)
   uint64_t *o_done = p_full + 2 * kTeams;        // [team][half] P.V complete
-  uint64_t *q_ready = o_done + 2 * kTeams;
+  uint64_t *sc_full = o_done + 2 * kTeams;       // [kScaleSlots] a tile's scales (an arrival of each loader warp)
+  uint64_t *q_ready = sc_full + L::kScaleSlots;
   uint64_t *fin = q_ready + 1;                   // [team] every MMA of the team complete
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::kOffMisc);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::kOffMisc + 8);
   float2 *row_info = reinterpret_cast<float2 *>(smem + L::kOffRow);
+  // of each run of 16 keys of tile j, at [j % kScaleSlots]: K's scale, log2 of V's, 1 / V's
+  float4 *runs = reinterpret_cast<float4 *>(smem + L::kOffRuns);
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   // work item: KV head share fastest, then chunk, then row block from the last (longest) one down
@@ -173,6 +177,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&o_done[t], 1);
     }
     mbar_init(q_ready, kSplitKeys ? 128 : kSoftmax);
+    for (int i = 0; i < L::kScaleSlots; ++i) mbar_init(&sc_full[i], kLoaders / 32);
     mbar_init(&fin[0], 1);
     mbar_init(&fin[1], 1);
     *abort_flag = 0;
@@ -279,29 +284,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       cmul = fmaxf(cmul * row_info[team * 128 + m].x, 1e-30f);
     }
 
-    // scales of this team's steps: lane i < 8 has those of run i (16 keys) of the next tile in flight (their block ids a
-    // step before that), and leaves them in shared memory for the warp when the tile is at hand
     const int n = steps(team);
-    float next_k = 1.f, next_v = 1.f;
-    int32_t next_blk = -1;
-    auto run_block = [&](int h) -> int32_t {   // of the tile of step h (an id out of range is reported by the loaders)
-      const int key = tile_of(team, h) * kN + 16 * lane;
-      if (lane >= 8 || h >= n || key >= seq_eff) return -1;
-      const int32_t bi = __ldg(table + (key >> bs_log2));
-      return bi >= 0 && bi < p.num_blocks ? bi : -1;
-    };
-    auto read_scales = [&](int32_t bi) {
-      next_k = next_v = 1.f;
-      if (bi >= 0) {
-        const int64_t at = (int64_t)bi * p.num_kv_heads + g;
-        next_k = __ldg(p.k_scales + at);
-        next_v = __ldg(p.v_scales + at);
-      }
-    };
-    read_scales(run_block(0));
-    next_blk = run_block(2);
-    float4 *runs = reinterpret_cast<float4 *>(smem + L::kOffRuns) + warp * 16;
-
     float m_ref = kNegInf;                       // reference maximum, log2 units
     float2 lacc = make_float2(0.f, 0.f);         // row sum in two parts
     const float2 ones = make_float2(1.f, 1.f);
@@ -309,18 +292,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t sb = sbuf(team) + lane_base, ob = obuf(team) + lane_base;
     for (int h = 0; h < n; ++h) {
       const int b = h & 1, tb = team * 2 + b;
-      if (b == 0) {
-        if (lane < 8) {
-          const bool good = block_scale_ok(next_k) && block_scale_ok(next_v);
-          if (!good) record_error(p.err, PA_ERR_DEVICE_CHECK);
-          runs[(h & 2) * 4 + lane] = good ? make_float4(next_k, __log2f(next_v), __fdividef(1.f, next_v), 0.f) : make_float4(1.f, 0.f, 1.f, 0.f);
-        }
-        __syncwarp();
-        read_scales(next_blk);
-        next_blk = run_block(h + 4);
-      }
-      const float4 *run = runs + (h & 2) * 4 + 4 * b;   // the half's four runs
-      ok = wait_all(&s_full[tb], (h >> 1) & 1);
+      const int j = tile_of(team, h), slot = j % L::kScaleSlots;
+      if (b == 0) ok = wait_all(&sc_full[slot], (j / L::kScaleSlots) & 1);
+      const float4 *run = runs + 8 * slot + 4 * b;   // the half's four runs
+      ok = ok && wait_all(&s_full[tb], (h >> 1) & 1);
       if (!ok) break;
       tc_fence_after();
       const uint32_t sh = sb + kHalf * b;
@@ -337,7 +312,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       tmem_ld32_finish(v[0]);
       tmem_ld32_finish(v[1]);
-      const int nvis = lim - tile_of(team, h) * kN - kHalf * b;
+      const int nvis = lim - j * kN - kHalf * b;
       if (!__all_sync(0xffffffffu, nvis >= kHalf)) {
 #pragma unroll
         for (int e = 0; e < kHalf; ++e)
@@ -564,19 +539,54 @@ __global__ void __launch_bounds__(kThreads, 1)
           *reinterpret_cast<uint4 *>(tile + (i & 1 ? to1 : to0) + i * 512 + pn * kPanel) = widen8(w[pn][i]);
       fence_async_smem();
     };
+    // Scales, by lanes 0 and 1 of each warp those of its two runs (1 for a run without tokens, and for a bad one after its
+    // report): tile j + 2's are published when the P.V of tile j - kStages, the last that used their place, is complete;
+    // the next tile's are in flight then, and the block ids of the one after it
+    auto run_block = [&](int j) -> int32_t {
+      const int key = j * kN + 32 * lw + 16 * lane;
+      if (lane >= 2 || j >= nkt || key >= seq_eff) return -1;
+      const int32_t bi = __ldg(table + (key >> bs_log2));
+      return bi >= 0 && bi < p.num_blocks ? bi : -1;
+    };
+    float sk = 1.f, sv = 1.f;
+    auto read_scales = [&](int32_t b) {
+      sk = sv = 1.f;
+      if (b >= 0) {
+        const int64_t at = (int64_t)b * p.num_kv_heads + g;
+        sk = __ldg(p.k_scales + at);
+        sv = __ldg(p.v_scales + at);
+      }
+    };
+    auto put_scales = [&](int j) {
+      if (lane < 2) {
+        const bool good = block_scale_ok(sk) && block_scale_ok(sv);
+        if (!good) record_error(p.err, PA_ERR_DEVICE_CHECK);
+        runs[8 * (j % L::kScaleSlots) + 2 * lw + lane] =
+            good ? make_float4(sk, __log2f(sv), __fdividef(1.f, sv), 0.f) : make_float4(1.f, 0.f, 1.f, 0.f);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sc_full[j % L::kScaleSlots]);
+    };
     Words kw, vw;
     Rows now = rows_of(0), next = now;
     if (nkt > 0) {
       if constexpr (!kRaw) load(now, kpool, kw);
       load(now, vpool, vw);
     }
+    for (int j = 0; j < 2; ++j) {
+      read_scales(run_block(j));
+      put_scales(j);
+    }
+    read_scales(run_block(2));
+    int32_t scale_blk = run_block(3);
     for (int j = 0; j < nkt; ++j) {
       const int s = j % kStages;
       if (j + 1 < nkt) next = rows_of(j + 1);
       if constexpr (!kRaw) {
-        if (j >= kStages && !wait_all(&k_free[s], ((j / kStages) - 1) & 1)) break;
-        widen(kw, now, smem + L::kOffK + s * kTile);
-        mbar_arrive(&k_full[s]);
+        const int ks = j % kKStages;
+        if (j >= kKStages && !wait_all(&k_free[ks], ((j / kKStages) - 1) & 1)) break;
+        widen(kw, now, smem + L::kOffK + ks * kKTile);
+        mbar_arrive(&k_full[ks]);
         if (j + 1 < nkt) load(next, kpool, kw);
       }
       if (j >= kStages && !wait_all(&v_free[s], ((j / kStages) - 1) & 1)) break;
@@ -584,6 +594,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_arrive(&v_full[s]);
       if (j + 1 < nkt) load(next, vpool, vw);
       now = next;
+      if (j + 2 < nkt) {
+        put_scales(j + 2);
+        read_scales(scale_blk);
+        scale_blk = run_block(j + 4);
+      }
     }
   } else if (kRaw && warp == kKWarp) {
     // ===================================================== K tiles as stored
