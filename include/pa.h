@@ -609,25 +609,26 @@ PA_API pa_status pa_copy_blocks_scaled(void *k_cache, void *v_cache, const pa_kv
  * pa_decode_scaled -- pa_decode over a block-scaled cache: K_i[p] is code *
  * k_block_scales[b][g] and V_i[p] code * v_block_scales[b][g], b the block of
  * position p.  Scales need not be powers of two; one out of [2^-64, 2^32] sets
- * PA_ERR_DEVICE_CHECK (the rows that read it are then undefined).  The tensor
- * cores multiply the codes as stored: K's scales meet the scores, V's the softmax
+ * PA_ERR_DEVICE_CHECK (the rows that read it are then undefined).  The products
+ * take the codes as they are: K's scales meet the scores, V's the softmax
  * weights, whose sum stays that of the weights without them, in fp32.  A weight
- * times V's scale is held to 2^-8 of itself for a bf16 output, to 2^-12 for any
- * other.
+ * times V's scale is rounded once to f16 (2^-11 of itself) for a 16-bit output
+ * and held to 2^-22 for an fp32 one.
  *   workspace   device, >= pa_decode_scaled_workspace_bytes(...) bytes for the
- *               same arguments or for a larger num_seqs or max_seq_len; else as
- *               for pa_decode
- *   all other arguments as for pa_decode.  Every shape of pa_decode is served by
- *   the tensor-core decode, whatever pa_set_decode_kernel says.
+ *               same heads and head_dim (the number and length of the sequences
+ *               do not matter); else as for pa_decode
+ *   all other arguments as for pa_decode.  Every shape of pa_decode is served,
+ *   whatever pa_set_decode_kernel says; how rows are cut is the library's choice
+ *   (no partition_size).
  */
 PA_API size_t pa_decode_scaled_workspace_bytes(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
-                                               int32_t head_dim, int32_t max_seq_len, int32_t partition_size);
+                                               int32_t head_dim, int32_t max_seq_len);
 PA_API pa_status pa_decode_scaled(const void *q, pa_dtype q_dtype, int32_t num_seqs, int32_t num_q_heads,
                                   const void *k_cache, const void *v_cache, const pa_kv_cache *cache,
                                   const float *k_block_scales, const float *v_block_scales,
                                   const int32_t *block_tables, int32_t max_blocks_per_seq, const int32_t *seq_lens,
-                                  int32_t max_seq_len, float scale, int32_t partition_size, void *workspace,
-                                  size_t workspace_bytes, void *out, pa_dtype out_dtype, pa_stream_t stream);
+                                  int32_t max_seq_len, float scale, void *workspace, size_t workspace_bytes, void *out,
+                                  pa_dtype out_dtype, pa_stream_t stream);
 
 /*
  * pa_prefill_chunk_scaled -- pa_prefill_chunk over a block-scaled cache (K, V

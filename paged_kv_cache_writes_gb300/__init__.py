@@ -115,10 +115,10 @@ def lib() -> ctypes.CDLL:
         L.pa_rope_and_cache.argtypes = [P, I64, P, I32, P, P, ctypes.c_int, I32, I64, P, P, I32, I32, I32, P, P, P, CACHE, P,
                                         P, P]
         L.pa_copy_blocks_scaled.argtypes = [P, P, CACHE, P, P, P, I32, P]
-        L.pa_decode_scaled_workspace_bytes.argtypes = [I32] * 6
+        L.pa_decode_scaled_workspace_bytes.argtypes = [I32] * 5
         L.pa_decode_scaled_workspace_bytes.restype = SZ
-        L.pa_decode_scaled.argtypes = [P, ctypes.c_int, I32, I32, P, P, CACHE, P, P, P, I32, P, I32, F, I32, P, SZ, P,
-                                       ctypes.c_int, P]
+        L.pa_decode_scaled.argtypes = [P, ctypes.c_int, I32, I32, P, P, CACHE, P, P, P, I32, P, I32, F, P, SZ, P, ctypes.c_int,
+                                       P]
         L.pa_prefill_chunk_scaled.argtypes = [P, ctypes.c_int, P, P, I32, I32, I32, P, P, CACHE, P, P, P, I32, P, I32, F, P,
                                               ctypes.c_int, P]
         L.pa_get_device_error.argtypes = [P, ctypes.POINTER(I32)]
@@ -566,15 +566,14 @@ def pa_copy_blocks_scaled(k_cache: torch.Tensor, v_cache: torch.Tensor, cache: P
 
 
 def pa_decode_scaled_workspace_bytes(num_seqs: int, num_q_heads: int, num_kv_heads: int, head_dim: int,
-                                     max_seq_len: int, partition_size: int = 0) -> int:
-    return int(lib().pa_decode_scaled_workspace_bytes(num_seqs, num_q_heads, num_kv_heads, head_dim, max_seq_len,
-                                                      partition_size))
+                                     max_seq_len: int) -> int:
+    return int(lib().pa_decode_scaled_workspace_bytes(num_seqs, num_q_heads, num_kv_heads, head_dim, max_seq_len))
 
 
 def pa_decode_scaled(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, cache: PaKvCache,
                      k_scales: torch.Tensor, v_scales: torch.Tensor, block_tables: torch.Tensor, seq_lens: torch.Tensor,
                      max_seq_len: int, scale: float, out: torch.Tensor, workspace: torch.Tensor | None = None,
-                     partition_size: int = 0, stream=None) -> None:
+                     stream=None) -> None:
     """pa_decode over a block-scaled fp8 cache (``k_scales``, ``v_scales``: float32 [num_blocks, Hkv]).
     ``workspace``: uint8 tensor of >= pa_decode_scaled_workspace_bytes(...) bytes."""
     a = _Args()
@@ -584,8 +583,8 @@ def pa_decode_scaled(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tens
     status = lib().pa_decode_scaled(
         a(q, "q"), _dtype_code(q.dtype), B, hq, a(k_cache, "k_cache"), a(v_cache, "v_cache"), ctypes.byref(cache), ks, vs,
         a(block_tables, "block_tables", _I32), block_tables.shape[1], a.of_sequences(seq_lens, "seq_lens", B), max_seq_len,
-        scale, partition_size, a.maybe(workspace, "workspace"), 0 if workspace is None else workspace.nbytes,
-        a(out, "out"), _dtype_code(out.dtype), a.stream(stream))
+        scale, a.maybe(workspace, "workspace"), 0 if workspace is None else workspace.nbytes, a(out, "out"),
+        _dtype_code(out.dtype), a.stream(stream))
     if status:
         raise PaError(status, "pa_decode_scaled")
 

@@ -651,6 +651,29 @@ size_t bounded_workspace(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_h
   return most_bytes;
 }
 
+// Shares and workspace of pa_decode_scaled: two pieces of every CTA, whatever the batch.
+struct ScaledLayout {
+  int32_t shares, share_heads;
+  size_t ml_off, acc_off, total;
+};
+pa_status scaled_layout(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, int32_t max_seq_len,
+                        ScaledLayout *l) {
+  if (num_seqs < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || num_q_heads % num_kv_heads || max_seq_len < 0)
+    return PA_ERR_INVALID_ARG;
+  if ((head_dim != 64 && head_dim != 128) || num_seqs > kMaxDecodeRows) return PA_ERR_UNSUPPORTED;
+  const int gqa = num_q_heads / num_kv_heads;
+  l->shares = (gqa + kScaledHeads - 1) / kScaledHeads;
+  l->share_heads = (gqa + l->shares - 1) / l->shares;
+  // tiles of 16 keys are counted in 64 bits, shares of a row in 32
+  if ((double)num_kv_heads * l->shares >= 2147483648.0 ||
+      (double)num_seqs * (max_seq_len / 16 + 1.0) * num_kv_heads * l->shares >= 4e18)
+    return PA_ERR_UNSUPPORTED;
+  l->ml_off = round256(kScaledCtas * sizeof(int4));
+  l->acc_off = l->ml_off + round256((size_t)2 * kScaledCtas * l->share_heads * 8);
+  l->total = l->acc_off + round256((size_t)2 * kScaledCtas * l->share_heads * head_dim * 4);
+  return PA_OK;
+}
+
 // Workspace of pa_evict: each head's list of moves (their number padded to 16
 // bytes, destinations, sources).
 struct EvictLayout {
@@ -678,18 +701,11 @@ struct Weights {
   float decay;
 };
 
-// The scales of a block-scaled cache.
-struct BlockScales {
-  const float *k, *v;
-};
-
-// bs: over a block-scaled cache.
 pa_status bounded_decode(const void *q, pa_dtype q_dtype, int32_t num_seqs, int32_t num_q_heads, const void *k_cache,
                          const void *v_cache, const pa_kv_cache *cache, const int32_t *block_tables,
                          int32_t max_blocks_per_seq, const int32_t *seq_lens, int32_t max_seq_len, int32_t window,
                          int32_t num_sinks, float scale, int32_t partition_size, void *workspace,
-                         size_t workspace_bytes, void *out, pa_dtype out_dtype, const Weights *wt,
-                         const BlockScales *bs, pa_stream_t stream) {
+                         size_t workspace_bytes, void *out, pa_dtype out_dtype, const Weights *wt, pa_stream_t stream) {
   pa_status st = check_decode(q, q_dtype, num_seqs, num_q_heads, k_cache, v_cache, cache, block_tables,
                               max_blocks_per_seq, seq_lens, max_seq_len, scale, partition_size, out, out_dtype);
   if (st != PA_OK) return st;
@@ -717,10 +733,6 @@ pa_status bounded_decode(const void *q, pa_dtype q_dtype, int32_t num_seqs, int3
   tp.shares = b.shares;
   tp.share_heads = b.share_heads;
   tp.direct = b.direct;
-  if (bs) {
-    tp.k_scales = bs->k;
-    tp.v_scales = bs->v;
-  }
   if (wt) {
     tp.scores = reinterpret_cast<float *>(ws + b.scores_off);
     tp.score_stride = b.score_stride;
@@ -730,8 +742,7 @@ pa_status bounded_decode(const void *q, pa_dtype q_dtype, int32_t num_seqs, int3
   if (!encode_decode_tc_maps(&maps, k_cache, v_cache, c)) return PA_ERR_CUDA;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e;
-  if (bs) e = q_dtype == PA_BF16 ? launch_decode_scaled_bf16q(tp, c.head_dim, maps, s) : launch_decode_scaled_f16q(tp, c.head_dim, maps, s);
-  else if (c.kv_dtype == PA_BF16) e = launch_decode_ext_bf16(tp, c.head_dim, maps, s);
+  if (c.kv_dtype == PA_BF16) e = launch_decode_ext_bf16(tp, c.head_dim, maps, s);
   else if (c.kv_dtype == PA_F16) e = launch_decode_ext_f16(tp, c.head_dim, maps, s);
   else if (q_dtype == PA_BF16) e = launch_decode_ext_fp8_bf16q(tp, c.head_dim, maps, s);
   else e = launch_decode_ext_fp8_f16q(tp, c.head_dim, maps, s);
@@ -792,28 +803,58 @@ pa_status pa_decode_window(const void *q, pa_dtype q_dtype, int32_t num_seqs, in
                            size_t workspace_bytes, void *out, pa_dtype out_dtype, pa_stream_t stream) {
   return bounded_decode(q, q_dtype, num_seqs, num_q_heads, k_cache, v_cache, cache, block_tables, max_blocks_per_seq,
                         seq_lens, max_seq_len, window, num_sinks, scale, partition_size, workspace, workspace_bytes,
-                        out, out_dtype, nullptr, nullptr, stream);
+                        out, out_dtype, nullptr, stream);
 }
 
-// no window: the block size does not matter
 size_t pa_decode_scaled_workspace_bytes(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
-                                        int32_t max_seq_len, int32_t partition_size) {
-  return bounded_workspace(num_seqs, num_q_heads, num_kv_heads, head_dim, 16, max_seq_len, INT32_MAX, 0, partition_size,
-                           false);
+                                        int32_t max_seq_len) {
+  ScaledLayout l;
+  return scaled_layout(num_seqs, num_q_heads, num_kv_heads, head_dim, max_seq_len, &l) == PA_OK ? l.total : 0;
 }
 
 pa_status pa_decode_scaled(const void *q, pa_dtype q_dtype, int32_t num_seqs, int32_t num_q_heads, const void *k_cache,
                            const void *v_cache, const pa_kv_cache *cache, const float *k_block_scales,
                            const float *v_block_scales, const int32_t *block_tables, int32_t max_blocks_per_seq,
-                           const int32_t *seq_lens, int32_t max_seq_len, float scale, int32_t partition_size,
-                           void *workspace, size_t workspace_bytes, void *out, pa_dtype out_dtype, pa_stream_t stream) {
+                           const int32_t *seq_lens, int32_t max_seq_len, float scale, void *workspace,
+                           size_t workspace_bytes, void *out, pa_dtype out_dtype, pa_stream_t stream) {
   pa_kv_cache c;
-  const pa_status st = check_scaled_cache(cache, k_block_scales, v_block_scales, &c);
+  pa_status st = check_scaled_cache(cache, k_block_scales, v_block_scales, &c);
   if (st != PA_OK) return st;
-  const BlockScales bs{k_block_scales, v_block_scales};
-  return bounded_decode(q, q_dtype, num_seqs, num_q_heads, k_cache, v_cache, &c, block_tables, max_blocks_per_seq,
-                        seq_lens, max_seq_len, INT32_MAX, 0, scale, partition_size, workspace, workspace_bytes, out,
-                        out_dtype, nullptr, &bs, stream);
+  st = check_decode(q, q_dtype, num_seqs, num_q_heads, k_cache, v_cache, &c, block_tables, max_blocks_per_seq, seq_lens,
+                    max_seq_len, scale, 0, out, out_dtype);
+  if (st != PA_OK) return st;
+  ScaledLayout l;
+  if ((st = scaled_layout(num_seqs, num_q_heads, c.num_kv_heads, c.head_dim, max_seq_len, &l)) != PA_OK) return st;
+  if (num_seqs == 0) return PA_OK;
+  if (!workspace || !aligned(workspace, 256) || workspace_bytes < l.total) return PA_ERR_INVALID_ARG;
+  DecodeScaledParams p{};
+  p.q = q;
+  p.k_cache = k_cache;
+  p.v_cache = v_cache;
+  p.k_scales = k_block_scales;
+  p.v_scales = v_block_scales;
+  p.block_tables = block_tables;
+  p.max_blocks_per_seq = max_blocks_per_seq;
+  p.seq_lens = seq_lens;
+  p.max_seq_len = max_seq_len;
+  p.num_seqs = num_seqs;
+  p.num_q_heads = num_q_heads;
+  p.num_kv_heads = c.num_kv_heads;
+  p.shares = l.shares;
+  p.share_heads = l.share_heads;
+  p.block_size = c.block_size;
+  p.num_blocks = c.num_blocks;
+  p.s_mult = scale * 1.4426950408889634f;
+  p.out = out;
+  p.out_f32 = out_dtype == PA_F32;
+  char *ws = static_cast<char *>(workspace);
+  p.joins = reinterpret_cast<int4 *>(ws);
+  p.ws_ml = reinterpret_cast<float2 *>(ws + l.ml_off);
+  p.ws_acc = reinterpret_cast<float *>(ws + l.acc_off);
+  p.err = device_error_word();
+  if (!p.err) return PA_ERR_CUDA;
+  return launch_decode_scaled(p, q_dtype, c.head_dim, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? PA_OK
+                                                                                                         : PA_ERR_CUDA;
 }
 
 size_t pa_evict_workspace_bytes(int32_t num_seqs, int32_t num_kv_heads, int32_t max_seq_len, int32_t budget) {
@@ -901,7 +942,7 @@ pa_status pa_decode_weights(const void *q, pa_dtype q_dtype, int32_t num_seqs, i
   const Weights wt{weights, weights_stride, num_weight_rows, weight_rows, fresh_from, decay};
   return bounded_decode(q, q_dtype, num_seqs, num_q_heads, k_cache, v_cache, cache, block_tables, max_blocks_per_seq,
                         seq_lens, max_seq_len, INT32_MAX, 0, scale, partition_size, workspace, workspace_bytes, out,
-                        out_dtype, &wt, nullptr, stream);
+                        out_dtype, &wt, stream);
 }
 
 }  // extern "C"

@@ -90,10 +90,6 @@
 // kernel over rows packed by a sliding window with visible first tokens
 // (pa_window.cuh), for any group size (wide groups cut into shares), K and V
 // loaded with an evict-first L2 policy, the scores written out for the weights.
-// Block-scaled fp8 caches (kBlk: pa_decode_scaled) add one scale per block, KV
-// head and pool: score and P are t = s k_scale + log2 v_scale, 2^(t - max), so that
-// the products stay those of the codes; the softmax sum takes 2^(t - max) / v_scale.
-// The scheduler warp reads a unit's scales with its block ids.
 // Small batches run "direct": no plan kernel, the scheduler warp of each CTA
 // deals the units from the lengths, and pa_finish.cu merges the split rows.
 //
@@ -156,8 +152,6 @@ struct DecodeTcParams {
   // turns b, b + grid, ... of the units (row, partition, kvh) that hold tokens, and pa_finish.cu's
   // kernel merges the split rows afterwards.
   int32_t direct;
-  // Block-scaled caches (kernels built with kBlk): [num_blocks][num_kv_heads] scales of K and V
-  const float *k_scales, *v_scales;
 };
 
 // The packed length under the window of a row of L tokens, and where its cut
@@ -235,12 +229,6 @@ struct TcUnit {
   int32_t blk[kMaxTiles * 8];
 };
 
-// Block-scaled caches: of each 16-key run of a unit's tiles, published with its
-// descriptor (run r of tile j at [8*j + r]), K's scale, log2 of V's and 1 / V's.
-struct __align__(16) RunScale {
-  float k, log2_v, inv_v, unused;
-};
-
 // Whether P goes into the second product as hi + lo: for a bf16 cache (8 bits
 // would be too few), and in the bounded-cache decodes for an f16 cache too,
 // whose softmax sum is then that of the unrounded P, as the accumulated
@@ -271,7 +259,7 @@ struct QTerms {
 // and P^T of one 128-key panel, holding the hi terms in rows 0..G-1, the lo
 // terms in rows G..2G-1 (and with three terms, the last in rows 2G..3G-1 of
 // Q^T or P^T).
-template <int G, bool kSplit, bool kFp8, int kQTerms = 1, int D = 128, int kPTerms = 2, bool kBlk = false>
+template <int G, bool kSplit, bool kFp8, int kQTerms = 1, int D = 128, int kPTerms = 2>
 struct TcGeo {
   static_assert(G == 4 || G == 8 || G == 16, "4, 8 or 16 query heads per KV head");
   static_assert(D == 128 || D == 64, "head_dim 128 or 64");
@@ -295,8 +283,7 @@ struct TcGeo {
   static constexpr int kOffP = kOffQ + kQBufs * kQBytes;                 // [2][4] P^T
   static constexpr int kOffRed = kOffP + 2 * kMaxTiles * kPBytes;        // float [2][4 warps][2][16]
   static constexpr int kOffInfo = kOffRed + 2 * 4 * 2 * 16 * 4;          // TcUnit [kInfo] (16-byte aligned)
-  static constexpr int kOffScale = kOffInfo + kInfo * (int)sizeof(TcUnit);   // kBlk: RunScale [kInfo][32]
-  static constexpr int kOffBar = kOffScale + (kBlk ? kInfo * kMaxTiles * 8 * 16 : 0);
+  static constexpr int kOffBar = kOffInfo + kInfo * (int)sizeof(TcUnit);
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;
   static constexpr int kOffRep = (kOffMisc + 16 + 15) / 16 * 16;         // int4 [kRep] reports (16-byte aligned)
   static constexpr int kOffRing = (kOffRep + kRep * 16 + 1023) / 1024 * 1024;  // [kSlots] K/V tiles
@@ -438,7 +425,7 @@ __device__ __forceinline__ int32_t query_scale_bits(float amax) {
 // kExt: a sliding window with first tokens that stay visible, groups cut into
 // shares, and the scores written out (the bounded-cache decodes).
 template <typename KV, typename QT, int G, int D = 128, int NL = 1, bool kSepMerge = false, bool kPadRows = false,
-          bool kExt = false, int kPTerms = 2, bool kBlk = false>
+          bool kExt = false, int kPTerms = 2>
 __device__ __forceinline__ void decode_tc_body(const DecodeTcParams &tp, const CUtensorMap *tmap_k,
                                                const CUtensorMap *tmap_v) {
   using namespace tc;
@@ -454,8 +441,7 @@ __device__ __forceinline__ void decode_tc_body(const DecodeTcParams &tp, const C
   constexpr bool kBf16 = std::is_same<QT, __nv_bfloat16>::value && !kFp8;
   constexpr bool kSplit = split_p<KV, QT, kExt>();   // 16-bit caches: P as hi + lo
   constexpr int kQTerms = QTerms<KV, QT>::value;
-  using GE = TcGeo<G, kSplit, kFp8, kQTerms, D, kPTerms, kBlk>;
-  static_assert(!kBlk || (kExt && kFp8), "block scales: fp8 caches, in the bounded-cache kernels");
+  using GE = TcGeo<G, kSplit, kFp8, kQTerms, D, kPTerms>;
   // The MMA warp consumes the ring in order, so a loader's wait for the consumption of
   // position g - S is never two phases behind while it has NL <= S positions in hand.
   static_assert(GE::kSlots >= NL, "at least as many ring slots as loaders (parity waits stay within one phase)");
@@ -491,7 +477,6 @@ __device__ __forceinline__ void decode_tc_body(const DecodeTcParams &tp, const C
   uint64_t *rep_full = fin + 1;               // [kRep] a split unit's partials stored (one arrival per softmax warp)
   uint64_t *rep_free = rep_full + kRep;       // [kRep] its report taken by the merge warp
   TcUnit *info = reinterpret_cast<TcUnit *>(smem + GE::kOffInfo);
-  RunScale *run_scales = reinterpret_cast<RunScale *>(smem + GE::kOffScale);   // kBlk
   float *red = reinterpret_cast<float *>(smem + GE::kOffRed);
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + GE::kOffMisc);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + GE::kOffMisc + 8);
@@ -728,19 +713,13 @@ __device__ __forceinline__ void decode_tc_body(const DecodeTcParams &tp, const C
             tmem_ld_cols<GE::kSCols>(col_s(b, j) + lane_base, raw);
             const int key = j * kKeys + tid;
             const bool kv = key < cur.ntok && !(kExt && key >= cur.gap_lo && key < cur.gap_hi);
-            float ck = c, lv = 0.f;   // kBlk: the scores meet K's scale here, and P will be that of p times V's scale
-            if constexpr (kBlk) {
-              const RunScale rs = run_scales[ib * (kMaxTiles * 8) + 8 * j + (tid >> 4)];
-              ck = c * rs.k;
-              lv = rs.log2_v;
-            }
 #pragma unroll
             for (int h = 0; h < G; ++h) {
               // fp8: hi + lo / 16, or hi + (mid + lo / 16) / 16
               const float sv = kQTerms == 3   ? fmaf(fmaf(raw[2 * G + h], 0.0625f, raw[G + h]), 0.0625f, raw[h])
                                : kQTerms == 2 ? fmaf(raw[G + h], 0.0625f, raw[h])
                                               : raw[h];
-              t[j][h] = kv ? kBlk ? fmaf(sv, ck, lv) : sv * c : kNegInf;
+              t[j][h] = kv ? sv * c : kNegInf;
               mloc[h] = fmaxf(mloc[h], t[j][h]);
             }
             if constexpr (kExt) {
@@ -790,8 +769,6 @@ __device__ __forceinline__ void decode_tc_body(const DecodeTcParams &tp, const C
         for (int j = 0; j < kMaxTiles; ++j) {
           if (j >= nt) break;
           uint8_t *pt = pb + j * GE::kPBytes;
-          float inv_v = 1.f;   // kBlk: the sum is that of p itself
-          if constexpr (kBlk) inv_v = run_scales[ib * (kMaxTiles * 8) + 8 * j + (tid >> 4)].inv_v;
 #pragma unroll
           for (int h = 0; h < G; h += 2) {
             const float msub0 = m_cur[h] == kNegInf ? 0.f : m_cur[h];
@@ -809,13 +786,8 @@ __device__ __forceinline__ void decode_tc_body(const DecodeTcParams &tp, const C
               put(2 * G + h, lo2);
               put(2 * G + h + 1, lo2 >> 8);
             }
-            if constexpr (kBlk) {
-              l_part[h] = fmaf(p0, inv_v, l_part[h]);
-              l_part[h + 1] = fmaf(p1, inv_v, l_part[h + 1]);
-            } else {
-              l_part[h] += p0;
-              l_part[h + 1] += p1;
-            }
+            l_part[h] += p0;
+            l_part[h + 1] += p1;
           }
         }
         fence_async_smem();
@@ -1252,15 +1224,6 @@ __device__ __forceinline__ void decode_tc_body(const DecodeTcParams &tp, const C
           if (bi < 0 || bi >= p.num_blocks) record_error(p.err, PA_ERR_DEVICE_CHECK);
           else blk = bi;
         }
-        if constexpr (kBlk) {
-          RunScale rs{1.f, 0.f, 1.f, 0.f};
-          if (blk >= 0) {
-            const float sk = __ldg(tp.k_scales + (int64_t)blk * hkv + kvk), sv = __ldg(tp.v_scales + (int64_t)blk * hkv + kvk);
-            if (block_scale_ok(sk) && block_scale_ok(sv)) rs = {sk, __log2f(sv), __frcp_rn(sv), 0.f};
-            else record_error(p.err, PA_ERR_DEVICE_CHECK);
-          }
-          run_scales[((u + k) % kInfo) * (kMaxTiles * 8) + lane] = rs;
-        }
         dst->blk[lane] = blk;
         // fused step: the row's new token, for this KV head, stored before the
         // unit that reads it (the row's last partition) is published
@@ -1572,12 +1535,12 @@ __device__ __forceinline__ void decode_tc_body(const DecodeTcParams &tp, const C
   }
 }
 
-template <typename KV, typename QT, int G, int D, bool kPadRows, bool kExt, int kPTerms, bool kBlk>
+template <typename KV, typename QT, int G, int D, bool kPadRows, bool kExt, int kPTerms>
 __global__ void __launch_bounds__(dtc::Roles::threads_for(dtc::Roles::loaders(G), dtc::Roles::sep_merge(G)), 1)
     decode_tc_kernel(const DecodeTcParams tp, const __grid_constant__ CUtensorMap tmap_k,
                      const __grid_constant__ CUtensorMap tmap_v) {
-  decode_tc_body<KV, QT, G, D, dtc::Roles::loaders(G), dtc::Roles::sep_merge(G), kPadRows, kExt, kPTerms, kBlk>(
-      tp, &tmap_k, &tmap_v);
+  decode_tc_body<KV, QT, G, D, dtc::Roles::loaders(G), dtc::Roles::sep_merge(G), kPadRows, kExt, kPTerms>(tp, &tmap_k,
+                                                                                                     &tmap_v);
 }
 
 // One CTA: count the split rows' merges and clear the merge list, and list
@@ -1662,14 +1625,14 @@ cudaError_t launch_decode_tc_plan(const DecodeTcParams &tp, cudaStream_t s) {
   return cudaLaunchKernelEx(&cfg, decode_tc_plan_kernel<kExt>, tp);
 }
 
-template <typename KV, typename QT, int G, int D, bool kPadRows, bool kExt = false, int kPTerms = 2, bool kBlk = false>
+template <typename KV, typename QT, int G, int D, bool kPadRows, bool kExt = false, int kPTerms = 2>
 cudaError_t launch_decode_tc_one(const DecodeTcParams &p, const PoolMaps &m, cudaStream_t s) {
   constexpr int smem =
       dtc::TcGeo<G, dtc::split_p<KV, QT, kExt>(), std::is_same<KV, uint8_t>::value, dtc::QTerms<KV, QT>::value, D,
-                 kPTerms, kBlk>::kSmemBytes;
+                 kPTerms>::kSmemBytes;
   cudaError_t e = cudaSuccess;
   if (!(kExt && p.direct) && (e = launch_decode_tc_plan<kExt>(p, s)) != cudaSuccess) return e;
-  if ((e = ensure_smem_limit<decode_tc_kernel<KV, QT, G, D, kPadRows, kExt, kPTerms, kBlk>>(smem)) != cudaSuccess) return e;
+  if ((e = ensure_smem_limit<decode_tc_kernel<KV, QT, G, D, kPadRows, kExt, kPTerms>>(smem)) != cudaSuccess) return e;
   int sms = 0;
   if ((e = current_sm_count(&sms)) != cudaSuccess) return e;
   if (kExt && p.direct) sms = (int)std::min<int64_t>(sms, (int64_t)p.d.num_seqs * p.d.max_partitions * p.d.num_kv_heads * p.shares);
@@ -1684,7 +1647,7 @@ cudaError_t launch_decode_tc_one(const DecodeTcParams &p, const PoolMaps &m, cud
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, decode_tc_kernel<KV, QT, G, D, kPadRows, kExt, kPTerms, kBlk>, p, m.k, m.v);
+  return cudaLaunchKernelEx(&cfg, decode_tc_kernel<KV, QT, G, D, kPadRows, kExt, kPTerms>, p, m.k, m.v);
 }
 
 // m: tensor maps over the pools, one box per cache block of one KV head: 16-bit
@@ -1712,17 +1675,17 @@ cudaError_t launch_decode_tc(const DecodeTcParams &p, int gqa, int head_dim, con
 
 // The bounded-cache decodes (kExt): every group size, a share of at most 16
 // (head_dim 64: 8) query heads per unit, run padded to 4, 8 or 16 rows.
-template <typename KV, typename QT, int kPTerms, bool kBlk = false>
+template <typename KV, typename QT, int kPTerms>
 cudaError_t launch_decode_ext_terms(const DecodeTcParams &p, int head_dim, const PoolMaps &m, cudaStream_t s) {
   switch (decode_ext_rows(p.share_heads)) {
     case 4:
-      return head_dim == 64 ? launch_decode_tc_one<KV, QT, 4, 64, true, true, kPTerms, kBlk>(p, m, s)
-                            : launch_decode_tc_one<KV, QT, 4, 128, true, true, kPTerms, kBlk>(p, m, s);
+      return head_dim == 64 ? launch_decode_tc_one<KV, QT, 4, 64, true, true, kPTerms>(p, m, s)
+                            : launch_decode_tc_one<KV, QT, 4, 128, true, true, kPTerms>(p, m, s);
     case 8:
-      return head_dim == 64 ? launch_decode_tc_one<KV, QT, 8, 64, true, true, kPTerms, kBlk>(p, m, s)
-                            : launch_decode_tc_one<KV, QT, 8, 128, true, true, kPTerms, kBlk>(p, m, s);
+      return head_dim == 64 ? launch_decode_tc_one<KV, QT, 8, 64, true, true, kPTerms>(p, m, s)
+                            : launch_decode_tc_one<KV, QT, 8, 128, true, true, kPTerms>(p, m, s);
     case 16:
-      if (head_dim == 128) return launch_decode_tc_one<KV, QT, 16, 128, true, true, kPTerms, kBlk>(p, m, s);
+      if (head_dim == 128) return launch_decode_tc_one<KV, QT, 16, 128, true, true, kPTerms>(p, m, s);
   }
   return cudaErrorInvalidValue;
 }
@@ -1734,14 +1697,6 @@ cudaError_t launch_decode_ext(const DecodeTcParams &p, int head_dim, const PoolM
     if (!p.d.out_f32) return launch_decode_ext_terms<KV, QT, 2>(p, head_dim, m, s);
   }
   return launch_decode_ext_terms<KV, QT, kFp8 ? 3 : 2>(p, head_dim, m, s);
-}
-
-template <typename QT>
-cudaError_t launch_decode_scaled(const DecodeTcParams &p, int head_dim, const PoolMaps &m, cudaStream_t s) {
-  if constexpr (std::is_same<QT, __nv_bfloat16>::value) {
-    if (!p.d.out_f32) return launch_decode_ext_terms<uint8_t, QT, 2, true>(p, head_dim, m, s);
-  }
-  return launch_decode_ext_terms<uint8_t, QT, 3, true>(p, head_dim, m, s);
 }
 
 }  // namespace pa

@@ -171,10 +171,6 @@ cudaError_t launch_decode_ext_f16(const DecodeTcParams &p, int head_dim, const P
 cudaError_t launch_decode_ext_fp8_bf16q(const DecodeTcParams &p, int head_dim, const PoolMaps &m, cudaStream_t s);
 cudaError_t launch_decode_ext_fp8_f16q(const DecodeTcParams &p, int head_dim, const PoolMaps &m, cudaStream_t s);
 
-// The same over a block-scaled cache (pa_decode_scaled).
-cudaError_t launch_decode_scaled_bf16q(const DecodeTcParams &p, int head_dim, const PoolMaps &m, cudaStream_t s);
-cudaError_t launch_decode_scaled_f16q(const DecodeTcParams &p, int head_dim, const PoolMaps &m, cudaStream_t s);
-
 // Bounded-cache decodes of at most kDirectRows rows and kDirectUnits units (row,
 // partition, KV head share), counted at the longest row, run without the plan kernel and its
 // scheduling (pa_decode_tc.cuh, `direct`).  Measured, plan against direct: one
@@ -257,6 +253,30 @@ constexpr int kMinScaleExp = -64, kMaxScaleExp = 32;
 __host__ __device__ __forceinline__ bool block_scale_ok(float s) {
   return s >= 5.421010862427522e-20f && s <= 4294967296.f;   // 2^-64, 2^32 (false for NaN)
 }
+
+// Decode over a block-scaled cache (pa_decode_scaled.cu).
+struct DecodeScaledParams {
+  const void *q;
+  const void *k_cache, *v_cache;
+  const float *k_scales, *v_scales;   // [num_blocks][num_kv_heads]
+  const int32_t *block_tables;
+  int32_t max_blocks_per_seq;
+  const int32_t *seq_lens;
+  int32_t max_seq_len, num_seqs, num_q_heads, num_kv_heads;
+  int32_t shares, share_heads;        // a group of query heads in shares of at most kScaledHeads
+  int32_t block_size;
+  int64_t num_blocks;
+  float s_mult;                       // scale * log2(e)
+  void *out;
+  int32_t out_f32;
+  // workspace: of each CTA the (row, share) it leaves to the next ones and their number, and two pieces' sums
+  int4 *joins;                        // [CTAs] {row, share, pieces or 0, 0}
+  float2 *ws_ml;                      // [2 CTAs][share_heads] (maximum, sum)
+  float *ws_acc;                      // [2 CTAs][share_heads][head_dim]
+  int32_t *err;
+};
+constexpr int kScaledHeads = 16, kScaledCtas = 4 * kPlanSms;
+cudaError_t launch_decode_scaled(const DecodeScaledParams &p, pa_dtype q_dtype, int head_dim, cudaStream_t s);
 
 // Rotation and cache write of a step's new tokens (pa_rope.cu).
 struct RopeParams {

@@ -12,10 +12,9 @@ times scale):
   that step, 2^-10: 2^-17 of the largest element, in the place of 2^-21.
 * the exponent of a weight is t = s + log2 vs - max: log2 vs is within 2 ulp of its value and t is rounded, so e grows
   by 2^-21 (1 + |log2 vs|); the same factor meets numerator and sum.
-* the second product takes w = p vs.  Decode: 256 w in e4m3 terms, w <= 1 at the row's largest: two hold it to 2^-8 of
-  itself or 2^-22 where it is small, three (f16 and fp32 outputs) to 2^-12 or 2^-26.  Chunks: f16, rounded once, 2^-11 or
-  2^-25 (w is at least 1 at the row's largest); for an fp32 output hi + lo, 2^-22 or 2^-25.  The small-value terms are of
-  the row's largest w: n of them times the largest code.
+* the second product takes w = p vs in f16, rounded once for a 16-bit output, 2^-11 of it or 2^-25 where it is small (it is
+  at least 1 at the row's largest); for an fp32 output hi + lo, 2^-22 or 2^-25.  The small-value terms are of the row's
+  largest w: n of them times the largest code.
 * the sum is that of the unrounded p, in fp32 over n terms: 2^-24 (16 + n / 16).
 * the stored output: half a step of its type."""
 import math
@@ -185,10 +184,7 @@ def attend(q, k, v, seen, scale, out, chunk):
     big = torch.einsum("rhgn,hnd->rhgd", w, vc.abs())
     count = seen.sum(-1).double()[:, None, None, None]
     rel = (2 * e + 2.0 ** -20)[..., None] + 2.0 ** -24 * (16 + count / 16)
-    if chunk:
-        rel, low = rel + (2.0 ** -22 if out == "f32" else 2.0 ** -11), 2.0 ** -25
-    else:
-        rel, low = (rel + 2.0 ** -8, 2.0 ** -22) if out == "bf16" else (rel + 2.0 ** -12, 2.0 ** -26)
+    rel, low = rel + (2.0 ** -22 if out == "f32" else 2.0 ** -11), 2.0 ** -25
     top = (w.amax(-1, keepdim=True) if n else 0.0) * 448.0
     b = rel * big + low * count * top
     b = b + HALF_STEP[out] * (o.abs() + b) + (2.0 ** -25 if out == "f16" else 1e-38)
@@ -199,17 +195,17 @@ def i32(x):
     return torch.tensor(x, dtype=torch.int32, device="cuda")
 
 
-def run_decode(pa, c, q, scale, out="f32", ps=0, stream=None):
+def run_decode(pa, c, q, scale, out="f32", stream=None):
     k, v, tables, desc, ks, vs = c.device(pa)
     n, hq, d = q.shape
     most = max(c.lens, default=0)
-    size = pa.pa_decode_scaled_workspace_bytes(n, hq, c.hkv, d, most, ps)
+    size = pa.pa_decode_scaled_workspace_bytes(n, hq, c.hkv, d, most)
     assert size > 0
     ws = torch.full((size,), 0x5A, dtype=torch.uint8, device="cuda")
     o = torch.full(q.shape, math.nan, dtype=DT[out], device="cuda")
     q, lens = q.cuda(), i32(c.lens)
     torch.cuda.synchronize()                       # (the call may go to another stream)
-    pa.pa_decode_scaled(q, k, v, desc, ks, vs, tables, lens, most, scale, o, ws, ps, stream=stream)
+    pa.pa_decode_scaled(q, k, v, desc, ks, vs, tables, lens, most, scale, o, ws, stream=stream)
     assert pa.pa_get_device_error(stream) == 0
     return o
 

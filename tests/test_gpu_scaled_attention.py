@@ -17,13 +17,13 @@ def queries(n, hq, d, qt, seed):
     return (1.5 * torch.randn((n, hq, d), generator=torch.Generator().manual_seed(seed))).to(DT[qt])
 
 
-def decode_case(lens, hq, hkv, d, bs, qt, out, seed=0, ps=0, scale=None, change=None, **kw):
+def decode_case(lens, hq, hkv, d, bs, qt, out, seed=0, scale=None, change=None, **kw):
     c = ScaledCache(lens, hkv, d, bs, seed, **kw)
     if change:
         change(c)
     q = queries(len(lens), hq, d, qt, seed + 1)
     scale = d ** -0.5 if scale is None else scale
-    o = run_decode(pa, c, q, scale, out, ps)
+    o = run_decode(pa, c, q, scale, out)
     for i, n in enumerate(lens):
         want, bound = attend(q[i:i + 1], c.rows("k", i, n), c.rows("v", i, n), causal(n, 1), scale, out, False)
         check(o[i:i + 1], want, bound, f"sequence {i} of {n} tokens")
@@ -51,9 +51,12 @@ def test_decode_heads_and_types(hq, hkv, d, bs, qt, out):
     decode_case(LENS, hq, hkv, d, bs, qt, out, seed=hq + d)
 
 
-@pytest.mark.parametrize("ps", [32, 96, 512, 1024])
-def test_decode_partitions(ps):
-    decode_case(LENS, 8, 2, 128, 16, "bf16", "f32", seed=ps, ps=ps)
+@pytest.mark.parametrize("n", [1, 2, 3, 7, 64, 300, 1100, 2500])
+def test_decode_numbers_of_rows(n):
+    """From rows cut into many pieces to many rows in one piece, past the rows a CTA has at hand at a time."""
+    g = torch.Generator().manual_seed(n)
+    lens = torch.randint(0, 6000 // n + 40, (n,), generator=g).tolist()
+    decode_case(lens, 4, 2, 64, 16, "bf16", "f32", seed=n)
 
 
 @pytest.mark.parametrize("d", [64, 128])
@@ -63,7 +66,6 @@ def test_decode_one_long_row_and_empty_rows(d):
 
 
 def test_decode_many_rows():
-    """Past the batches that are dealt without the plan kernel, split rows among them."""
     g = torch.Generator().manual_seed(5)
     lens = torch.randint(1, 900, (160,), generator=g).tolist()
     decode_case(lens, 8, 2, 128, 16, "bf16", "bf16", seed=9)

@@ -97,16 +97,15 @@ ATTENTION = [
 
 def attention(**kw):
     return {**dict(q=FAR, dt=1, n=4, hq=32, k=5 * FAR, v=6 * FAR, ks=7 * FAR, vs=8 * FAR, bt=FAKE, mb=8, sl=FAKE, msl=100, scale=0.1,
-                   ps=0, ws=FAKE, wsb=1 << 30, out=2 * FAR, odt=1, cu=FAKE, qs=FAKE, mq=10), **kw}
+                   ws=FAKE, wsb=1 << 30, out=2 * FAR, odt=1, cu=FAKE, qs=FAKE, mq=10), **kw}
 
 
 @pytest.mark.parametrize("kw,desc_kw,want", ATTENTION + [
-    (dict(ps=48), {}, 1), (dict(ws=None), {}, 1), (dict(ws=FAKE + 16), {}, 1), (dict(wsb=100), {}, 1), (dict(n=1 << 20), {}, 2)])
+    (dict(ws=None), {}, 1), (dict(ws=FAKE + 16), {}, 1), (dict(wsb=100), {}, 1), (dict(n=1 << 20), {}, 2)])
 def test_decode_refusals(pa, kw, desc_kw, want):
     a, d = attention(**kw), desc(pa, **desc_kw)
     assert pa.lib().pa_decode_scaled(a["q"], a["dt"], a["n"], a["hq"], a["k"], a["v"], ctypes.byref(d), a["ks"], a["vs"], a["bt"],
-                                     a["mb"], a["sl"], a["msl"], a["scale"], a["ps"], a["ws"], a["wsb"], a["out"], a["odt"],
-                                     None) == want
+                                     a["mb"], a["sl"], a["msl"], a["scale"], a["ws"], a["wsb"], a["out"], a["odt"], None) == want
 
 
 @pytest.mark.parametrize("kw,desc_kw,want", ATTENTION + [
@@ -124,7 +123,8 @@ def test_workspace_serves_smaller_batches(pa):
     for n in (1, 2, 7, 63):
         for most in (1, 100, 5000, 20000):
             assert pa.pa_decode_scaled_workspace_bytes(n, 32, 8, 128, most) <= big
-    assert pa.pa_decode_scaled_workspace_bytes(4, 30, 8, 128, 100) == 0
+    for bad in ((4, 30, 8, 128, 100), (-1, 32, 8, 128, 100), (4, 32, 8, 96, 100), (4, 32, 8, 128, -1), (1 << 20, 32, 8, 128, 100)):
+        assert pa.pa_decode_scaled_workspace_bytes(*bad) == 0
 
 
 def test_model_codes():
