@@ -669,8 +669,9 @@ pa_status scaled_layout(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_he
       (double)num_seqs * (max_seq_len / 16 + 1.0) * num_kv_heads * l->shares >= 4e18)
     return PA_ERR_UNSUPPORTED;
   l->ml_off = round256(kScaledCtas * sizeof(int4));
-  l->acc_off = l->ml_off + round256((size_t)2 * kScaledCtas * l->share_heads * 8);
-  l->total = l->acc_off + round256((size_t)2 * kScaledCtas * l->share_heads * head_dim * 4);
+  const size_t heads = l->share_heads <= 8 ? 8 : 16;
+  l->acc_off = l->ml_off + round256(2 * kScaledCtas * heads * 8);
+  l->total = l->acc_off + round256(2 * kScaledCtas * heads * head_dim * 4);
   return PA_OK;
 }
 

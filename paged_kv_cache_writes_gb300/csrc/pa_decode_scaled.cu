@@ -9,12 +9,13 @@
 // product takes the codes as they are; the sum takes 1 / sv_p, in fp32, from
 // unrounded w: a token whose values are tiny may hold most of the softmax.
 //
-// Bound by HBM: 2 head_dim bytes per token and KV head.  Everything between the
-// load and the products therefore stays in the registers of one warp: no shared
-// memory, no barrier, no hand-over between roles.  A warp takes 16 keys at a time
-// and all (up to 8 or 16) query heads of the KV head:
+// Bound by HBM: 2 head_dim bytes per token and KV head.  Everything between the load and the products therefore stays in
+// one warp: no barrier, no hand-over between roles.  A warp takes 16 keys at a time and all (up to 8 or 16) query heads of
+// the KV head:
 //   S (16 keys x 8 heads)     = K (16 x D) . Q^T       mma.sync m16n8k16, f16
 //   O^T (16 d x 8 heads) +=     V^T (16 d x 16 keys) . P^T
+// Each lane copies the codes that it will itself need, two tiles ahead, into places of its own in shared memory
+// (cp.async): the bytes in flight cost no registers, and no lane waits for another.
 // The codes are widened to f16 in registers, exactly.  Any order of the D products
 // will do, so the fragments are loaded as memory has them: a thread's K codes are
 // 16 consecutive ones of a row per 64, and Q's fragments are laid out once to
@@ -30,12 +31,10 @@
 // hand-overs between its roles: 64 sequences of 300-16000, 64/8 heads 279 us against
 // XXX; 33 of 1-5000, head_dim 64, f16 72 against XXX.)
 //
-// Work.  The tiles of 16 keys of all (row, KV head share) in order are cut into equal
-// ranges, one per CTA (four warps, four CTAs per SM; fewer CTAs where a range would
-// fall under kMinTiles): whatever the lengths, all finish together.  Every CTA finds
-// its range from the lengths alone.  Within a range each (row, share) is a piece,
-// its tiles dealt to the warps in turn and joined through shared memory.  A piece
-// that is a whole row is final; others leave their sums in the workspace, at most
+// Work.  The tiles of 16 keys of all (row, KV head share) in order are cut into equal ranges, one per CTA (eight warps, two
+// CTAs per SM; fewer CTAs where a range would fall under kMinTiles): whatever the lengths, all finish together.  Every CTA
+// finds its range from the lengths alone.  Within a range each (row, share) is a piece, its tiles dealt to the warps in turn
+// and joined through shared memory.  A piece that is a whole row is final; others leave their sums in the workspace, at most
 // two per CTA, and a second launch joins them.
 #include <algorithm>
 #include <type_traits>
@@ -47,25 +46,21 @@
 namespace pa {
 namespace {
 
-constexpr int kWarps = 4, kThreads = 32 * kWarps;
+constexpr int kWarps = 8, kThreads = 32 * kWarps;
+constexpr int kStages = 3;                // tiles of a warp in shared memory
 constexpr int kTile = 16;                 // keys per step of a warp
-constexpr int kMinTiles = 16;             // tiles per CTA at least (while there are enough)
+constexpr int kMinTiles = 32;             // tiles per CTA at least (while there are enough)
 constexpr int kChunk = 1024;              // rows whose tile counts a CTA has at hand
 constexpr float kRescaleLog2 = 8.f;       // O is rescaled when a score exceeds the reference maximum by 2^8
 #define kNegInfF (-__int_as_float(0x7f800000))
 
-// Codes once read are not read again by this launch.
-__device__ __forceinline__ uint4 ld16(const void *p, uint64_t policy) {
-  uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.L2::cache_hint.v4.u32 {%0, %1, %2, %3}, [%4], %5;"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p), "l"(policy));
-  return v;
+// Copies of codes to shared memory.  (Without an L2 policy: the same copies with an evict-first one, the addresses checked
+// to be in bounds and aligned, ended in an SM exception; plain loads with it had not.)
+__device__ __forceinline__ void copy16(void *dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
 }
-__device__ __forceinline__ uint2 ld8(const void *p, uint64_t policy) {
-  uint2 v;
-  asm volatile("ld.global.nc.L1::no_allocate.L2::cache_hint.v2.u32 {%0, %1}, [%2], %3;" : "=r"(v.x), "=r"(v.y) : "l"(p), "l"(policy));
-  return v;
+__device__ __forceinline__ void copy8(void *dst, const void *src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
 }
 
 // Two e4m3 codes (the low 16 bits) -> f16x2, exactly.
@@ -74,9 +69,10 @@ __device__ __forceinline__ uint32_t widen2(uint32_t w) {
   return *reinterpret_cast<const uint32_t *>(&h);
 }
 
-// c (16 x 8) += a (16 x 16) . b (16 x 8), f16 operands.
+// c (16 x 8) += a (16 x 16) . b (16 x 8), f16 operands.  (volatile: the whole warp has to execute it together, so that it
+// must not be moved into a branch)
 __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
                : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
@@ -113,11 +109,23 @@ struct Cut {
   }
 };
 
+// CTAs per SM: the O of 16 query heads of 128 elements takes 64 registers more
+template <int D, int NT>
+constexpr int ctas_per_sm() {
+  return D == 128 && NT == 2 ? 1 : 2;
+}
+template <int D>
+constexpr int kRingBytes = kWarps *kStages * 2 * kTile * D;
+
 template <typename QT, int D, int NT, bool kLo>
-__global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) decode_scaled_kernel(const DecodeScaledParams p) {
-  constexpr int kHeads = 8 * NT, kSteps = D / 16, kHalves = D / 64;
+__global__ void __launch_bounds__(kThreads, ctas_per_sm<D, NT>()) decode_scaled_kernel(const DecodeScaledParams p) {
+  constexpr int kHeads = 8 * NT, kSteps = D / 16, kHalves = D / 64, kRows = NT * kSteps * 4;
   constexpr bool kBf16 = std::is_same<QT, __nv_bfloat16>::value;
-  __shared__ float part[kWarps][kHeads][D];
+  // [warp][stage]: K as [row 0 or 1][half][lane] of 16 bytes, V as [key 0 .. 3][lane] of D / 8; between pieces the warps'
+  // sums, float [warp][kRows][lane]
+  extern __shared__ __align__(16) uint8_t ring[];
+  static_assert(kRows * 128 <= kStages * 2 * kTile * D, "a warp's sums fit in its part of the ring");
+  float *part = reinterpret_cast<float *>(ring);
   __shared__ float2 part_ml[kWarps][kHeads];
   __shared__ int64_t warp_sum[kWarps];
   __shared__ int64_t tiles_end[kChunk];    // of the present chunk of rows: tiles up to and including row i
@@ -126,7 +134,6 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) decode_scaled_kerne
   // (each launch waits for what precedes it; the joining one is launched while this one runs)
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const uint64_t policy = tc::l2_evict_first();
   const int units = p.num_kv_heads * p.shares, gqa = p.num_q_heads / p.num_kv_heads;
 
   // ---- this CTA's range of tiles
@@ -278,63 +285,67 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) decode_scaled_kerne
         for (int e = 0; e < 4; ++e) o[nt][i][e] = 0.f;
     }
 
-    // ---- the piece's tiles, every kWarps-th to this warp: codes and scales a tile ahead, block ids two
+    // ---- the piece's tiles, every kWarps-th to this warp: lane i has the block id and the scales of the warp's tile 32 w + i
+    // (w the present window), and those of the next window; codes two tiles ahead
     const int32_t *table = p.block_tables + (int64_t)row * p.max_blocks_per_seq;
     const int bs_log2 = p.block_size == 32 ? 5 : 4;
     const char *kpool = static_cast<const char *>(p.k_cache), *vpool = static_cast<const char *>(p.v_cache);
-    const int last = tile0 + count;
-    auto block_of = [&](int tile) -> int32_t {   // -1: past the piece, no token, or out of range
-      const int key = tile * kTile;
-      if (tile >= last || key >= len) return -1;
-      const int32_t bi = __ldg(table + (key >> bs_log2));
-      if (bi >= 0 && bi < p.num_blocks) return bi;
-      record_error(p.err, PA_ERR_DEVICE_CHECK);
-      return -1;
+    const int mine = (count - warp + kWarps - 1) / kWarps;   // this warp's tiles
+    struct Window {
+      int32_t blk;                         // -1: past the piece, no token, or out of range
+      float k, log2_v, inv_v;
     };
-    using KWords = uint32_t[2][4 * kHalves];     // rows g, g + 8: 16 codes of each 64
-    using VWords = uint32_t[4][D / 32];          // keys 2t, 2t + 1, 2t + 8, 2t + 9: D / 8 codes from g D / 8 on
-    KWords kw;
-    VWords vw;
-    float sk, sv;
-    // the tile's first row in the pool (a tile without a block reads the pool's first rows, unused)
-    auto row_of = [&](int32_t b, int tile) {
-      return b < 0 ? (int64_t)0 : ((int64_t)b * p.num_kv_heads + kvh) * p.block_size + ((tile * kTile) & (p.block_size - 1));
-    };
-    auto load_k = [&](int32_t b, int tile) {
-      const char *src = kpool + (row_of(b, tile) + g) * D + t * 16;
-#pragma unroll
-      for (int r = 0; r < 2; ++r)
-#pragma unroll
-        for (int j = 0; j < kHalves; ++j) {
-          const uint4 x = ld16(src + r * 8 * D + j * 64, policy);
-          kw[r][4 * j] = x.x, kw[r][4 * j + 1] = x.y, kw[r][4 * j + 2] = x.z, kw[r][4 * j + 3] = x.w;
-        }
-    };
-    auto load_v = [&](int32_t b, int tile) {
-      const char *src = vpool + (row_of(b, tile) + 2 * t) * D + g * (D / 8);
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const char *at = src + ((r & 1) + (r >> 1) * 8) * D;
-        if constexpr (D == 128) {
-          const uint4 x = ld16(at, policy);
-          vw[r][0] = x.x, vw[r][1] = x.y, vw[r][2] = x.z, vw[r][3] = x.w;
+    auto window = [&](int first) {
+      Window w{-1, 1.f, 0.f, 1.f};
+      const int i = first + lane, key = (tile0 + warp + kWarps * i) * kTile;
+      if (i < mine && key < len) {
+        const int32_t bi = __ldg(table + (key >> bs_log2));
+        if (bi >= 0 && bi < p.num_blocks) {
+          w.blk = bi;
+          const int64_t at = (int64_t)bi * p.num_kv_heads + kvh;
+          const float sk = __ldg(p.k_scales + at), sv = __ldg(p.v_scales + at);
+          if (block_scale_ok(sk) && block_scale_ok(sv)) w = {bi, sk, __log2f(sv), __fdividef(1.f, sv)};
+          else record_error(p.err, PA_ERR_DEVICE_CHECK);
         } else {
-          const uint2 x = ld8(at, policy);
-          vw[r][0] = x.x, vw[r][1] = x.y;
+          record_error(p.err, PA_ERR_DEVICE_CHECK);
         }
       }
+      return w;
     };
-    auto load_scales = [&](int32_t b) {
-      const int64_t at = b < 0 ? 0 : (int64_t)b * p.num_kv_heads + kvh;
-      sk = __ldg(p.k_scales + at);
-      sv = __ldg(p.v_scales + at);
+    uint8_t *stage0 = ring + warp * (kStages * 2 * kTile * D);
+    // the codes of a tile in block b (-1: the pool's first rows, unused); always a group, so that they count in order
+    auto copy_tile = [&](int i, int32_t b) {
+      if (i < mine) {
+        const int off = ((tile0 + warp + kWarps * i) * kTile) & (p.block_size - 1);
+        const int64_t at = b < 0 ? (int64_t)0 : (((int64_t)b * p.num_kv_heads + kvh) * p.block_size + off) * D;
+        uint8_t *dst = stage0 + i % kStages * (2 * kTile * D);
+        const char *ks = kpool + at + g * D + t * 16;
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+          for (int j = 0; j < kHalves; ++j) copy16(dst + ((r * kHalves + j) * 32 + lane) * 16, ks + r * 8 * D + j * 64);
+        const char *vs = vpool + at + 2 * t * D + g * (D / 8);
+        dst += kTile * D;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const char *src = vs + ((r & 1) + (r >> 1) * 8) * D;
+          if constexpr (D == 128) copy16(dst + (r * 32 + lane) * 16, src);
+          else copy8(dst + (r * 32 + lane) * 8, src);
+        }
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    int tile = tile0 + warp;
-    int32_t blk = block_of(tile), next_blk = block_of(tile + kWarps);
-    load_k(blk, tile);
-    load_scales(blk);
-    load_v(blk, tile);
-    for (; tile < last; tile += kWarps) {
+    Window now = window(0), next = window(32);
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) copy_tile(i, __shfl_sync(0xffffffffu, now.blk, i));
+    for (int i = 0; i < mine; ++i) {
+      const int32_t blk = __shfl_sync(0xffffffffu, now.blk, i & 31);
+      const float ks = __shfl_sync(0xffffffffu, now.k, i & 31), lv = __shfl_sync(0xffffffffu, now.log2_v, i & 31);
+      const float iv = __shfl_sync(0xffffffffu, now.inv_v, i & 31);
+      const int ahead = (i & 31) + kStages - 1;
+      const int32_t ahead_blk = __shfl_sync(0xffffffffu, ahead < 32 ? now.blk : next.blk, ahead & 31);
+      const uint8_t *src = stage0 + i % kStages * (2 * kTile * D);
+      asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
       // scores of keys g, g + 8 and heads 2t, 2t + 1
       float s[NT][4], s2[NT][4];           // two chains of MMAs
 #pragma unroll
@@ -342,26 +353,36 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) decode_scaled_kerne
 #pragma unroll
         for (int e = 0; e < 4; ++e) s[nt][e] = s2[nt][e] = 0.f;
 #pragma unroll
-      for (int m = 0; m < kSteps; ++m) {
-        const uint32_t a0 = widen2(kw[0][m]), a1 = widen2(kw[1][m]), a2 = widen2(kw[0][m] >> 16), a3 = widen2(kw[1][m] >> 16);
+      for (int j = 0; j < kHalves; ++j) {
+        const uint4 x = *reinterpret_cast<const uint4 *>(src + (j * 32 + lane) * 16);
+        const uint4 y = *reinterpret_cast<const uint4 *>(src + ((kHalves + j) * 32 + lane) * 16);
+        const uint32_t r0[4] = {x.x, x.y, x.z, x.w}, r1[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) mma(m & 1 ? s2[nt] : s[nt], a0, a1, a2, a3, qb[nt][m][0], qb[nt][m][1]);
-      }
-      load_k(next_blk, tile + kWarps);
-      // scales of this tile; the next one's in flight
-      float ks = sk, lv = 0.f, iv = 1.f;
-      if (blk >= 0) {
-        if (block_scale_ok(sk) && block_scale_ok(sv)) {
-          lv = __log2f(sv);
-          iv = __fdividef(1.f, sv);
-        } else {
-          record_error(p.err, PA_ERR_DEVICE_CHECK);
-          ks = 1.f;
+        for (int q = 0; q < 4; ++q) {
+          const uint32_t a0 = widen2(r0[q]), a1 = widen2(r1[q]), a2 = widen2(r0[q] >> 16), a3 = widen2(r1[q] >> 16);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) mma(q & 1 ? s2[nt] : s[nt], a0, a1, a2, a3, qb[nt][4 * j + q][0], qb[nt][4 * j + q][1]);
         }
       }
-      load_scales(next_blk);
-      const int nvis = blk < 0 ? 0 : len - tile * kTile;   // keys of the tile that exist
-      float top = kNegInfF;                                // how far a score is above its reference
+      uint32_t vw[4][D / 32];              // V codes of keys 2t, 2t + 1, 2t + 8, 2t + 9
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const uint8_t *at = src + kTile * D + (r * 32 + lane) * (D / 8);
+        if constexpr (D == 128) {
+          const uint4 x = *reinterpret_cast<const uint4 *>(at);
+          vw[r][0] = x.x, vw[r][1] = x.y, vw[r][2] = x.z, vw[r][3] = x.w;
+        } else {
+          const uint2 x = *reinterpret_cast<const uint2 *>(at);
+          vw[r][0] = x.x, vw[r][1] = x.y;
+        }
+      }
+      copy_tile(i + kStages - 1, ahead_blk);   // (the place of tile i - 1, which this lane has read)
+      if ((i & 31) == 31) {
+        now = next;
+        next = window(i + 33);
+      }
+      const int nvis = blk < 0 ? 0 : len - (tile0 + warp + kWarps * i) * kTile;   // keys of the tile that exist
+      float top = kNegInfF;                                                      // how far a score is above its reference
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -434,13 +455,12 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) decode_scaled_kerne
           }
         }
       }
-      load_v(next_blk, tile + kWarps);
-      blk = next_blk;
-      next_blk = block_of(tile + 2 * kWarps);
     }
 
-    // ---- join the warps
-    __syncthreads();                       // the last piece's join is done
+    // ---- join the warps, each of whose sums goes to its own part of the ring
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncwarp();
+    float *mine_part = part + warp * (kStages * 2 * kTile * D / 4);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -450,49 +470,54 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) decode_scaled_kerne
         for (int off = 4; off < 32; off <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
         const int h = nt * 8 + 2 * t + i;
         if (g == 0) part_ml[warp][h] = make_float2(m_ref[nt][i], sum);
-#pragma unroll
-        for (int k = 0; k < kSteps; ++k)
-          *reinterpret_cast<float2 *>(&part[warp][h][g * (D / 8) + 2 * k]) = make_float2(o[nt][k][i], o[nt][k][2 + i]);
       }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int k = 0; k < kSteps; ++k)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) mine_part[(4 * (nt * kSteps + k) + e) * 32 + lane] = o[nt][k][e];
     __syncthreads();
     const bool whole = count == n, starts = tile0 == 0;
     const int64_t slot = 2 * (int64_t)worker + (starts ? 1 : 0);
-    // 8 elements of a head per thread
-    for (int e = tid; e < heads * (D / 8); e += kThreads) {
-      const int h = e / (D / 8), d = e % (D / 8) * 8;
-      float M = kNegInfF, sum = 0.f, x[8];
+    // a step's accumulators (elements d, d + 1 of heads 2t, 2t + 1) per warp and turn
+    for (int k = warp; k < NT * kSteps; k += kWarps) {
+      const int ha = k / kSteps * 8 + 2 * t, d = g * (D / 8) + 2 * (k % kSteps);
+      float M[2] = {kNegInfF, kNegInfF}, sum[2] = {0.f, 0.f}, x[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) M = fmaxf(M, part_ml[w][h].x);
+      for (int w = 0; w < kWarps; ++w)
 #pragma unroll
-      for (int k = 0; k < 8; ++k) x[k] = 0.f;
+        for (int i = 0; i < 2; ++i) M[i] = fmaxf(M[i], part_ml[w][ha + i].x);
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
-        const float2 ml = part_ml[w][h];
-        const float sc = ml.x == kNegInfF ? 0.f : fast_exp2(ml.x - M);
-        sum = fmaf(ml.y, sc, sum);
-        const float4 a = *reinterpret_cast<const float4 *>(&part[w][h][d]), b = *reinterpret_cast<const float4 *>(&part[w][h][d + 4]);
-        x[0] = fmaf(a.x, sc, x[0]), x[1] = fmaf(a.y, sc, x[1]), x[2] = fmaf(a.z, sc, x[2]), x[3] = fmaf(a.w, sc, x[3]);
-        x[4] = fmaf(b.x, sc, x[4]), x[5] = fmaf(b.y, sc, x[5]), x[6] = fmaf(b.z, sc, x[6]), x[7] = fmaf(b.w, sc, x[7]);
+        float sc[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float2 ml = part_ml[w][ha + i];
+          sc[i] = ml.x == kNegInfF ? 0.f : fast_exp2(ml.x - M[i]);
+          sum[i] = fmaf(ml.y, sc[i], sum[i]);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = fmaf(part[w * (kStages * 2 * kTile * D / 4) + (4 * k + e) * 32 + lane], sc[e & 1], x[e]);
       }
       if (whole) {
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        const int64_t at = ((int64_t)row * p.num_q_heads + h0 + h) * D + d;
-        if (p.out_f32) {
-          float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(p.out) + at);
-          dst[0] = make_float4(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv);
-          dst[1] = make_float4(x[4] * inv, x[5] * inv, x[6] * inv, x[7] * inv);
-        } else {
-          *reinterpret_cast<uint4 *>(static_cast<QT *>(p.out) + at) =
-              make_uint4(tc::pack2(x[0] * inv, x[1] * inv, QT{}), tc::pack2(x[2] * inv, x[3] * inv, QT{}),
-                         tc::pack2(x[4] * inv, x[5] * inv, QT{}), tc::pack2(x[6] * inv, x[7] * inv, QT{}));
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          if (ha + i >= heads) continue;
+          const float inv = sum[i] == 0.f ? 0.f : 1.f / sum[i];
+          const int64_t at = ((int64_t)row * p.num_q_heads + h0 + ha + i) * D + d;
+          if (p.out_f32) *reinterpret_cast<float2 *>(static_cast<float *>(p.out) + at) = make_float2(x[i] * inv, x[2 + i] * inv);
+          else *reinterpret_cast<uint32_t *>(static_cast<QT *>(p.out) + at) = tc::pack2(x[i] * inv, x[2 + i] * inv, QT{});
         }
       } else {
-        float4 *dst = reinterpret_cast<float4 *>(p.ws_acc + (slot * p.share_heads + h) * D + d);
-        dst[0] = make_float4(x[0], x[1], x[2], x[3]);
-        dst[1] = make_float4(x[4], x[5], x[6], x[7]);
-        if (d == 0) p.ws_ml[slot * p.share_heads + h] = make_float2(M, sum);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) p.ws_acc[(slot * kRows + 4 * k + e) * 32 + lane] = x[e];
+        if (g == 0 && k % kSteps == 0)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) p.ws_ml[slot * kHeads + ha + i] = make_float2(M[i], sum[i]);
       }
     }
+    __syncthreads();                       // the ring and part_ml are free
     if (starts && !whole) {                // it goes on in the CTAs up to that of its last tile
       joined = true;
       if (tid == 0) p.joins[worker] = make_int4(row, share, cut.worker(pos - tile0 + n - 1) - worker + 1, 0);
@@ -502,75 +527,77 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) decode_scaled_kerne
   if (!joined && tid == 0) p.joins[worker] = make_int4(0, 0, 0, 0);
 }
 
-// The second launch: CTA (w, h) joins the pieces of the (row, share) that CTA w began and did not end, query head h:
-// slot 2w + 1, then slots 2(w + 1), 2(w + 2), ...; its warps share the pieces.
-template <typename QT, int D>
+// The second launch: CTA (w, k) joins the pieces of the (row, share) that CTA w began and did not end, accumulators of step
+// k: slot 2w + 1, then slots 2(w + 1), 2(w + 2), ...; its warps share the pieces.
+template <typename QT, int D, int NT>
 __global__ void __launch_bounds__(kThreads) decode_scaled_join_kernel(const DecodeScaledParams p) {
-  __shared__ float part[kWarps][D];
-  __shared__ float2 part_ml[kWarps];
+  constexpr int kHeads = 8 * NT, kSteps = D / 16, kRows = NT * kSteps * 4;
+  __shared__ float part[kWarps][4][32];
+  __shared__ float2 part_ml[kWarps][2][4];
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int w0 = blockIdx.x, h = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int w0 = blockIdx.x, step = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
   const int4 j = __ldcg(p.joins + w0);
   if (j.z == 0) return;
   const int gqa = p.num_q_heads / p.num_kv_heads, kvh = j.y / p.shares, h_first = (j.y - kvh * p.shares) * p.share_heads;
-  if (h >= min(p.share_heads, gqa - h_first)) return;
-  constexpr int kPer = D / 32, kDeep = 4;  // elements per lane, pieces in flight
-  float M = kNegInfF, l = 0.f, acc[kPer];
-#pragma unroll
-  for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
+  const int heads = min(p.share_heads, gqa - h_first), ha = step / kSteps * 8 + 2 * t;
+  constexpr int kDeep = 4;                 // pieces in flight
+  float M[2] = {kNegInfF, kNegInfF}, l[2] = {0.f, 0.f}, x[4] = {0.f, 0.f, 0.f, 0.f};
   for (int q0 = warp; q0 < j.z; q0 += kDeep * kWarps) {
-    float2 ml[kDeep];
-    float x[kDeep][kPer];
+    float2 ml[kDeep][2];
+    float y[kDeep][4];
 #pragma unroll
     for (int k = 0; k < kDeep; ++k) {
       const int q = min(q0 + k * kWarps, j.z - 1);
-      const int64_t at = (q == 0 ? 2 * (int64_t)w0 + 1 : 2 * ((int64_t)w0 + q)) * p.share_heads + h;
-      ml[k] = __ldcg(p.ws_ml + at);
-      if constexpr (kPer == 4) {
-        const float4 y = __ldcg(reinterpret_cast<const float4 *>(p.ws_acc + at * D) + lane);
-        x[k][0] = y.x, x[k][1] = y.y, x[k][2] = y.z, x[k][3] = y.w;
-      } else {
-        const float2 y = __ldcg(reinterpret_cast<const float2 *>(p.ws_acc + at * D) + lane);
-        x[k][0] = y.x, x[k][1] = y.y;
-      }
+      const int64_t slot = q == 0 ? 2 * (int64_t)w0 + 1 : 2 * ((int64_t)w0 + q);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) ml[k][i] = __ldcg(p.ws_ml + slot * kHeads + ha + i);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) y[k][e] = __ldcg(p.ws_acc + (slot * kRows + 4 * step + e) * 32 + lane);
     }
 #pragma unroll
     for (int k = 0; k < kDeep; ++k) {
       if (q0 + k * kWarps >= j.z) break;
-      const float m = fmaxf(M, ml[k].x), ref = m == kNegInfF ? 0.f : m;
-      const float so = fast_exp2(M - ref), sn = fast_exp2(ml[k].x - ref);
-      M = m;
-      l = l * so + ml[k].y * sn;
 #pragma unroll
-      for (int e = 0; e < kPer; ++e) acc[e] = acc[e] * so + x[k][e] * sn;
+      for (int i = 0; i < 2; ++i) {
+        const float m = fmaxf(M[i], ml[k][i].x), ref = m == kNegInfF ? 0.f : m;
+        const float so = fast_exp2(M[i] - ref), sn = fast_exp2(ml[k][i].x - ref);
+        M[i] = m;
+        l[i] = l[i] * so + ml[k][i].y * sn;
+        x[i] = x[i] * so + y[k][i] * sn;
+        x[2 + i] = x[2 + i] * so + y[k][2 + i] * sn;
+      }
     }
   }
-  if (lane == 0) part_ml[warp] = make_float2(M, l);
 #pragma unroll
-  for (int e = 0; e < kPer; ++e) part[warp][lane * kPer + e] = acc[e];
+  for (int e = 0; e < 4; ++e) part[warp][e][lane] = x[e];
+  if (g == 0)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) part_ml[warp][i][t] = make_float2(M[i], l[i]);
   __syncthreads();
-  const int64_t out = ((int64_t)j.x * p.num_q_heads + kvh * gqa + h_first + h) * D;
-  for (int d = threadIdx.x; d < D; d += kThreads) {
-    float top = kNegInfF, sum = 0.f, x = 0.f;
+  if (warp >= 2 || ha + warp >= heads) return;   // warp i: head 2t + i
+  float top = kNegInfF, sum = 0.f, a = 0.f, b = 0.f;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, part_ml[w].x);
+  for (int w = 0; w < kWarps; ++w) top = fmaxf(top, part_ml[w][warp][t].x);
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      const float sc = part_ml[w].x == kNegInfF ? 0.f : fast_exp2(part_ml[w].x - top);
-      sum = fmaf(part_ml[w].y, sc, sum);
-      x = fmaf(part[w][d], sc, x);
-    }
-    x = sum == 0.f ? 0.f : x / sum;
-    if (p.out_f32) static_cast<float *>(p.out)[out + d] = x;
-    else static_cast<QT *>(p.out)[out + d] = Elem<QT>::from_f32(x);
+  for (int w = 0; w < kWarps; ++w) {
+    const float2 ml = part_ml[w][warp][t];
+    const float sc = ml.x == kNegInfF ? 0.f : fast_exp2(ml.x - top);
+    sum = fmaf(ml.y, sc, sum);
+    a = fmaf(part[w][warp][lane], sc, a);
+    b = fmaf(part[w][2 + warp][lane], sc, b);
   }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  const int64_t at = ((int64_t)j.x * p.num_q_heads + kvh * gqa + h_first + ha + warp) * D + g * (D / 8) + 2 * (step % kSteps);
+  if (p.out_f32) *reinterpret_cast<float2 *>(static_cast<float *>(p.out) + at) = make_float2(a * inv, b * inv);
+  else *reinterpret_cast<uint32_t *>(static_cast<QT *>(p.out) + at) = tc::pack2(a * inv, b * inv, QT{});
 }
 
 template <typename K>
-cudaError_t launch(K kernel, dim3 grid, const DecodeScaledParams &p, cudaStream_t s) {
+cudaError_t launch(K kernel, dim3 grid, int smem, const DecodeScaledParams &p, cudaStream_t s) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -580,21 +607,26 @@ cudaError_t launch(K kernel, dim3 grid, const DecodeScaledParams &p, cudaStream_
   return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
-template <typename QT, int D, int NT>
+template <typename QT, int D, int NT, bool kLo>
 cudaError_t launch_heads(const DecodeScaledParams &p, cudaStream_t s) {
   int sms = 0;
   cudaError_t e = current_sm_count(&sms);
+  if (e == cudaSuccess) e = ensure_smem_limit<decode_scaled_kernel<QT, D, NT, kLo>>(kRingBytes<D>);
   if (e != cudaSuccess) return e;
-  const unsigned ctas = (unsigned)std::min(sms, kPlanSms) * (NT == 1 ? 4 : 3);
-  e = p.out_f32 ? launch(decode_scaled_kernel<QT, D, NT, true>, dim3(ctas), p, s)
-                : launch(decode_scaled_kernel<QT, D, NT, false>, dim3(ctas), p, s);
-  return e != cudaSuccess ? e : launch(decode_scaled_join_kernel<QT, D>, dim3(ctas, (unsigned)p.share_heads), p, s);
+  const unsigned ctas = (unsigned)(std::min(sms, kPlanSms) * ctas_per_sm<D, NT>());
+  if ((e = launch(decode_scaled_kernel<QT, D, NT, kLo>, dim3(ctas), kRingBytes<D>, p, s)) != cudaSuccess) return e;
+  return launch(decode_scaled_join_kernel<QT, D, NT>, dim3(ctas, NT * (D / 16)), 0, p, s);
+}
+
+template <typename QT, int D>
+cudaError_t launch_dim(const DecodeScaledParams &p, cudaStream_t s) {
+  if (p.share_heads <= 8) return p.out_f32 ? launch_heads<QT, D, 1, true>(p, s) : launch_heads<QT, D, 1, false>(p, s);
+  return p.out_f32 ? launch_heads<QT, D, 2, true>(p, s) : launch_heads<QT, D, 2, false>(p, s);
 }
 
 template <typename QT>
 cudaError_t launch_type(const DecodeScaledParams &p, int head_dim, cudaStream_t s) {
-  if (head_dim == 64) return p.share_heads <= 8 ? launch_heads<QT, 64, 1>(p, s) : launch_heads<QT, 64, 2>(p, s);
-  return p.share_heads <= 8 ? launch_heads<QT, 128, 1>(p, s) : launch_heads<QT, 128, 2>(p, s);
+  return head_dim == 64 ? launch_dim<QT, 64>(p, s) : launch_dim<QT, 128>(p, s);
 }
 
 }  // namespace

@@ -271,11 +271,11 @@ struct DecodeScaledParams {
   int32_t out_f32;
   // workspace: of each CTA the (row, share) it leaves to the next ones and their number, and two pieces' sums
   int4 *joins;                        // [CTAs] {row, share, pieces or 0, 0}
-  float2 *ws_ml;                      // [2 CTAs][share_heads] (maximum, sum)
-  float *ws_acc;                      // [2 CTAs][share_heads][head_dim]
+  float2 *ws_ml;                      // [2 CTAs][8 or 16 heads] (maximum, sum)
+  float *ws_acc;                      // [2 CTAs][8 or 16 heads' elements, as the accumulators have them]
   int32_t *err;
 };
-constexpr int kScaledHeads = 16, kScaledCtas = 4 * kPlanSms;
+constexpr int kScaledHeads = 16, kScaledCtas = 2 * kPlanSms;
 cudaError_t launch_decode_scaled(const DecodeScaledParams &p, pa_dtype q_dtype, int head_dim, cudaStream_t s);
 
 // Rotation and cache write of a step's new tokens (pa_rope.cu).
