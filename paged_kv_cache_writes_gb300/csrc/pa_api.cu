@@ -664,7 +664,7 @@ pa_status scaled_layout(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_he
   const int gqa = num_q_heads / num_kv_heads;
   l->shares = (gqa + kScaledHeads - 1) / kScaledHeads;
   l->share_heads = (gqa + l->shares - 1) / l->shares;
-  // tiles of 16 keys are counted in 64 bits, shares of a row in 32
+  // tiles of 32 keys are counted in 64 bits, shares of a row in 32
   if ((double)num_kv_heads * l->shares >= 2147483648.0 ||
       (double)num_seqs * (max_seq_len / 16 + 1.0) * num_kv_heads * l->shares >= 4e18)
     return PA_ERR_UNSUPPORTED;

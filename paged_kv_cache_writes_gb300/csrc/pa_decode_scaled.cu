@@ -9,13 +9,12 @@
 // product takes the codes as they are; the sum takes 1 / sv_p, in fp32, from
 // unrounded w: a token whose values are tiny may hold most of the softmax.
 //
-// Bound by HBM: 2 head_dim bytes per token and KV head.  Everything between the load and the products therefore stays in
-// one warp: no barrier, no hand-over between roles.  A warp takes 16 keys at a time and all (up to 8 or 16) query heads of
-// the KV head:
+// Bound by HBM: 2 head_dim bytes per token and KV head.  Everything between the load and the products therefore stays in the
+// registers of one warp: no shared memory, no barrier, no hand-over between roles.  A warp takes 32 keys at a time, in two
+// halves, and all (up to 8 or 16) query heads of the KV head:
 //   S (16 keys x 8 heads)     = K (16 x D) . Q^T       mma.sync m16n8k16, f16
 //   O^T (16 d x 8 heads) +=     V^T (16 d x 16 keys) . P^T
-// Each lane copies the codes that it will itself need, two tiles ahead, into places of its own in shared memory
-// (cp.async): the bytes in flight cost no registers, and no lane waits for another.
+// The next tile's K is loaded as soon as S is done with this one's, V's likewise after the second product.
 // The codes are widened to f16 in registers, exactly.  Any order of the D products
 // will do, so the fragments are loaded as memory has them: a thread's K codes are
 // 16 consecutive ones of a row per 64, and Q's fragments are laid out once to
@@ -25,14 +24,13 @@
 // x 8 matrices.  The queries are f16 as they are, or bf16 times a power of two that
 // puts a row's largest element in [2^14, 2^15) (exact for every element above 2^-28
 // of it).  P is rounded once to f16 for a 16-bit output, else taken as hi + lo.
-// Per 16 keys with D = 128 a warp issues about 190 instructions, 16 of them MMAs, for
-// 4 KB of codes: a quarter of what an SM could issue at the copy rate.  (The
-// tensor-memory decode of pa_decode_tc.cuh, given block scales, was bound by the
-// hand-overs between its roles: 64 sequences of 300-16000, 64/8 heads 279 us against
-// XXX; 33 of 1-5000, head_dim 64, f16 72 against XXX.)
+// (The tensor-memory decode of pa_decode_tc.cuh, given block scales, was bound by the hand-overs between its roles: 64
+// sequences of 300-16000, 64/8 heads 279 us against XXX; 33 of 1-5000, head_dim 64, f16 72 against XXX.  Tiles of 16 keys
+// left each warp one chain of dependent steps: 222 us.  With the codes copied to shared memory two tiles ahead: 248; an
+// SM's loads in flight are not what it is short of.)
 //
-// Work.  The tiles of 16 keys of all (row, KV head share) in order are cut into equal ranges, one per CTA (eight warps, two
-// CTAs per SM; fewer CTAs where a range would fall under kMinTiles): whatever the lengths, all finish together.  Every CTA
+// Work.  The tiles of 32 keys of all (row, KV head share) in order are cut into equal ranges, one per CTA (six or eight
+// warps, two CTAs per SM; fewer CTAs where a range would fall under kMinTiles): whatever the lengths, all finish together.  Every CTA
 // finds its range from the lengths alone.  Within a range each (row, share) is a piece, its tiles dealt to the warps in turn
 // and joined through shared memory.  A piece that is a whole row is final; others leave their sums in the workspace, at most
 // two per CTA, and a second launch joins them.
@@ -46,21 +44,28 @@
 namespace pa {
 namespace {
 
-constexpr int kWarps = 8, kThreads = 32 * kWarps;
-constexpr int kStages = 3;                // tiles of a warp in shared memory
-constexpr int kTile = 16;                 // keys per step of a warp
-constexpr int kMinTiles = 32;             // tiles per CTA at least (while there are enough)
+constexpr int kTile = 32, kHalf = 16;     // keys per step of a warp, and per MMA
+constexpr int kMinTiles = 8;              // tiles per CTA at least, while there are enough: about one per warp
+// What a piece costs beside its tiles (its queries, the first codes' latency, the join of the warps), in tiles: about 3 us,
+// where an SM's share of the copy rate brings a tile in 0.4 (head_dim 64: 0.2) us
+template <int D>
+constexpr int kPieceCost = D == 128 ? 8 : 12;
 constexpr int kChunk = 1024;              // rows whose tile counts a CTA has at hand
 constexpr float kRescaleLog2 = 8.f;       // O is rescaled when a score exceeds the reference maximum by 2^8
 #define kNegInfF (-__int_as_float(0x7f800000))
 
-// Copies of codes to shared memory.  (Without an L2 policy: the same copies with an evict-first one, the addresses checked
-// to be in bounds and aligned, ended in an SM exception; plain loads with it had not.)
-__device__ __forceinline__ void copy16(void *dst, const void *src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+// Codes once read are not read again by this launch.
+__device__ __forceinline__ uint4 ld16(const void *p, uint64_t policy) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.L2::cache_hint.v4.u32 {%0, %1, %2, %3}, [%4], %5;"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p), "l"(policy));
+  return v;
 }
-__device__ __forceinline__ void copy8(void *dst, const void *src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+__device__ __forceinline__ uint2 ld8(const void *p, uint64_t policy) {
+  uint2 v;
+  asm volatile("ld.global.nc.L1::no_allocate.L2::cache_hint.v2.u32 {%0, %1}, [%2], %3;" : "=r"(v.x), "=r"(v.y) : "l"(p), "l"(policy));
+  return v;
 }
 
 // Two e4m3 codes (the low 16 bits) -> f16x2, exactly.
@@ -84,14 +89,22 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   return y;
 }
 
-// A row's tokens, checked, and its tiles (an empty row has one, without keys).
+// A row's tokens, checked, and what a share of it costs, in tiles (an empty row has one, without keys).
 __device__ __forceinline__ int row_len(const DecodeScaledParams &p, int row, bool report) {
   const int raw = __ldg(p.seq_lens + row);
   const int most = (int)min((int64_t)p.max_seq_len, (int64_t)p.max_blocks_per_seq * p.block_size);
   if (report && (raw < 0 || raw > most)) record_error(p.err, PA_ERR_DEVICE_CHECK);
   return min(max(raw, 0), most);
 }
-__device__ __forceinline__ int row_tiles(int len) { return max(1, (len + kTile - 1) / kTile); }
+template <int D>
+__device__ __forceinline__ int row_cost(int len) {
+  return kPieceCost<D> + max(1, (len + kTile - 1) / kTile);
+}
+
+// a / b for a >= 0, b > 0: numbers of 32 bits, the usual ones, take a fifth of the time.
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+  return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
 
 // The cut of `total` tiles into `workers` ranges, the first `rem` one tile longer.
 struct Cut {
@@ -99,41 +112,43 @@ struct Cut {
   int workers;
   __device__ Cut(int64_t total, int ctas) {
     workers = (int)max((int64_t)1, min((int64_t)ctas, total / kMinTiles));
-    base = total / workers;
+    base = quotient(total, workers);
     rem = total - base * workers;
   }
   __device__ int64_t begin(int w) const { return w * base + min((int64_t)w, rem); }
   __device__ int worker(int64_t tile) const {
     const int64_t longer = rem * (base + 1);
-    return (int)(tile < longer ? tile / (base + 1) : rem + (tile - longer) / base);
+    return (int)(tile < longer ? quotient(tile, base + 1) : rem + quotient(tile - longer, base));
   }
 };
 
-// CTAs per SM: the O of 16 query heads of 128 elements takes 64 registers more
+// Warps per CTA, and CTAs per SM: by the registers of a thread, 168 for 8 heads of 128 elements or 16 of 64 (12 warps), 255
+// for 16 of 128, 128 for 8 of 64
+template <int D, int NT>
+constexpr int warps_of() {
+  return (D == 128) == (NT == 1) ? 6 : 8;
+}
 template <int D, int NT>
 constexpr int ctas_per_sm() {
   return D == 128 && NT == 2 ? 1 : 2;
 }
-template <int D>
-constexpr int kRingBytes = kWarps *kStages * 2 * kTile * D;
 
 template <typename QT, int D, int NT, bool kLo>
-__global__ void __launch_bounds__(kThreads, ctas_per_sm<D, NT>()) decode_scaled_kernel(const DecodeScaledParams p) {
+__global__ void __launch_bounds__(32 * warps_of<D, NT>(), ctas_per_sm<D, NT>()) decode_scaled_kernel(const DecodeScaledParams p) {
   constexpr int kHeads = 8 * NT, kSteps = D / 16, kHalves = D / 64, kRows = NT * kSteps * 4;
   constexpr bool kBf16 = std::is_same<QT, __nv_bfloat16>::value;
-  // [warp][stage]: K as [row 0 or 1][half][lane] of 16 bytes, V as [key 0 .. 3][lane] of D / 8; between pieces the warps'
-  // sums, float [warp][kRows][lane]
-  extern __shared__ __align__(16) uint8_t ring[];
-  static_assert(kRows * 128 <= kStages * 2 * kTile * D, "a warp's sums fit in its part of the ring");
-  float *part = reinterpret_cast<float *>(ring);
+  constexpr int kWarps = warps_of<D, NT>(), kThreads = 32 * kWarps;
+  extern __shared__ __align__(16) float part[];   // [warp][kRows][lane]: the warps' sums
   __shared__ float2 part_ml[kWarps][kHeads];
   __shared__ int64_t warp_sum[kWarps];
   __shared__ int64_t tiles_end[kChunk];    // of the present chunk of rows: tiles up to and including row i
+  __shared__ int row_lens[kChunk];
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
   // (each launch waits for what precedes it; the joining one is launched while this one runs)
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const uint64_t policy = tc::l2_evict_first();
   const int units = p.num_kv_heads * p.shares, gqa = p.num_q_heads / p.num_kv_heads;
 
   // ---- this CTA's range of tiles
@@ -148,15 +163,21 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<D, NT>()) decode_scaled_
     for (int i = 0; i < kWarps; ++i) s += warp_sum[i];
     return s;
   };
-  // rows [first, first + kChunk): tiles_end, and their sum
-  auto scan_chunk = [&](int first) {
-    constexpr int kPer = kChunk / kThreads;
+  // rows [first, first + kChunk): their lengths and tiles_end, and the sum of their tiles
+  auto scan_chunk = [&](int first, bool report) {
+    constexpr int kPer = (kChunk + kThreads - 1) / kThreads;
     int mine[kPer];
     int64_t sum = 0;
     const int r0 = first + tid * kPer;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-      mine[i] = r0 + i < p.num_seqs ? row_tiles(row_len(p, r0 + i, false)) : 0;
+      mine[i] = tid * kPer + i < kChunk && r0 + i < p.num_seqs ? row_len(p, r0 + i, report) : -1;
+    }
+    __syncthreads();                       // (the lengths in use so far are no longer)
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      if (mine[i] >= 0) row_lens[tid * kPer + i] = mine[i];
+      mine[i] = mine[i] >= 0 ? row_cost<D>(mine[i]) : 0;
       sum += mine[i];
     }
     int64_t x = sum;
@@ -165,7 +186,6 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<D, NT>()) decode_scaled_
       const int64_t y = __shfl_up_sync(0xffffffffu, x, off);
       if (lane >= off) x += y;
     }
-    __syncthreads();
     if (lane == 31) warp_sum[warp] = x;
     __syncthreads();
     int64_t before = x - sum, total = 0;
@@ -177,20 +197,18 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<D, NT>()) decode_scaled_
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       before += mine[i];
-      tiles_end[tid * kPer + i] = before;
+      if (tid * kPer + i < kChunk) tiles_end[tid * kPer + i] = before;
     }
     __syncthreads();
     return total;
   };
   int chunk = 0;
-  int64_t chunk_total = scan_chunk(0), total = chunk_total;
+  int64_t chunk_total = scan_chunk(0, blockIdx.x == 0), total = chunk_total;
   if (p.num_seqs > kChunk) {
     int64_t x = 0;
-    for (int r = kChunk + tid; r < p.num_seqs; r += kThreads) x += row_tiles(row_len(p, r, false));
+    for (int r = kChunk + tid; r < p.num_seqs; r += kThreads) x += row_cost<D>(row_len(p, r, blockIdx.x == 0));
     total += block_sum(x);
   }
-  if (blockIdx.x == 0)
-    for (int r = tid; r < p.num_seqs; r += kThreads) (void)row_len(p, r, true);
   const Cut cut(total * units, gridDim.x);
   const int worker = blockIdx.x;
   if (worker >= cut.workers) {
@@ -202,39 +220,115 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<D, NT>()) decode_scaled_
   int64_t chunk_first = 0;                 // tiles (of one share) before the chunk
   bool joined = false;                     // a piece of this CTA goes on in the next one
 
+  // the first piece: the chunk's first row with tiles_end above the range's first tile, by two ballots
+  while (pos >= (chunk_first + chunk_total) * units) {
+    chunk_first += chunk_total;
+    chunk += kChunk;
+    chunk_total = scan_chunk(chunk, false);
+  }
+  const int64_t in_chunk = quotient(pos, units) - chunk_first;   // (rows are whole multiples of `units` tiles)
+  static_assert(kChunk == 1024, "a ballot of ballots");
+  const int some = __ffs(__ballot_sync(0xffffffffu, tiles_end[32 * lane + 31] > in_chunk)) - 1;
+  int at = 32 * some + __ffs(__ballot_sync(0xffffffffu, tiles_end[32 * some + lane] > in_chunk)) - 1;   // row, in the chunk
+  int64_t before = at ? tiles_end[at - 1] : 0;
+  constexpr int kCost = kPieceCost<D>;     // a share is kCost places, then its n tiles
+  int n = (int)(tiles_end[at] - before) - kCost;
+  int share = (int)quotient(pos - (chunk_first + before) * units, n + kCost);
+  int place = (int)(pos - (chunk_first + before) * units - (int64_t)share * (n + kCost));
+
   while (pos < end) {
     // ---- the piece at pos: row, share, tiles [tile0, tile0 + count) of n
-    while (pos >= (chunk_first + chunk_total) * units) {
-      chunk_first += chunk_total;
-      chunk += kChunk;
-      chunk_total = scan_chunk(chunk);
-    }
-    const int64_t in_chunk = pos / units - chunk_first;   // (rows are whole multiples of `units` tiles)
-    int lo = 0, hi = kChunk - 1;           // the first row of the chunk with tiles_end > in_chunk
-    while (lo < hi) {
-      const int mid = (lo + hi) >> 1;
-      if (tiles_end[mid] > in_chunk) hi = mid;
-      else lo = mid + 1;
-    }
-    const int row = chunk + lo;
-    const int64_t before = lo ? tiles_end[lo - 1] : 0;
-    const int n = (int)(tiles_end[lo] - before);
-    const int64_t row_first = (chunk_first + before) * units;
-    const int share = (int)((pos - row_first) / n), tile0 = (int)(pos - row_first - (int64_t)share * n);
-    const int count = (int)min((int64_t)(n - tile0), end - pos);
+    const int places = (int)min((int64_t)(n + kCost - place), end - pos);
+    const int tile0 = max(place - kCost, 0), count = max(place + places - kCost, 0) - tile0;
+    if (count == 0) break;                 // the range ends before the share's first tile
+    const int row = chunk + at, len = row_lens[at];
     const int kvh = share / p.shares, h_first = (share - kvh * p.shares) * p.share_heads;
     const int heads = min(p.share_heads, gqa - h_first), h0 = kvh * gqa + h_first;
-    const int len = row_len(p, row, false);
 
-    // ---- Q's fragments: element pairs 4m, 4m + 1 and 4m + 2, 4m + 3 of this thread's codes, m = 0 .. kSteps - 1
-    uint32_t qb[NT][kSteps][2];
-    float factor[NT][2];                   // of heads 2t, 2t + 1: scale log2(e), over the row's power of two
+    // ---- the piece's tiles, every kWarps-th to this warp: codes and scales a tile ahead, block ids two
+    const int32_t *table = p.block_tables + (int64_t)row * p.max_blocks_per_seq;
+    const int bs_log2 = p.block_size == 32 ? 5 : 4;
+    const char *kpool = static_cast<const char *>(p.k_cache) + g * D + t * 16;
+    const char *vpool = static_cast<const char *>(p.v_cache) + 2 * t * D + g * (D / 8);
+    const int last = tile0 + count;
+    struct Blocks {
+      int32_t half[2];                     // block ids of the tile's halves; -1: past the piece, no token, or out of range
+    };
+    auto read_blocks = [&](int tile) {     // as the table has them
+      Blocks b;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const int h = nt * 8 + g;
-      float amax = 0.f;
+      for (int h = 0; h < 2; ++h) {
+        const int key = tile * kTile + h * kHalf;
+        b.half[h] = tile < last && key < len ? __ldg(table + (key >> bs_log2)) : -1;
+      }
+      return b;
+    };
+    // (checked when they are used: a check at once would wait for the table)
+    auto check_blocks = [&](Blocks b, int tile) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        if (b.half[h] < 0 || b.half[h] >= p.num_blocks) {
+          if (tile < last && tile * kTile + h * kHalf < len) record_error(p.err, PA_ERR_DEVICE_CHECK);
+          b.half[h] = -1;
+        }
+      return b;
+    };
+    uint32_t kw[2][2][4 * kHalves];        // [half][row g or g + 8]: 16 codes of each 64
+    uint32_t vw[2][4][D / 32];             // [half][keys 2t, 2t + 1, 2t + 8, 2t + 9]: D / 8 codes from g D / 8 on
+    float sk[2], sv[2];
+    // bytes before a half's first row in the pools (a half without a block reads the pools' first rows, unused)
+    auto at_of = [&](int32_t b, int h) {
+      const int off = h * (p.block_size - kHalf);   // blocks of 16: each half its own; of 32: its upper half
+      return b < 0 ? (int64_t)0 : (((int64_t)b * p.num_kv_heads + kvh) * p.block_size + off) * D;
+    };
+    auto load_k = [&](const Blocks &b) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const char *src = kpool + at_of(b.half[h], h);
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+          for (int j = 0; j < kHalves; ++j) {
+            const uint4 x = ld16(src + r * 8 * D + j * 64, policy);
+            kw[h][r][4 * j] = x.x, kw[h][r][4 * j + 1] = x.y, kw[h][r][4 * j + 2] = x.z, kw[h][r][4 * j + 3] = x.w;
+          }
+      }
+    };
+    auto load_v = [&](const Blocks &b) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const char *src = vpool + at_of(b.half[h], h);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const char *at = src + ((r & 1) + (r >> 1) * 8) * D;
+          if constexpr (D == 128) {
+            const uint4 x = ld16(at, policy);
+            vw[h][r][0] = x.x, vw[h][r][1] = x.y, vw[h][r][2] = x.z, vw[h][r][3] = x.w;
+          } else {
+            const uint2 x = ld8(at, policy);
+            vw[h][r][0] = x.x, vw[h][r][1] = x.y;
+          }
+        }
+      }
+    };
+    auto load_scales = [&](const Blocks &b) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int64_t at = b.half[h] < 0 ? 0 : (int64_t)b.half[h] * p.num_kv_heads + kvh;
+        sk[h] = __ldg(p.k_scales + at);
+        sv[h] = __ldg(p.v_scales + at);
+      }
+    };
+    int tile = tile0 + warp;
+    Blocks now = read_blocks(tile), next = read_blocks(tile + kWarps);
+    // ---- Q's fragments: element pairs 4m, 4m + 1 and 4m + 2, 4m + 3 of this thread's codes, m = 0 .. kSteps - 1 (loaded
+    // beside the block ids, laid out while the first codes are in flight)
+    uint32_t qb[NT][kSteps][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int j = 0; j < kHalves; ++j) {
+        const int h = nt * 8 + g;
         uint4 a = make_uint4(0, 0, 0, 0), b = a;
         if (h < heads) {
           const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const QT *>(p.q) + ((int64_t)row * p.num_q_heads + h0 + h) * D + j * 64 + t * 16);
@@ -243,14 +337,25 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<D, NT>()) decode_scaled_
         }
         const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          qb[nt][4 * j + (i >> 1)][i & 1] = w[i];
-          if constexpr (kBf16)
-            amax = fmaxf(amax, fmaxf(__uint_as_float((w[i] << 16) & 0x7fffffffu), __uint_as_float(w[i] & 0x7fff0000u)));
-        }
+        for (int i = 0; i < 8; ++i) qb[nt][4 * j + (i >> 1)][i & 1] = w[i];
       }
+    now = check_blocks(now, tile);
+    if (tile < last) {
+      load_k(now);
+      load_scales(now);
+      load_v(now);
+    }
+    float factor[NT][2];                   // of heads 2t, 2t + 1: scale log2(e), over the row's power of two
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
       float back = 1.f;
       if constexpr (kBf16) {
+        float amax = 0.f;
+#pragma unroll
+        for (int m = 0; m < kSteps; ++m)
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            amax = fmaxf(amax, fmaxf(__uint_as_float((qb[nt][m][i] << 16) & 0x7fffffffu), __uint_as_float(qb[nt][m][i] & 0x7fff0000u)));
         amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
         amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
         const int eb = max(1, (int)((__float_as_uint(amax) >> 23) & 0xff));
@@ -285,118 +390,78 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<D, NT>()) decode_scaled_
         for (int e = 0; e < 4; ++e) o[nt][i][e] = 0.f;
     }
 
-    // ---- the piece's tiles, every kWarps-th to this warp: lane i has the block id and the scales of the warp's tile 32 w + i
-    // (w the present window), and those of the next window; codes two tiles ahead
-    const int32_t *table = p.block_tables + (int64_t)row * p.max_blocks_per_seq;
-    const int bs_log2 = p.block_size == 32 ? 5 : 4;
-    const char *kpool = static_cast<const char *>(p.k_cache), *vpool = static_cast<const char *>(p.v_cache);
-    const int mine = (count - warp + kWarps - 1) / kWarps;   // this warp's tiles
-    struct Window {
-      int32_t blk;                         // -1: past the piece, no token, or out of range
-      float k, log2_v, inv_v;
-    };
-    auto window = [&](int first) {
-      Window w{-1, 1.f, 0.f, 1.f};
-      const int i = first + lane, key = (tile0 + warp + kWarps * i) * kTile;
-      if (i < mine && key < len) {
-        const int32_t bi = __ldg(table + (key >> bs_log2));
-        if (bi >= 0 && bi < p.num_blocks) {
-          w.blk = bi;
-          const int64_t at = (int64_t)bi * p.num_kv_heads + kvh;
-          const float sk = __ldg(p.k_scales + at), sv = __ldg(p.v_scales + at);
-          if (block_scale_ok(sk) && block_scale_ok(sv)) w = {bi, sk, __log2f(sv), __fdividef(1.f, sv)};
-          else record_error(p.err, PA_ERR_DEVICE_CHECK);
-        } else {
-          record_error(p.err, PA_ERR_DEVICE_CHECK);
+    for (; tile < last; tile += kWarps) {
+      // scores of each half's keys g, g + 8 and heads 2t, 2t + 1
+      float s[2][NT][4];
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[h][nt][e] = 0.f;
+#pragma unroll
+      for (int m = 0; m < kSteps; ++m)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t a0 = widen2(kw[h][0][m]), a1 = widen2(kw[h][1][m]);
+          const uint32_t a2 = widen2(kw[h][0][m] >> 16), a3 = widen2(kw[h][1][m] >> 16);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) mma(s[h][nt], a0, a1, a2, a3, qb[nt][m][0], qb[nt][m][1]);
         }
+      const bool more = tile + kWarps < last;
+      next = check_blocks(next, tile + kWarps);
+      if (more) load_k(next);
+      float ks[2], lv[2], iv[2];           // this tile's scales, the next one's in flight
+      bool full = true;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const bool good = block_scale_ok(sk[h]) && block_scale_ok(sv[h]);
+        if (!good && now.half[h] >= 0) record_error(p.err, PA_ERR_DEVICE_CHECK);
+        ks[h] = good ? sk[h] : 1.f;
+        lv[h] = good ? __log2f(sv[h]) : 0.f;
+        iv[h] = good ? __fdividef(1.f, sv[h]) : 1.f;
+        full = full && now.half[h] >= 0;
       }
-      return w;
-    };
-    uint8_t *stage0 = ring + warp * (kStages * 2 * kTile * D);
-    // the codes of a tile in block b (-1: the pool's first rows, unused); always a group, so that they count in order
-    auto copy_tile = [&](int i, int32_t b) {
-      if (i < mine) {
-        const int off = ((tile0 + warp + kWarps * i) * kTile) & (p.block_size - 1);
-        const int64_t at = b < 0 ? (int64_t)0 : (((int64_t)b * p.num_kv_heads + kvh) * p.block_size + off) * D;
-        uint8_t *dst = stage0 + i % kStages * (2 * kTile * D);
-        const char *ks = kpool + at + g * D + t * 16;
+      if (more) load_scales(next);
+      const int nvis = len - tile * kTile; // keys of the tile that exist
+      full = full && nvis >= kTile;
+      // x: how far a score times V's scale is above the reference, log2 units
+      float x[2][NT][4], top = kNegInfF;
+      auto relative = [&]() {
 #pragma unroll
-        for (int r = 0; r < 2; ++r)
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
-          for (int j = 0; j < kHalves; ++j) copy16(dst + ((r * kHalves + j) * 32 + lane) * 16, ks + r * 8 * D + j * 64);
-        const char *vs = vpool + at + 2 * t * D + g * (D / 8);
-        dst += kTile * D;
+          for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const char *src = vs + ((r & 1) + (r >> 1) * 8) * D;
-          if constexpr (D == 128) copy16(dst + (r * 32 + lane) * 16, src);
-          else copy8(dst + (r * 32 + lane) * 8, src);
-        }
-      }
-      asm volatile("cp.async.commit_group;" ::: "memory");
-    };
-    Window now = window(0), next = window(32);
+            for (int e = 0; e < 4; ++e) x[h][nt][e] = fmaf(s[h][nt][e], factor[nt][e & 1] * ks[h], lv[h] - m_ref[nt][e & 1]);
+        if (!full)
 #pragma unroll
-    for (int i = 0; i < kStages - 1; ++i) copy_tile(i, __shfl_sync(0xffffffffu, now.blk, i));
-    for (int i = 0; i < mine; ++i) {
-      const int32_t blk = __shfl_sync(0xffffffffu, now.blk, i & 31);
-      const float ks = __shfl_sync(0xffffffffu, now.k, i & 31), lv = __shfl_sync(0xffffffffu, now.log2_v, i & 31);
-      const float iv = __shfl_sync(0xffffffffu, now.inv_v, i & 31);
-      const int ahead = (i & 31) + kStages - 1;
-      const int32_t ahead_blk = __shfl_sync(0xffffffffu, ahead < 32 ? now.blk : next.blk, ahead & 31);
-      const uint8_t *src = stage0 + i % kStages * (2 * kTile * D);
-      asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
-      // scores of keys g, g + 8 and heads 2t, 2t + 1
-      float s[NT][4], s2[NT][4];           // two chains of MMAs
+          for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[nt][e] = s2[nt][e] = 0.f;
+              for (int e = 0; e < 4; ++e)
+                if (now.half[h] < 0 || h * kHalf + (e < 2 ? g : g + 8) >= nvis) x[h][nt][e] = kNegInfF;
+      };
+      relative();
 #pragma unroll
-      for (int j = 0; j < kHalves; ++j) {
-        const uint4 x = *reinterpret_cast<const uint4 *>(src + (j * 32 + lane) * 16);
-        const uint4 y = *reinterpret_cast<const uint4 *>(src + ((kHalves + j) * 32 + lane) * 16);
-        const uint32_t r0[4] = {x.x, x.y, x.z, x.w}, r1[4] = {y.x, y.y, y.z, y.w};
+      for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const uint32_t a0 = widen2(r0[q]), a1 = widen2(r1[q]), a2 = widen2(r0[q] >> 16), a3 = widen2(r1[q] >> 16);
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) mma(q & 1 ? s2[nt] : s[nt], a0, a1, a2, a3, qb[nt][4 * j + q][0], qb[nt][4 * j + q][1]);
-        }
-      }
-      uint32_t vw[4][D / 32];              // V codes of keys 2t, 2t + 1, 2t + 8, 2t + 9
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const uint8_t *at = src + kTile * D + (r * 32 + lane) * (D / 8);
-        if constexpr (D == 128) {
-          const uint4 x = *reinterpret_cast<const uint4 *>(at);
-          vw[r][0] = x.x, vw[r][1] = x.y, vw[r][2] = x.z, vw[r][3] = x.w;
-        } else {
-          const uint2 x = *reinterpret_cast<const uint2 *>(at);
-          vw[r][0] = x.x, vw[r][1] = x.y;
-        }
-      }
-      copy_tile(i + kStages - 1, ahead_blk);   // (the place of tile i - 1, which this lane has read)
-      if ((i & 31) == 31) {
-        now = next;
-        next = window(i + 33);
-      }
-      const int nvis = blk < 0 ? 0 : len - (tile0 + warp + kWarps * i) * kTile;   // keys of the tile that exist
-      float top = kNegInfF;                                                      // how far a score is above its reference
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float x = fmaf(s[nt][e] + s2[nt][e], factor[nt][e & 1] * ks, lv);
-          s[nt][e] = (e < 2 ? g : g + 8) < nvis ? x : kNegInfF;
-          top = fmaxf(top, s[nt][e] - m_ref[nt][e & 1]);   // (NaN, -inf less -inf, is ignored)
-        }
+          for (int e = 0; e < 4; e += 2) top = tc::fmax3(top, x[h][nt][e], x[h][nt][e + 1]);
       if (__any_sync(0xffffffffu, top > kRescaleLog2)) {
+        // new references, the maxima (before the first, the reference is -inf, and x is +inf or -inf)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            float m = fmaxf(s[nt][i], s[nt][2 + i]);
+            float m = kNegInfF;
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+              for (int e = i; e < 4; e += 2)
+                if (x[h][nt][e] != kNegInfF) m = fmaxf(m, fmaf(s[h][nt][e], factor[nt][i] * ks[h], lv[h]));
 #pragma unroll
             for (int off = 4; off < 32; off <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
             m = fmaxf(m, m_ref[nt][i]);
@@ -409,58 +474,66 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<D, NT>()) decode_scaled_
               o[nt][k][2 + i] *= alpha;
             }
           }
+        relative();
       }
       // P, its sum, and its fragments
-      uint32_t pb[NT][2], pl[NT][2];
+      uint32_t pb[2][NT][2], pl[2][NT][2];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        float w[4];
+      for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) w[e] = s[nt][e] == kNegInfF ? 0.f : fast_exp2(s[nt][e] - m_ref[nt][e & 1]);
+        for (int nt = 0; nt < NT; ++nt) {
+          float w[4];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) l[nt][i] = fmaf(w[i] + w[2 + i], iv, l[nt][i]);
+          for (int e = 0; e < 4; ++e) w[e] = fast_exp2(x[h][nt][e]);
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {   // keys g, g + 8
-          const __half2 hi = __floats2half2_rn(w[2 * r], w[2 * r + 1]);
-          pb[nt][r] = transpose8(*reinterpret_cast<const uint32_t *>(&hi));
-          if constexpr (kLo) {          // the rest, exact in fp32, rounded too
-            const float2 h = __half22float2(hi);
-            const __half2 low = __floats2half2_rn(w[2 * r] - h.x, w[2 * r + 1] - h.y);
-            pl[nt][r] = transpose8(*reinterpret_cast<const uint32_t *>(&low));
+          for (int i = 0; i < 2; ++i) l[nt][i] = fmaf(w[i] + w[2 + i], iv[h], l[nt][i]);
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {   // keys g, g + 8
+            const __half2 hi = __floats2half2_rn(w[2 * r], w[2 * r + 1]);
+            pb[h][nt][r] = transpose8(*reinterpret_cast<const uint32_t *>(&hi));
+            if constexpr (kLo) {          // the rest, exact in fp32, rounded too
+              const float2 f = __half22float2(hi);
+              const __half2 low = __floats2half2_rn(w[2 * r] - f.x, w[2 * r + 1] - f.y);
+              pl[h][nt][r] = transpose8(*reinterpret_cast<const uint32_t *>(&low));
+            }
           }
         }
+      if (!full) {   // V of keys that do not exist may hold anything, and P is 0 there
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            if (now.half[h] < 0 || h * kHalf + 2 * t + (r & 1) + (r >> 1) * 8 >= nvis)
+#pragma unroll
+              for (int k = 0; k < D / 32; ++k) vw[h][r][k] = 0;
+        __syncwarp();
       }
-      if (nvis < kTile) {   // V of keys that do not exist may hold anything, and P is 0 there
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-          if (2 * t + (r & 1) + (r >> 1) * 8 >= nvis)
+      for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int k = 0; k < D / 32; ++k) vw[r][k] = 0;
-      }
+        for (int k = 0; k < D / 32; ++k) { // four elements of each key at a time
+          uint32_t a[2][2];                // [keys 2t.., 2t + 8..][elements 0 and 1, 2 and 3]: bytes of the two keys in turn
 #pragma unroll
-      for (int k = 0; k < D / 32; ++k) {   // four elements of each key at a time
-        uint32_t a[2][2];                  // [keys 2t.., 2t + 8..][elements 0 and 1, 2 and 3]: bytes of the two keys in turn
+          for (int r = 0; r < 2; ++r) {
+            a[r][0] = __byte_perm(vw[h][2 * r][k], vw[h][2 * r + 1][k], 0x5140);
+            a[r][1] = __byte_perm(vw[h][2 * r][k], vw[h][2 * r + 1][k], 0x7362);
+          }
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          a[r][0] = __byte_perm(vw[2 * r][k], vw[2 * r + 1][k], 0x5140);
-          a[r][1] = __byte_perm(vw[2 * r][k], vw[2 * r + 1][k], 0x7362);
-        }
+          for (int i = 0; i < 2; ++i) {
+            const uint32_t a0 = widen2(a[0][i]), a1 = widen2(a[0][i] >> 16), a2 = widen2(a[1][i]), a3 = widen2(a[1][i] >> 16);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const uint32_t a0 = widen2(a[0][i]), a1 = widen2(a[0][i] >> 16), a2 = widen2(a[1][i]), a3 = widen2(a[1][i] >> 16);
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            mma(o[nt][2 * k + i], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
-            if constexpr (kLo) mma(o[nt][2 * k + i], a0, a1, a2, a3, pl[nt][0], pl[nt][1]);
+            for (int nt = 0; nt < NT; ++nt) {
+              mma(o[nt][2 * k + i], a0, a1, a2, a3, pb[h][nt][0], pb[h][nt][1]);
+              if constexpr (kLo) mma(o[nt][2 * k + i], a0, a1, a2, a3, pl[h][nt][0], pl[h][nt][1]);
+            }
           }
         }
-      }
+      if (more) load_v(next);
+      now = next;
+      next = read_blocks(tile + 2 * kWarps);
     }
 
-    // ---- join the warps, each of whose sums goes to its own part of the ring
-    asm volatile("cp.async.wait_group 0;" ::: "memory");
-    __syncwarp();
-    float *mine_part = part + warp * (kStages * 2 * kTile * D / 4);
+    // ---- join the warps
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -476,95 +549,123 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<D, NT>()) decode_scaled_
 #pragma unroll
       for (int k = 0; k < kSteps; ++k)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) mine_part[(4 * (nt * kSteps + k) + e) * 32 + lane] = o[nt][k][e];
+        for (int e = 0; e < 4; ++e) part[(warp * kRows + 4 * (nt * kSteps + k) + e) * 32 + lane] = o[nt][k][e];
     __syncthreads();
     const bool whole = count == n, starts = tile0 == 0;
     const int64_t slot = 2 * (int64_t)worker + (starts ? 1 : 0);
     // a step's accumulators (elements d, d + 1 of heads 2t, 2t + 1) per warp and turn
-    for (int k = warp; k < NT * kSteps; k += kWarps) {
-      const int ha = k / kSteps * 8 + 2 * t, d = g * (D / 8) + 2 * (k % kSteps);
-      float M[2] = {kNegInfF, kNegInfF}, sum[2] = {0.f, 0.f}, x[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int ha = nt * 8 + 2 * t;
+      float2 ml[kWarps][2];
+      float M[2] = {kNegInfF, kNegInfF}, sum[2] = {0.f, 0.f}, sc[kWarps][2], inv[2];
 #pragma unroll
       for (int w = 0; w < kWarps; ++w)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) M[i] = fmaxf(M[i], part_ml[w][ha + i].x);
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        float sc[2];
-#pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const float2 ml = part_ml[w][ha + i];
-          sc[i] = ml.x == kNegInfF ? 0.f : fast_exp2(ml.x - M[i]);
-          sum[i] = fmaf(ml.y, sc[i], sum[i]);
+          ml[w][i] = part_ml[w][ha + i];
+          M[i] = fmaxf(M[i], ml[w][i].x);
         }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) x[e] = fmaf(part[w * (kStages * 2 * kTile * D / 4) + (4 * k + e) * 32 + lane], sc[e & 1], x[e]);
-      }
-      if (whole) {
+      for (int w = 0; w < kWarps; ++w)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          if (ha + i >= heads) continue;
-          const float inv = sum[i] == 0.f ? 0.f : 1.f / sum[i];
-          const int64_t at = ((int64_t)row * p.num_q_heads + h0 + ha + i) * D + d;
-          if (p.out_f32) *reinterpret_cast<float2 *>(static_cast<float *>(p.out) + at) = make_float2(x[i] * inv, x[2 + i] * inv);
-          else *reinterpret_cast<uint32_t *>(static_cast<QT *>(p.out) + at) = tc::pack2(x[i] * inv, x[2 + i] * inv, QT{});
+          sc[w][i] = ml[w][i].x == kNegInfF ? 0.f : fast_exp2(ml[w][i].x - M[i]);
+          sum[i] = fmaf(ml[w][i].y, sc[w][i], sum[i]);
         }
-      } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) p.ws_acc[(slot * kRows + 4 * k + e) * 32 + lane] = x[e];
-        if (g == 0 && k % kSteps == 0)
+      for (int i = 0; i < 2; ++i) inv[i] = sum[i] == 0.f ? 0.f : 1.f / sum[i];
+      for (int k = warp; k < kSteps; k += kWarps) {
+        float x[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int i = 0; i < 2; ++i) p.ws_ml[slot * kHeads + ha + i] = make_float2(M[i], sum[i]);
+        for (int w = 0; w < kWarps; ++w)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[e] = fmaf(part[(w * kRows + 4 * (nt * kSteps + k) + e) * 32 + lane], sc[w][e & 1], x[e]);
+        if (whole) {
+          const int64_t to = ((int64_t)row * p.num_q_heads + h0 + ha) * D + g * (D / 8) + 2 * k;
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            if (ha + i >= heads) continue;
+            if (p.out_f32) *reinterpret_cast<float2 *>(static_cast<float *>(p.out) + to + i * D) = make_float2(x[i] * inv[i], x[2 + i] * inv[i]);
+            else *reinterpret_cast<uint32_t *>(static_cast<QT *>(p.out) + to + i * D) = tc::pack2(x[i] * inv[i], x[2 + i] * inv[i], QT{});
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) p.ws_acc[(slot * kRows + 4 * (nt * kSteps + k) + e) * 32 + lane] = x[e];
+          if (g == 0 && k == 0)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) p.ws_ml[slot * kHeads + ha + i] = make_float2(M[i], sum[i]);
+        }
       }
     }
-    __syncthreads();                       // the ring and part_ml are free
+    __syncthreads();                       // part and part_ml are free
     if (starts && !whole) {                // it goes on in the CTAs up to that of its last tile
       joined = true;
-      if (tid == 0) p.joins[worker] = make_int4(row, share, cut.worker(pos - tile0 + n - 1) - worker + 1, 0);
+      if (tid == 0) p.joins[worker] = make_int4(row, share, cut.worker(pos - place + n + kCost - 1) - worker + 1, 0);
     }
-    pos += count;
+    // the next piece begins a share: of this row, of the next one
+    pos += places;
+    place = 0;
+    if (++share == units && pos < end) {
+      share = 0;
+      if (++at == kChunk) {
+        chunk_first += chunk_total;
+        chunk += kChunk;
+        chunk_total = scan_chunk(chunk, false);
+        at = 0;
+      }
+      before = at ? tiles_end[at - 1] : 0;
+      n = (int)(tiles_end[at] - before) - kCost;
+    }
   }
   if (!joined && tid == 0) p.joins[worker] = make_int4(0, 0, 0, 0);
 }
 
-// The second launch: CTA (w, k) joins the pieces of the (row, share) that CTA w began and did not end, accumulators of step
-// k: slot 2w + 1, then slots 2(w + 1), 2(w + 2), ...; its warps share the pieces.
+// The second launch: CTA (w, step) joins the pieces of the (row, share) that CTA w began and did not end, one step's
+// accumulators (elements d, d + 1 of heads 2t, 2t + 1): slot 2w + 1, then slots 2(w + 1), 2(w + 2), ...; its warps share
+// the pieces.
+constexpr int kJoinWarps = 4;
 template <typename QT, int D, int NT>
-__global__ void __launch_bounds__(kThreads) decode_scaled_join_kernel(const DecodeScaledParams p) {
+__global__ void __launch_bounds__(32 * kJoinWarps) decode_scaled_join_kernel(const DecodeScaledParams p) {
   constexpr int kHeads = 8 * NT, kSteps = D / 16, kRows = NT * kSteps * 4;
-  __shared__ float part[kWarps][4][32];
-  __shared__ float2 part_ml[kWarps][2][4];
+  __shared__ float part[kJoinWarps][4][32];
+  __shared__ float2 part_ml[kJoinWarps][2][4];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int w0 = blockIdx.x, step = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
   const int4 j = __ldcg(p.joins + w0);
   if (j.z == 0) return;
   const int gqa = p.num_q_heads / p.num_kv_heads, kvh = j.y / p.shares, h_first = (j.y - kvh * p.shares) * p.share_heads;
   const int heads = min(p.share_heads, gqa - h_first), ha = step / kSteps * 8 + 2 * t;
-  constexpr int kDeep = 4;                 // pieces in flight
+  constexpr int kDeep = 8;                 // pieces in flight
   float M[2] = {kNegInfF, kNegInfF}, l[2] = {0.f, 0.f}, x[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int q0 = warp; q0 < j.z; q0 += kDeep * kWarps) {
+  for (int q0 = warp; q0 < j.z; q0 += kDeep * kJoinWarps) {
     float2 ml[kDeep][2];
     float y[kDeep][4];
 #pragma unroll
     for (int k = 0; k < kDeep; ++k) {
-      const int q = min(q0 + k * kWarps, j.z - 1);
-      const int64_t slot = q == 0 ? 2 * (int64_t)w0 + 1 : 2 * ((int64_t)w0 + q);
+      const int q = q0 + k * kJoinWarps;
+      const int64_t slot = 2 * ((int64_t)w0 + min(q, j.z - 1)) + (q == 0 ? 1 : 0);
 #pragma unroll
       for (int i = 0; i < 2; ++i) ml[k][i] = __ldcg(p.ws_ml + slot * kHeads + ha + i);
 #pragma unroll
       for (int e = 0; e < 4; ++e) y[k][e] = __ldcg(p.ws_acc + (slot * kRows + 4 * step + e) * 32 + lane);
     }
 #pragma unroll
-    for (int k = 0; k < kDeep; ++k) {
-      if (q0 + k * kWarps >= j.z) break;
+    for (int i = 0; i < 2; ++i) {
+      float m = M[i];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const float m = fmaxf(M[i], ml[k][i].x), ref = m == kNegInfF ? 0.f : m;
-        const float so = fast_exp2(M[i] - ref), sn = fast_exp2(ml[k][i].x - ref);
-        M[i] = m;
-        l[i] = l[i] * so + ml[k][i].y * sn;
-        x[i] = x[i] * so + y[k][i] * sn;
-        x[2 + i] = x[2 + i] * so + y[k][2 + i] * sn;
+      for (int k = 0; k < kDeep; ++k) m = fmaxf(m, ml[k][i].x);   // (the last piece may be there twice)
+      const float ref = m == kNegInfF ? 0.f : m, so = fast_exp2(M[i] - ref);
+      M[i] = m;
+      l[i] *= so;
+      x[i] *= so;
+      x[2 + i] *= so;
+#pragma unroll
+      for (int k = 0; k < kDeep; ++k) {
+        const float sn = q0 + k * kJoinWarps < j.z ? fast_exp2(ml[k][i].x - ref) : 0.f;
+        l[i] = fmaf(ml[k][i].y, sn, l[i]);
+        x[i] = fmaf(y[k][i], sn, x[i]);
+        x[2 + i] = fmaf(y[k][2 + i], sn, x[2 + i]);
       }
     }
   }
@@ -577,9 +678,9 @@ __global__ void __launch_bounds__(kThreads) decode_scaled_join_kernel(const Deco
   if (warp >= 2 || ha + warp >= heads) return;   // warp i: head 2t + i
   float top = kNegInfF, sum = 0.f, a = 0.f, b = 0.f;
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) top = fmaxf(top, part_ml[w][warp][t].x);
+  for (int w = 0; w < kJoinWarps; ++w) top = fmaxf(top, part_ml[w][warp][t].x);
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
+  for (int w = 0; w < kJoinWarps; ++w) {
     const float2 ml = part_ml[w][warp][t];
     const float sc = ml.x == kNegInfF ? 0.f : fast_exp2(ml.x - top);
     sum = fmaf(ml.y, sc, sum);
@@ -587,16 +688,16 @@ __global__ void __launch_bounds__(kThreads) decode_scaled_join_kernel(const Deco
     b = fmaf(part[w][2 + warp][lane], sc, b);
   }
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  const int64_t at = ((int64_t)j.x * p.num_q_heads + kvh * gqa + h_first + ha + warp) * D + g * (D / 8) + 2 * (step % kSteps);
-  if (p.out_f32) *reinterpret_cast<float2 *>(static_cast<float *>(p.out) + at) = make_float2(a * inv, b * inv);
-  else *reinterpret_cast<uint32_t *>(static_cast<QT *>(p.out) + at) = tc::pack2(a * inv, b * inv, QT{});
+  const int64_t to = ((int64_t)j.x * p.num_q_heads + kvh * gqa + h_first + ha + warp) * D + g * (D / 8) + 2 * (step % kSteps);
+  if (p.out_f32) *reinterpret_cast<float2 *>(static_cast<float *>(p.out) + to) = make_float2(a * inv, b * inv);
+  else *reinterpret_cast<uint32_t *>(static_cast<QT *>(p.out) + to) = tc::pack2(a * inv, b * inv, QT{});
 }
 
 template <typename K>
-cudaError_t launch(K kernel, dim3 grid, int smem, const DecodeScaledParams &p, cudaStream_t s) {
+cudaError_t launch(K kernel, dim3 grid, int warps, int smem, const DecodeScaledParams &p, cudaStream_t s) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = grid;
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(32 * warps);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -611,11 +712,12 @@ template <typename QT, int D, int NT, bool kLo>
 cudaError_t launch_heads(const DecodeScaledParams &p, cudaStream_t s) {
   int sms = 0;
   cudaError_t e = current_sm_count(&sms);
-  if (e == cudaSuccess) e = ensure_smem_limit<decode_scaled_kernel<QT, D, NT, kLo>>(kRingBytes<D>);
+  constexpr int warps = warps_of<D, NT>(), smem = warps * 8 * NT * D * 4;
+  if (e == cudaSuccess) e = ensure_smem_limit<decode_scaled_kernel<QT, D, NT, kLo>>(smem);
   if (e != cudaSuccess) return e;
   const unsigned ctas = (unsigned)(std::min(sms, kPlanSms) * ctas_per_sm<D, NT>());
-  if ((e = launch(decode_scaled_kernel<QT, D, NT, kLo>, dim3(ctas), kRingBytes<D>, p, s)) != cudaSuccess) return e;
-  return launch(decode_scaled_join_kernel<QT, D, NT>, dim3(ctas, NT * (D / 16)), 0, p, s);
+  if ((e = launch(decode_scaled_kernel<QT, D, NT, kLo>, dim3(ctas), warps, smem, p, s)) != cudaSuccess) return e;
+  return launch(decode_scaled_join_kernel<QT, D, NT>, dim3(ctas, NT * (D / 16)), kJoinWarps, 0, p, s);
 }
 
 template <typename QT, int D>
