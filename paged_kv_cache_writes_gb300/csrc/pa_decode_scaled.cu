@@ -49,7 +49,7 @@ constexpr int kMinTiles = 8;              // tiles per CTA at least, while there
 // What a piece costs beside its tiles (its queries, the first codes' latency, the join of the warps), in tiles: about 3 us,
 // where an SM's share of the copy rate brings a tile in 0.4 (head_dim 64: 0.2) us
 template <int D>
-constexpr int kPieceCost = D == 128 ? 8 : 12;
+constexpr int kPieceCost = D == 128 ? 12 : 16;
 constexpr int kChunk = 1024;              // rows whose tile counts a CTA has at hand
 constexpr float kRescaleLog2 = 8.f;       // O is rescaled when a score exceeds the reference maximum by 2^8
 #define kNegInfF (-__int_as_float(0x7f800000))
