@@ -112,60 +112,69 @@ __device__ __forceinline__ bool token_row(const RopeParams &p, int64_t t, const 
 }
 
 // One token's rows [0, rows): its q heads, then (unless a block-scaled launch's other warps do them) its k and v heads.
-// Thread: unit `tid % units` of the rows tid / units, + threads / units, ...
-template <typename T, bool kFp8>
+// Thread: unit `tid % units` of the rows tid / units, + threads / units, ..., kBatch of them in flight together.
+template <typename T, bool kFp8, int kBatch>
 __device__ __forceinline__ void token_rows(const RopeParams &p, int64_t t, int rows, int tid, int threads) {
-  const float *row;
-  if (!token_row(p, t, &row)) return;
   const int d = p.head_dim, units = d >> 4, k = tid & (units - 1), step = threads / units;
   const Place at = place_of(k, p.rope, p.interleaved);
+  // 0: a query, 1: K, 2: V, and its head
+  auto kind_of = [&](int h) { return h < p.num_q_heads ? 0 : h < p.num_q_heads + p.num_kv_heads ? 1 : 2; };
+  auto head_of = [&](int h, int kind) { return kind == 0 ? h : kind == 1 ? h - p.num_q_heads : h - p.num_q_heads - p.num_kv_heads; };
+  int64_t slot = rows > p.num_q_heads ? __ldg(p.slots + t) : -1;
+  Item x[kBatch];
+  auto load = [&](int h0) {
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int h = h0 + i * step, kind = kind_of(h);
+      if (h >= rows) continue;
+      const T *src = static_cast<const T *>(kind == 0 ? p.q : kind == 1 ? p.k : p.v) + t * (kind ? p.stride : p.q_stride) + (int64_t)head_of(h, kind) * d;
+      x[i] = {*reinterpret_cast<const uint4 *>(src + at.a), *reinterpret_cast<const uint4 *>(src + at.b)};
+    }
+  };
+  load(tid / units);                       // (beside the position and the slot)
+  const float *row;
+  if (!token_row(p, t, &row)) return;
   Angles ang;
   if (at.angle >= 0) load_angles(ang, row, p.rope, at.angle);
-  int64_t slot = -1;
-  if (rows > p.num_q_heads) {
-    slot = __ldg(p.slots + t);
-    if (slot >= p.num_blocks * p.block_size) {
-      record_error(p.err, PA_ERR_DEVICE_CHECK);
-      slot = -1;
-    }
+  if (slot >= p.num_blocks * p.block_size) {
+    record_error(p.err, PA_ERR_DEVICE_CHECK);
+    slot = -1;
   }
   const int64_t blk = slot < 0 ? 0 : slot / p.block_size, off = slot < 0 ? 0 : slot - blk * p.block_size;
-  for (int h = tid / units; h < rows; h += step) {
-    // 0: a query, 1: K, 2: V
-    const int kind = h < p.num_q_heads ? 0 : h < p.num_q_heads + p.num_kv_heads ? 1 : 2;
-    if (kind && slot < 0) break;
-    const int hh = kind == 0 ? h : kind == 1 ? h - p.num_q_heads : h - p.num_q_heads - p.num_kv_heads;
-    const T *src = static_cast<const T *>(kind == 0 ? p.q : kind == 1 ? p.k : p.v) + t * (kind ? p.stride : p.q_stride) + (int64_t)hh * d;
-    Item x{__ldg(reinterpret_cast<const uint4 *>(src + at.a)), __ldg(reinterpret_cast<const uint4 *>(src + at.b))};
-    const bool turned = kind < 2 && at.angle >= 0;
-    float f[16];
-    if (turned || (kFp8 && kind)) unpack_item<T>(x, f);
-    if (turned) {
-      rotate(f, ang, p.interleaved);
-      if (!kFp8 || !kind) x = pack_item<T>(f);
-    }
-    if (kFp8 && kind) {
-      const float *hs = kind == 1 ? p.k_hs : p.v_hs;
-      const float s = hs ? __ldg(hs + hh) : kind == 1 ? p.k_scale : p.v_scale;
+  for (int h0 = tid / units; h0 < rows; h0 += kBatch * step) {
+    if (h0 >= kBatch * step) load(h0);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) f[i] = __fdiv_rn(f[i], s);
-      const uint4 c = code_item(f);
-      uint8_t *dst = static_cast<uint8_t *>(kind == 1 ? p.k_cache : p.v_cache) + ((blk * p.num_kv_heads + hh) * p.block_size + off) * d;
-      *reinterpret_cast<uint2 *>(dst + at.a) = make_uint2(c.x, c.y);
-      *reinterpret_cast<uint2 *>(dst + at.b) = make_uint2(c.z, c.w);
-    } else {
-      T *dst = kind == 0 ? static_cast<T *>(p.q_out) + (t * p.num_q_heads + hh) * d
-                         : static_cast<T *>(kind == 1 ? p.k_cache : p.v_cache) + ((blk * p.num_kv_heads + hh) * p.block_size + off) * d;
-      *reinterpret_cast<uint4 *>(dst + at.a) = x.a;
-      *reinterpret_cast<uint4 *>(dst + at.b) = x.b;
+    for (int i = 0; i < kBatch; ++i) {
+      const int h = h0 + i * step, kind = kind_of(h), hh = head_of(h, kind);
+      if (h >= rows || (kind && slot < 0)) continue;
+      const bool turned = kind < 2 && at.angle >= 0;
+      float f[16];
+      if (turned || (kFp8 && kind)) unpack_item<T>(x[i], f);
+      if (turned) rotate(f, ang, p.interleaved);
+      if (kFp8 && kind) {
+        const float *hs = kind == 1 ? p.k_hs : p.v_hs;
+        const float s = hs ? __ldg(hs + hh) : kind == 1 ? p.k_scale : p.v_scale;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) f[e] = __fdiv_rn(f[e], s);
+        const uint4 c = code_item(f);
+        uint8_t *dst = static_cast<uint8_t *>(kind == 1 ? p.k_cache : p.v_cache) + ((blk * p.num_kv_heads + hh) * p.block_size + off) * d;
+        *reinterpret_cast<uint2 *>(dst + at.a) = make_uint2(c.x, c.y);
+        *reinterpret_cast<uint2 *>(dst + at.b) = make_uint2(c.z, c.w);
+      } else {
+        if (turned) x[i] = pack_item<T>(f);
+        T *dst = kind == 0 ? static_cast<T *>(p.q_out) + (t * p.num_q_heads + hh) * d
+                           : static_cast<T *>(kind == 1 ? p.k_cache : p.v_cache) + ((blk * p.num_kv_heads + hh) * p.block_size + off) * d;
+        *reinterpret_cast<uint4 *>(dst + at.a) = x[i].a;
+        *reinterpret_cast<uint4 *>(dst + at.b) = x[i].b;
+      }
     }
   }
 }
 
-// q may be q_out: no __restrict__; a thread reads its 16 elements before it writes them
-template <typename T, bool kFp8>
+// q may be q_out: no __restrict__, and plain loads of the rows; a thread reads its 16 elements before it writes them
+template <typename T, bool kFp8, int kBatch>
 __global__ void __launch_bounds__(512) rope_kernel(const RopeParams p) {
-  token_rows<T, kFp8>(p, blockIdx.x, p.num_q_heads + 2 * p.num_kv_heads, threadIdx.x, blockDim.x);
+  token_rows<T, kFp8, kBatch>(p, blockIdx.x, p.num_q_heads + 2 * p.num_kv_heads, threadIdx.x, blockDim.x);
 }
 
 // The smallest power of two 2^e, -64 <= e <= 32, with amax <= 448 * 2^e = 1.75 * 2^(8 + e), or 2^32.
@@ -268,17 +277,21 @@ __device__ __forceinline__ void scaled_block(const RopeParams &p, int64_t t0, ui
   }
 }
 
-// CTAs [0, q_ctas): the queries, a token each.  The others, by warps: warp w takes the blocks whose first new
+constexpr int kQueryBatch = 4;   // the registers of the blocks' rows leave few warps, which need their loads in flight
+
+// CTAs from unit_ctas on: the queries, q_threads threads a token.  The others, by warps: warp w takes the blocks whose first new
 // token is one of tokens g * window .. + window - 1, KV head and side w % (2 Hkv), g = w / (2 Hkv).  A window of one
 // token spreads a decode step over the GPU; a window of 32 leaves few warps without a block of a long prompt.
 template <typename T, int D, int kBs>
-__global__ void __launch_bounds__(kThreads) rope_scaled_kernel(const RopeParams p, int q_ctas, int window) {
-  if ((int)blockIdx.x < q_ctas) {
-    token_rows<T, false>(p, blockIdx.x, p.num_q_heads, threadIdx.x, kThreads);
+__global__ void __launch_bounds__(kThreads) rope_scaled_kernel(const RopeParams p, int unit_ctas, int q_threads, int window) {
+  if ((int)blockIdx.x >= unit_ctas) {
+    const int group = threadIdx.x / q_threads;
+    const int64_t t = (int64_t)(blockIdx.x - unit_ctas) * (kThreads / q_threads) + group;
+    if (t < p.num_tokens) token_rows<T, false, kQueryBatch>(p, t, p.num_q_heads, threadIdx.x - group * q_threads, q_threads);
     return;
   }
   const int lane = threadIdx.x & 31;
-  const int64_t w = (int64_t)(blockIdx.x - q_ctas) * (kThreads / 32) + (threadIdx.x >> 5);
+  const int64_t w = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
   const int sides = 2 * p.num_kv_heads, hs = (int)(w % sides);
   const int64_t t0 = w / sides * window;
   if (t0 >= p.num_tokens) return;
@@ -323,12 +336,24 @@ template <typename T, int D, int kBs>
 cudaError_t launch_scaled(const RopeParams &p, cudaStream_t s) {
   // about 32 warps per SM while the tokens last
   int window = 1;
-  while (window < 32 && (int64_t)p.num_tokens * 2 * p.num_kv_heads > (int64_t)window * 32 * kPlanSms) window *= 2;
+  while (window < 32 && (int64_t)p.num_tokens * 2 * p.num_kv_heads > (int64_t)window * 64 * kPlanSms) window *= 2;
   const int64_t warps = ((int64_t)p.num_tokens + window - 1) / window * 2 * p.num_kv_heads;
   const int64_t units = (warps + kThreads / 32 - 1) / (kThreads / 32);
-  const int64_t q_ctas = p.num_q_heads ? p.num_tokens : 0;
+  int q_threads = 32;
+  while (q_threads < kThreads && q_threads * kQueryBatch < p.num_q_heads * (D / 16)) q_threads *= 2;
+  const int per_cta = kThreads / q_threads;
+  const int64_t q_ctas = p.num_q_heads ? ((int64_t)p.num_tokens + per_cta - 1) / per_cta : 0;
   if (units + q_ctas > 2147483647ll) return cudaErrorInvalidValue;
-  rope_scaled_kernel<T, D, kBs><<<(unsigned)(units + q_ctas), kThreads, 0, s>>>(p, (int)q_ctas, window);
+  rope_scaled_kernel<T, D, kBs><<<(unsigned)(units + q_ctas), kThreads, 0, s>>>(p, (int)units, q_threads, window);
+  return cudaGetLastError();
+}
+
+template <typename T, bool kFp8, int kBatch>
+cudaError_t launch_rows(const RopeParams &p, int64_t units, cudaStream_t s) {
+  // kBatch units per thread, in as few turns of at most 512 threads as the token's need
+  const int64_t want = (units + kBatch - 1) / kBatch, turns = (want + 511) / 512;
+  const int threads = (int)(((want + turns - 1) / turns + 31) / 32 * 32);
+  rope_kernel<T, kFp8, kBatch><<<p.num_tokens, threads, 0, s>>>(p);
   return cudaGetLastError();
 }
 
@@ -338,12 +363,11 @@ cudaError_t launch_of(const RopeParams &p, cudaStream_t s) {
     if (p.head_dim == 64) return p.block_size == 16 ? launch_scaled<T, 64, 16>(p, s) : launch_scaled<T, 64, 32>(p, s);
     return p.block_size == 16 ? launch_scaled<T, 128, 16>(p, s) : launch_scaled<T, 128, 32>(p, s);
   }
-  // as few turns of at most 512 threads as the token's rows need, all of them of the same width
-  const int64_t want = ((int64_t)p.num_q_heads + 2 * p.num_kv_heads) * (p.head_dim / 16), turns = (want + 511) / 512;
-  const int threads = (int)(((want + turns - 1) / turns + 31) / 32 * 32);
-  if (p.fp8) rope_kernel<T, true><<<p.num_tokens, threads, 0, s>>>(p);
-  else rope_kernel<T, false><<<p.num_tokens, threads, 0, s>>>(p);
-  return cudaGetLastError();
+  // 2 rows per thread while all threads are resident at once, 4 beyond that
+  const int64_t units = ((int64_t)p.num_q_heads + 2 * p.num_kv_heads) * (p.head_dim / 16);
+  const bool few = (units + 1) / 2 * p.num_tokens <= 2048ll * kPlanSms;
+  if (p.fp8) return few ? launch_rows<T, true, 2>(p, units, s) : launch_rows<T, true, 4>(p, units, s);
+  return few ? launch_rows<T, false, 2>(p, units, s) : launch_rows<T, false, 4>(p, units, s);
 }
 
 // grid.x = pair, grid.y = 0 (K) / 1 (V): a block's rows and its heads' scales.
