@@ -20,6 +20,11 @@
 // comes from a warp reduction, the scale from its exponent, then the rows go out
 // as codes.  Rows the block held before are read only if its scale grows.  There
 // are no atomics: the warp of a block's first new token does the block.
+//
+// Bounds and times, bf16 rows, head_dim 128: 4 x 2048 tokens of 64 + 2 x 8 heads take 59.6 us into a bf16 cache (5.7 TB/s,
+// 84 % of a plain copy's rate) and 62.9 us into a block-scaled one (5.1 TB/s: the blocks' chain of slots, rows, largest
+// element, codes runs with 16 warps per SM).  64 tokens take 2.5 and 4.1 us: a launch and its chain of loads (position,
+// table row, row; slots first for blocks), not bytes.
 #include "pa_common.cuh"
 #include "pa_internal.h"
 #include "pa_tcgen05.cuh"
@@ -277,7 +282,10 @@ __device__ __forceinline__ void scaled_block(const RopeParams &p, int64_t t0, ui
   }
 }
 
-constexpr int kQueryBatch = 4;   // the registers of the blocks' rows leave few warps, which need their loads in flight
+// Rows in flight per thread of the queries: where the blocks' rows take 124 registers and more there are 16 warps per SM,
+// which need 8 (4 x 2048 tokens, 64 heads: 63 us; with 4: 69); at 80 registers 4 (a ragged batch: 6.0 us; with 8: 6.9).
+template <int D, int kBs>
+constexpr int kQueryBatch = D * kBs >= 2048 ? 8 : 4;
 
 // CTAs from unit_ctas on: the queries, q_threads threads a token.  The others, by warps: warp w takes the blocks whose first new
 // token is one of tokens g * window .. + window - 1, KV head and side w % (2 Hkv), g = w / (2 Hkv).  A window of one
@@ -287,7 +295,7 @@ __global__ void __launch_bounds__(kThreads) rope_scaled_kernel(const RopeParams 
   if ((int)blockIdx.x >= unit_ctas) {
     const int group = threadIdx.x / q_threads;
     const int64_t t = (int64_t)(blockIdx.x - unit_ctas) * (kThreads / q_threads) + group;
-    if (t < p.num_tokens) token_rows<T, false, kQueryBatch>(p, t, p.num_q_heads, threadIdx.x - group * q_threads, q_threads);
+    if (t < p.num_tokens) token_rows<T, false, kQueryBatch<D, kBs>>(p, t, p.num_q_heads, threadIdx.x - group * q_threads, q_threads);
     return;
   }
   const int lane = threadIdx.x & 31;
@@ -339,8 +347,12 @@ cudaError_t launch_scaled(const RopeParams &p, cudaStream_t s) {
   while (window < 32 && (int64_t)p.num_tokens * 2 * p.num_kv_heads > (int64_t)window * 64 * kPlanSms) window *= 2;
   const int64_t warps = ((int64_t)p.num_tokens + window - 1) / window * 2 * p.num_kv_heads;
   const int64_t units = (warps + kThreads / 32 - 1) / (kThreads / 32);
+  // 2 or 4 of a token's rows per thread while all threads are resident at once (64 tokens: 4.0 us; 4.7 with 8), kQueryBatch beyond that
+  const int q_units = p.num_q_heads * (D / 16);
+  const int64_t resident = 512ll * kPlanSms;
+  const int rows = (int64_t)p.num_tokens * q_units <= 2 * resident ? 2 : (int64_t)p.num_tokens * q_units <= 4 * resident ? 4 : kQueryBatch<D, kBs>;
   int q_threads = 32;
-  while (q_threads < kThreads && q_threads * kQueryBatch < p.num_q_heads * (D / 16)) q_threads *= 2;
+  while (q_threads < kThreads && q_threads * rows < q_units) q_threads *= 2;
   const int per_cta = kThreads / q_threads;
   const int64_t q_ctas = p.num_q_heads ? ((int64_t)p.num_tokens + per_cta - 1) / per_cta : 0;
   if (units + q_ctas > 2147483647ll) return cudaErrorInvalidValue;
