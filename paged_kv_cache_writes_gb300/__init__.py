@@ -477,18 +477,17 @@ def pa_evict(k_cache: torch.Tensor, v_cache: torch.Tensor, cache: PaKvCache, blo
         raise PaError(status, "pa_evict")
 
 
-def _heads_rows(a: _Args, t: torch.Tensor, name: str, tokens: int, d: int, dtype: torch.dtype):
+def _heads_rows(a: _Args, t: torch.Tensor, name: str, shape, dtype: torch.dtype):
     """(pointer, token stride) of [tokens, heads, head_dim] rows with unit inner strides."""
-    if t.dim() != 3 or t.shape[0] != tokens or t.shape[2] != d:
-        raise ValueError(f"{name} must be [tokens, heads, head_dim]")
     if t.get_device() != a.device:
         raise ValueError(f"{name} must be a CUDA tensor on the current device")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}")
+    tokens, heads, d = shape
     stride = t.stride()
     if stride[2] != 1 or stride[1] != d:
         raise ValueError(f"{name} must have unit inner strides")
-    return t.data_ptr(), stride[0]
+    return t.data_ptr(), stride[0] if tokens > 1 else heads * d
 
 
 def _block_scales(a: _Args, k_scales: torch.Tensor, v_scales: torch.Tensor, cache: PaKvCache):
@@ -508,15 +507,12 @@ def pa_rope_and_cache(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, 
     stored as it comes (q must be None).  q, k and v may be views into one QKV tensor.  ``k_scales``, ``v_scales``: float32
     [num_blocks, Hkv] of a block-scaled fp8 cache, which this call chooses and raises."""
     a = _Args()
-    if k.dim() != 3:
-        raise ValueError("k must be [tokens, heads, head_dim]")
-    T, hkv, d = k.shape
-    if hkv != cache.num_kv_heads or d != cache.head_dim or v.shape != k.shape:
+    shape, dtype = k.shape, k.dtype
+    if len(shape) != 3 or shape[1] != cache.num_kv_heads or shape[2] != cache.head_dim or v.shape != shape:
         raise ValueError("k and v must be [tokens, num_kv_heads, head_dim]")
-    kp, stride = _heads_rows(a, k, "k", T, d, k.dtype)
-    vp, v_stride = _heads_rows(a, v, "v", T, d, k.dtype)
-    if T <= 1:
-        stride = v_stride = hkv * d
+    T, _, d = shape
+    kp, stride = _heads_rows(a, k, "k", shape, dtype)
+    vp, v_stride = _heads_rows(a, v, "v", shape, dtype)
     if v_stride != stride:
         raise ValueError("k and v must have equal token strides")
     a.pools(k_cache, v_cache, cache)
@@ -524,13 +520,14 @@ def pa_rope_and_cache(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, 
         raise ValueError("slot_mapping must have one entry per token")
     qp, q_stride, qo, hq = None, 0, None, 0
     if q is not None:
-        qp, q_stride = _heads_rows(a, q, "q", T, d, k.dtype)
-        hq = q.shape[1]
-        if T <= 1:
-            q_stride = hq * d
-        if q_out is None or q_out.shape != q.shape:
+        q_shape = q.shape
+        if len(q_shape) != 3 or q_shape[0] != T or q_shape[2] != d:
+            raise ValueError("q must be [tokens, num_q_heads, head_dim]")
+        hq = q_shape[1]
+        qp, q_stride = _heads_rows(a, q, "q", q_shape, dtype)
+        if q_out is None or q_out.shape != q_shape:
             raise ValueError("q_out must have q's shape")
-        qo = a(q_out, "q_out", k.dtype)
+        qo = a(q_out, "q_out", dtype)
     pos, table, num_pos, rope = None, None, 0, 0
     if cos_sin is not None:
         if cos_sin.dim() != 2 or positions is None or positions.shape != (T,):
@@ -544,7 +541,7 @@ def pa_rope_and_cache(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, 
         if k_scales is None or v_scales is None:
             raise ValueError("k_scales and v_scales go together")
         ks, vs = _block_scales(a, k_scales, v_scales, cache)
-    status = lib().pa_rope_and_cache(qp, q_stride, qo, hq, kp, vp, _dtype_code(k.dtype), T, stride, pos, table, num_pos, rope,
+    status = lib().pa_rope_and_cache(qp, q_stride, qo, hq, kp, vp, _dtype_code(dtype), T, stride, pos, table, num_pos, rope,
                                      interleaved, a(slot_mapping, "slot_mapping", torch.int64), a(k_cache, "k_cache"),
                                      a(v_cache, "v_cache"), ctypes.byref(cache), ks, vs, a.stream(stream))
     if status:
