@@ -583,8 +583,10 @@ PA_API pa_status pa_evict(void *k_cache, void *v_cache, const pa_kv_cache *cache
  * the power of two as above, and the codes of the held tokens become
  * e4m3(code * old / new), exact but for codes that fall below e4m3's normal
  * range.  The new codes are e4m3(x / scale); slots behind the new ones are not
- * touched.  New tokens of one block are expected within block_size consecutive
- * tokens of the call (as sequences' tokens in order are).  A block to be added
+ * touched.  New tokens of one block must be within block_size consecutive
+ * tokens of the call, each in a slot of its own (as a sequence's tokens in order
+ * are; padding between them counts): else that block's codes and scale are
+ * undefined.  A block to be added
  * to whose scale is out of range sets PA_ERR_DEVICE_CHECK and keeps its tokens;
  * the new ones are not stored.  A block shared with another sequence is copied
  * first (pa_bm_append's pairs, pa_copy_blocks_scaled).

@@ -348,9 +348,9 @@ cudaError_t launch_scaled(const RopeParams &p, cudaStream_t s) {
   const int64_t warps = ((int64_t)p.num_tokens + window - 1) / window * 2 * p.num_kv_heads;
   const int64_t units = (warps + kThreads / 32 - 1) / (kThreads / 32);
   // 2 or 4 of a token's rows per thread while all threads are resident at once (64 tokens: 4.0 us; 4.7 with 8), kQueryBatch beyond that
-  const int q_units = p.num_q_heads * (D / 16);
+  const int64_t q_units = (int64_t)p.num_q_heads * (D / 16);
   const int64_t resident = 512ll * kPlanSms;
-  const int rows = (int64_t)p.num_tokens * q_units <= 2 * resident ? 2 : (int64_t)p.num_tokens * q_units <= 4 * resident ? 4 : kQueryBatch<D, kBs>;
+  const int rows = p.num_tokens * q_units <= 2 * resident ? 2 : p.num_tokens * q_units <= 4 * resident ? 4 : kQueryBatch<D, kBs>;
   int q_threads = 32;
   while (q_threads < kThreads && q_threads * rows < q_units) q_threads *= 2;
   const int per_cta = kThreads / q_threads;
