@@ -31,7 +31,13 @@
 // A team's score buffer is two halves of 64 keys, each with its own softmax step: while a team's threads work on one half,
 // the tensor cores compute the other half's scores and the P.V of the one before.  P (f16 pairs; hi + lo) goes over its own
 // half.  (With one buffer of 128 keys a team waited for P.V and the next Q.K^T in turn: 821 us against 721 for 4 chunks of
-// 2048 at 2048, 64/8 heads.)
+// 2048 at 2048, 64/8 heads; 698 now.)
+//
+// Bound by the softmax warps, two per scheduler, one step's chain after another: scores, maximum, weights, hand-over.  At 698
+// us the tensor pipe is busy 51 % of the time, the issue slots 52 %, the special functions 26 %.  What was tried on that chain
+// and cost more than it gave: scores and P in buffers of their own, so that Q.K^T waits for no P.V (one more wait per step:
+// 752), the next step's scores loaded under this one's exponentials (814), the two teams' exponentials in turn by a barrier
+// (726), one arrival per warp instead of per thread (706), a rolled loop for the queries' terms (710).
 //
 // Loaders: four warps, 32 keys of a tile each, a key tile ahead in registers (8-byte loads, a row of codes per 8 lanes),
 // widened into the MMAs' 128-byte-swizzled panels.  Codes staged by bulk copies instead would cost shared memory's
