@@ -561,7 +561,7 @@ PA_API pa_status pa_evict(void *k_cache, void *v_cache, const pa_kv_cache *cache
  *                 slot: the token's K and V are not stored, its query is
  *                 rotated)
  *   positions     device int32 [num_tokens]; a negative one marks a padding
- *                 token, nothing of which is read or written
+ *                 token, for which nothing is written
  *   cos_sin       device fp32 [num_positions][rope_dim], 16-byte aligned: cosines,
  *                 then sines, of each position's rope_dim / 2 angles
  *   rope_dim      a multiple of 16, at most head_dim; 0: keys are stored as they

@@ -31,11 +31,12 @@
 // A team's score buffer is two halves of 64 keys, each with its own softmax step: while a team's threads work on one half,
 // the tensor cores compute the other half's scores and the P.V of the one before.  P (f16 pairs; hi + lo) goes over its own
 // half.  (With one buffer of 128 keys a team waited for P.V and the next Q.K^T in turn: 821 us against 721 for 4 chunks of
-// 2048 at 2048, 64/8 heads; 698 now.)
+// 2048 at 2048, 64/8 heads; 682 now.)
 //
-// Bound by the softmax warps, two per scheduler, one step's chain after another: scores, maximum, weights, hand-over.  At 698
-// us the tensor pipe is busy 51 % of the time, the issue slots 52 %, the special functions 26 %.  What was tried on that chain
-// and cost more than it gave: scores and P in buffers of their own, so that Q.K^T waits for no P.V (one more wait per step:
+// Bound by the softmax warps, two per scheduler, one step's chain after another: scores, maximum, weights, hand-over.  At 682
+// us the tensor pipe is busy 52 % of the time, the issue slots 52 %, the special functions 27 %.  (Scales published for four key
+// tiles at once, so that a team waits for them every eighth step: 682 against 694.)  What was tried on that chain
+// at 695 and cost more than it gave: scores and P in buffers of their own, so that Q.K^T waits for no P.V (one more wait per step:
 // 752), the next step's scores loaded under this one's exponentials (814), the two teams' exponentials in turn by a barrier
 // (726), one arrival per warp instead of per thread (706), a rolled loop for the queries' terms (710).
 //
@@ -62,6 +63,7 @@ constexpr int kTeams = 2, kSoftmax = kTeams * 128;
 constexpr int kLoadWarp0 = kSoftmax / 32, kLoaders = 128, kMmaWarp = kLoadWarp0 + 4, kKWarp = kMmaWarp + kTeams;
 constexpr int kThreads = (kKWarp + 1) * 32;
 constexpr int kHalf = 64;                      // keys per softmax step
+constexpr int kGroup = 4;                      // key tiles whose scales are published together: a warp's 32 runs
 constexpr int kPanel = kN * 128;               // 64 elements of 128 rows
 constexpr float kRescaleLog2 = 8.f;            // O is rescaled when the maximum exceeds its reference by 2^8
 
@@ -76,16 +78,15 @@ struct Layout {
   static constexpr int kTile = kN * D * 2;                     // a Q or V tile (Q: f16, or two terms of codes)
   static constexpr int kKTile = kRaw ? kN * D : kTile;
   static constexpr int kStages = 2, kKStages = kRaw ? 3 : 2;   // V, K tiles in flight
-  static constexpr int kScaleSlots = kStages + 2;              // key tiles whose scales are at hand
   static constexpr int kOffQ = 0;
   static constexpr int kOffK = kOffQ + (kSplitKeys ? 1 : 2) * kTile;
   static constexpr int kOffV = kOffK + kKStages * kKTile;
   static constexpr int kOffBar = kOffV + kStages * kTile;
-  static constexpr int kNumBars = 2 * kStages + 2 * kKStages + 3 * 2 * kTeams + kScaleSlots + 2 + kTeams;   // (even: 16-byte alignment behind them)
+  static constexpr int kNumBars = 2 * kStages + 2 * kKStages + 3 * 2 * kTeams + 2 + 2 + kTeams;   // (even: 16-byte alignment behind them)
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;
   static constexpr int kOffRow = kOffMisc + 16;                // float2 [kTeams][128]
-  static constexpr int kOffRuns = (kOffRow + kTeams * 128 * 8 + 15) / 16 * 16;  // float4 [kScaleSlots][8 runs]
-  static constexpr int kBytes = kOffRuns + kScaleSlots * 8 * 16 + 1024;   // + alignment slack
+  static constexpr int kOffRuns = (kOffRow + kTeams * 128 * 8 + 15) / 16 * 16;  // float4 [2 groups][kGroup tiles][8 runs]
+  static constexpr int kBytes = kOffRuns + 2 * kGroup * 8 * 16 + 1024;   // + alignment slack
   static_assert(kBytes <= 227 * 1024 && kOffRow % 8 == 0 && kOffRuns % 16 == 0, "shared memory");
   static constexpr int kStage = kOffBar - kSoftmax / 32 * 4096;   // kSplitKeys: 4 KB per softmax warp for the output's way
   static_assert(kOffV % 1024 == 0 && (!kSplitKeys || kStage >= 128 * D * 4), "room for the teams' halves of O before it");
@@ -125,13 +126,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t *s_full = k_free + kKStages;          // [team][half] scores of its step h (half h & 1, phase h >> 1)
   uint64_t *p_full = s_full + 2 * kTeams;        // [team][half] P written over them (128 arrivals)
   uint64_t *o_done = p_full + 2 * kTeams;        // [team][half] P.V complete
-  uint64_t *sc_full = o_done + 2 * kTeams;       // [kScaleSlots] a tile's scales (an arrival of each loader warp)
-  uint64_t *q_ready = sc_full + L::kScaleSlots;
+  uint64_t *sc_full = o_done + 2 * kTeams;       // [2] the scales of tiles kGroup G .. + kGroup - 1 (G & 1)
+  uint64_t *q_ready = sc_full + 2;
   uint64_t *fin = q_ready + 1;                   // [team] every MMA of the team complete
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::kOffMisc);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::kOffMisc + 8);
   float2 *row_info = reinterpret_cast<float2 *>(smem + L::kOffRow);
-  // of each run of 16 keys of tile j, at [j % kScaleSlots]: K's scale, log2 of V's, 1 / V's
+  // of each run of 16 keys of tile j, at [j % (2 kGroup)]: K's scale, log2 of V's, 1 / V's
   float4 *runs = reinterpret_cast<float4 *>(smem + L::kOffRuns);
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -183,7 +184,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&o_done[t], 1);
     }
     mbar_init(q_ready, kSplitKeys ? 128 : kSoftmax);
-    for (int i = 0; i < L::kScaleSlots; ++i) mbar_init(&sc_full[i], kLoaders / 32);
+    for (int i = 0; i < 2; ++i) mbar_init(&sc_full[i], 1);
     mbar_init(&fin[0], 1);
     mbar_init(&fin[1], 1);
     *abort_flag = 0;
@@ -298,9 +299,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t sb = sbuf(team) + lane_base, ob = obuf(team) + lane_base;
     for (int h = 0; h < n; ++h) {
       const int b = h & 1, tb = team * 2 + b;
-      const int j = tile_of(team, h), slot = j % L::kScaleSlots;
-      if (b == 0) ok = wait_all(&sc_full[slot], (j / L::kScaleSlots) & 1);
-      const float4 *run = runs + 8 * slot + 4 * b;   // the half's four runs
+      const int j = tile_of(team, h);
+      if ((h & (kGroup * (kSplitKeys ? 1 : 2) - 1)) == 0) ok = wait_all(&sc_full[(j / kGroup) & 1], (j / (2 * kGroup)) & 1);
+      const float4 *run = runs + 8 * (j % (2 * kGroup)) + 4 * b;   // the half's four runs
       ok = ok && wait_all(&s_full[tb], (h >> 1) & 1);
       if (!ok) break;
       tc_fence_after();
@@ -545,15 +546,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           *reinterpret_cast<uint4 *>(tile + (i & 1 ? to1 : to0) + i * 512 + pn * kPanel) = widen8(w[pn][i]);
       fence_async_smem();
     };
-    // Scales, by lanes 0 and 1 of each warp those of its two runs (1 for a run without tokens, and for a bad one after its
-    // report): tile j + 2's are published when the P.V of tile j - kStages, the last that used their place, is complete;
-    // the next tile's are in flight then, and the block ids of the one after it
-    auto run_block = [&](int j) -> int32_t {
-      const int key = j * kN + 32 * lw + 16 * lane;
-      if (lane >= 2 || j >= nkt || key >= seq_eff) return -1;
+    // Scales, by loader warp 0, a run to each lane (1 for a run without tokens, and for a bad one after its report): those of
+    // tiles kGroup G .. + kGroup - 1 are published when the P.V of tile kGroup (G - 2) + kGroup - 1, the last that used their
+    // place, is complete; the next group's are in flight then, and the block ids of the one after it
+    auto run_block = [&](int group) -> int32_t {
+      const int j = kGroup * group + (lane >> 3), key = j * kN + 16 * (lane & 7);
+      if (j >= nkt || key >= seq_eff) return -1;
       const int32_t bi = __ldg(table + (key >> bs_log2));
       return bi >= 0 && bi < p.num_blocks ? bi : -1;
     };
+    static_assert(kGroup * 8 == 32, "a warp's runs");
     float sk = 1.f, sv = 1.f;
     auto read_scales = [&](int32_t b) {
       sk = sv = 1.f;
@@ -563,15 +565,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         sv = __ldg(p.v_scales + at);
       }
     };
-    auto put_scales = [&](int j) {
-      if (lane < 2) {
-        const bool good = block_scale_ok(sk) && block_scale_ok(sv);
-        if (!good) record_error(p.err, PA_ERR_DEVICE_CHECK);
-        runs[8 * (j % L::kScaleSlots) + 2 * lw + lane] =
-            good ? make_float4(sk, __log2f(sv), __fdividef(1.f, sv), 0.f) : make_float4(1.f, 0.f, 1.f, 0.f);
-      }
+    auto put_scales = [&](int group) {
+      const bool good = block_scale_ok(sk) && block_scale_ok(sv);
+      if (!good) record_error(p.err, PA_ERR_DEVICE_CHECK);
+      runs[32 * (group & 1) + lane] = good ? make_float4(sk, __log2f(sv), __fdividef(1.f, sv), 0.f) : make_float4(1.f, 0.f, 1.f, 0.f);
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sc_full[j % L::kScaleSlots]);
+      if (lane == 0) mbar_arrive(&sc_full[group & 1]);
     };
     Words kw, vw;
     Rows now = rows_of(0), next = now;
@@ -579,12 +578,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       if constexpr (!kRaw) load(now, kpool, kw);
       load(now, vpool, vw);
     }
-    for (int j = 0; j < 2; ++j) {
-      read_scales(run_block(j));
-      put_scales(j);
+    int32_t scale_blk = -1;
+    if (lw == 0) {
+      scale_blk = run_block(0);
+      const int32_t second = run_block(1);
+      read_scales(scale_blk);
+      scale_blk = run_block(2);
+      put_scales(0);
+      read_scales(second);
+      put_scales(1);
+      read_scales(scale_blk);
+      scale_blk = run_block(3);
     }
-    read_scales(run_block(2));
-    int32_t scale_blk = run_block(3);
     for (int j = 0; j < nkt; ++j) {
       const int s = j % kStages;
       if (j + 1 < nkt) next = rows_of(j + 1);
@@ -600,10 +605,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_arrive(&v_full[s]);
       if (j + 1 < nkt) load(next, vpool, vw);
       now = next;
-      if (j + 2 < nkt) {
-        put_scales(j + 2);
+      if (lw == 0 && j % kGroup == kStages - 1 && j > kGroup) {
+        const int group = j / kGroup + 1;
+        put_scales(group);
         read_scales(scale_blk);
-        scale_blk = run_block(j + 4);
+        scale_blk = run_block(group + 2);
       }
     }
   } else if (kRaw && warp == kKWarp) {

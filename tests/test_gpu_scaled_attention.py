@@ -83,6 +83,12 @@ def test_chunks_two_ctas_per_sm(d, qt, out):
     chunk_case([900, 701, 640], [900, 300, 640], 32, 4, d, 16, qt, out, seed=d)
 
 
+@pytest.mark.parametrize("qt,out", [("bf16", "bf16"), ("f16", "f32")])
+def test_chunks_of_many_key_tiles(qt, out):
+    """Scales come by groups of key tiles: sequences that end in every part of a group, two query tiles per CTA."""
+    chunk_case([2600, 1025, 1600, 1100], [500, 300, 200, 300], 32, 4, 64, 16, qt, out, seed=21)
+
+
 def test_chunk_far_into_a_context():
     chunk_case([6000], [130], 8, 2, 128, 32, "bf16", "f32", seed=3)
 
