@@ -485,7 +485,7 @@ def _heads_rows(a: _Args, t: torch.Tensor, name: str, shape, dtype: torch.dtype)
         raise TypeError(f"{name} must be {dtype}")
     tokens, heads, d = shape
     stride = t.stride()
-    if stride[2] != 1 or stride[1] != d:
+    if stride[2] != 1 or (stride[1] != d and heads > 1):
         raise ValueError(f"{name} must have unit inner strides")
     return t.data_ptr(), stride[0] if tokens > 1 else heads * d
 

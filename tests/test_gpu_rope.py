@@ -191,3 +191,20 @@ def test_binding_refusals():
     with pytest.raises(pa.PaError):
         call(cos_sin=torch.from_numpy(table(50, 24)).cuda())       # rope_dim 24
     assert pa.pa_get_device_error() == 0
+
+
+def test_one_head_of_any_stride():
+    """A single head's stride between heads says nothing: rows as a transposed view gives them."""
+    s = Step(9, 1, 1, 64, 16, "bf16", 64, seed=12)
+    q, k, v = s.parts(s.qkv.cuda())
+    pos, tab, slots = torch.from_numpy(s.pos).cuda(), torch.from_numpy(s.table).cuda(), torch.from_numpy(s.slots).cuda()
+    got = []
+    for change in (lambda x: x, lambda x: x.contiguous().view(1, 9, 64).transpose(0, 1)):
+        kc, vc = s.k0.cuda(), s.v0.cuda()
+        out = torch.empty((9, 1, 64), dtype=torch.bfloat16, device="cuda")
+        pa.pa_rope_and_cache(change(q), change(k), change(v), pos, tab, slots, kc, vc, pa.kv_cache_desc(kc), out)
+        got.append((kc, vc, out))
+    assert change(k).stride(1) != 64
+    for a, b in zip(*got):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+    assert pa.pa_get_device_error() == 0
