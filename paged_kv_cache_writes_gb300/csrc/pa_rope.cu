@@ -21,8 +21,8 @@
 // as codes.  Rows the block held before are read only if its scale grows.  There
 // are no atomics: the warp of a block's first new token does the block.
 //
-// Bounds and times, bf16 rows, head_dim 128: 4 x 2048 tokens of 64 + 2 x 8 heads take 59.6 us into a bf16 cache (5.7 TB/s,
-// 84 % of a plain copy's rate) and 62.9 us into a block-scaled one (5.1 TB/s: the blocks' chain of slots, rows, largest
+// Bounds and times, bf16 rows, head_dim 128: 4 x 2048 tokens of 64 + 2 x 8 heads take 52.4 us into a bf16 cache (6.5 TB/s,
+// 95 % of a plain copy's rate) and 62.9 us into a block-scaled one (5.1 TB/s: the blocks' chain of slots, rows, largest
 // element, codes runs with 16 warps per SM).  64 tokens take 2.5 and 4.1 us: a launch and its chain of loads (position,
 // table row, row; slots first for blocks), not bytes.
 #include "pa_common.cuh"
@@ -361,9 +361,9 @@ cudaError_t launch_scaled(const RopeParams &p, cudaStream_t s) {
 }
 
 template <typename T, bool kFp8, int kBatch>
-cudaError_t launch_rows(const RopeParams &p, int64_t units, cudaStream_t s) {
-  // kBatch units per thread, in as few turns of at most 512 threads as the token's need
-  const int64_t want = (units + kBatch - 1) / kBatch, turns = (want + 511) / 512;
+cudaError_t launch_rows(const RopeParams &p, int64_t units, int most, cudaStream_t s) {
+  // kBatch units per thread, in as few turns of at most `most` threads as the token's need
+  const int64_t want = (units + kBatch - 1) / kBatch, turns = (want + most - 1) / most;
   const int threads = (int)(((want + turns - 1) / turns + 31) / 32 * 32);
   rope_kernel<T, kFp8, kBatch><<<p.num_tokens, threads, 0, s>>>(p);
   return cudaGetLastError();
@@ -375,11 +375,13 @@ cudaError_t launch_of(const RopeParams &p, cudaStream_t s) {
     if (p.head_dim == 64) return p.block_size == 16 ? launch_scaled<T, 64, 16>(p, s) : launch_scaled<T, 64, 32>(p, s);
     return p.block_size == 16 ? launch_scaled<T, 128, 16>(p, s) : launch_scaled<T, 128, 32>(p, s);
   }
-  // 2 rows per thread while all threads are resident at once, 4 beyond that
+  // 2 rows per thread while all threads are resident at once, 4 beyond that, in CTAs small enough for one to start as another
+  // ends (4 x 2048 tokens, 64 + 2 x 8 heads, bf16 cache: turns of 128 threads 52.4 us, of 64 52.7, of 192 and more 59;
+  // fp8 cache: 64.8, 60.6, 65.4)
   const int64_t units = ((int64_t)p.num_q_heads + 2 * p.num_kv_heads) * (p.head_dim / 16);
   const bool few = (units + 1) / 2 * p.num_tokens <= 2048ll * kPlanSms;
-  if (p.fp8) return few ? launch_rows<T, true, 2>(p, units, s) : launch_rows<T, true, 4>(p, units, s);
-  return few ? launch_rows<T, false, 2>(p, units, s) : launch_rows<T, false, 4>(p, units, s);
+  if (p.fp8) return few ? launch_rows<T, true, 2>(p, units, 512, s) : launch_rows<T, true, 4>(p, units, 64, s);
+  return few ? launch_rows<T, false, 2>(p, units, 512, s) : launch_rows<T, false, 4>(p, units, 128, s);
 }
 
 // grid.x = pair, grid.y = 0 (K) / 1 (V): a block's rows and its heads' scales.
