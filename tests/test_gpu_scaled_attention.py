@@ -180,3 +180,71 @@ def test_same_bits_twice_and_on_a_stream(case):
         d = run_chunks(pa, c, q, rows, 0.1, "bf16", stream=s)[0]
     torch.cuda.synchronize()
     assert torch.equal(a.view(torch.uint8), b.view(torch.uint8)) and torch.equal(a.view(torch.uint8), d.view(torch.uint8))
+
+
+@pytest.mark.parametrize("hq,hkv", [(128, 1), (64, 1), (66, 2)])
+def test_wide_groups(hq, hkv):
+    """Groups of more query heads than a share has."""
+    for d, bs in ((64, 32), (128, 16)):
+        decode_case([1, 300, 40], hq, hkv, d, bs, "bf16", "f32", seed=hq + d)
+        chunk_case([1, 300, 40], [1, 20, 40], hq, hkv, d, bs, "f16", "f16", seed=hq + d)
+
+
+@pytest.mark.parametrize("case", ["decode", "chunk"])
+@pytest.mark.parametrize("bad", [-1, 1 << 29])
+def test_bad_blocks_are_reported(case, bad):
+    """A block id out of range where a token is: an error, nothing read there, the other sequences served."""
+    c = ScaledCache([100, 300, 70], 2, 128, 16, 15)
+    c.tables[1, 7] = bad
+    k, v, tables, desc, ks, vs = c.device(pa)
+    lens = torch.tensor(c.lens, dtype=torch.int32, device="cuda")
+    if case == "decode":
+        q = queries(3, 8, 128, "bf16", 16)
+        o = torch.empty_like(q, device="cuda")
+        ws = torch.empty(pa.pa_decode_scaled_workspace_bytes(3, 8, 2, 128, 300), dtype=torch.uint8, device="cuda")
+        pa.pa_decode_scaled(q.cuda(), k, v, desc, ks, vs, tables, lens, 300, 0.1, o, ws)
+        rows = [(0, 0, 1), (2, 2, 3)]
+    else:
+        q = queries(140, 8, 128, "bf16", 16)
+        o = torch.empty_like(q, device="cuda")
+        cu, start = (torch.tensor(x, dtype=torch.int32, device="cuda") for x in ([0, 20, 120, 140], [80, 200, 50]))
+        pa.pa_prefill_chunk_scaled(q.cuda(), cu, start, 100, k, v, desc, ks, vs, tables, lens, 300, 0.1, o)
+        rows = [(0, 0, 20), (2, 120, 140)]
+    assert pa.pa_get_device_error() == 4
+    for i, a, b in rows:
+        n = c.lens[i]
+        want, bound = attend(q[a:b], c.rows("k", i, n), c.rows("v", i, n), causal(n, b - a), 0.1, "bf16", case == "chunk")
+        check(o[a:b], want, bound, f"sequence {i}")
+
+
+@pytest.mark.parametrize("length", [-3, 301, 1 << 30])
+def test_bad_lengths_are_reported(length):
+    """A decode length below 0 or beyond max_seq_len: an error, cut to what is there, the other sequences served."""
+    c = ScaledCache([100, 300, 70], 2, 128, 16, 17)
+    k, v, tables, desc, ks, vs = c.device(pa)
+    lens = torch.tensor([100, length, 70], dtype=torch.int32, device="cuda")
+    q = queries(3, 8, 128, "bf16", 18)
+    o = torch.empty_like(q, device="cuda")
+    ws = torch.empty(pa.pa_decode_scaled_workspace_bytes(3, 8, 2, 128, 300), dtype=torch.uint8, device="cuda")
+    pa.pa_decode_scaled(q.cuda(), k, v, desc, ks, vs, tables, lens, 300, 0.1, o, ws)
+    assert pa.pa_get_device_error() == 4
+    for i, n in ((0, 100), (1, 0 if length < 0 else 300), (2, 70)):
+        want, bound = attend(q[i:i + 1], c.rows("k", i, n), c.rows("v", i, n), causal(n, 1), 0.1, "bf16", False)
+        check(o[i:i + 1], want, bound, f"sequence {i}")
+
+
+def test_calls_without_rows():
+    c = ScaledCache([20], 2, 128, 16, 19)
+    k, v, tables, desc, ks, vs = c.device(pa)
+    none = torch.empty((0, 8, 128), dtype=torch.bfloat16, device="cuda")
+    some = torch.zeros(1, dtype=torch.int32, device="cuda")
+    pa.pa_decode_scaled(none, k, v, desc, ks, vs, tables[:0], some[:0], 0, 0.1, none)
+    pa.pa_prefill_chunk_scaled(none, some, some[:0], 0, k, v, desc, ks, vs, tables[:0], some[:0], 0, 0.1, none)
+    row = torch.full((1, 8, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    out = row.clone()                                  # (a chunk without rows; the row behind it is no chunk's)
+    pa.pa_prefill_chunk_scaled(row, torch.cat([some, some]), some, 5, k, v, desc, ks, vs, tables, some, 20, 0.1, out)
+    assert torch.equal(out, row)
+    x = torch.empty((0, 2, 128), dtype=torch.bfloat16, device="cuda")
+    pa.pa_rope_and_cache(None, x, x, None, None, torch.empty(0, dtype=torch.int64, device="cuda"), k, v, desc, k_scales=ks, v_scales=vs)
+    pa.pa_copy_blocks_scaled(k, v, desc, ks, vs, torch.empty((0, 2), dtype=torch.int32, device="cuda"))
+    assert pa.pa_get_device_error() == 0
