@@ -614,8 +614,10 @@ PA_API pa_status pa_copy_blocks_scaled(void *k_cache, void *v_cache, const pa_kv
  * PA_ERR_DEVICE_CHECK (the rows that read it are then undefined).  The products
  * take the codes as they are: K's scales meet the scores, V's the softmax
  * weights, whose sum stays that of the weights without them, in fp32.  A weight
- * times V's scale is rounded once to f16 (2^-11 of itself) for a 16-bit output
- * and held to 2^-22 for an fp32 one.
+ * is held to 2^-11 of itself for a 16-bit output and to 2^-22 for an fp32 one
+ * (2^-17 in a row whose V scales lie more than 2^8 apart), or to 2^-24 of the
+ * row's largest weight if that is more, whatever the scales.  A score (in log2
+ * units) plus log2 of V's scale is an fp32 number, within 2^-21 of 1 + its size.
  *   workspace   device, >= pa_decode_scaled_workspace_bytes(...) bytes for the
  *               same heads and head_dim (the number and length of the sequences
  *               do not matter); else as for pa_decode

@@ -23,7 +23,10 @@
 // P goes from the first product's layout to the second's by a transposing move of 8
 // x 8 matrices.  The queries are f16 as they are, or bf16 times a power of two that
 // puts a row's largest element in [2^14, 2^15) (exact for every element above 2^-28
-// of it).  P is rounded once to f16 for a 16-bit output, else taken as hi + lo.
+// of it).  P (the weights w) is rounded once to f16 for a 16-bit output, else taken as hi + lo.  From a piece's first tile on
+// that has a V scale under 2^-8 of the largest that the warp has met, P is two bf16 terms for either, within 2^-17, and V's codes are
+// widened to bf16: f16 would lose the tokens of small values (pa_internal.h).  (That loop apart costs the other one 1 % of the
+// batch of 64, a branch within one loop 2 %.)
 // (The tensor-memory decode of pa_decode_tc.cuh, given block scales, was bound by the hand-overs between its roles: 64
 // sequences of 300-16000, 64/8 heads 279 us against 176; 33 of 1-5000, 40/8 heads of 64, f16 72 against 27.  Tiles of 16 keys
 // left each warp one chain of dependent steps: 222 us.  With the codes copied to shared memory two tiles ahead: 248; an
@@ -53,7 +56,9 @@ constexpr int kMinTiles = 8;              // tiles per CTA at least, while there
 template <int D>
 constexpr int kPieceCost = D == 128 ? 12 : 16;
 constexpr int kChunk = 1024;              // rows whose tile counts a CTA has at hand
-constexpr float kRescaleLog2 = 8.f;       // O is rescaled when a score exceeds the reference maximum by 2^8
+// A weight times V's scale is 2^kTopLog2 where the reference was taken, and O is rescaled before one exceeds 2^kRescaleLog2: as high as
+// f16 allows, so that a small one keeps what bits it can.
+constexpr float kTopLog2 = 7.f, kRescaleLog2 = 15.f;
 #define kNegInfF (-__int_as_float(0x7f800000))
 
 // Codes once read are not read again by this launch.
@@ -76,10 +81,22 @@ __device__ __forceinline__ uint32_t widen2(uint32_t w) {
   return *reinterpret_cast<const uint32_t *>(&h);
 }
 
-// c (16 x 8) += a (16 x 16) . b (16 x 8), f16 operands.  (volatile: the whole warp has to execute it together, so that it
-// must not be moved into a branch)
+// The same -> bf16x2, exactly (the upper halves of the fp32 patterns).
+__device__ __forceinline__ uint32_t widen2_bf16(uint32_t w) {
+  const float2 f = unpack2_e4m3(w);
+  return __byte_perm(__float_as_uint(f.x), __float_as_uint(f.y), 0x7632);
+}
+
+// c (16 x 8) += a (16 x 16) . b (16 x 8), f16 operands (or bf16 ones).  (volatile: the whole warp has to execute it
+// together, so that it must not be moved into a branch)
 __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
   asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
                : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
@@ -378,7 +395,7 @@ __global__ void __launch_bounds__(32 * warps_of<D, NT>(), ctas_per_sm<D, NT>()) 
     }
 
     float o[NT][kSteps][4];                // O^T: step i's rows g, g + 8 are elements g (D / 8) + 2 i, + 1; heads 2t, 2t + 1
-    float m_ref[NT][2], l[NT][2];
+    float m_ref[NT][2], l[NT][2], v_top = 0.f;   // v_top: the largest of V's scales in this warp's tiles so far
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -392,148 +409,172 @@ __global__ void __launch_bounds__(32 * warps_of<D, NT>(), ctas_per_sm<D, NT>()) 
         for (int e = 0; e < 4; ++e) o[nt][i][e] = 0.f;
     }
 
-    for (; tile < last; tile += kWarps) {
-      // scores of each half's keys g, g + 8 and heads 2t, 2t + 1
-      float s[2][NT][4];
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) s[h][nt][e] = 0.f;
-#pragma unroll
-      for (int m = 0; m < kSteps; ++m)
+    // this warp's tiles, until one needs P and V in bf16; then (kWide) the rest of them
+    auto walk = [&](auto in_bf16) {
+      constexpr bool kWide = decltype(in_bf16)::value;
+      for (; tile < last; tile += kWarps) {
+        const bool more = tile + kWarps < last;
+        float ks[2], lv[2], iv[2], v_low = -kNegInfF;   // this tile's scales (the next one's come in flight), the smallest of V's
+        bool full = true;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const uint32_t a0 = widen2(kw[h][0][m]), a1 = widen2(kw[h][1][m]);
-          const uint32_t a2 = widen2(kw[h][0][m] >> 16), a3 = widen2(kw[h][1][m] >> 16);
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) mma(s[h][nt], a0, a1, a2, a3, qb[nt][m][0], qb[nt][m][1]);
+          const bool good = block_scale_ok(sk[h]) && block_scale_ok(sv[h]);
+          if (!good && now.half[h] >= 0) record_error(p.err, PA_ERR_DEVICE_CHECK);
+          ks[h] = good ? sk[h] : 1.f;
+          lv[h] = good ? __log2f(sv[h]) : 0.f;
+          iv[h] = good ? __fdividef(1.f, sv[h]) : 1.f;
+          full = full && now.half[h] >= 0;
+          if (now.half[h] >= 0) {
+            v_low = fminf(v_low, good ? sv[h] : 1.f);
+            v_top = fmaxf(v_top, good ? sv[h] : 1.f);
+          }
         }
-      const bool more = tile + kWarps < last;
-      next = check_blocks(next, tile + kWarps);
-      if (more) load_k(next);
-      float ks[2], lv[2], iv[2];           // this tile's scales, the next one's in flight
-      bool full = true;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const bool good = block_scale_ok(sk[h]) && block_scale_ok(sv[h]);
-        if (!good && now.half[h] >= 0) record_error(p.err, PA_ERR_DEVICE_CHECK);
-        ks[h] = good ? sk[h] : 1.f;
-        lv[h] = good ? __log2f(sv[h]) : 0.f;
-        iv[h] = good ? __fdividef(1.f, sv[h]) : 1.f;
-        full = full && now.half[h] >= 0;
-      }
-      if (more) load_scales(next);
-      const int nvis = len - tile * kTile; // keys of the tile that exist
-      full = full && nvis >= kTile;
-      // x: how far a score times V's scale is above the reference, log2 units
-      float x[2][NT][4], top = kNegInfF;
-      auto relative = [&]() {
+        // (every lane has the same scales; the vote makes it sure that they take one branch)
+        if (!kWide && __any_sync(0xffffffffu, v_low * kNarrowScales < v_top)) return;
+        // scores of each half's keys g, g + 8 and heads 2t, 2t + 1
+        float s[2][NT][4];
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) x[h][nt][e] = fmaf(s[h][nt][e], factor[nt][e & 1] * ks[h], lv[h] - m_ref[nt][e & 1]);
-        if (!full)
+            for (int e = 0; e < 4; ++e) s[h][nt][e] = 0.f;
+#pragma unroll
+        for (int m = 0; m < kSteps; ++m)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t a0 = widen2(kw[h][0][m]), a1 = widen2(kw[h][1][m]);
+            const uint32_t a2 = widen2(kw[h][0][m] >> 16), a3 = widen2(kw[h][1][m] >> 16);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma(s[h][nt], a0, a1, a2, a3, qb[nt][m][0], qb[nt][m][1]);
+          }
+        next = check_blocks(next, tile + kWarps);
+        if (more) load_k(next);
+        if (more) load_scales(next);
+        const int nvis = len - tile * kTile; // keys of the tile that exist
+        full = full && nvis >= kTile;
+        // x: how far a score times V's scale is above the reference, log2 units
+        float x[2][NT][4], top = kNegInfF;
+        auto relative = [&]() {
 #pragma unroll
           for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-              for (int e = 0; e < 4; ++e)
-                if (now.half[h] < 0 || h * kHalf + (e < 2 ? g : g + 8) >= nvis) x[h][nt][e] = kNegInfF;
-      };
-      relative();
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int e = 0; e < 4; e += 2) top = tc::fmax3(top, x[h][nt][e], x[h][nt][e + 1]);
-      if (__any_sync(0xffffffffu, top > kRescaleLog2)) {
-        // new references, the maxima (before the first, the reference is -inf, and x is +inf or -inf)
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            float m = kNegInfF;
+              for (int e = 0; e < 4; ++e) x[h][nt][e] = fmaf(s[h][nt][e], factor[nt][e & 1] * ks[h], lv[h] - m_ref[nt][e & 1]);
+          if (!full)
 #pragma unroll
             for (int h = 0; h < 2; ++h)
 #pragma unroll
-              for (int e = i; e < 4; e += 2)
-                if (x[h][nt][e] != kNegInfF) m = fmaxf(m, fmaf(s[h][nt][e], factor[nt][i] * ks[h], lv[h]));
+              for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int off = 4; off < 32; off <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-            m = fmaxf(m, m_ref[nt][i]);
-            const float alpha = m == kNegInfF ? 1.f : fast_exp2(m_ref[nt][i] - m);
-            m_ref[nt][i] = m;
-            l[nt][i] *= alpha;
-#pragma unroll
-            for (int k = 0; k < kSteps; ++k) {
-              o[nt][k][i] *= alpha;
-              o[nt][k][2 + i] *= alpha;
-            }
-          }
+                for (int e = 0; e < 4; ++e)
+                  if (now.half[h] < 0 || h * kHalf + (e < 2 ? g : g + 8) >= nvis) x[h][nt][e] = kNegInfF;
+        };
         relative();
-      }
-      // P, its sum, and its fragments
-      uint32_t pb[2][NT][2], pl[2][NT][2];
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          float w[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) w[e] = fast_exp2(x[h][nt][e]);
-#pragma unroll
-          for (int i = 0; i < 2; ++i) l[nt][i] = fmaf(w[i] + w[2 + i], iv[h], l[nt][i]);
-#pragma unroll
-          for (int r = 0; r < 2; ++r) {   // keys g, g + 8
-            const __half2 hi = __floats2half2_rn(w[2 * r], w[2 * r + 1]);
-            pb[h][nt][r] = transpose8(*reinterpret_cast<const uint32_t *>(&hi));
-            if constexpr (kLo) {          // the rest, exact in fp32, rounded too
-              const float2 f = __half22float2(hi);
-              const __half2 low = __floats2half2_rn(w[2 * r] - f.x, w[2 * r + 1] - f.y);
-              pl[h][nt][r] = transpose8(*reinterpret_cast<const uint32_t *>(&low));
-            }
-          }
-        }
-      if (!full) {   // V of keys that do not exist may hold anything, and P is 0 there
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
-          for (int r = 0; r < 4; ++r)
-            if (now.half[h] < 0 || h * kHalf + 2 * t + (r & 1) + (r >> 1) * 8 >= nvis)
+          for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-              for (int k = 0; k < D / 32; ++k) vw[h][r][k] = 0;
-        __syncwarp();
-      }
+            for (int e = 0; e < 4; e += 2) top = tc::fmax3(top, x[h][nt][e], x[h][nt][e + 1]);
+        if (__any_sync(0xffffffffu, top > kRescaleLog2)) {
+          // new references, the maxima (before the first, the reference is -inf, and x is +inf or -inf)
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+          for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int k = 0; k < D / 32; ++k) { // four elements of each key at a time
-          uint32_t a[2][2];                // [keys 2t.., 2t + 8..][elements 0 and 1, 2 and 3]: bytes of the two keys in turn
+            for (int i = 0; i < 2; ++i) {
+              float m = kNegInfF;
 #pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            a[r][0] = __byte_perm(vw[h][2 * r][k], vw[h][2 * r + 1][k], 0x5140);
-            a[r][1] = __byte_perm(vw[h][2 * r][k], vw[h][2 * r + 1][k], 0x7362);
+              for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int e = i; e < 4; e += 2)
+                  if (x[h][nt][e] != kNegInfF) m = fmaxf(m, fmaf(s[h][nt][e], factor[nt][i] * ks[h], lv[h]));
+#pragma unroll
+              for (int off = 4; off < 32; off <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+              m = fmaxf(m - kTopLog2, m_ref[nt][i]);
+              const float alpha = m == kNegInfF ? 1.f : fast_exp2(m_ref[nt][i] - m);
+              m_ref[nt][i] = m;
+              l[nt][i] *= alpha;
+#pragma unroll
+              for (int k = 0; k < kSteps; ++k) {
+                o[nt][k][i] *= alpha;
+                o[nt][k][2 + i] *= alpha;
+              }
+            }
+          relative();
+        }
+        // the weights times V's scale, in the place of the scores, and the sum without it
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[h][nt][e] = fast_exp2(x[h][nt][e]);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) l[nt][i] = fmaf(x[h][nt][i] + x[h][nt][2 + i], iv[h], l[nt][i]);
           }
+        if (!full) {   // V of keys that do not exist may hold anything, and P is 0 there
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const uint32_t a0 = widen2(a[0][i]), a1 = widen2(a[0][i] >> 16), a2 = widen2(a[1][i]), a3 = widen2(a[1][i] >> 16);
+          for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              mma(o[nt][2 * k + i], a0, a1, a2, a3, pb[h][nt][0], pb[h][nt][1]);
-              if constexpr (kLo) mma(o[nt][2 * k + i], a0, a1, a2, a3, pl[h][nt][0], pl[h][nt][1]);
+            for (int r = 0; r < 4; ++r)
+              if (now.half[h] < 0 || h * kHalf + 2 * t + (r & 1) + (r >> 1) * 8 >= nvis)
+#pragma unroll
+                for (int k = 0; k < D / 32; ++k) vw[h][r][k] = 0;
+          __syncwarp();
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t pb[NT][2], pl[NT][2];   // P's fragments, and (two terms) those of the rest, exact in fp32, rounded too
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {  // keys g, g + 8
+              const float wa = x[h][nt][2 * r], wb = x[h][nt][2 * r + 1];
+              if constexpr (kWide) {
+                const uint32_t hi = tc::pack2(wa, wb, __nv_bfloat16{});
+                pb[nt][r] = transpose8(hi);
+                pl[nt][r] = transpose8(tc::pack2(wa - __uint_as_float(hi << 16), wb - __uint_as_float(hi & 0xffff0000u), __nv_bfloat16{}));
+              } else {
+                const __half2 hi = __floats2half2_rn(wa, wb);
+                pb[nt][r] = transpose8(*reinterpret_cast<const uint32_t *>(&hi));
+                if constexpr (kLo) {
+                  const float2 f = __half22float2(hi);
+                  pl[nt][r] = transpose8(tc::pack2(wa - f.x, wb - f.y, __half{}));
+                }
+              }
+            }
+#pragma unroll
+          for (int k = 0; k < D / 32; ++k) {   // four elements of each key at a time
+            uint32_t a[2][2];              // [keys 2t.., 2t + 8..][elements 0 and 1, 2 and 3]: bytes of the two keys in turn
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              a[r][0] = __byte_perm(vw[h][2 * r][k], vw[h][2 * r + 1][k], 0x5140);
+              a[r][1] = __byte_perm(vw[h][2 * r][k], vw[h][2 * r + 1][k], 0x7362);
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              auto w2 = [](uint32_t c) { return kWide ? widen2_bf16(c) : widen2(c); };
+              const uint32_t a0 = w2(a[0][i]), a1 = w2(a[0][i] >> 16), a2 = w2(a[1][i]), a3 = w2(a[1][i] >> 16);
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                float (&c)[4] = o[nt][2 * k + i];
+                if constexpr (kWide) mma_bf16(c, a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
+                else mma(c, a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
+                if constexpr (kWide) mma_bf16(c, a0, a1, a2, a3, pl[nt][0], pl[nt][1]);
+                else if constexpr (kLo) mma(c, a0, a1, a2, a3, pl[nt][0], pl[nt][1]);
+              }
             }
           }
         }
-      if (more) load_v(next);
-      now = next;
-      next = read_blocks(tile + 2 * kWarps);
-    }
+        if (more) load_v(next);
+        now = next;
+        next = read_blocks(tile + 2 * kWarps);
+      }
+    };
+    walk(std::false_type{});
+    walk(std::true_type{});
 
     // ---- join the warps
 #pragma unroll

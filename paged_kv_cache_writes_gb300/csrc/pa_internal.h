@@ -254,6 +254,12 @@ __host__ __device__ __forceinline__ bool block_scale_ok(float s) {
   return s >= 5.421010862427522e-20f && s <= 4294967296.f;   // 2^-64, 2^32 (false for NaN)
 }
 
+// Weights times V's scales are f16 while the scales that meet in an accumulator are within kNarrowScales of each other: one that f16
+// holds to 2^-25 where the largest is 2^7 at least is then held to 2^-32 * kNarrowScales = 2^-24 of the softmax's largest weight
+// times its own scale.  Beyond that they are two bf16 terms, which have fp32's range, so that tokens of small values are not
+// lost beside tokens of large ones.
+constexpr float kNarrowScales = 256.f;
+
 // Decode over a block-scaled cache (pa_decode_scaled.cu).
 struct DecodeScaledParams {
   const void *q;
