@@ -636,9 +636,8 @@ PA_API pa_status pa_decode_scaled(const void *q, pa_dtype q_dtype, int32_t num_s
 
 /*
  * pa_prefill_chunk_scaled -- pa_prefill_chunk over a block-scaled cache (K, V
- * and scales as for pa_decode_scaled).  A softmax weight times V's scale is
- * rounded once to f16 for a 16-bit output and held to 2^-22 for an fp32 one.
- * bf16 queries are taken to 2^-17 of their row's largest element with a bf16
+ * and scales as for pa_decode_scaled, the weights held as there).  bf16 queries
+ * are taken to 2^-17 of their row's largest element with a bf16
  * output, to 2^-28 of it otherwise.  A NaN among the cached V of a chunk may reach
  * the chunk's rows in front of it too.  Every shape of pa_prefill_chunk is served
  * on the tensor cores.

@@ -11,8 +11,9 @@
 // tiny may hold most of the softmax.  A run of 16 keys lies in one block.
 //
 // Operands.  V's codes are widened to f16, exactly, on their way into shared memory, and w is rounded once to f16 for a
-// 16-bit output (kLo false), else taken as hi + lo.  K, for bf16 queries and a bf16 output (raw_k): the codes as stored
-// (kind::f8f6f4), a query row being two e4m3 terms of its elements times a power of two that puts the largest in [128,
+// 16-bit output (kLo false), else taken as hi + lo.  In a CTA whose keys' V scales lie more than 2^8 apart (the loaders look
+// first) both are bf16 instead, w in two terms, within 2^-17: f16 would lose the tokens of small values (pa_internal.h).
+// K, for bf16 queries and a bf16 output (raw_k): the codes as stored (kind::f8f6f4), a query row being two e4m3 terms of its elements times a power of two that puts the largest in [128,
 // 256): elements down to 2^-9 of it are exact, smaller ones off by 2^-17 of it at most.  Otherwise K is widened too, and
 // bf16 query rows are multiplied by a power of two that puts their largest element in [2^14, 2^15) and rounded to f16,
 // exact for every element above 2^-28 of it.  (Raw K tiles come by bulk copies and cost no warp anything; widening takes
@@ -66,6 +67,7 @@ constexpr int kHalf = 64;                      // keys per softmax step
 constexpr int kGroup = 4;                      // key tiles whose scales are published together: a warp's 32 runs
 constexpr int kPanel = kN * 128;               // 64 elements of 128 rows
 constexpr float kRescaleLog2 = 8.f;            // O is rescaled when the maximum exceeds its reference by 2^8
+constexpr float kTopLog2 = 7.f;                // w at the reference, 2^15 at most: as high as f16 allows, for the small ones' sake
 
 // K as stored for bf16 queries and outputs.
 template <typename QT, bool kLo>
@@ -86,7 +88,8 @@ struct Layout {
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;
   static constexpr int kOffRow = kOffMisc + 16;                // float2 [kTeams][128]
   static constexpr int kOffRuns = (kOffRow + kTeams * 128 * 8 + 15) / 16 * 16;  // float4 [2 groups][kGroup tiles][8 runs]
-  static constexpr int kBytes = kOffRuns + 2 * kGroup * 8 * 16 + 1024;   // + alignment slack
+  static constexpr int kOffRange = kOffRuns + 2 * kGroup * 8 * 16;       // float2 [loader warps]
+  static constexpr int kBytes = kOffRange + kLoaders / 32 * 8 + 1024;    // + alignment slack
   static_assert(kBytes <= 227 * 1024 && kOffRow % 8 == 0 && kOffRuns % 16 == 0, "shared memory");
   static constexpr int kStage = kOffBar - kSoftmax / 32 * 4096;   // kSplitKeys: 4 KB per softmax warp for the output's way
   static_assert(kOffV % 1024 == 0 && (!kSplitKeys || kStage >= 128 * D * 4), "room for the teams' halves of O before it");
@@ -102,6 +105,14 @@ __device__ __forceinline__ uint4 widen8(uint2 w) {
   auto two = [](uint32_t x) {
     const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(x & 0xffffu), __NV_E4M3);
     return *reinterpret_cast<const uint32_t *>(&h);
+  };
+  return make_uint4(two(w.x), two(w.x >> 16), two(w.y), two(w.y >> 16));
+}
+// The same -> bf16 values, exactly (the upper halves of the fp32 patterns).
+__device__ __forceinline__ uint4 widen8_bf16(uint2 w) {
+  auto two = [](uint32_t x) {
+    const float2 f = unpack2_e4m3(x);
+    return __byte_perm(__float_as_uint(f.x), __float_as_uint(f.y), 0x7632);
   };
   return make_uint4(two(w.x), two(w.x >> 16), two(w.y), two(w.y >> 16));
 }
@@ -131,6 +142,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t *fin = q_ready + 1;                   // [team] every MMA of the team complete
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::kOffMisc);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::kOffMisc + 8);
+  volatile int *wide_flag = reinterpret_cast<volatile int *>(smem + L::kOffMisc + 12);   // V and w in bf16; set when sc_full[0] is
   float2 *row_info = reinterpret_cast<float2 *>(smem + L::kOffRow);
   // of each run of 16 keys of tile j, at [j % (2 kGroup)]: K's scale, log2 of V's, 1 / V's
   float4 *runs = reinterpret_cast<float4 *>(smem + L::kOffRuns);
@@ -292,99 +304,113 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 
     const int n = steps(team);
-    float m_ref = kNegInf;                       // reference maximum, log2 units
+    float m_ref = kNegInf, msub = 0.f;           // reference maximum, log2 units, and what exponents are less of
     float2 lacc = make_float2(0.f, 0.f);         // row sum in two parts
     const float2 ones = make_float2(1.f, 1.f);
     bool ok = true;
     const uint32_t sb = sbuf(team) + lane_base, ob = obuf(team) + lane_base;
-    for (int h = 0; h < n; ++h) {
-      const int b = h & 1, tb = team * 2 + b;
-      const int j = tile_of(team, h);
-      if ((h & (kGroup * (kSplitKeys ? 1 : 2) - 1)) == 0) ok = wait_all(&sc_full[(j / kGroup) & 1], (j / (2 * kGroup)) & 1);
-      const float4 *run = runs + 8 * (j % (2 * kGroup)) + 4 * b;   // the half's four runs
-      ok = ok && wait_all(&s_full[tb], (h >> 1) & 1);
-      if (!ok) break;
-      tc_fence_after();
-      const uint32_t sh = sb + kHalf * b;
-      float v[2][32];
-      tmem_ld32_start(sh, v[0]);
-      tmem_ld32_start(sh + 32, v[1]);
-      // run r's score factor, log2 units (not 0: a masked score stays -inf), and log2 of V's scale
-      float factor[4], add[4];
+    auto softmax = [&](auto in_bf16) {
+      constexpr bool kWide = decltype(in_bf16)::value;
+      for (int h = 0; h < n; ++h) {
+        const int b = h & 1, tb = team * 2 + b;
+        const int j = tile_of(team, h);
+        if ((h & (kGroup * (kSplitKeys ? 1 : 2) - 1)) == 0) ok = wait_all(&sc_full[(j / kGroup) & 1], (j / (2 * kGroup)) & 1);
+        const float4 *run = runs + 8 * (j % (2 * kGroup)) + 4 * b;   // the half's four runs
+        ok = ok && wait_all(&s_full[tb], (h >> 1) & 1);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t sh = sb + kHalf * b;
+        float v[2][32];
+        tmem_ld32_start(sh, v[0]);
+        tmem_ld32_start(sh + 32, v[1]);
+        // run r's score factor, log2 units (not 0: a masked score stays -inf), and log2 of V's scale
+        float factor[4], add[4];
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const float4 x = run[r];
-        factor[r] = fmaxf(cmul * x.x, 1e-37f);
-        add[r] = x.y;
-      }
-      tmem_ld32_finish(v[0]);
-      tmem_ld32_finish(v[1]);
-      const int nvis = lim - j * kN - kHalf * b;
-      if (!__all_sync(0xffffffffu, nvis >= kHalf)) {
+        for (int r = 0; r < 4; ++r) {
+          const float4 x = run[r];
+          factor[r] = fmaxf(cmul * x.x, 1e-37f);
+          add[r] = x.y;
+        }
+        tmem_ld32_finish(v[0]);
+        tmem_ld32_finish(v[1]);
+        const int nvis = lim - j * kN - kHalf * b;
+        if (!__all_sync(0xffffffffu, nvis >= kHalf)) {
 #pragma unroll
-        for (int e = 0; e < kHalf; ++e)
-          if (e >= nvis) v[e >> 5][e & 31] = kNegInf;
-      }
-      // maximum of a + log2 sv
-      float mt = kNegInf;
+          for (int e = 0; e < kHalf; ++e)
+            if (e >= nvis) v[e >> 5][e & 31] = kNegInf;
+        }
+        // maximum of a + log2 sv
+        float mt = kNegInf;
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const float *x = &v[r >> 1][16 * (r & 1)];
-        float c0 = fmax3(x[0], x[1], x[2]), c1 = fmax3(x[3], x[4], x[5]);
-        c0 = fmax3(c0, x[6], x[7]), c1 = fmax3(c1, x[8], x[9]);
-        c0 = fmax3(c0, x[10], x[11]), c1 = fmax3(c1, x[12], x[13]);
-        mt = fmaxf(mt, fmaf(fmax3(fmaxf(c0, c1), x[14], x[15]), factor[r], add[r]));
-      }
-      const bool rescale = mt > m_ref + kRescaleLog2;
-      if (__any_sync(0xffffffffu, rescale)) {
-        const float alpha = rescale ? fast_exp2(m_ref - mt) : 1.f;
-        if (h > 0) {   // O holds the P.V of steps 0 .. h - 1: the last of them has to be complete
-          ok = wait_all(&o_done[tb ^ 1], ((h - 1) >> 1) & 1);
-          if (!ok) break;
-          tc_fence_after();
+        for (int r = 0; r < 4; ++r) {
+          const float *x = &v[r >> 1][16 * (r & 1)];
+          float c0 = fmax3(x[0], x[1], x[2]), c1 = fmax3(x[3], x[4], x[5]);
+          c0 = fmax3(c0, x[6], x[7]), c1 = fmax3(c1, x[8], x[9]);
+          c0 = fmax3(c0, x[10], x[11]), c1 = fmax3(c1, x[12], x[13]);
+          mt = fmaxf(mt, fmaf(fmax3(fmaxf(c0, c1), x[14], x[15]), factor[r], add[r]));
+        }
+        const bool rescale = mt > m_ref + kRescaleLog2;
+        if (__any_sync(0xffffffffu, rescale)) {
+          const float alpha = rescale ? fast_exp2(m_ref - mt) : 1.f;
+          if (h > 0) {   // O holds the P.V of steps 0 .. h - 1: the last of them has to be complete
+            ok = wait_all(&o_done[tb ^ 1], ((h - 1) >> 1) & 1);
+            if (!ok) break;
+            tc_fence_after();
 #pragma unroll 1
-          for (int c0 = 0; c0 < D; c0 += 16) {
-            float o[16];
-            uint32_t ow[16];
-            tmem_ld16(ob + c0, o);
+            for (int c0 = 0; c0 < D; c0 += 16) {
+              float o[16];
+              uint32_t ow[16];
+              tmem_ld16(ob + c0, o);
 #pragma unroll
-            for (int e = 0; e < 16; ++e) ow[e] = __float_as_uint(o[e] * alpha);
-            tmem_st16(ob + c0, ow);
+              for (int e = 0; e < 16; ++e) ow[e] = __float_as_uint(o[e] * alpha);
+              tmem_st16(ob + c0, ow);
+            }
+          }
+          if (rescale) {
+            lacc = make_float2(lacc.x * alpha, lacc.y * alpha);
+            m_ref = mt;
+            msub = mt - kTopLog2;
           }
         }
-        if (rescale) {
-          lacc = make_float2(lacc.x * alpha, lacc.y * alpha);
-          m_ref = mt;
-        }
-      }
-      const float msub = m_ref == kNegInf ? 0.f : m_ref;
-      // w = 2^(a + log2 sv - m_ref), rounded to f16, and the sum of w / sv
+        // w = 2^(a + log2 sv - msub), rounded to f16 (or in two terms), and the sum of w / sv
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const float *x = &v[r >> 1][16 * (r & 1)];
-        const float nr = add[r] - msub, iv = run[r].z;
-        const float2 cc = make_float2(factor[r], factor[r]), nm = make_float2(nr, nr);
-        float2 sum[2] = {{0.f, 0.f}, {0.f, 0.f}};
-        uint32_t w[8], wl[8];
+        for (int r = 0; r < 4; ++r) {
+          const float *x = &v[r >> 1][16 * (r & 1)];
+          const float nr = add[r] - msub, iv = run[r].z;
+          const float2 cc = make_float2(factor[r], factor[r]), nm = make_float2(nr, nr);
+          float2 sum[2] = {{0.f, 0.f}, {0.f, 0.f}};
+          uint32_t w[8], wl[8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const float2 a = ffma2(make_float2(x[2 * k], x[2 * k + 1]), cc, nm);
-          const float2 pk = make_float2(fast_exp2(a.x), fast_exp2(a.y));
-          if constexpr (kLo) w[k] = f16x2_split(pk.x, pk.y, wl[k]);
-          else asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w[k]) : "f"(pk.y), "f"(pk.x));
-          sum[k & 1] = ffma2(pk, ones, sum[k & 1]);
+          for (int k = 0; k < 8; ++k) {
+            const float2 a = ffma2(make_float2(x[2 * k], x[2 * k + 1]), cc, nm);
+            const float2 pk = make_float2(fast_exp2(a.x), fast_exp2(a.y));
+            if constexpr (kWide) {
+              w[k] = pack2(pk.x, pk.y, __nv_bfloat16{});
+              wl[k] = pack2(pk.x - __uint_as_float(w[k] << 16), pk.y - __uint_as_float(w[k] & 0xffff0000u), __nv_bfloat16{});
+            } else if constexpr (kLo) {
+              w[k] = f16x2_split(pk.x, pk.y, wl[k]);
+            } else {
+              asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w[k]) : "f"(pk.y), "f"(pk.x));
+            }
+            sum[k & 1] = ffma2(pk, ones, sum[k & 1]);
+          }
+          lacc = ffma2(make_float2(sum[0].x + sum[1].x, sum[0].y + sum[1].y), make_float2(iv, iv), lacc);
+          if constexpr (kLo || kWide) {   // hi, lo of 16 keys over their own 16 columns
+            tmem_st8(sh + 16 * r, w);
+            tmem_st8(sh + 16 * r + 8, wl);
+          } else {
+            tmem_st8(sh + 8 * r, w);
+          }
         }
-        lacc = ffma2(make_float2(sum[0].x + sum[1].x, sum[0].y + sum[1].y), make_float2(iv, iv), lacc);
-        if constexpr (kLo) {   // hi, lo of 16 keys over their own 16 columns
-          tmem_st8(sh + 16 * r, w);
-          tmem_st8(sh + 16 * r + 8, wl);
-        } else {
-          tmem_st8(sh + 8 * r, w);
-        }
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(&p_full[tb]);
       }
-      tmem_wait_st();
-      tc_fence_before();
-      mbar_arrive(&p_full[tb]);
+    };
+    if (n > 0) {
+      ok = wait_all(&sc_full[0], 0);
+      // (the vote: a branch that the whole warp is known to take)
+      if (ok) __any_sync(0xffffffffu, *wide_flag) ? softmax(std::true_type{}) : softmax(std::false_type{});
     }
     float l = lacc.x + lacc.y;
     if (ok && n > 0) ok = wait_all(&o_done[team * 2 + ((n - 1) & 1)], ((n - 1) >> 1) & 1);
@@ -531,7 +557,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int pn = 0; pn < kPanels; ++pn) w[pn][i] = ld_nc8(pool + x.at[i >> 2] + ((4 * i) & 15) * D + pn * 64);
     };
     const uint32_t to0 = (32 * lw + rr0) * 128 + ((q ^ rr0) << 4), to1 = to0 ^ 64;   // row 4 i + rr0: its chunk q ^ (row & 7)
-    auto widen = [&](Words &w, const Rows &x, uint8_t *tile) {
+    auto widen = [&](Words &w, const Rows &x, uint8_t *tile, auto wider) {
       if (x.n[0] + x.n[1] < 32) {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
@@ -543,7 +569,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = 0; i < 8; ++i)
 #pragma unroll
         for (int pn = 0; pn < kPanels; ++pn)
-          *reinterpret_cast<uint4 *>(tile + (i & 1 ? to1 : to0) + i * 512 + pn * kPanel) = widen8(w[pn][i]);
+          *reinterpret_cast<uint4 *>(tile + (i & 1 ? to1 : to0) + i * 512 + pn * kPanel) = wider(w[pn][i]);
       fence_async_smem();
     };
     // Scales, by loader warp 0, a run to each lane (1 for a run without tokens, and for a bad one after its report): those of
@@ -578,40 +604,77 @@ __global__ void __launch_bounds__(kThreads, 1)
       if constexpr (!kRaw) load(now, kpool, kw);
       load(now, vpool, vw);
     }
-    int32_t scale_blk = -1;
+    int32_t scale_blk = -1, second = -1;
     if (lw == 0) {
       scale_blk = run_block(0);
-      const int32_t second = run_block(1);
+      second = run_block(1);
       read_scales(scale_blk);
       scale_blk = run_block(2);
+    }
+    // The least and the largest of V's scales of all the CTA's keys (bad ones are reported where they are published).  Its loads
+    // run beside those of the first scales: 4 chunks of 2048 take 685 us with the scan and without it, 699 with the scan first.
+    bool wide;
+    {
+      float low = -kNegInf, top = 0.f;
+      const int blocks = (max(keys0, keys1) + p.block_size - 1) >> bs_log2;
+#pragma unroll 4
+      for (int i = lw * 32 + lane; i < blocks; i += kLoaders) {
+        const int32_t bi = __ldg(table + i);
+        const bool in = bi >= 0 && bi < p.num_blocks;
+        const float s = __ldg(p.v_scales + (in ? (int64_t)bi * p.num_kv_heads + g : 0));
+        if (in && block_scale_ok(s)) low = fminf(low, s), top = fmaxf(top, s);
+      }
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) {
+        low = fminf(low, __shfl_xor_sync(0xffffffffu, low, off));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+      }
+      float2 *range = reinterpret_cast<float2 *>(smem + L::kOffRange);
+      if (lane == 0) range[lw] = make_float2(low, top);
+      asm volatile("bar.sync 2, %0;" ::"n"(kLoaders) : "memory");
+      const float2 x = range[lane % (kLoaders / 32)];
+      low = x.x, top = x.y;
+#pragma unroll
+      for (int off = kLoaders / 64; off > 0; off >>= 1) {
+        low = fminf(low, __shfl_xor_sync(0xffffffffu, low, off));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+      }
+      wide = __any_sync(0xffffffffu, low * kNarrowScales < top);
+      if (lw == 0 && lane == 0) *wide_flag = wide;
+    }
+    if (lw == 0) {
       put_scales(0);
       read_scales(second);
       put_scales(1);
       read_scales(scale_blk);
       scale_blk = run_block(3);
     }
-    for (int j = 0; j < nkt; ++j) {
-      const int s = j % kStages;
-      if (j + 1 < nkt) next = rows_of(j + 1);
-      if constexpr (!kRaw) {
-        const int ks = j % kKStages;
-        if (j >= kKStages && !wait_all(&k_free[ks], ((j / kKStages) - 1) & 1)) break;
-        widen(kw, now, smem + L::kOffK + ks * kKTile);
-        mbar_arrive(&k_full[ks]);
-        if (j + 1 < nkt) load(next, kpool, kw);
+    auto walk = [&](auto wider) {
+      for (int j = 0; j < nkt; ++j) {
+        const int s = j % kStages;
+        if (j + 1 < nkt) next = rows_of(j + 1);
+        if constexpr (!kRaw) {
+          const int ks = j % kKStages;
+          if (j >= kKStages && !wait_all(&k_free[ks], ((j / kKStages) - 1) & 1)) break;
+          widen(kw, now, smem + L::kOffK + ks * kKTile, [](uint2 c) { return widen8(c); });
+          mbar_arrive(&k_full[ks]);
+          if (j + 1 < nkt) load(next, kpool, kw);
+        }
+        if (j >= kStages && !wait_all(&v_free[s], ((j / kStages) - 1) & 1)) break;
+        widen(vw, now, smem + L::kOffV + s * kTile, wider);
+        mbar_arrive(&v_full[s]);
+        if (j + 1 < nkt) load(next, vpool, vw);
+        now = next;
+        if (lw == 0 && j % kGroup == kStages - 1 && j > kGroup) {
+          const int group = j / kGroup + 1;
+          put_scales(group);
+          read_scales(scale_blk);
+          scale_blk = run_block(group + 2);
+        }
       }
-      if (j >= kStages && !wait_all(&v_free[s], ((j / kStages) - 1) & 1)) break;
-      widen(vw, now, smem + L::kOffV + s * kTile);
-      mbar_arrive(&v_full[s]);
-      if (j + 1 < nkt) load(next, vpool, vw);
-      now = next;
-      if (lw == 0 && j % kGroup == kStages - 1 && j > kGroup) {
-        const int group = j / kGroup + 1;
-        put_scales(group);
-        read_scales(scale_blk);
-        scale_blk = run_block(group + 2);
-      }
-    }
+    };
+    if (wide) walk([](uint2 c) { return widen8_bf16(c); });
+    else walk([](uint2 c) { return widen8(c); });
   } else if (kRaw && warp == kKWarp) {
     // ===================================================== K tiles as stored
     // one box per cache block that holds a key; what the tile's other rows hold is masked in the scores
@@ -645,7 +708,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // runs the schedule, the elected lane's predicate issues: operands stay in uniform registers)
     const bool leader = elect_one();
     const int team = warp - kMmaWarp, n = steps(team);
-    const uint32_t idesc_s = umma_idesc(0, kHalf, false), idesc_o = umma_idesc(0, D, true);
+    const uint32_t idesc_s = umma_idesc(0, kHalf, false);
     constexpr bool kSw64 = kRaw && D == 64;     // rows of 64 bytes
     const uint32_t q_at = smem_u32(smem + L::kOffQ) + (kSplitKeys ? 0 : team * kTile), k_at = smem_u32(smem + L::kOffK);
     const uint64_t qdesc = kSw64 ? umma_desc_sw64(q_at, 16, 512) : umma_desc(q_at, 16);
@@ -677,29 +740,35 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     if (n > 0) issue_s(0);
     if (n > 1 && ok) issue_s(1);
-    for (int h = 0; h < n && ok; ++h) {
-      const int j = tile_of(team, h), b = h & 1, slot = j % kStages;
-      if (b == 0) ok = wait_all(&v_full[slot], (j / kStages) & 1);
-      ok = ok && wait_all(&p_bar[b], (h >> 1) & 1);
-      if (!ok) break;
-      tc_fence_after();
-      const uint64_t vd = vdesc0 + ((slot * kTile + b * kHalf * 128) >> 4);
-      const uint32_t pa = s_at + kHalf * b;
+    auto walk = [&](auto in_bf16) {
+      constexpr bool kWide = decltype(in_bf16)::value;
+      const uint32_t idesc_o = umma_idesc(kWide ? 1 : 0, D, true);
+      for (int h = 0; h < n && ok; ++h) {
+        const int j = tile_of(team, h), b = h & 1, slot = j % kStages;
+        if (b == 0) ok = wait_all(&v_full[slot], (j / kStages) & 1);
+        ok = ok && wait_all(&p_bar[b], (h >> 1) & 1);
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t vd = vdesc0 + ((slot * kTile + b * kHalf * 128) >> 4);
+        const uint32_t pa = s_at + kHalf * b;
 #pragma unroll
-      for (int kk = 0; kk < 4; ++kk) {
-        constexpr int kStep = (16 * 128) >> 4;
-        const uint32_t acc = h + kk > 0 ? 1u : 0u;
-        if constexpr (kLo) {
-          umma_ts_if(leader, o_at, pa + 16 * kk, vd + kk * kStep, idesc_o, acc);
-          umma_ts_if(leader, o_at, pa + 16 * kk + 8, vd + kk * kStep, idesc_o, 1u);
-        } else {
-          umma_ts_if(leader, o_at, pa + 8 * kk, vd + kk * kStep, idesc_o, acc);
+        for (int kk = 0; kk < 4; ++kk) {
+          constexpr int kStep = (16 * 128) >> 4;
+          const uint32_t acc = h + kk > 0 ? 1u : 0u;
+          if constexpr (kLo || kWide) {
+            umma_ts_if(leader, o_at, pa + 16 * kk, vd + kk * kStep, idesc_o, acc);
+            umma_ts_if(leader, o_at, pa + 16 * kk + 8, vd + kk * kStep, idesc_o, 1u);
+          } else {
+            umma_ts_if(leader, o_at, pa + 8 * kk, vd + kk * kStep, idesc_o, acc);
+          }
         }
+        umma_commit_if(leader, &o_bar[b]);
+        if (b || h + 1 == n) umma_commit_if(leader, &v_free[slot]);
+        if (h + 2 < n) issue_s(h + 2);
       }
-      umma_commit_if(leader, &o_bar[b]);
-      if (b || h + 1 == n) umma_commit_if(leader, &v_free[slot]);
-      if (h + 2 < n) issue_s(h + 2);
-    }
+    };
+    if (n > 0 && ok) ok = wait_all(&sc_full[0], 0);
+    if (n > 0 && ok) __any_sync(0xffffffffu, *wide_flag) ? walk(std::true_type{}) : walk(std::false_type{});
     // key tiles that only the other team walks
     if constexpr (!kSplitKeys)
       for (int j = (n + 1) / 2; j < nkt && ok; ++j) {

@@ -80,7 +80,7 @@ def run(case, lens, rows, hq, hkv, d, bs, qt, out, where, small, large, seed):
         quiet(o[cu[i]:cu[i + 1]], want, bound, f"sequence {i}: {r} of {n} tokens")
 
 
-@pytest.mark.parametrize("case", ["decode"])
+@pytest.mark.parametrize("case", ["decode", "chunk"])
 @pytest.mark.parametrize("qt,out", OUT)
 @pytest.mark.parametrize("where", ["first", "last", "some", "most"])
 @pytest.mark.parametrize("ratio", [7, 8, 9, 14, 20, 26, 36])
@@ -88,7 +88,7 @@ def test_quiet_tokens_beside_loud_ones(case, qt, out, where, ratio):
     run(case, [40, 300, 1111], [40, 100, 150], 8, 2, 128, 16, qt, out, where, -6, ratio - 6, seed=ratio)
 
 
-@pytest.mark.parametrize("case", ["decode"])
+@pytest.mark.parametrize("case", ["decode", "chunk"])
 @pytest.mark.parametrize("qt,out", [("bf16", "bf16"), ("bf16", "f32"), ("f16", "f32")])
 @pytest.mark.parametrize("where", ["first", "some"])
 @pytest.mark.parametrize("bs", [16, 32])
@@ -106,9 +106,12 @@ def test_decode_of_many_tiles_per_warp(qt, out, d):
         run("decode", lens, None, 16, 4, d, 32, qt, out, where, -10, 20, seed=d)
 
 
-@pytest.mark.parametrize("case", ["decode"])
+@pytest.mark.parametrize("case", ["decode", "chunk"])
 @pytest.mark.parametrize("hq,hkv,d,bs", [(32, 2, 64, 16), (17, 1, 64, 32), (32, 2, 128, 32), (20, 2, 128, 16), (5, 5, 64, 16)])
 def test_heads(case, hq, hkv, d, bs):
-    """Every kernel's form of the heads."""
+    """Every kernel's form of the heads, and (chunks) two query tiles per CTA and one."""
     for qt, out in OUT:
         run(case, [50, 901], [50, 30], hq, hkv, d, bs, qt, out, "some", -8, 12, seed=hq + d)
+    if case == "chunk":
+        for qt, out in OUT:
+            run(case, [1100, 700], [700, 700], 32, 4, d, bs, qt, out, "some", -8, 12, seed=hq + d)
