@@ -116,6 +116,12 @@ __device__ __forceinline__ uint4 widen8_bf16(uint2 w) {
   };
   return make_uint4(two(w.x), two(w.x >> 16), two(w.y), two(w.y >> 16));
 }
+// Two f16 values, an infinity made NaN: x + 0 x.
+__device__ __forceinline__ uint32_t nan_for_inf(uint32_t x) {
+  uint32_t y;
+  asm("fma.rn.f16x2 %0, %1, %2, %1;" : "=r"(y) : "r"(x), "r"(0u));
+  return y;
+}
 
 template <typename QT, int D, bool kSplitKeys, bool kLo>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -261,7 +267,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int off = kC / 2; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
             const int eb = max(1, (int)((__float_as_uint(amax) >> 23) & 0xff));
             const int e = amax > 0.f ? max(-126, min(126, (kRaw ? 134 : 141) - eb)) : 0;
-            const float sc = __uint_as_float((uint32_t)(e + 127) << 23);
+            // (an infinity makes the whole row NaN, as every score of the row is infinite or NaN: e4m3 has no infinity, and a row
+            // of scores that are all -inf would pass for one that sees no key)
+            const float sc = __uint_as_float(amax == -kNegInf ? 0x7fc00000u : (uint32_t)(e + 127) << 23);
             back = __uint_as_float((uint32_t)(127 - e) << 23);   // 2^-e
             if constexpr (kRaw) {
               const float sign = p.s_mult < 0.f ? -sc : sc;
@@ -290,6 +298,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (ch == 0) {
             row_info[(kSplitKeys ? 0 : team * 128) + mr].x = back;
             if (kSplitKeys) row_info[128 + mr].x = back;
+          }
+          if constexpr (!kBf16) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) ws[k] = nan_for_inf(ws[k]);
           }
           if constexpr (!kRaw)
             *reinterpret_cast<uint4 *>(qt + (ch >> 3) * kPanel + mr * 128 + (((ch & 7) ^ (mr & 7)) << 4)) =
