@@ -611,7 +611,8 @@ PA_API pa_status pa_copy_blocks_scaled(void *k_cache, void *v_cache, const pa_kv
  * pa_decode_scaled -- pa_decode over a block-scaled cache: K_i[p] is code *
  * k_block_scales[b][g] and V_i[p] code * v_block_scales[b][g], b the block of
  * position p.  Scales need not be powers of two; one out of [2^-64, 2^32] sets
- * PA_ERR_DEVICE_CHECK (the rows that read it are then undefined).  The products
+ * PA_ERR_DEVICE_CHECK (the rows that read it are then undefined).  A block id out
+ * of range sets it too, and the block's tokens are left out.  The products
  * take the codes as they are: K's scales meet the scores, V's the softmax
  * weights, whose sum stays that of the weights without them, in fp32.  A weight
  * is held to 2^-11 of itself for a 16-bit output and to 2^-22 for an fp32 one

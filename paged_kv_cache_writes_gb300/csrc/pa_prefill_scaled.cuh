@@ -66,6 +66,7 @@ constexpr int kThreads = (kKWarp + 1) * 32;
 constexpr int kHalf = 64;                      // keys per softmax step
 constexpr int kGroup = 4;                      // key tiles whose scales are published together: a warp's 32 runs
 constexpr int kPanel = kN * 128;               // 64 elements of 128 rows
+constexpr int32_t kNoKeys = -1, kLost = -2;    // in a block id's place: behind the sequence's end, or an id out of range
 constexpr float kRescaleLog2 = 8.f;            // O is rescaled when the maximum exceeds its reference by 2^8
 constexpr float kTopLog2 = 7.f;                // w at the reference, 2^15 at most: as high as f16 allows, for the small ones' sake
 
@@ -584,19 +585,22 @@ __global__ void __launch_bounds__(kThreads, 1)
           *reinterpret_cast<uint4 *>(tile + (i & 1 ? to1 : to0) + i * 512 + pn * kPanel) = wider(w[pn][i]);
       fence_async_smem();
     };
-    // Scales, by loader warp 0, a run to each lane (1 for a run without tokens, and for a bad one after its report): those of
-    // tiles kGroup G .. + kGroup - 1 are published when the P.V of tile kGroup (G - 2) + kGroup - 1, the last that used their
-    // place, is complete; the next group's are in flight then, and the block ids of the one after it
+    // Scales, by loader warp 0, a run to each lane (1 for a run without tokens, and for a bad one after its report; log2 of V's
+    // is -inf for a lost run, whose K and V are zeros, which leaves its keys out of the softmax): those of tiles kGroup G ..
+    // + kGroup - 1 are published when the P.V of tile kGroup (G - 2) + kGroup - 1, the last that used their place, is complete;
+    // the next group's are in flight then, and the block ids of the one after it
     auto run_block = [&](int group) -> int32_t {
       const int j = kGroup * group + (lane >> 3), key = j * kN + 16 * (lane & 7);
-      if (j >= nkt || key >= seq_eff) return -1;
+      if (j >= nkt || key >= seq_eff) return kNoKeys;
       const int32_t bi = __ldg(table + (key >> bs_log2));
-      return bi >= 0 && bi < p.num_blocks ? bi : -1;
+      return bi >= 0 && bi < p.num_blocks ? bi : kLost;
     };
     static_assert(kGroup * 8 == 32, "a warp's runs");
     float sk = 1.f, sv = 1.f;
+    bool lost = false;
     auto read_scales = [&](int32_t b) {
       sk = sv = 1.f;
+      lost = b == kLost;
       if (b >= 0) {
         const int64_t at = (int64_t)b * p.num_kv_heads + g;
         sk = __ldg(p.k_scales + at);
@@ -606,7 +610,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto put_scales = [&](int group) {
       const bool good = block_scale_ok(sk) && block_scale_ok(sv);
       if (!good) record_error(p.err, PA_ERR_DEVICE_CHECK);
-      runs[32 * (group & 1) + lane] = good ? make_float4(sk, __log2f(sv), __fdividef(1.f, sv), 0.f) : make_float4(1.f, 0.f, 1.f, 0.f);
+      if (!good) sk = sv = 1.f;
+      runs[32 * (group & 1) + lane] = make_float4(sk, lost ? kNegInf : __log2f(sv), __fdividef(1.f, sv), 0.f);
       __syncwarp();
       if (lane == 0) mbar_arrive(&sc_full[group & 1]);
     };
@@ -616,7 +621,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if constexpr (!kRaw) load(now, kpool, kw);
       load(now, vpool, vw);
     }
-    int32_t scale_blk = -1, second = -1;
+    int32_t scale_blk = kNoKeys, second = kNoKeys;
     if (lw == 0) {
       scale_blk = run_block(0);
       second = run_block(1);
@@ -689,13 +694,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     else walk([](uint2 c) { return widen8(c); });
   } else if (kRaw && warp == kKWarp) {
     // ===================================================== K tiles as stored
-    // one box per cache block that holds a key; what the tile's other rows hold is masked in the scores
+    // one box per cache block that holds a key; what the rows behind the end hold is masked in the scores
     const int bs = p.block_size, per_tile = kN / bs;
-    auto block = [&](int j) -> int32_t {   // lane i: the id of block i of tile j (-1: none; out of range: the loaders report it)
+    // lane i: the id of block i of tile j; for one out of range (the loaders report it) that of the block behind the pool, whose
+    // box the copy fills with zeros
+    auto block = [&](int j) -> int32_t {
       const int key = j * kN + lane * bs;
-      if (lane >= per_tile || j >= nkt || key >= seq_eff) return -1;
+      if (lane >= per_tile || j >= nkt || key >= seq_eff) return kNoKeys;
       const int32_t bi = __ldg(table + (key >> bs_log2));
-      return bi >= 0 && bi < p.num_blocks ? bi : -1;
+      return bi >= 0 && bi < p.num_blocks ? bi : (int32_t)p.num_blocks;
     };
     int32_t next = block(0);
     int issued = 0;
