@@ -585,10 +585,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           *reinterpret_cast<uint4 *>(tile + (i & 1 ? to1 : to0) + i * 512 + pn * kPanel) = wider(w[pn][i]);
       fence_async_smem();
     };
-    // Scales, by loader warp 0, a run to each lane (1 for a run without tokens, and for a bad one after its report; log2 of V's
-    // is -inf for a lost run, whose K and V are zeros, which leaves its keys out of the softmax): those of tiles kGroup G ..
-    // + kGroup - 1 are published when the P.V of tile kGroup (G - 2) + kGroup - 1, the last that used their place, is complete;
-    // the next group's are in flight then, and the block ids of the one after it
+    // Scales, by loader warp 0, a run to each lane (1 for a run without tokens; -inf as log2 of V's, which leaves its keys out of
+    // the softmax, for one whose block is lost, its K and V being zeros, or has a scale out of range): those of tiles kGroup G
+    // .. + kGroup - 1 are published when the P.V of tile kGroup (G - 2) + kGroup - 1, the last that used their place, is
+    // complete; the next group's are in flight then, and the block ids of the one after it
     auto run_block = [&](int group) -> int32_t {
       const int j = kGroup * group + (lane >> 3), key = j * kN + 16 * (lane & 7);
       if (j >= nkt || key >= seq_eff) return kNoKeys;
@@ -597,10 +597,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     static_assert(kGroup * 8 == 32, "a warp's runs");
     float sk = 1.f, sv = 1.f;
-    bool lost = false;
     auto read_scales = [&](int32_t b) {
-      sk = sv = 1.f;
-      lost = b == kLost;
+      sk = 1.f;
+      sv = b == kLost ? 0.f : 1.f;           // (out of range)
       if (b >= 0) {
         const int64_t at = (int64_t)b * p.num_kv_heads + g;
         sk = __ldg(p.k_scales + at);
@@ -610,8 +609,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto put_scales = [&](int group) {
       const bool good = block_scale_ok(sk) && block_scale_ok(sv);
       if (!good) record_error(p.err, PA_ERR_DEVICE_CHECK);
-      if (!good) sk = sv = 1.f;
-      runs[32 * (group & 1) + lane] = make_float4(sk, lost ? kNegInf : __log2f(sv), __fdividef(1.f, sv), 0.f);
+      runs[32 * (group & 1) + lane] = good ? make_float4(sk, __log2f(sv), __fdividef(1.f, sv), 0.f) : make_float4(1.f, kNegInf, 1.f, 0.f);
       __syncwarp();
       if (lane == 0) mbar_arrive(&sc_full[group & 1]);
     };

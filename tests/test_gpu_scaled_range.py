@@ -107,6 +107,14 @@ def test_decode_of_many_tiles_per_warp(qt, out, d):
 
 
 @pytest.mark.parametrize("case", ["decode", "chunk"])
+@pytest.mark.parametrize("where", ["first", "last", "some"])
+def test_far_into_a_context(case, where):
+    for qt, out in OUT:
+        run(case, [6001, 4300], [130, 20], 8, 2, 128, 16, qt, out, where, -8, 10, seed=3)
+        run(case, [9000], [64], 8, 1, 64, 16, qt, out, where, -8, 14, seed=4)
+
+
+@pytest.mark.parametrize("case", ["decode", "chunk"])
 @pytest.mark.parametrize("hq,hkv,d,bs", [(32, 2, 64, 16), (17, 1, 64, 32), (32, 2, 128, 32), (20, 2, 128, 16), (5, 5, 64, 16)])
 def test_heads(case, hq, hkv, d, bs):
     """Every kernel's form of the heads, and (chunks) two query tiles per CTA and one."""
