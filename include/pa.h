@@ -574,7 +574,7 @@ PA_API pa_status pa_evict(void *k_cache, void *v_cache, const pa_kv_cache *cache
  * The block-scaled cache.  An fp8 pool in which a code of block b and KV head h
  * means code * scales[b][h], one fp32 scale per block and head and pool; the
  * descriptor's k_scale and v_scale are not used and its per-head scales must be
- * NULL.  Scales are in [2^-64, 2^32].  This call chooses them: powers of two, so
+ * NULL.  Scales are in [2^-64, 2^32]; the two arrays must not overlap.  This call chooses them: powers of two, so
  * that changing one later only moves the codes' exponents.  For a block whose
  * first slot is among the call's new tokens: the smallest 2^e with
  * |x| <= 448 * 2^e for every finite new x (2^-64 at least; 2^32 at most, larger
@@ -582,13 +582,16 @@ PA_API pa_status pa_evict(void *k_cache, void *v_cache, const pa_kv_cache *cache
  * first new one: the scale it has, if the new elements fit in 448 times it; else
  * the power of two as above, and the codes of the held tokens become
  * e4m3(code * old / new), exact but for codes that fall below e4m3's normal
- * range.  The new codes are e4m3(x / scale); slots behind the new ones are not
- * touched.  New tokens of one block must be within block_size consecutive
- * tokens of the call, each in a slot of its own (as a sequence's tokens in order
- * are; padding between them counts): else that block's codes and scale are
- * undefined.  A block to be added
- * to whose scale is out of range sets PA_ERR_DEVICE_CHECK and keeps its tokens;
- * the new ones are not stored.  A block shared with another sequence is copied
+ * range if old is a power of two, else rounded to e4m3 once more.  The new codes
+ * are e4m3(x / scale).  Slots behind the new ones, and slots left out between
+ * them, are not touched, though the scale may be another afterwards: what they
+ * held is no longer a value.  So a call's tokens are the last ones of their block;
+ * one token inside a block is not replaced alone.  New tokens of one block must
+ * be within block_size consecutive tokens of the call, each in a slot of its own
+ * (as a sequence's tokens in order are; padding between them counts): else that
+ * block's codes and scale are undefined.  A block to be added to whose scale is
+ * out of range sets PA_ERR_DEVICE_CHECK and keeps its tokens; the new ones are not
+ * stored.  A block shared with another sequence is copied
  * first (pa_bm_append's pairs, pa_copy_blocks_scaled).
  * pa_evict does not take a block-scaled cache: it moves rows between blocks.
  */

@@ -28,11 +28,11 @@
 // widened to bf16: f16 would lose the tokens of small values (pa_internal.h).  (That loop apart costs the other one 1 % of the
 // batch of 64, a branch within one loop 2 %.)
 // (The tensor-memory decode of pa_decode_tc.cuh, given block scales, was bound by the hand-overs between its roles: 64
-// sequences of 300-16000, 64/8 heads 279 us against 176; 33 of 1-5000, 40/8 heads of 64, f16 72 against 27.  Tiles of 16 keys
+// sequences of 300-16000, 64/8 heads 279 us against 175; 33 of 1-5000, 40/8 heads of 64, f16 72 against 27.  Tiles of 16 keys
 // left each warp one chain of dependent steps: 222 us.  With the codes copied to shared memory two tiles ahead: 248; an
-// SM's loads in flight are not what it is short of.)  The batch of 64 runs at 6.1 TB/s, 90 % of a plain copy's rate.  Few tokens
-// cost 7.6 us whatever they are: two launches and the chain lengths, block ids, codes, join; one sequence of 31999 tokens
-// takes 22.6 us, 26 tiles to each CTA.
+// SM's loads in flight are not what it is short of.)  The batch of 64 runs at 6.0 TB/s, 89 % of a plain copy's rate (178 us; 193 with V
+// scales 2^12 apart, 184 with an fp32 output).  Few tokens cost 7.6 us whatever they are: two launches and the chain lengths,
+// block ids, codes, join; one sequence of 31999 tokens takes 22.8 us, 26 tiles to each CTA.
 //
 // Work.  The tiles of 32 keys of all (row, KV head share) in order are cut into equal ranges, one per CTA (six or eight
 // warps, two CTAs per SM; fewer CTAs where a range would fall under kMinTiles): whatever the lengths, all finish together.  Every CTA
@@ -51,8 +51,10 @@ namespace {
 
 constexpr int kTile = 32, kHalf = 16;     // keys per step of a warp, and per MMA
 constexpr int kMinTiles = 8;              // tiles per CTA at least, while there are enough: about one per warp
-// What a piece costs beside its tiles (its queries, the first codes' latency, the join of the warps), in tiles: about 3 us,
-// where an SM's share of the copy rate brings a tile in 0.4 (head_dim 64: 0.2) us
+// What a piece costs beside its tiles (its queries, the first codes' latency, the join of the warps), in tiles: some 3 us,
+// which is 8 (head_dim 64: 15) tiles at an SM's share of the copy rate.  Chosen by time: with 1, 8, 12 and 16 tiles 64 sequences of
+// 300-16000 take 195, 181, 177 and 177 us; at head_dim 64, with 1, 8, 16 and 24, 126, 114, 108 and 109, and 33 of 1-5000 44, 31,
+// 27 and 28.
 template <int D>
 constexpr int kPieceCost = D == 128 ? 12 : 16;
 constexpr int kChunk = 1024;              // rows whose tile counts a CTA has at hand

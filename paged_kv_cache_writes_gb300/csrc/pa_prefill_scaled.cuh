@@ -32,10 +32,10 @@
 // A team's score buffer is two halves of 64 keys, each with its own softmax step: while a team's threads work on one half,
 // the tensor cores compute the other half's scores and the P.V of the one before.  P (f16 pairs; hi + lo) goes over its own
 // half.  (With one buffer of 128 keys a team waited for P.V and the next Q.K^T in turn: 821 us against 721 for 4 chunks of
-// 2048 at 2048, 64/8 heads; 682 now.)
+// 2048 at 2048, 64/8 heads; 688 now, 959 with V scales 2^12 apart, 923 with an fp32 output.)
 //
-// Bound by the softmax warps, two per scheduler, one step's chain after another: scores, maximum, weights, hand-over.  At 682
-// us the tensor pipe is busy 52 % of the time, the issue slots 52 %, the special functions 27 %.  (Scales published for four key
+// Bound by the softmax warps, two per scheduler, one step's chain after another: scores, maximum, weights, hand-over.  At 688
+// us the tensor pipe is busy 51 % of the time, the issue slots 51 %, the special functions 26 %.  (Scales published for four key
 // tiles at once, so that a team waits for them every eighth step: 682 against 694.)  What was tried on that chain
 // at 695 and cost more than it gave: scores and P in buffers of their own, so that Q.K^T waits for no P.V (one more wait per step:
 // 752), the next step's scores loaded under this one's exponentials (814), the two teams' exponentials in turn by a barrier

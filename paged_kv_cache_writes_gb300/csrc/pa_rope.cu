@@ -242,7 +242,8 @@ __device__ __forceinline__ void scaled_block(const RopeParams &p, int64_t t0, ui
     if (amax <= kMaxCode * was) {
       scale = was;
     } else {
-      // the tokens the block holds, by its new scale (code * was / scale is exact in fp32: scale is a power of two)
+      // the tokens the block holds, by its new scale (code * was / scale is exact in fp32 if `was` is a power of two as scale is;
+      // another one's 24 bits times a code's 4 are rounded to fp32 first)
       const float by = was / scale;
       for (int e = lane; e < first * (D / 16); e += 32) {
         const uint4 c = *reinterpret_cast<const uint4 *>(pool + e * 16);
